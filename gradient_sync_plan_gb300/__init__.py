@@ -49,7 +49,10 @@ EXPORTS = ["ddp_status_string", "ddp_abi_version", "ddp_last_cuda_error", "ddp_d
            "ddp_bucket_allreduce_view_fp16",
            "ddp_reducer_create", "ddp_reducer_set_max_ctas", "ddp_reducer_prepare", "ddp_reducer_mark_ready",
            "ddp_reducer_finalize",
-           "ddp_reducer_launch_order", "ddp_reducer_bucket_times", "ddp_reducer_destroy"]
+           "ddp_reducer_launch_order", "ddp_reducer_bucket_times", "ddp_reducer_destroy",
+           "ddp_grad_set_workspace_bytes", "ddp_grad_set_create", "ddp_grad_norm", "ddp_grad_clip", "ddp_grad_norm_clip",
+           "ddp_grad_set_destroy", "ddp_sync_norm_workspace_bytes", "ddp_sync_buckets_norm", "ddp_adamw_create",
+           "ddp_adamw_step", "ddp_adamw_destroy"]
 
 
 class DDPError(RuntimeError):
@@ -118,6 +121,20 @@ def lib() -> ctypes.CDLL:
             L.ddp_reducer_launch_order.argtypes = [vp, P(i32), i32, P(i32)]
             L.ddp_reducer_bucket_times.argtypes = [vp, P(ctypes.c_float), i32, P(i32)]
             L.ddp_reducer_destroy.argtypes = [vp]
+            f64, u8 = ctypes.c_double, ctypes.c_uint8
+            L.ddp_grad_set_workspace_bytes.argtypes = [i32, i32, P(i64), i32, P(i64)]
+            L.ddp_grad_set_create.argtypes = [i32, i32, P(vp), P(i64), i32, vp, i64, P(vp)]
+            L.ddp_grad_norm.argtypes = [vp, vp, vp]
+            L.ddp_grad_clip.argtypes = [vp, vp, f64, vp]
+            L.ddp_grad_norm_clip.argtypes = [vp, vp, f64, vp]
+            L.ddp_grad_set_destroy.argtypes = [vp]
+            L.ddp_sync_norm_workspace_bytes.argtypes = [i32, i32, P(i64), i32, i32, P(i64)]
+            L.ddp_sync_buckets_norm.argtypes = [i32, i32, P(vp), P(i64), P(i32), P(i64), i32, P(i64), P(vp), i32, i32,
+                                                i32, vp, vp, i64, vp]
+            L.ddp_adamw_create.argtypes = [i32, i32, P(vp), P(vp), i32, P(vp), P(vp), P(vp), P(i64), P(u8), vp, vp, vp,
+                                           P(vp)]
+            L.ddp_adamw_step.argtypes = [vp, f64, f64, f64, f64, f64, vp, f64, vp]
+            L.ddp_adamw_destroy.argtypes = [vp]
             for name in EXPORTS[4:]:   # every entry point from ddp_set_max_ctas on returns a status
                 getattr(L, name).restype = i32
             _lib = L
@@ -629,3 +646,183 @@ class Reducer:
         except Exception:
             pass
 
+
+
+def _tensor_table(rows: Sequence[Sequence], what: str, dtypes, like: Optional[list] = None):
+    """rows[r][i] -> (pointers, numels, tensors' dtype or None): contiguous CUDA
+    tensors of one of `dtypes`, the sizes of `like` (or rank 0's) at every rank."""
+    ptrs, numels, dtype = [], like, None
+    for row in rows:
+        n = [t.numel() for t in row]
+        numels = n if numels is None else numels
+        if n != numels:
+            raise ValueError(f"{what}: every rank needs the same tensors")
+        for t in row:
+            dtype = t.dtype if dtype is None else dtype
+            if t.dtype != dtype or t.dtype not in dtypes or not t.is_contiguous():
+                raise ValueError(f"{what} must be contiguous and of one type of {', '.join(map(str, dtypes))}")
+            _check_memory(t, "device", what)
+            ptrs.append(t.data_ptr())
+    return ptrs, numels, dtype
+
+
+def _rank_words(t, world: int, dtype, what: str):
+    """A [world] device tensor of one 32-bit word a rank."""
+    if t.dtype != dtype or t.numel() != world or not t.is_contiguous():
+        raise ValueError(f"{what}: a contiguous {dtype} tensor with one element a rank")
+    _check_memory(t, "device", what)
+    return t.data_ptr()
+
+
+class GradSet:
+    """The gradients of one model at every rank (grads[r][i]), for their global
+    norm and clipping (ddp_grad_set_*).  The tensors are checked once; each call
+    is then one ctypes call.  `norms` holds the last norms, one a rank.  The
+    workspace is allocated on the current stream: a call on another stream comes
+    after it (wait_stream), and so do AdamW's and SyncNormCall's."""
+
+    def __init__(self, grads):
+        torch = _torch()
+        self.world = len(grads)
+        ptrs, numels, dtype = _tensor_table(grads, "gradients", (torch.float32, torch.bfloat16))
+        code = BF16 if dtype == torch.bfloat16 else F32
+        sizes, n = _i64_array(numels or []), len(numels or [])
+        need = ctypes.c_int64(0)
+        _check("ddp_grad_set_workspace_bytes",
+               lib().ddp_grad_set_workspace_bytes(self.world, n, sizes, code, ctypes.byref(need)))
+        device = grads[0][0].device if n else "cuda"
+        self._workspace = torch.empty(need.value // 8, dtype=torch.float64, device=device)
+        self.norms = torch.empty(self.world, dtype=torch.float32, device=device)
+        self._keep = grads
+        h = ctypes.c_void_p()
+        _check("ddp_grad_set_create",
+               lib().ddp_grad_set_create(self.world, n, _vp_array(ptrs), sizes, code, self._workspace.data_ptr(),
+                                         need.value, ctypes.byref(h)))
+        self._h = h
+
+    def _norms(self, t):
+        return self.norms.data_ptr() if t is None or t is self.norms else _rank_words(t, self.world, _torch().float32, "norms")
+
+    def norm(self, out=None, stream=None):
+        """norms[r] of every rank, into `out` or self.norms; returns that tensor."""
+        _check("ddp_grad_norm", lib().ddp_grad_norm(self._h, self._norms(out), _stream(stream)))
+        return self.norms if out is None else out
+
+    def clip(self, max_norm: float, norms=None, stream=None) -> None:
+        """Scale each rank's gradients by min(1, max_norm / (norms[r] + 1e-6)), in place."""
+        _check("ddp_grad_clip", lib().ddp_grad_clip(self._h, self._norms(norms), max_norm, _stream(stream)))
+
+    def norm_clip(self, max_norm: float, out=None, stream=None):
+        """norm() and clip() by it; returns the norms before clipping."""
+        _check("ddp_grad_norm_clip", lib().ddp_grad_norm_clip(self._h, self._norms(out), max_norm, _stream(stream)))
+        return self.norms if out is None else out
+
+    def close(self):
+        if getattr(self, "_h", None):
+            lib().ddp_grad_set_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class SyncNormCall(SyncCall):
+    """SyncCall that also returns the norm of the averaged gradients
+    (ddp_sync_buckets_norm): a [world] tensor, the same value for every rank."""
+
+    def __init__(self, grads, plan, buckets=None, divisor=None, algo=DDP_ALGO_VIEW):
+        super().__init__(grads, plan, buckets, divisor, algo)
+        torch = _torch()
+        need = ctypes.c_int64(0)
+        _check("ddp_sync_norm_workspace_bytes",
+               lib().ddp_sync_norm_workspace_bytes(self.world, self.n_params, self._numel, self.K, self.dtype,
+                                                   ctypes.byref(need)))
+        device = grads[0][0].device if self.n_params else "cuda"
+        self._workspace = torch.empty(need.value // 8, dtype=torch.float64, device=device)
+        self._workspace_bytes = need.value
+        self.norms = torch.empty(self.world, dtype=torch.float32, device=device)
+
+    def __call__(self, stream=None):
+        _check("ddp_sync_buckets_norm",
+               lib().ddp_sync_buckets_norm(self.world, self.n_params, self._grads, self._numel, self._b_of, self._off,
+                                           self.K, self._bn, self._buckets, self.dtype, self.divisor, self.algo,
+                                           self.norms.data_ptr(), self._workspace.data_ptr(), self._workspace_bytes,
+                                           _stream(stream)))
+        return self.norms
+
+
+def ddp_sync_buckets_norm(grads: Sequence[Sequence], plan, buckets: Optional[Sequence[Sequence]] = None,
+                          divisor: Optional[int] = None, algo: int = DDP_ALGO_VIEW, stream=None):
+    """ddp_sync_buckets, and the norm of the averaged gradients ([world], one value)."""
+    call = SyncNormCall(grads, plan, buckets, divisor, algo)
+    norms = call(stream)
+    if stream is not None:                # the call's memory goes back to the allocator: not before `stream` is done
+        torch = _torch()
+        s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+        call._workspace.record_stream(s)
+        norms.record_stream(s)
+    return norms
+
+
+class AdamW:
+    """AdamW over every tensor of every rank, clipping included (ddp_adamw_*).
+
+    params, grads, exp_avg, exp_avg_sq: [r][i] device tensors (registration
+    order); gradients float32 or bfloat16, the others float32.  copies: bf16
+    tensors that receive the new weights.  no_decay: one truth value a tensor,
+    true where weight decay does not apply.  steps: int32 [world], the steps
+    taken so far (zeros if None)."""
+
+    def __init__(self, params, grads, exp_avg, exp_avg_sq, copies=None, no_decay=None, steps=None, stream=None):
+        torch = _torch()
+        self.world = len(params)
+        pp, numels, _ = _tensor_table(params, "params", (torch.float32,))
+        sizes = numels or []
+        for rows, what in ((grads, "grads"), (exp_avg, "exp_avg"), (exp_avg_sq, "exp_avg_sq"), (copies, "copies")):
+            if rows is not None and len(rows) != self.world:
+                raise ValueError(f"{what}: one row a rank")
+        gp, _, gdt = _tensor_table(grads, "grads", (torch.float32, torch.bfloat16), sizes)
+        mp, _, _ = _tensor_table(exp_avg, "exp_avg", (torch.float32,), sizes)
+        vp, _, _ = _tensor_table(exp_avg_sq, "exp_avg_sq", (torch.float32,), sizes)
+        cp = None
+        if copies is not None:
+            cp = _vp_array(_tensor_table(copies, "copies", (torch.bfloat16,), sizes)[0])
+        mask = None
+        if no_decay is not None:
+            if len(no_decay) != len(sizes):
+                raise ValueError("no_decay: one value a tensor")
+            mask = (ctypes.c_uint8 * max(len(sizes), 1))(*[1 if x else 0 for x in no_decay])
+        device = params[0][0].device if sizes else "cuda"
+        self.steps = torch.zeros(self.world, dtype=torch.int32, device=device) if steps is None else steps
+        word = _rank_words(self.steps, self.world, torch.int32, "steps")
+        self._workspace = torch.empty(2, dtype=torch.float64, device=device)       # DDP_ADAMW_WORKSPACE_BYTES
+        self._keep = (params, grads, exp_avg, exp_avg_sq, copies)
+        h = ctypes.c_void_p()
+        _check("ddp_adamw_create",
+               lib().ddp_adamw_create(self.world, len(sizes), _vp_array(pp), _vp_array(gp),
+                                      BF16 if gdt == torch.bfloat16 else F32, _vp_array(mp), _vp_array(vp), cp,
+                                      _i64_array(sizes), mask, word, self._workspace.data_ptr(), _stream(stream),
+                                      ctypes.byref(h)))
+        self._h = h
+
+    def step(self, lr: float, betas: Tuple[float, float] = (0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.0,
+             norms=None, max_norm: float = 0.0, stream=None) -> None:
+        """One step.  norms ([world], as GradSet.norm or SyncNormCall return):
+        clip to max_norm, and skip a rank whose norm is not finite."""
+        n = None if norms is None else _rank_words(norms, self.world, _torch().float32, "norms")
+        _check("ddp_adamw_step",
+               lib().ddp_adamw_step(self._h, lr, betas[0], betas[1], eps, weight_decay, n, max_norm, _stream(stream)))
+
+    def close(self):
+        if getattr(self, "_h", None):
+            lib().ddp_adamw_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass

@@ -1,0 +1,326 @@
+// optim_api.cpp -- the C ABI of the gradient norm, clipping, the sync that
+// returns the norm, and AdamW: argument checks, tables, launches.
+//
+// A grad set or an AdamW handle checks its tensors once, when it is made, and
+// keeps the table that its launches pass to the kernels; a call then costs its
+// launches and nothing that grows with the number of tensors but the table's
+// copy into them.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <memory>
+#include <utility>
+#include <vector>
+
+#include "ddp_abi_guard.h"
+#include "ddp.h"
+#include "ddp_trace.h"
+#include "optim_internal.h"
+
+using namespace ddpk;
+
+struct ddp_grad_set {
+    int32_t world = 0, dtype = 0;
+    std::vector<GradRange> ranges;                             // by rank, then by address
+    std::vector<int32_t> rank_first;                           // first partial of each rank, and their end
+    std::vector<std::pair<uintptr_t, uintptr_t>> spans;        // the memory of the tensors and the workspace, sorted
+    double* partials = nullptr;
+};
+
+struct ddp_adamw {
+    int32_t world = 0, grad_dtype = 0;
+    bool copies = false;
+    std::vector<AdamWItem> items;
+    std::vector<std::pair<uintptr_t, uintptr_t>> spans;        // what a step writes, sorted
+    int32_t* steps = nullptr;
+    int32_t* arrivals = nullptr;
+};
+
+namespace {
+
+using Span = std::pair<uintptr_t, uintptr_t>;      // [first, second) in bytes
+
+Span span_of(const void* p, int64_t bytes) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    return Span{a, a + (uintptr_t)bytes};
+}
+
+// Sorts the spans; true if two of them share a byte.
+bool any_overlap(std::vector<Span>* v) {
+    std::sort(v->begin(), v->end());
+    for (size_t i = 1; i < v->size(); ++i)
+        if ((*v)[i].first < (*v)[i - 1].second) return true;
+    return false;
+}
+
+// True if s shares a byte with one of the sorted, disjoint spans.
+bool hits_any(const std::vector<Span>& sorted, Span s) {
+    auto it = std::lower_bound(sorted.begin(), sorted.end(), Span{s.second, 0});
+    return it != sorted.begin() && std::prev(it)->second > s.first;
+}
+
+// World, tensor count and sizes shared by the three creating calls.
+int32_t check_sizes(int32_t world, int32_t n_params, const int64_t* numel, int32_t dtype) {
+    const int32_t st = common_checks(world, 0, dtype);
+    if (st) return st;
+    if (n_params < 0 || (n_params > 0 && !numel)) return DDP_ERR_INVALID;
+    for (int32_t i = 0; i < n_params; ++i) {
+        const int32_t s = common_checks(world, numel[i], dtype);
+        if (s) return s;
+    }
+    return DDP_OK;
+}
+
+int32_t check_ptr(const void* p, int64_t align) {
+    if (!p) return DDP_ERR_INVALID;
+    return reinterpret_cast<uintptr_t>(p) % (uintptr_t)align ? DDP_ERR_ALIGN : DDP_OK;
+}
+
+// Appends tensor (p, bytes) of rank r, joined to the range before it where it continues it.
+void add_range(std::vector<GradRange>* v, void* p, int64_t bytes, int32_t r) {
+    char* c = static_cast<char*>(p);
+    if (!v->empty() && v->back().rank == r && v->back().ptr + v->back().bytes == c) v->back().bytes += bytes;
+    else v->push_back(GradRange{c, bytes, r});
+}
+
+// The most tiles that tensors of these sizes can take, wherever they lie.
+int64_t most_tiles(int32_t n_params, const int64_t* numel, int64_t es) {
+    int64_t t = 0;
+    for (int32_t i = 0; i < n_params; ++i)
+        if (numel[i] > 0) t += (numel[i] * es + kNormAlign - 1) / kNormTile + 2;
+    return t;
+}
+
+bool bad_max_norm(double max_norm) { return !(max_norm > 0.0) || !((float)max_norm > 0.f); }
+
+}  // namespace
+
+extern "C" {
+
+int32_t ddp_grad_set_workspace_bytes(int32_t world, int32_t n_params, const int64_t* numel, int32_t dtype,
+                                     int64_t* bytes) try {
+    DDP_TRACE_CALL();
+    if (!bytes) return DDP_ERR_INVALID;
+    const int32_t st = check_sizes(world, n_params, numel, dtype);
+    if (st) return st;
+    *bytes = 8 * std::max<int64_t>(1, world * most_tiles(n_params, numel, elem_bytes(dtype)));
+    return DDP_OK;
+} DDP_ABI_CATCH
+
+int32_t ddp_grad_set_create(int32_t world, int32_t n_params, void* const* grads, const int64_t* numel, int32_t dtype,
+                            void* workspace, int64_t workspace_bytes, ddp_grad_set** out) try {
+    DDP_TRACE_CALL();
+    if (!out) return DDP_ERR_INVALID;
+    *out = nullptr;
+    int64_t need = 0;
+    int32_t st = ddp_grad_set_workspace_bytes(world, n_params, numel, dtype, &need);
+    if (st) return st;
+    if (n_params > 0 && !grads) return DDP_ERR_INVALID;
+    if ((st = check_ptr(workspace, 8))) return st;
+    if (workspace_bytes < need) return DDP_ERR_CAPACITY;
+    if (need / 8 > INT32_MAX) return DDP_ERR_CAPACITY;
+    const int64_t es = elem_bytes(dtype);
+    std::unique_ptr<ddp_grad_set> s(new ddp_grad_set());
+    s->world = world;
+    s->dtype = dtype;
+    s->partials = static_cast<double*>(workspace);
+    s->spans.push_back(span_of(workspace, need));
+    int64_t tiles = 0;
+    std::vector<Span> rank;
+    for (int32_t r = 0; r < world; ++r) {
+        rank.clear();
+        for (int32_t i = 0; i < n_params; ++i) {
+            if (numel[i] == 0) continue;
+            const void* g = grads[(int64_t)r * n_params + i];
+            if ((st = check_ptr(g, es))) return st;
+            rank.push_back(span_of(g, numel[i] * es));
+        }
+        std::sort(rank.begin(), rank.end());
+        s->spans.insert(s->spans.end(), rank.begin(), rank.end());
+        s->rank_first.push_back((int32_t)tiles);
+        const size_t from = s->ranges.size();
+        for (const Span& g : rank)
+            add_range(&s->ranges, reinterpret_cast<void*>(g.first), (int64_t)(g.second - g.first), r);
+        for (size_t k = from; k < s->ranges.size(); ++k) tiles += range_tiles(s->ranges[k].ptr, s->ranges[k].bytes);
+    }
+    s->rank_first.push_back((int32_t)tiles);
+    if (any_overlap(&s->spans)) return DDP_ERR_INVALID;
+    *out = s.release();
+    return DDP_OK;
+} DDP_ABI_CATCH
+
+int32_t ddp_grad_norm(ddp_grad_set* s, float* norms, void* stream) try {
+    DDP_TRACE_CALL();
+    if (!s) return DDP_ERR_INVALID;
+    int32_t st = check_ptr(norms, 4);
+    if (st) return st;
+    if (hits_any(s->spans, span_of(norms, 4 * (int64_t)s->world))) return DDP_ERR_INVALID;
+    cudaStream_t q = (cudaStream_t)stream;
+    st = cuda_status(launch_norm_partials(s->ranges.data(), (int64_t)s->ranges.size(), s->dtype, s->partials, q));
+    if (st) return st;
+    return cuda_status(launch_norm_final(s->partials, s->rank_first.data(), s->world, 1, norms, q));
+} DDP_ABI_CATCH
+
+int32_t ddp_grad_clip(ddp_grad_set* s, const float* norms, double max_norm, void* stream) try {
+    DDP_TRACE_CALL();
+    if (!s || bad_max_norm(max_norm)) return DDP_ERR_INVALID;
+    const int32_t st = check_ptr(norms, 4);
+    if (st) return st;
+    if (hits_any(s->spans, span_of(norms, 4 * (int64_t)s->world))) return DDP_ERR_INVALID;
+    return cuda_status(launch_clip(s->ranges.data(), (int64_t)s->ranges.size(), s->dtype, norms, (float)max_norm,
+                                   (cudaStream_t)stream));
+} DDP_ABI_CATCH
+
+int32_t ddp_grad_norm_clip(ddp_grad_set* s, float* norms, double max_norm, void* stream) try {
+    DDP_TRACE_CALL();
+    if (!s || bad_max_norm(max_norm)) return DDP_ERR_INVALID;
+    const int32_t st = ddp_grad_norm(s, norms, stream);
+    return st ? st : ddp_grad_clip(s, norms, max_norm, stream);
+} DDP_ABI_CATCH
+
+int32_t ddp_grad_set_destroy(ddp_grad_set* s) try {
+    DDP_TRACE_CALL();
+    delete s;
+    return DDP_OK;
+} DDP_ABI_CATCH
+
+int32_t ddp_sync_norm_workspace_bytes(int32_t world, int32_t n_params, const int64_t* numel, int32_t n_buckets,
+                                      int32_t dtype, int64_t* bytes) try {
+    DDP_TRACE_CALL();
+    if (!bytes || n_buckets < 0) return DDP_ERR_INVALID;
+    const int32_t st = check_sizes(world, n_params, numel, dtype);
+    if (st) return st;
+    *bytes = 8 * std::max<int64_t>(1, most_tiles(n_params, numel, elem_bytes(dtype)));
+    return DDP_OK;
+} DDP_ABI_CATCH
+
+int32_t ddp_sync_buckets_norm(int32_t world, int32_t n_params, void* const* grads, const int64_t* numel,
+                              const int32_t* bucket_of_param, const int64_t* offset_of_param, int32_t n_buckets,
+                              const int64_t* bucket_numel, void* const* buckets, int32_t dtype, int32_t divisor,
+                              int32_t algo, float* norms, void* workspace, int64_t workspace_bytes, void* stream) try {
+    DDP_TRACE_CALL();
+    int64_t need = 0;
+    int32_t st = ddp_sync_norm_workspace_bytes(world, n_params, numel, n_buckets, dtype, &need);
+    if (st) return st;
+    if ((st = check_ptr(norms, 4)) || (st = check_ptr(workspace, 8))) return st;
+    if (workspace_bytes < need || need / 8 > INT32_MAX) return DDP_ERR_CAPACITY;
+    if (n_params > 0 && !grads) return DDP_ERR_INVALID;
+    const int64_t es = elem_bytes(dtype);
+    const Span own[2] = {span_of(norms, 4 * (int64_t)world), span_of(workspace, need)};
+    if (own[0].first < own[1].second && own[1].first < own[0].second) return DDP_ERR_INVALID;
+    for (int64_t k = 0; k < (int64_t)world * n_params; ++k) {
+        const Span g = span_of(grads[k], numel[k % n_params] * es);
+        for (const Span& o : own)
+            if (g.first < o.second && o.first < g.second) return DDP_ERR_INVALID;
+    }
+    st = ddp_sync_buckets(world, n_params, grads, numel, bucket_of_param, offset_of_param, n_buckets, bucket_numel,
+                          buckets, dtype, divisor, algo, stream);
+    if (st) return st;
+    // every rank holds the same average now: rank 0's norm is everybody's
+    std::vector<GradRange> ranges;
+    for (int32_t i = 0; i < n_params; ++i)
+        if (numel[i] > 0) add_range(&ranges, grads[i], numel[i] * es, 0);
+    int32_t first[2] = {0, 0};
+    for (const GradRange& g : ranges) first[1] += (int32_t)range_tiles(g.ptr, g.bytes);
+    double* partials = static_cast<double*>(workspace);
+    cudaStream_t q = (cudaStream_t)stream;
+    if ((st = cuda_status(launch_norm_partials(ranges.data(), (int64_t)ranges.size(), dtype, partials, q)))) return st;
+    return cuda_status(launch_norm_final(partials, first, 1, world, norms, q));
+} DDP_ABI_CATCH
+
+int32_t ddp_adamw_create(int32_t world, int32_t n_params, void* const* params, const void* const* grads,
+                         int32_t grad_dtype, void* const* exp_avg, void* const* exp_avg_sq, void* const* copies,
+                         const int64_t* numel, const uint8_t* no_decay, int32_t* steps, void* workspace, void* stream,
+                         ddp_adamw** out) try {
+    DDP_TRACE_CALL();
+    if (!out) return DDP_ERR_INVALID;
+    *out = nullptr;
+    int32_t st = check_sizes(world, n_params, numel, grad_dtype);
+    if (st) return st;
+    if (n_params > 0 && (!params || !grads || !exp_avg || !exp_avg_sq)) return DDP_ERR_INVALID;
+    if ((st = check_ptr(steps, 4)) || (st = check_ptr(workspace, 8))) return st;
+    std::unique_ptr<ddp_adamw> a(new ddp_adamw());
+    a->world = world;
+    a->grad_dtype = grad_dtype;
+    a->copies = copies != nullptr;
+    a->steps = steps;
+    a->arrivals = static_cast<int32_t*>(workspace);
+    a->spans.push_back(span_of(steps, 4 * (int64_t)world));
+    a->spans.push_back(span_of(workspace, DDP_ADAMW_WORKSPACE_BYTES));
+    std::vector<Span> read;
+    const int64_t gs = elem_bytes(grad_dtype);
+    int64_t tiles = 0;
+    for (int32_t r = 0; r < world; ++r)
+        for (int32_t i = 0; i < n_params; ++i) {
+            if (numel[i] == 0) continue;
+            const int64_t k = (int64_t)r * n_params + i;
+            AdamWItem it{static_cast<float*>(params[k]),
+                         static_cast<float*>(exp_avg[k]),
+                         static_cast<float*>(exp_avg_sq[k]),
+                         grads[k],
+                         copies ? copies[k] : nullptr,
+                         numel[i],
+                         r,
+                         no_decay && no_decay[i] ? 0 : 1};
+            if ((st = check_ptr(it.p, 4)) || (st = check_ptr(it.m, 4)) || (st = check_ptr(it.v, 4)) ||
+                (st = check_ptr(it.g, gs)) || (copies && (st = check_ptr(it.copy, 2))))
+                return st;
+            for (const void* p : {(const void*)it.p, (const void*)it.m, (const void*)it.v})
+                a->spans.push_back(span_of(p, 4 * it.numel));
+            if (copies) a->spans.push_back(span_of(it.copy, 2 * it.numel));
+            read.push_back(span_of(it.g, gs * it.numel));
+            // a tensor that continues the one before it in every array joins it
+            AdamWItem* b = a->items.empty() ? nullptr : &a->items.back();
+            if (b && b->rank == r && b->decay == it.decay && b->p + b->numel == it.p && b->m + b->numel == it.m &&
+                b->v + b->numel == it.v && static_cast<const char*>(b->g) + gs * b->numel == it.g &&
+                (!copies || static_cast<char*>(b->copy) + 2 * b->numel == it.copy))
+                b->numel += it.numel;
+            else
+                a->items.push_back(it);
+        }
+    for (const AdamWItem& it : a->items) tiles += adamw_tiles(it, grad_dtype);
+    if (tiles > INT32_MAX) return DDP_ERR_CAPACITY;
+    if (any_overlap(&a->spans)) return DDP_ERR_INVALID;
+    for (const Span& g : read)
+        if (hits_any(a->spans, g)) return DDP_ERR_INVALID;
+    if ((st = cuda_status(cudaMemsetAsync(workspace, 0, DDP_ADAMW_WORKSPACE_BYTES, (cudaStream_t)stream)))) return st;
+    *out = a.release();
+    return DDP_OK;
+} DDP_ABI_CATCH
+
+int32_t ddp_adamw_step(ddp_adamw* a, double lr, double beta1, double beta2, double eps, double weight_decay,
+                       const float* norms, double max_norm, void* stream) try {
+    DDP_TRACE_CALL();
+    if (!a) return DDP_ERR_INVALID;
+    if (!(lr >= 0.0) || !std::isfinite(lr) || !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) ||
+        !((float)eps > 0.f) || !std::isfinite(eps) || !(weight_decay >= 0.0) || !std::isfinite(weight_decay))
+        return DDP_ERR_INVALID;
+    if (norms) {
+        if (bad_max_norm(max_norm)) return DDP_ERR_INVALID;
+        const int32_t st = check_ptr(norms, 4);
+        if (st) return st;
+        if (hits_any(a->spans, span_of(norms, 4 * (int64_t)a->world))) return DDP_ERR_INVALID;
+    }
+    const AdamWScalars s{(float)lr,
+                         (float)beta1,
+                         (float)(1.0 - beta1),
+                         (float)std::log(beta1),
+                         (float)beta2,
+                         (float)(1.0 - beta2),
+                         (float)std::log(beta2),
+                         (float)eps,
+                         (float)(lr * weight_decay),
+                         (float)max_norm};
+    return cuda_status(launch_adamw(a->items.data(), (int64_t)a->items.size(), a->world, a->grad_dtype, a->copies, s,
+                                    norms, a->steps, a->arrivals, (cudaStream_t)stream));
+} DDP_ABI_CATCH
+
+int32_t ddp_adamw_destroy(ddp_adamw* a) try {
+    DDP_TRACE_CALL();
+    delete a;
+    return DDP_OK;
+} DDP_ABI_CATCH
+
+}  // extern "C"

@@ -25,8 +25,8 @@
  *   - Ownership: the caller owns every host and device buffer.  The library
  *     allocates no device memory at run time (the no-alloc entry point's
  *     64 MiB array is a static device array) and keeps no pointer after a
- *     call returns (except a ddp_reducer, which keeps the tables it was
- *     created with).  State kept between calls: cached device attributes,
+ *     call returns (except a ddp_reducer, a ddp_grad_set and a ddp_adamw, which
+ *     keep the tables they were created with).  State kept between calls: cached device attributes,
  *     the two process-wide settings (ddp_set_max_ctas, ddp_set_fused_kernel)
  *     and the device status word (ddp_device_status).
  *   - Streams: `stream` is a cudaStream_t passed as void* (NULL = the legacy
@@ -620,6 +620,122 @@ int32_t ddp_bucket_allreduce_view_bf16(int32_t world, int32_t n_in_bucket, void*
 int32_t ddp_bucket_allreduce_view_fp16(int32_t world, int32_t n_in_bucket, void* const* grads,
                                        const int64_t* numel, const int64_t* offset, int64_t bucket_numel,
                                        int32_t divisor, void* stream);
+
+/*
+ * ddp_grad_set -- the gradients of one model at every rank, for the global
+ * gradient norm and clipping: what a training step does with them between the
+ * sync and the optimizer (or, on each rank's own gradients, before the sync).
+ *
+ * The set checks the tensors once and keeps their table, so that a call costs
+ * its launches, however many tensors there are.
+ *
+ *   ddp_grad_norm       norms[r] = sqrt(sum of g^2 over every element of rank
+ *                       r's tensors).  Squares are added in binary32 within a
+ *                       warp's few thousand and in binary64 beyond it; where a
+ *                       square would leave binary32's range it is taken in
+ *                       binary64, so that a norm is right whenever it is itself
+ *                       a binary32 number.  An infinity or NaN among the
+ *                       gradients makes the norm one.  No elements: 0.
+ *                       The additions' order depends on the tensors' sizes and
+ *                       addresses only: neither ddp_set_max_ctas nor a repeat
+ *                       changes a bit.
+ *   ddp_grad_clip       g <- c g with c = min(1, max_norm / (norms[r] + 1e-6)),
+ *                       rounded once to the gradients' type; c = 1 leaves rank
+ *                       r's gradients untouched.  An infinite norm gives c = 0
+ *                       (and NaN where the gradient is infinite), a NaN norm
+ *                       NaN: test the norms if that may happen.
+ *   ddp_grad_norm_clip  the two in order.
+ *
+ *   grads[world*n_params] host table of device pointers, rank-major; no two
+ *                         tensors may overlap.  Entries of empty tensors may be
+ *                         NULL
+ *   numel[n_params]       elements of each tensor (>= 0)
+ *   dtype                 a ddp_dtype
+ *   workspace             device memory, 8-byte aligned, of at least
+ *                         ddp_grad_set_workspace_bytes (DDP_ERR_CAPACITY if
+ *                         smaller); the set keeps it, the caller owns it.  Calls
+ *                         on one set share it: order them (one stream, or events)
+ *   norms[world]          device float32, outside the tensors and the workspace
+ *   max_norm              > 0 (may be infinite)
+ * The set keeps these pointers until it is destroyed, the caller keeps the
+ * memory.
+ */
+typedef struct ddp_grad_set ddp_grad_set;
+int32_t ddp_grad_set_workspace_bytes(int32_t world, int32_t n_params, const int64_t* numel, int32_t dtype,
+                                     int64_t* bytes);
+int32_t ddp_grad_set_create(int32_t world, int32_t n_params, void* const* grads, const int64_t* numel, int32_t dtype,
+                            void* workspace, int64_t workspace_bytes, ddp_grad_set** out);
+int32_t ddp_grad_norm(ddp_grad_set* set, float* norms, void* stream);
+int32_t ddp_grad_clip(ddp_grad_set* set, const float* norms, double max_norm, void* stream);
+int32_t ddp_grad_norm_clip(ddp_grad_set* set, float* norms, double max_norm, void* stream);
+int32_t ddp_grad_set_destroy(ddp_grad_set* set);
+
+/*
+ * ddp_sync_buckets_norm -- ddp_sync_buckets, and the norm of the gradients it
+ * leaves: every rank then holds the same averaged gradients, so norms[0 ..
+ * world) all receive their one global norm (as ddp_grad_norm; NaN and infinity
+ * as there).  The gradients' bits are those of ddp_sync_buckets.
+ *
+ *   norms[world]     device float32, outside the gradients and the workspace
+ *   workspace        device memory, 8-byte aligned, of at least
+ *                    ddp_sync_norm_workspace_bytes; its contents need not be set.
+ *                    Calls that overlap on the GPU need one each
+ * Other arguments as for ddp_sync_buckets (any algo it takes).
+ */
+int32_t ddp_sync_norm_workspace_bytes(int32_t world, int32_t n_params, const int64_t* numel, int32_t n_buckets,
+                                      int32_t dtype, int64_t* bytes);
+int32_t ddp_sync_buckets_norm(int32_t world, int32_t n_params, void* const* grads, const int64_t* numel,
+                              const int32_t* bucket_of_param, const int64_t* offset_of_param, int32_t n_buckets,
+                              const int64_t* bucket_numel, void* const* buckets, int32_t dtype, int32_t divisor,
+                              int32_t algo, float* norms, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * ddp_adamw -- the optimizer step that follows the sync: AdamW over every
+ * tensor of every rank in one pass, with clipping by the global norm in its
+ * prologue, so that clipping reads and writes no gradient of its own.
+ *
+ * ddp_adamw_step, for rank r with t = steps[r] + 1, c = min(1, max_norm /
+ * (norms[r] + 1e-6)) if norms is given and 1 otherwise, all in binary32:
+ *     g' = c g
+ *     exp_avg    <- beta1 exp_avg + (1 - beta1) g'
+ *     exp_avg_sq <- beta2 exp_avg_sq + (1 - beta2) g'^2
+ *     param      <- param - lr weight_decay param
+ *                   - lr (exp_avg / (1 - beta1^t)) / (sqrt(exp_avg_sq / (1 - beta2^t)) + eps)
+ *     copy       <- param rounded to bf16 (nearest even)
+ *     steps[r]   <- t
+ * With norms, a rank whose norm is infinite or NaN is left exactly as it was,
+ * its step count too (the step is skipped, as after an overflow under loss
+ * scaling).  The gradients are only read.  The count advances on the device,
+ * so a captured graph's replays are successive steps; lr and the other scalars
+ * are the call's.
+ *
+ *   params, exp_avg, exp_avg_sq [world*n_params]  host tables of device pointers
+ *                        to float32 tensors, rank-major, updated in place
+ *   grads[world*n_params] gradients of grad_dtype (DDP_F32, DDP_BF16)
+ *   copies[world*n_params] bf16 tensors that receive the new weights, for models
+ *                        that compute in bf16; NULL: none
+ *   numel[n_params]      elements of each tensor (>= 0)
+ *   no_decay[n_params]   non-zero: this tensor gets no weight decay (biases,
+ *                        norms' weights); NULL: all decay
+ *   steps[world]         device int32: steps taken so far, 0 at the start
+ *   workspace            DDP_ADAMW_WORKSPACE_BYTES of device memory, 8-byte
+ *                        aligned; create clears it on `stream`, and steps must
+ *                        come after that.  Steps of one handle must not overlap
+ *                        on the GPU
+ *   lr >= 0, 0 <= beta < 1, eps > 0, weight_decay >= 0, max_norm > 0 with norms
+ * Nothing that a step writes may overlap anything else of the handle;
+ * gradients may overlap each other (ranks may share one).  The handle keeps the
+ * pointers until it is destroyed, the caller keeps the memory.
+ */
+#define DDP_ADAMW_WORKSPACE_BYTES 16
+typedef struct ddp_adamw ddp_adamw;
+int32_t ddp_adamw_create(int32_t world, int32_t n_params, void* const* params, const void* const* grads,
+                         int32_t grad_dtype, void* const* exp_avg, void* const* exp_avg_sq, void* const* copies,
+                         const int64_t* numel, const uint8_t* no_decay, int32_t* steps, void* workspace, void* stream,
+                         ddp_adamw** out);
+int32_t ddp_adamw_step(ddp_adamw* adamw, double lr, double beta1, double beta2, double eps, double weight_decay,
+                       const float* norms, double max_norm, void* stream);
+int32_t ddp_adamw_destroy(ddp_adamw* adamw);
 
 #ifdef __cplusplus
 }
