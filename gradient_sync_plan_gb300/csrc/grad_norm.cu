@@ -9,6 +9,8 @@
 // are taken element by element.  The table travels in the kernel's parameters.
 // A tile's partial sum depends on the tile alone and the partials are added in
 // a fixed order, so a norm does not depend on the grid that computed it.
+#include <cooperative_groups.h>
+
 #include <algorithm>
 #include <climits>
 
@@ -90,20 +92,40 @@ struct RankFirst {
     int32_t first[DDP_MAX_WORLD + 1];
 };
 
-// One block a rank: its partials added in binary64, each thread's in order,
-// then the threads' sums.
+// A cluster of C blocks a rank: its partials added in binary64, each thread's
+// in order, then the threads' sums, then the blocks'.  One block reads some
+// 100 GB/s, so that the 350 thousand partials of a 355M-parameter sync would
+// take it 30 us; eight share them.
 constexpr int kFinalThreads = 512;
+constexpr int kFinalBlocks = 8;
+template <int C>
 __global__ void __launch_bounds__(kFinalThreads) k_norm_final(const double* partials, const __grid_constant__ RankFirst rf,
                                                               float* norms, int copies) {
     __shared__ double sh[kFinalThreads / 32];
+    __shared__ double block[C];
     pdl_release();
     pdl_acquire();
-    const int r = blockIdx.x;
-    double d = 0.0;
-    for (int k = rf.first[r] + (int)threadIdx.x; k < rf.first[r + 1]; k += kFinalThreads) d += partials[k];
-    const double t = block_sum(warp_sum(d), sh);
-    if (threadIdx.x == 0)
-        for (int k = 0; k < copies; ++k) norms[r * copies + k] = (float)sqrt(t);
+    const int r = blockIdx.x / C, c = blockIdx.x % C;
+    const int end = rf.first[r + 1];
+    constexpr int kStep = C * kFinalThreads;
+    double d[4] = {0.0, 0.0, 0.0, 0.0};          // four loads in flight
+    int k = rf.first[r] + c * kFinalThreads + (int)threadIdx.x;
+    for (; k + 3 * kStep < end; k += 4 * kStep)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) d[u] += partials[k + u * kStep];
+    for (; k < end; k += kStep) d[0] += partials[k];
+    double t = block_sum(warp_sum((d[0] + d[1]) + (d[2] + d[3])), sh);
+    if constexpr (C > 1) {
+        auto cluster = cooperative_groups::this_cluster();
+        if (threadIdx.x == 0) cluster.map_shared_rank(block, 0)[c] = t;
+        cluster.sync();
+        if (threadIdx.x == 0 && c == 0) {
+            t = block[0];
+            for (int q = 1; q < C; ++q) t += block[q];
+        }
+    }
+    if (threadIdx.x == 0 && c == 0)
+        for (int q = 0; q < copies; ++q) norms[r * copies + q] = (float)sqrt(t);
 }
 
 // min(1, max_norm / (norm + 1e-6)); a NaN stays one.
@@ -206,7 +228,12 @@ cudaError_t launch_norm_final(const double* partials, const int32_t* rank_first,
                               cudaStream_t st) {
     RankFirst rf;
     std::copy(rank_first, rank_first + ranks + 1, rf.first);
-    return launch_dependent(k_norm_final, dim3(ranks), dim3(kFinalThreads), 0, st, partials, rf, norms, copies);
+    int32_t most = 0;
+    for (int r = 0; r < ranks; ++r) most = std::max(most, rank_first[r + 1] - rank_first[r]);
+    if (most <= 8 * kFinalThreads)
+        return launch_dependent(k_norm_final<1>, dim3(ranks), dim3(kFinalThreads), 0, st, partials, rf, norms, copies);
+    return launch_cluster<kFinalBlocks>(k_norm_final<kFinalBlocks>, dim3(ranks * kFinalBlocks), dim3(kFinalThreads), st,
+                                        partials, rf, norms, copies);
 }
 
 cudaError_t launch_clip(const GradRange* ranges, int64_t n, int dtype, const float* norms, float max_norm,

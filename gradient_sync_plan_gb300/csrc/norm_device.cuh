@@ -14,6 +14,27 @@
 
 namespace ddpk {
 
+// launch_dependent for a kernel whose blocks form clusters of C.
+template <int C, class... KArgs, class... Args>
+inline cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, cudaStream_t st, Args&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = C;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...);
+    const cudaError_t last = cudaGetLastError();
+    return e != cudaSuccess ? e : last;
+}
+
 __device__ __forceinline__ float f32_of(float4 v, int l) { return l == 0 ? v.x : l == 1 ? v.y : l == 2 ? v.z : v.w; }
 __device__ __forceinline__ float f32_of(uint4 v, int l) {
     const uint32_t w = (l >> 1) == 0 ? v.x : (l >> 1) == 1 ? v.y : (l >> 1) == 2 ? v.z : v.w;
@@ -31,6 +52,10 @@ __device__ __forceinline__ double warp_sum(double s) {
     return s;
 }
 
+// Whether a warp's sum of squares can be trusted in binary32 (a zero too, if
+// every value is one: the caller looks).
+__device__ __forceinline__ bool in_square_range(float w) { return w >= 0x1p-90f && w <= 0x1p126f; }
+
 // The sum of squares of every value in the warp's U vectors a lane; all lanes
 // must call it, all get the sum.  Lanes without data pass zero vectors.
 template <class E, int U>
@@ -44,7 +69,7 @@ __device__ __forceinline__ double warp_sum_squares(const typename E::V (&x)[U]) 
             s[l & 3] = fmaf(f, f, s[l & 3]);
         }
     const float w = warp_sum((s[0] + s[1]) + (s[2] + s[3]));
-    if (w >= 0x1p-90f && w <= 0x1p126f) return (double)w;
+    if (in_square_range(w)) return (double)w;
     bool some = false;                           // zeros alone need no second pass
 #pragma unroll
     for (int u = 0; u < U; ++u)

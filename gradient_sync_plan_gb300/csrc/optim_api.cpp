@@ -29,6 +29,23 @@ struct ddp_grad_set {
     double* partials = nullptr;
 };
 
+struct ddp_sync_norm {
+    int32_t world = 0, n_params = 0, n_buckets = 0, dtype = 0, divisor = 0, algo = 0;
+    // the arguments of ddp_sync_buckets
+    std::vector<void*> grads, buckets;
+    std::vector<int64_t> numel, offset, bucket_numel;
+    std::vector<int32_t> bucket_of;
+    // the view algorithms' members, those that continue one another joined
+    std::vector<SyncMember> members;
+    std::vector<void*> ptrs;
+    int32_t member_tiles = 0;
+    // rank 0's gradients, for a norm pass after a sync without one
+    std::vector<GradRange> ranges;
+    int32_t range_tiles = 0;
+    std::vector<std::pair<uintptr_t, uintptr_t>> spans;        // the gradients, buckets and the workspace, sorted
+    double* partials = nullptr;
+};
+
 struct ddp_adamw {
     int32_t world = 0, grad_dtype = 0;
     bool copies = false;
@@ -186,48 +203,155 @@ int32_t ddp_grad_set_destroy(ddp_grad_set* s) try {
     return DDP_OK;
 } DDP_ABI_CATCH
 
-int32_t ddp_sync_norm_workspace_bytes(int32_t world, int32_t n_params, const int64_t* numel, int32_t n_buckets,
-                                      int32_t dtype, int64_t* bytes) try {
+int32_t ddp_sync_norm_workspace_bytes(int32_t world, int32_t n_params, const int64_t* numel, int32_t dtype,
+                                      int64_t* bytes) try {
     DDP_TRACE_CALL();
-    if (!bytes || n_buckets < 0) return DDP_ERR_INVALID;
+    if (!bytes) return DDP_ERR_INVALID;
     const int32_t st = check_sizes(world, n_params, numel, dtype);
     if (st) return st;
-    *bytes = 8 * std::max<int64_t>(1, most_tiles(n_params, numel, elem_bytes(dtype)));
+    const int64_t tile = sync_norm_tile(world, dtype);
+    int64_t tiles = 0;
+    for (int32_t i = 0; i < n_params; ++i)
+        if (numel[i] > 0) tiles += numel[i] / tile + 2;
+    *bytes = 8 * std::max<int64_t>({1, tiles, most_tiles(n_params, numel, elem_bytes(dtype))});
     return DDP_OK;
 } DDP_ABI_CATCH
 
-int32_t ddp_sync_buckets_norm(int32_t world, int32_t n_params, void* const* grads, const int64_t* numel,
-                              const int32_t* bucket_of_param, const int64_t* offset_of_param, int32_t n_buckets,
-                              const int64_t* bucket_numel, void* const* buckets, int32_t dtype, int32_t divisor,
-                              int32_t algo, float* norms, void* workspace, int64_t workspace_bytes, void* stream) try {
+int32_t ddp_sync_norm_create(int32_t world, int32_t n_params, void* const* grads, const int64_t* numel,
+                             const int32_t* bucket_of_param, const int64_t* offset_of_param, int32_t n_buckets,
+                             const int64_t* bucket_numel, void* const* buckets, int32_t dtype, int32_t divisor,
+                             int32_t algo, void* workspace, int64_t workspace_bytes, ddp_sync_norm** out) try {
     DDP_TRACE_CALL();
+    if (!out) return DDP_ERR_INVALID;
+    *out = nullptr;
     int64_t need = 0;
-    int32_t st = ddp_sync_norm_workspace_bytes(world, n_params, numel, n_buckets, dtype, &need);
+    int32_t st = ddp_sync_norm_workspace_bytes(world, n_params, numel, dtype, &need);
     if (st) return st;
-    if ((st = check_ptr(norms, 4)) || (st = check_ptr(workspace, 8))) return st;
+    if (n_buckets < 0 || divisor < 0) return DDP_ERR_INVALID;
+    const bool hook = algo == DDP_ALGO_BF16_HOOK || algo == DDP_ALGO_BF16_HOOK_VIEW || algo == DDP_ALGO_FP16_HOOK_VIEW;
+    const bool needs_buckets = algo == DDP_ALGO_FUSED || algo == DDP_ALGO_STAGED || algo == DDP_ALGO_BF16_HOOK;
+    if (!hook && !needs_buckets && algo != DDP_ALGO_VIEW) return DDP_ERR_INVALID;
+    if (hook && dtype != DDP_F32) return DDP_ERR_INVALID;
+    if (n_params > 0 && (!grads || !bucket_of_param || !offset_of_param)) return DDP_ERR_INVALID;
+    if (n_buckets > 0 && (!bucket_numel || (needs_buckets && !buckets))) return DDP_ERR_INVALID;
+    if ((st = check_ptr(workspace, 8))) return st;
     if (workspace_bytes < need || need / 8 > INT32_MAX) return DDP_ERR_CAPACITY;
-    if (n_params > 0 && !grads) return DDP_ERR_INVALID;
-    const int64_t es = elem_bytes(dtype);
-    const Span own[2] = {span_of(norms, 4 * (int64_t)world), span_of(workspace, need)};
-    if (own[0].first < own[1].second && own[1].first < own[0].second) return DDP_ERR_INVALID;
-    for (int64_t k = 0; k < (int64_t)world * n_params; ++k) {
-        const Span g = span_of(grads[k], numel[k % n_params] * es);
-        for (const Span& o : own)
-            if (g.first < o.second && o.first < g.second) return DDP_ERR_INVALID;
+    for (int32_t k = 0; k < n_buckets; ++k)
+        if ((st = common_checks(world, bucket_numel[k], dtype))) return st;
+    std::unique_ptr<ddp_sync_norm> s(new ddp_sync_norm());
+    s->world = world;
+    s->n_params = n_params;
+    s->n_buckets = n_buckets;
+    s->dtype = dtype;
+    s->divisor = divisor;
+    s->algo = algo;
+    s->partials = static_cast<double*>(workspace);
+    const int64_t all = (int64_t)world * n_params, es = elem_bytes(dtype);
+    if (n_params > 0) {
+        s->grads.assign(grads, grads + all);
+        s->numel.assign(numel, numel + n_params);
+        s->bucket_of.assign(bucket_of_param, bucket_of_param + n_params);
+        s->offset.assign(offset_of_param, offset_of_param + n_params);
     }
-    st = ddp_sync_buckets(world, n_params, grads, numel, bucket_of_param, offset_of_param, n_buckets, bucket_numel,
-                          buckets, dtype, divisor, algo, stream);
+    if (n_buckets > 0) s->bucket_numel.assign(bucket_numel, bucket_numel + n_buckets);
+    // the plan: members inside their buckets, in offset order, disjoint
+    std::vector<int32_t> order;
+    for (int32_t p = 0; p < n_params; ++p) {
+        const int32_t k = bucket_of_param[p];
+        if (k < 0 || k >= n_buckets) return DDP_ERR_INVALID;
+        if (offset_of_param[p] < 0 || offset_of_param[p] > bucket_numel[k] - numel[p]) return DDP_ERR_INVALID;
+        if (numel[p] > 0) order.push_back(p);
+    }
+    std::sort(order.begin(), order.end(), [&](int32_t a, int32_t b) {
+        return bucket_of_param[a] != bucket_of_param[b] ? bucket_of_param[a] < bucket_of_param[b]
+                                                        : offset_of_param[a] < offset_of_param[b];
+    });
+    for (size_t i = 1; i < order.size(); ++i) {
+        const int32_t a = order[i - 1], b = order[i];
+        if (bucket_of_param[a] == bucket_of_param[b] && offset_of_param[a] + numel[a] > offset_of_param[b])
+            return DDP_ERR_INVALID;
+    }
+    // the memory
+    s->spans.push_back(span_of(workspace, need));
+    for (int64_t k = 0; k < all; ++k) {
+        const int64_t n = numel[k % n_params];
+        if (n == 0) continue;
+        if ((st = check_ptr(grads[k], es))) return st;
+        s->spans.push_back(span_of(grads[k], n * es));
+    }
+    if (any_overlap(&s->spans)) return DDP_ERR_INVALID;
+    if (needs_buckets && n_buckets > 0) {        // buckets may share memory with each other across k
+        s->buckets.assign(buckets, buckets + (int64_t)world * n_buckets);
+        const int64_t bs = algo == DDP_ALGO_BF16_HOOK ? 2 : es;
+        for (int64_t k = 0; k < (int64_t)world * n_buckets; ++k) {
+            const int64_t n = bucket_numel[k % n_buckets];
+            if (n == 0) continue;
+            if ((st = check_ptr(buckets[k], bs))) return st;
+            if (hits_any(s->spans, span_of(buckets[k], n * bs))) return DDP_ERR_INVALID;
+        }
+    }
+    // a member that continues the one before it, in its bucket and at every rank, joins it
+    s->ptrs.reserve(order.size() * (size_t)world);
+    int32_t bucket = -1;
+    for (int32_t p : order) {
+        const int32_t k = bucket_of_param[p];
+        SyncMember* m = bucket == k ? &s->members.back() : nullptr;
+        bool joins = m && m->offset + m->numel == offset_of_param[p];
+        for (int32_t r = 0; joins && r < world; ++r)
+            joins = static_cast<char*>(m->ptrs[r]) + m->numel * es == grads[(int64_t)r * n_params + p];
+        bucket = k;
+        if (joins) {
+            m->numel += numel[p];
+            continue;
+        }
+        void* const* at = s->ptrs.data() + s->ptrs.size();
+        for (int32_t r = 0; r < world; ++r) s->ptrs.push_back(grads[(int64_t)r * n_params + p]);
+        s->members.push_back(SyncMember{numel[p], offset_of_param[p], chunk_len(bucket_numel[k], world), at});
+    }
+    for (const SyncMember& m : s->members) s->member_tiles += (int32_t)sync_norm_tiles(world, m, dtype);
+    // every rank holds the same average after the sync: rank 0's norm is everybody's
+    for (int32_t p = 0; p < n_params; ++p)
+        if (numel[p] > 0) add_range(&s->ranges, grads[p], numel[p] * es, 0);
+    for (const GradRange& g : s->ranges) s->range_tiles += (int32_t)range_tiles(g.ptr, g.bytes);
+    *out = s.release();
+    return DDP_OK;
+} DDP_ABI_CATCH
+
+int32_t ddp_sync_norm_run(ddp_sync_norm* s, float* norms, void* stream) try {
+    DDP_TRACE_CALL();
+    if (!s) return DDP_ERR_INVALID;
+    int32_t st = check_ptr(norms, 4);
     if (st) return st;
-    // every rank holds the same average now: rank 0's norm is everybody's
-    std::vector<GradRange> ranges;
-    for (int32_t i = 0; i < n_params; ++i)
-        if (numel[i] > 0) add_range(&ranges, grads[i], numel[i] * es, 0);
-    int32_t first[2] = {0, 0};
-    for (const GradRange& g : ranges) first[1] += (int32_t)range_tiles(g.ptr, g.bytes);
-    double* partials = static_cast<double*>(workspace);
+    if (hits_any(s->spans, span_of(norms, 4 * (int64_t)s->world))) return DDP_ERR_INVALID;
     cudaStream_t q = (cudaStream_t)stream;
-    if ((st = cuda_status(launch_norm_partials(ranges.data(), (int64_t)ranges.size(), dtype, partials, q)))) return st;
-    return cuda_status(launch_norm_final(partials, first, 1, world, norms, q));
+    const bool view = s->algo == DDP_ALGO_VIEW || s->algo == DDP_ALGO_BF16_HOOK_VIEW || s->algo == DDP_ALGO_FP16_HOOK_VIEW;
+    int32_t first[2] = {0, 0};
+    // the kernel with the norm is a register kernel: where the TMA-staged view
+    // kernel is asked for, or the CTA budget is one that it needs, the sync
+    // runs as ddp_sync_buckets runs it and the norm takes a pass over rank 0
+    if (view && fused_kernel_override() != DDP_FUSED_TMA && !cta_cap_is_tight()) {
+        const int dtype = s->algo == DDP_ALGO_BF16_HOOK_VIEW   ? kDtypeHook
+                          : s->algo == DDP_ALGO_FP16_HOOK_VIEW ? kDtypeHook16
+                                                               : s->dtype;
+        first[1] = s->member_tiles;
+        st = cuda_status(launch_sync_norm(s->world, s->members.data(), (int64_t)s->members.size(), dtype,
+                                          make_div(s->divisor), s->partials, q));
+    } else {
+        st = ddp_sync_buckets(s->world, s->n_params, s->grads.data(), s->numel.data(), s->bucket_of.data(),
+                              s->offset.data(), s->n_buckets, s->bucket_numel.data(),
+                              s->buckets.empty() ? nullptr : s->buckets.data(), s->dtype, s->divisor, s->algo, stream);
+        if (st) return st;
+        first[1] = s->range_tiles;
+        st = cuda_status(launch_norm_partials(s->ranges.data(), (int64_t)s->ranges.size(), s->dtype, s->partials, q));
+    }
+    if (st) return st;
+    return cuda_status(launch_norm_final(s->partials, first, 1, s->world, norms, q));
+} DDP_ABI_CATCH
+
+int32_t ddp_sync_norm_destroy(ddp_sync_norm* s) try {
+    DDP_TRACE_CALL();
+    delete s;
+    return DDP_OK;
 } DDP_ABI_CATCH
 
 int32_t ddp_adamw_create(int32_t world, int32_t n_params, void* const* params, const void* const* grads,

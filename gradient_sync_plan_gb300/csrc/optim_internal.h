@@ -37,6 +37,20 @@ cudaError_t launch_norm_final(const double* partials, const int32_t* rank_first,
 cudaError_t launch_clip(const GradRange* ranges, int64_t n, int dtype, const float* norms, float max_norm,
                         cudaStream_t stream);
 
+// ---- view sync with the norm in its epilogue (sync_norm.cu) ----------------
+// One bucket member: its elements, its place in its bucket, its bucket's chunk
+// length and its `world` pointers.
+struct SyncMember {
+    int64_t numel, offset, clen;
+    void* const* ptrs;
+};
+// Elements of one tile, and the tiles (one partial each) that a member takes.
+int64_t sync_norm_tile(int world, int dtype);
+int64_t sync_norm_tiles(int world, const SyncMember& m, int dtype);
+// dtype: a ddp_dtype or one of the hooks' (kDtypeHook, kDtypeHook16).
+cudaError_t launch_sync_norm(int world, const SyncMember* members, int64_t n, int dtype, DivSpec div, double* partials,
+                             cudaStream_t stream);
+
 // ---- AdamW (adamw.cu) ------------------------------------------------------
 // One tensor of one rank.  g is float32 or bf16 (the call's grad dtype), copy
 // bf16 or null, the others float32.

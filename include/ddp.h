@@ -25,8 +25,8 @@
  *   - Ownership: the caller owns every host and device buffer.  The library
  *     allocates no device memory at run time (the no-alloc entry point's
  *     64 MiB array is a static device array) and keeps no pointer after a
- *     call returns (except a ddp_reducer, a ddp_grad_set and a ddp_adamw, which
- *     keep the tables they were created with).  State kept between calls: cached device attributes,
+ *     call returns (except a ddp_reducer, a ddp_grad_set, a ddp_sync_norm and a
+ *     ddp_adamw, which keep the tables they were created with).  State kept between calls: cached device attributes,
  *     the two process-wide settings (ddp_set_max_ctas, ddp_set_fused_kernel)
  *     and the device status word (ddp_device_status).
  *   - Streams: `stream` is a cudaStream_t passed as void* (NULL = the legacy
@@ -671,23 +671,37 @@ int32_t ddp_grad_norm_clip(ddp_grad_set* set, float* norms, double max_norm, voi
 int32_t ddp_grad_set_destroy(ddp_grad_set* set);
 
 /*
- * ddp_sync_buckets_norm -- ddp_sync_buckets, and the norm of the gradients it
- * leaves: every rank then holds the same averaged gradients, so norms[0 ..
- * world) all receive their one global norm (as ddp_grad_norm; NaN and infinity
- * as there).  The gradients' bits are those of ddp_sync_buckets.
+ * ddp_sync_norm -- ddp_sync_buckets, and the norm of the gradients it leaves:
+ * every rank then holds the same averaged gradients, so norms[0 .. world) all
+ * receive their one global norm (as ddp_grad_norm; NaN and infinity as there).
+ * The gradients' bits are those of ddp_sync_buckets.
  *
- *   norms[world]     device float32, outside the gradients and the workspace
- *   workspace        device memory, 8-byte aligned, of at least
- *                    ddp_sync_norm_workspace_bytes; its contents need not be set.
- *                    Calls that overlap on the GPU need one each
- * Other arguments as for ddp_sync_buckets (any algo it takes).
+ * With a view algorithm the norm comes from the values the sync has in
+ * registers and costs no pass over the gradients.  With the others, with
+ * DDP_FUSED_TMA forced, or under a CTA cap below four CTAs per SM, the sync
+ * runs as ddp_sync_buckets runs it and the norm reads one rank's gradients
+ * afterwards; the squares are then added in another order, so a norm's last
+ * bits can differ between the two.
+ *
+ * The handle checks its arguments and lays out its tables once; a run then
+ * costs its launches.
+ *   workspace     device memory, 8-byte aligned, of at least
+ *                 ddp_sync_norm_workspace_bytes (DDP_ERR_CAPACITY if smaller);
+ *                 its contents need not be set.  Runs of one handle share it:
+ *                 order them
+ *   norms[world]  device float32, outside the gradients and the workspace
+ * Other arguments as for ddp_sync_buckets (any algo it takes).  The handle keeps
+ * the pointers until it is destroyed, the caller keeps the memory.
  */
-int32_t ddp_sync_norm_workspace_bytes(int32_t world, int32_t n_params, const int64_t* numel, int32_t n_buckets,
-                                      int32_t dtype, int64_t* bytes);
-int32_t ddp_sync_buckets_norm(int32_t world, int32_t n_params, void* const* grads, const int64_t* numel,
-                              const int32_t* bucket_of_param, const int64_t* offset_of_param, int32_t n_buckets,
-                              const int64_t* bucket_numel, void* const* buckets, int32_t dtype, int32_t divisor,
-                              int32_t algo, float* norms, void* workspace, int64_t workspace_bytes, void* stream);
+typedef struct ddp_sync_norm ddp_sync_norm;
+int32_t ddp_sync_norm_workspace_bytes(int32_t world, int32_t n_params, const int64_t* numel, int32_t dtype,
+                                      int64_t* bytes);
+int32_t ddp_sync_norm_create(int32_t world, int32_t n_params, void* const* grads, const int64_t* numel,
+                             const int32_t* bucket_of_param, const int64_t* offset_of_param, int32_t n_buckets,
+                             const int64_t* bucket_numel, void* const* buckets, int32_t dtype, int32_t divisor,
+                             int32_t algo, void* workspace, int64_t workspace_bytes, ddp_sync_norm** out);
+int32_t ddp_sync_norm_run(ddp_sync_norm* sync, float* norms, void* stream);
+int32_t ddp_sync_norm_destroy(ddp_sync_norm* sync);
 
 /*
  * ddp_adamw -- the optimizer step that follows the sync: AdamW over every

@@ -241,7 +241,8 @@ def test_sync_norm_keeps_the_syncs_bits(world, sizes, layout, dtype, algo):
     if algo in (ddp.DDP_ALGO_FUSED, ddp.DDP_ALGO_STAGED, ddp.DDP_ALGO_BF16_HOOK):
         buckets = [[torch.empty(int(n), dtype=bt, device="cuda") for n in plan[2]] for _ in range(world)]
     ddp.ddp_sync_buckets(other, plan, buckets, algo=algo)
-    norms = ddp.ddp_sync_buckets_norm(views, plan, buckets, algo=algo)
+    call = ddp.SyncNormCall(views, plan, buckets, algo=algo)
+    norms = call()
     torch.cuda.synchronize()
     _check_held(held, "sync norm")
     for r in range(world):
@@ -282,7 +283,7 @@ def test_sync_norm_of_extreme_values(world, n, value, check):
         row[1].mul_(0.0 if abs(value) < 1 else 1.0)
     views[0][0][n // 2] = value
     plan = ddp.ddp_plan_buckets([n, 13], ddp.F32)
-    got = float(ddp.ddp_sync_buckets_norm(views, plan)[0])
+    got = float(ddp.SyncNormCall(views, plan)()[0])
     assert check(got)
     if math.isfinite(got):
         want = _norm64(views[0])

@@ -49,12 +49,12 @@ def test_grad_set_sizes_that_overflow_are_refused():
     L, out = ddp.lib(), ctypes.c_int64(-1)
     for n in ((1 << 62) + 16, (1 << 63) - 1, ddp.MAX_NUMEL + 1):
         assert L.ddp_grad_set_workspace_bytes(1, 1, _i64(n), 0, ctypes.byref(out)) == -5
-        assert L.ddp_sync_norm_workspace_bytes(1, 1, _i64(n), 1, 0, ctypes.byref(out)) == -5
+        assert L.ddp_sync_norm_workspace_bytes(1, 1, _i64(n), 0, ctypes.byref(out)) == -5
     assert out.value == -1
     assert L.ddp_grad_set_workspace_bytes(1, 1, None, 0, ctypes.byref(out)) == -1
     assert L.ddp_grad_set_workspace_bytes(1, -1, _i64(1), 0, ctypes.byref(out)) == -1
     assert L.ddp_grad_set_workspace_bytes(1, 1, _i64(1), 0, None) == -1
-    assert L.ddp_sync_norm_workspace_bytes(1, 1, _i64(1), -1, 0, ctypes.byref(out)) == -1
+    assert L.ddp_sync_norm_workspace_bytes(1, 1, _i64(1), 0, None) == -1
 
 
 def test_grad_set_takes_empty_tensors_without_pointers():
@@ -80,23 +80,42 @@ def test_norm_and_clip_refusals():
     L.ddp_grad_set_destroy(h)
 
 
-def test_sync_norm_refusals():
-    L = ddp.lib()
-    need = ctypes.c_int64(0)
-    assert L.ddp_sync_norm_workspace_bytes(2, 1, _i64(8), 1, 0, ctypes.byref(need)) == 0 and need.value > 0
+def _sync(world=2, grads=(H, H + 4096), dtype=0, divisor=2, algo=ddp.DDP_ALGO_VIEW, ws=WS, ws_bytes=1 << 20, numel=(8,),
+          bucket=(0,), offset=(0,), bucket_numel=(8,), buckets=None, table=True, out=True):
+    h, n = ctypes.c_void_p(1), len(numel)
+    st = ddp.lib().ddp_sync_norm_create(world, n, _vp(*grads) if table else None, _i64(*numel),
+                                        (ctypes.c_int32 * n)(*bucket), _i64(*offset), len(bucket_numel),
+                                        _i64(*bucket_numel), None if buckets is None else _vp(*buckets), dtype, divisor,
+                                        algo, ws, ws_bytes, ctypes.byref(h) if out else None)
+    assert not out or st == 0 or h.value is None
+    return st, h
 
-    def call(world=2, grads=(H, H + 4096), dtype=0, divisor=2, algo=ddp.DDP_ALGO_VIEW, norms=NORMS, ws=WS,
-             ws_bytes=need.value, numel=8, table=True):
-        return L.ddp_sync_buckets_norm(world, 1, _vp(*grads) if table else None, _i64(numel), (ctypes.c_int32 * 1)(0),
-                                       _i64(0), 1, _i64(8), None, dtype, divisor, algo, norms, ws, ws_bytes, None)
-    for want, kw in ((-1, dict(world=0)), (-1, dict(dtype=5)), (-1, dict(norms=None)), (-2, dict(norms=NORMS + 1)),
-                     (-1, dict(ws=None)), (-2, dict(ws=WS + 4)), (-5, dict(ws_bytes=need.value - 1)),
-                     (-1, dict(norms=H + 28)), (-1, dict(ws=H + 4096)), (-1, dict(norms=WS)), (-1, dict(table=False)),
-                     (-1, dict(algo=ddp.DDP_ALGO_DRYRUN)), (-1, dict(algo=99)), (-1, dict(divisor=-1)),
-                     (-1, dict(algo=ddp.DDP_ALGO_FUSED)), (-1, dict(algo=ddp.DDP_ALGO_BF16_HOOK_VIEW, dtype=1)),
-                     (-1, dict(numel=9)), (-1, dict(grads=(H, H + 16))), (-1, dict(grads=(H, None))),
-                     (-2, dict(grads=(H, H + 4098)))):
-        assert call(**kw) == want, kw
+
+@pytest.mark.parametrize("want,kw", [
+    (-1, dict(world=0)), (-5, dict(world=513)), (-1, dict(dtype=5)), (-1, dict(divisor=-1)), (-1, dict(out=False)),
+    (-1, dict(ws=None)), (-2, dict(ws=WS + 4)), (-5, dict(ws_bytes=8)), (-1, dict(ws=H + 4096)), (-1, dict(table=False)),
+    (-1, dict(algo=ddp.DDP_ALGO_DRYRUN)), (-1, dict(algo=99)), (-1, dict(algo=ddp.DDP_ALGO_FUSED)),
+    (-1, dict(algo=ddp.DDP_ALGO_BF16_HOOK_VIEW, dtype=1)), (-1, dict(numel=(9,))), (-1, dict(numel=(-1,))),
+    (-1, dict(offset=(1,))), (-1, dict(offset=(-1,))), (-1, dict(bucket=(1,))), (-1, dict(bucket=(-1,))),
+    (-5, dict(bucket_numel=(ddp.MAX_NUMEL + 1,))), (-1, dict(bucket_numel=(-1,))),
+    (-1, dict(grads=(H, H + 16))), (-1, dict(grads=(H, None))), (-2, dict(grads=(H, H + 4098))),
+    (-1, dict(grads=(H, H + 64, H + 4096, H + 8192), numel=(8, 8), bucket=(0, 0), offset=(0, 7), bucket_numel=(16,))),
+    (-1, dict(algo=ddp.DDP_ALGO_FUSED, buckets=(H + (1 << 20), None))),
+    (-1, dict(algo=ddp.DDP_ALGO_FUSED, buckets=(H + (1 << 20), H + 16))),
+    (-2, dict(algo=ddp.DDP_ALGO_FUSED, buckets=(H + (1 << 20), H + (2 << 20) + 2))),
+])
+def test_sync_norm_create_refusals(want, kw):
+    assert _sync(**kw)[0] == want
+
+
+def test_sync_norm_run_refusals():
+    L = ddp.lib()
+    st, h = _sync()
+    assert st == 0
+    for norms, want in ((None, -1), (NORMS + 1, -2), (H + 28, -1), (H + 4096 - 4, -1), (WS, -1)):
+        assert L.ddp_sync_norm_run(h, norms, None) == want
+    assert L.ddp_sync_norm_run(None, NORMS, None) == -1
+    assert L.ddp_sync_norm_destroy(h) == 0 and L.ddp_sync_norm_destroy(None) == 0
 
 
 def _adamw(world=1, n=1, p=(H,), g=(H + (1 << 20),), m=(H + (2 << 20),), v=(H + (3 << 20),), c=None, sizes=(8,),
