@@ -116,12 +116,7 @@ __global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Adam
     pdl_release();
     pdl_acquire();
     for (int tile = blockIdx.x; tile < b.tiles; tile += gridDim.x) {
-        int lo = 0, hi = b.n - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (b.tile_end[mid] > tile) hi = mid; else lo = mid + 1;
-        }
-        const int i = lo;
+        const int i = first_past(b.tile_end, b.n, tile);
         const int64_t n = b.numel[i];
         const int64_t e0 = (int64_t)(tile - (i ? b.tile_end[i - 1] : 0)) * kAdamTile - b.lead[i];
         const bool vec = b.flags[i] & 1;

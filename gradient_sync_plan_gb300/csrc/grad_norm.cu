@@ -40,11 +40,7 @@ int64_t range_tiles(const void* ptr, int64_t bytes) {
 // The range that holds `tile`, and where the tile starts in memory.
 template <int CAP>
 __device__ __forceinline__ int range_of(const RangeTab<CAP>& b, int tile, uintptr_t* base) {
-    int lo = 0, hi = b.n - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (b.tile_end[mid] > tile) hi = mid; else lo = mid + 1;
-    }
+    const int lo = first_past(b.tile_end, b.n, tile);
     const int first = lo ? b.tile_end[lo - 1] : 0;
     *base = (reinterpret_cast<uintptr_t>(b.ptr[lo]) & ~(uintptr_t)(kNormAlign - 1)) + (uintptr_t)(tile - first) * kNormTile;
     return lo;

@@ -52,8 +52,8 @@ __device__ __forceinline__ double warp_sum(double s) {
     return s;
 }
 
-// Whether a warp's sum of squares can be trusted in binary32 (a zero too, if
-// every value is one: the caller looks).
+// Whether a warp's sum of squares can be trusted in binary32 (so can a zero, if
+// every value is one).
 __device__ __forceinline__ bool in_square_range(float w) { return w >= 0x1p-90f && w <= 0x1p126f; }
 
 // The sum of squares of every value in the warp's U vectors a lane; all lanes
@@ -90,6 +90,23 @@ __device__ __forceinline__ double warp_sum_squares(const typename E::V (&x)[U]) 
         }
     }
     return warp_sum(d);
+}
+
+// The first of n ascending ends that lies past x (x is below the last end).
+// Each lane looks at one entry of a stride, then at one of the stretch that is
+// left: two rounds of loads for up to 1024 entries, where halving takes ten,
+// one behind the other.  The whole warp must call it.
+__device__ __forceinline__ int first_past(const int32_t* ends, int n, int x) {
+    const int lane = threadIdx.x & 31;
+    int from = 0;
+    int stride = 1;
+    while (stride * 32 < n) stride *= 32;
+    for (;; stride /= 32) {
+        const int at = min(from + (lane + 1) * stride, n) - 1;
+        const unsigned past = __ballot_sync(0xffffffffu, ends[at] > x);
+        from += (__ffs(past) - 1) * stride;
+        if (stride == 1) return from;
+    }
 }
 
 // One value a warp -> their sum in thread 0 (undefined elsewhere), added in

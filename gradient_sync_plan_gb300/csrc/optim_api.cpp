@@ -39,6 +39,7 @@ struct ddp_sync_norm {
     std::vector<SyncMember> members;
     std::vector<void*> ptrs;
     int32_t member_tiles = 0;
+    int vecs = 0;
     // rank 0's gradients, for a norm pass after a sync without one
     std::vector<GradRange> ranges;
     int32_t range_tiles = 0;
@@ -108,6 +109,13 @@ int64_t most_tiles(int32_t n_params, const int64_t* numel, int64_t es) {
     for (int32_t i = 0; i < n_params; ++i)
         if (numel[i] > 0) t += (numel[i] * es + kNormAlign - 1) / kNormTile + 2;
     return t;
+}
+
+// Vectors a thread of the sync with norm takes.
+int sync_vecs(int32_t world, int32_t n_params, const int64_t* numel, int32_t dtype) {
+    int64_t n = 0;
+    for (int32_t i = 0; i < n_params; ++i) n += numel[i];
+    return sync_norm_vecs(world, n, dtype);
 }
 
 bool bad_max_norm(double max_norm) { return !(max_norm > 0.0) || !((float)max_norm > 0.f); }
@@ -209,7 +217,7 @@ int32_t ddp_sync_norm_workspace_bytes(int32_t world, int32_t n_params, const int
     if (!bytes) return DDP_ERR_INVALID;
     const int32_t st = check_sizes(world, n_params, numel, dtype);
     if (st) return st;
-    const int64_t tile = sync_norm_tile(world, dtype);
+    const int64_t tile = (int64_t)kThreads * sync_vecs(world, n_params, numel, dtype) * (16 / elem_bytes(dtype));
     int64_t tiles = 0;
     for (int32_t i = 0; i < n_params; ++i)
         if (numel[i] > 0) tiles += numel[i] / tile + 2;
@@ -308,7 +316,8 @@ int32_t ddp_sync_norm_create(int32_t world, int32_t n_params, void* const* grads
         for (int32_t r = 0; r < world; ++r) s->ptrs.push_back(grads[(int64_t)r * n_params + p]);
         s->members.push_back(SyncMember{numel[p], offset_of_param[p], chunk_len(bucket_numel[k], world), at});
     }
-    for (const SyncMember& m : s->members) s->member_tiles += (int32_t)sync_norm_tiles(world, m, dtype);
+    s->vecs = sync_vecs(world, n_params, numel, dtype);
+    for (const SyncMember& m : s->members) s->member_tiles += (int32_t)sync_norm_tiles(world, m, s->vecs, dtype);
     // every rank holds the same average after the sync: rank 0's norm is everybody's
     for (int32_t p = 0; p < n_params; ++p)
         if (numel[p] > 0) add_range(&s->ranges, grads[p], numel[p] * es, 0);
@@ -334,7 +343,7 @@ int32_t ddp_sync_norm_run(ddp_sync_norm* s, float* norms, void* stream) try {
                           : s->algo == DDP_ALGO_FP16_HOOK_VIEW ? kDtypeHook16
                                                                : s->dtype;
         first[1] = s->member_tiles;
-        st = cuda_status(launch_sync_norm(s->world, s->members.data(), (int64_t)s->members.size(), dtype,
+        st = cuda_status(launch_sync_norm(s->world, s->members.data(), (int64_t)s->members.size(), s->vecs, dtype,
                                           make_div(s->divisor), s->partials, q));
     } else {
         st = ddp_sync_buckets(s->world, s->n_params, s->grads.data(), s->numel.data(), s->bucket_of.data(),

@@ -44,12 +44,13 @@ struct SyncMember {
     int64_t numel, offset, clen;
     void* const* ptrs;
 };
-// Elements of one tile, and the tiles (one partial each) that a member takes.
-int64_t sync_norm_tile(int world, int dtype);
-int64_t sync_norm_tiles(int world, const SyncMember& m, int dtype);
+// Vectors a thread takes of a tile when a rank's members have numel elements,
+// and the tiles (one partial each) of one member.
+int sync_norm_vecs(int world, int64_t numel, int dtype);
+int64_t sync_norm_tiles(int world, const SyncMember& m, int vecs, int dtype);
 // dtype: a ddp_dtype or one of the hooks' (kDtypeHook, kDtypeHook16).
-cudaError_t launch_sync_norm(int world, const SyncMember* members, int64_t n, int dtype, DivSpec div, double* partials,
-                             cudaStream_t stream);
+cudaError_t launch_sync_norm(int world, const SyncMember* members, int64_t n, int vecs, int dtype, DivSpec div,
+                             double* partials, cudaStream_t stream);
 
 // ---- AdamW (adamw.cu) ------------------------------------------------------
 // One tensor of one rank.  g is float32 or bf16 (the call's grad dtype), copy

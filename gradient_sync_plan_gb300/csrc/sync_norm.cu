@@ -29,6 +29,7 @@ struct SyncTab {
     int32_t n;
     int32_t tiles;
     int32_t world;
+    int32_t vecs;                // vectors a thread takes of a tile
     int32_t div_mode;
     float div_operand;
     int64_t numel[MEMBERS];
@@ -79,41 +80,65 @@ __device__ __forceinline__ float sum_squares(uint4 y) {
 __device__ __forceinline__ float sum_squares(float f) { return f * f; }
 __device__ __forceinline__ float sum_squares(uint16_t h) { return sum_squares(bf16_to_f32(h)); }
 
-// E: element type; G: ranks whose loads are in flight together; U: vectors a
-// thread takes of a tile, one after the other: with few ranks the registers
-// that leaves free hold more blocks per SM, and those the loads in flight.
-template <class E, int G, int U, class TAB>
-__global__ void __launch_bounds__(kThreads, 4) k_sync_norm(const __grid_constant__ TAB b, double* partials) {
+// Zero if and only if every value is a zero of either sign.
+__device__ __forceinline__ uint32_t magnitude_bits(float f) { return __float_as_uint(f) << 1; }
+__device__ __forceinline__ uint32_t magnitude_bits(uint16_t h) { return (uint32_t)(h & 0x7FFFu); }
+__device__ __forceinline__ uint32_t magnitude_bits(float4 y) {
+    return (__float_as_uint(y.x) | __float_as_uint(y.y) | __float_as_uint(y.z) | __float_as_uint(y.w)) << 1;
+}
+__device__ __forceinline__ uint32_t magnitude_bits(uint4 y) { return (y.x | y.y | y.z | y.w) & 0x7FFF7FFFu; }
+
+// E: element type; G: ranks whose loads are in flight together; B: vectors a
+// thread folds side by side; MINB: blocks an SM has room for.
+template <class E, int G, int B, int MINB, class TAB>
+__global__ void __launch_bounds__(kThreads, MINB) k_sync_norm(const __grid_constant__ TAB b, double* partials) {
     using V = typename E::V;
     using S = typename E::S;
     constexpr int L = E::L;
-    constexpr int kTile = kThreads * U * L;
-    __shared__ double sh[kThreads / 32];
+    constexpr int kRow = kThreads * L;           // elements the block takes with one vector a thread
+    __shared__ float sh[kThreads / 32];
+    __shared__ double sh64[kThreads / 32];
+    __shared__ int odd;                          // a warp's sum is out of binary32's safe range
+    if (threadIdx.x == 0) odd = 0;
+    __syncthreads();
     pdl_release();
     pdl_acquire();
     const int world = b.world;
     for (int tile = blockIdx.x; tile < b.tiles; tile += gridDim.x) {
-        int lo = 0, hi = b.n - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (b.tile_end[mid] > tile) hi = mid; else lo = mid + 1;
-        }
-        const int i = lo;
+        const int i = first_past(b.tile_end, b.n, tile);
         // pieces: vectors at 16-byte boundaries, or elements where the ranks'
         // pointers do not line up; positions count from e0, [head, tail) are the member's
+        const int tile_len = kRow * b.vecs;
         const int step = b.lead[i] >= 0 ? L : 1;
-        const int64_t e0 = (int64_t)(tile - (i ? b.tile_end[i - 1] : 0)) * kTile - max((int)b.lead[i], 0);
+        const int64_t e0 = (int64_t)(tile - (i ? b.tile_end[i - 1] : 0)) * tile_len - max((int)b.lead[i], 0);
         const int head = e0 < 0 ? (int)-e0 : 0;
-        const int tail = (int)min((int64_t)kTile, b.numel[i] - e0);
+        const int tail = (int)min((int64_t)tile_len, b.numel[i] - e0);
         const int64_t q0 = b.offset[i] + e0;
         const int j0 = chunk_of(q0 + head, b.clen[i], b.inv_clen[i]);
-        const int near = (int)min((int64_t)kTile, (int64_t)(j0 + 1) * b.clen[i] - q0);     // where chunk j0 ends
+        const int near = (int)min((int64_t)tile_len, (int64_t)(j0 + 1) * b.clen[i] - q0);     // where chunk j0 ends
         char* const* pp = b.ptr + (size_t)i * world;
         auto at = [&](int r) -> const char* { return pp[r]; };
         auto start_of = [&](int j) { return j + 1 == world ? 0 : j + 1; };
         float s = 0.f;
+        uint32_t bits = 0;                       // of every value's, but the sign
+        int a = 0;
+        if (B > 1 && step == L && head == 0) {   // rows of whole vectors of chunk j0, several at a time
 #pragma unroll 1
-        for (int a = threadIdx.x * step; a < kTile; a += kThreads * step) {
+            for (; a + B * kRow <= min(tail, near); a += B * kRow) {
+                const int64_t byte = (e0 + a + (int)threadIdx.x * L) * (int64_t)sizeof(S);
+                V y[B];
+                fold_ring_vecs<E, G, B>(at, world, start_of(j0), byte, kThreads * 16, y);
+#pragma unroll
+                for (int u = 0; u < B; ++u) y[u] = average_v<E>(y[u], b.div_mode, b.div_operand);
+                for (int r = 0; r < world; ++r)
+#pragma unroll
+                    for (int u = 0; u < B; ++u) st_stream<V>(pp[r] + byte + u * (kThreads * 16), y[u]);
+#pragma unroll
+                for (int u = 0; u < B; ++u) s += sum_squares(y[u]), bits |= magnitude_bits(y[u]);
+            }
+        }
+#pragma unroll 1
+        for (a += threadIdx.x * step; a < tail; a += kThreads * step) {
             const int first = max(a, head), end = min(a + step, tail);
             if (first >= end) continue;
             int j = j0;
@@ -127,6 +152,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_sync_norm(const __grid_constant
                 const V y = average_v<E>(fold_ring_vec<E, G>(at, world, start_of(j), byte), b.div_mode, b.div_operand);
                 for (int r = 0; r < world; ++r) st_stream<V>(pp[r] + byte, y);
                 s += sum_squares(y);
+                bits |= magnitude_bits(y);
                 continue;
             }
 #pragma unroll 1
@@ -135,27 +161,45 @@ __global__ void __launch_bounds__(kThreads, 4) k_sync_norm(const __grid_constant
                 const S y = average_s<E>(fold_ring_scalar<E>(at, world, start_of(j), e0 + e), b.div_mode, b.div_operand);
                 for (int r = 0; r < world; ++r) reinterpret_cast<S*>(pp[r])[e0 + e] = y;
                 s += sum_squares(y);
+                bits |= magnitude_bits(y);
             }
         }
-        double w = warp_sum(s);
-        if (!in_square_range((float)w)) {        // squared again in binary64, from what this thread wrote to rank 0
+        const float w = warp_sum(s);
+        const bool again = !in_square_range(w) && __any_sync(0xffffffffu, bits != 0);     // zeros are exact
+        if ((threadIdx.x & 31) == 0) {
+            sh[threadIdx.x >> 5] = w;
+            if (again) odd = 1;
+        }
+        __syncthreads();
+        if (odd) {
+            // squared again in binary64, from what the block wrote to rank 0
             const S* mine = reinterpret_cast<const S*>(pp[0]) + e0;
             double d = 0.0;
 #pragma unroll 1
-            for (int a = threadIdx.x * step; a < kTile; a += kThreads * step)
-                for (int e = max(a, head); e < min(a + step, tail); ++e) d += square(mine[e]);
-            w = warp_sum(d);
+            for (int e = head + (int)threadIdx.x; e < tail; e += kThreads) d += square(mine[e]);
+            const double t = block_sum(warp_sum(d), sh64);
+            if (threadIdx.x == 0) partials[tile] = t, odd = 0;
+        } else if (threadIdx.x < kThreads / 32) {
+            float t = sh[threadIdx.x];
+#pragma unroll
+            for (int d = kThreads / 64; d; d >>= 1) t += __shfl_xor_sync((1u << (kThreads / 32)) - 1, t, d);
+            if (threadIdx.x == 0) partials[tile] = (double)t;
         }
-        const double t = block_sum(w, sh);
-        if (threadIdx.x == 0) partials[tile] = t;
         __syncthreads();                         // sh is free for the next tile
     }
 }
 
-// Vectors a thread takes of a tile: enough loads in flight with few ranks.
-static int vecs_of(int world) { return world <= 2 ? 4 : world <= 4 ? 2 : 1; }
-
-int64_t sync_norm_tile(int world, int dtype) { return (int64_t)kThreads * vecs_of(world) * (dtype == DDP_BF16 ? 8 : 4); }
+// Vectors a thread takes of a tile: more of them share a block's fixed costs
+// (its start, the search, the sum), fewer spread a small call over the SMs,
+// and over many ranks one keeps each rank's stream in address order: 355M fp32
+// on 8 ranks 3.28 ms with one, 3.34 with four; on 2 ranks 1.33 and 0.82 ms.
+constexpr int kSms = 152;
+int sync_norm_vecs(int world, int64_t numel, int dtype) {
+    const int64_t vectors = numel / (16 / elem_bytes(dtype));
+    int v = world <= 4 ? 4 : 1;
+    while (v > 1 && vectors < (int64_t)v * kThreads * kSms * 16) v /= 2;
+    return v;
+}
 
 // Elements past a 16-byte boundary that every rank's pointer is, or -1.
 static int lead_of(int world, const SyncMember& m, int64_t es) {
@@ -165,13 +209,14 @@ static int lead_of(int world, const SyncMember& m, int64_t es) {
     return (int)((int64_t)q / es);
 }
 
-template <class E, int G, int U, class TAB>
-static cudaError_t sync_tables(int world, const SyncMember* members, int64_t n, DivSpec div, double* partials,
+template <class E, int G, int B, int MINB, class TAB>
+static cudaError_t sync_tables(int world, const SyncMember* members, int64_t n, int vecs, DivSpec div, double* partials,
                                cudaStream_t st) {
-    constexpr int64_t kTile = (int64_t)kThreads * U * E::L;
+    const int64_t tile = (int64_t)kThreads * vecs * E::L;
     const int most = std::min(TAB::kMembers, TAB::kPtrs / world);
     TAB b;
     b.world = world;
+    b.vecs = vecs;
     b.div_mode = div.mode;
     b.div_operand = div.operand;
     int64_t i = 0;
@@ -181,7 +226,7 @@ static cudaError_t sync_tables(int world, const SyncMember* members, int64_t n, 
         for (; i < n && b.n < most; ++i, ++b.n) {
             const SyncMember& m = members[i];
             const int lead = lead_of(world, m, (int64_t)sizeof(typename E::S));
-            b.tiles += (int32_t)((std::max(lead, 0) + m.numel + kTile - 1) / kTile);
+            b.tiles += (int32_t)((std::max(lead, 0) + m.numel + tile - 1) / tile);
             b.numel[b.n] = m.numel;
             b.offset[b.n] = m.offset;
             b.clen[b.n] = m.clen;
@@ -190,7 +235,7 @@ static cudaError_t sync_tables(int world, const SyncMember* members, int64_t n, 
             b.lead[b.n] = (int8_t)lead;
             for (int r = 0; r < world; ++r) b.ptr[(size_t)b.n * world + r] = static_cast<char*>(m.ptrs[r]);
         }
-        const cudaError_t e = launch_dependent(k_sync_norm<E, G, U, TAB>, dim3(cap_ctas(b.tiles)), dim3(kThreads), 0, st,
+        const cudaError_t e = launch_dependent(k_sync_norm<E, G, B, MINB, TAB>, dim3(cap_ctas(b.tiles)), dim3(kThreads), 0, st,
                                                b, partials);
         if (e != cudaSuccess) return e;
         partials += b.tiles;
@@ -199,29 +244,33 @@ static cudaError_t sync_tables(int world, const SyncMember* members, int64_t n, 
 }
 
 template <class E, class TAB>
-static cudaError_t sync_world(int world, const SyncMember* m, int64_t n, DivSpec div, double* partials, cudaStream_t st) {
-    if (world <= 2) return sync_tables<E, 2, 4, TAB>(world, m, n, div, partials, st);
-    if (world <= 4) return sync_tables<E, 4, 2, TAB>(world, m, n, div, partials, st);
-    return sync_tables<E, 8, 1, TAB>(world, m, n, div, partials, st);
+static cudaError_t sync_world(int world, const SyncMember* m, int64_t n, int vecs, DivSpec div, double* partials,
+                              cudaStream_t st) {
+    // 6.9 TB/s each on the 355M decoder; without side-by-side vectors 6.2 on 2
+    // ranks, with four blocks of 8 ranks' loads 6.7 on 8
+    if (world <= 2) return sync_tables<E, 2, 2, 4, TAB>(world, m, n, vecs, div, partials, st);
+    if (world <= 4) return sync_tables<E, 4, 1, 4, TAB>(world, m, n, vecs, div, partials, st);
+    return sync_tables<E, 4, 1, 5, TAB>(world, m, n, vecs, div, partials, st);
 }
 
 template <class E>
-static cudaError_t sync_size(int world, const SyncMember* m, int64_t n, DivSpec div, double* partials, cudaStream_t st) {
-    if (n <= SyncSmall::kMembers && n * world <= SyncSmall::kPtrs)
-        return sync_world<E, SyncSmall>(world, m, n, div, partials, st);
-    return sync_world<E, SyncLarge>(world, m, n, div, partials, st);
-}
-
-cudaError_t launch_sync_norm(int world, const SyncMember* members, int64_t n, int dtype, DivSpec div, double* partials,
+static cudaError_t sync_size(int world, const SyncMember* m, int64_t n, int vecs, DivSpec div, double* partials,
                              cudaStream_t st) {
-    if (dtype == DDP_F32) return sync_size<EF32>(world, members, n, div, partials, st);
-    if (dtype == kDtypeHook) return sync_size<EHOOK>(world, members, n, div, partials, st);
-    if (dtype == kDtypeHook16) return sync_size<EHOOK16>(world, members, n, div, partials, st);
-    return sync_size<EBF16>(world, members, n, div, partials, st);
+    if (n <= SyncSmall::kMembers && n * world <= SyncSmall::kPtrs)
+        return sync_world<E, SyncSmall>(world, m, n, vecs, div, partials, st);
+    return sync_world<E, SyncLarge>(world, m, n, vecs, div, partials, st);
 }
 
-int64_t sync_norm_tiles(int world, const SyncMember& m, int dtype) {
-    const int64_t t = sync_norm_tile(world, dtype);
+cudaError_t launch_sync_norm(int world, const SyncMember* members, int64_t n, int vecs, int dtype, DivSpec div,
+                             double* partials, cudaStream_t st) {
+    if (dtype == DDP_F32) return sync_size<EF32>(world, members, n, vecs, div, partials, st);
+    if (dtype == kDtypeHook) return sync_size<EHOOK>(world, members, n, vecs, div, partials, st);
+    if (dtype == kDtypeHook16) return sync_size<EHOOK16>(world, members, n, vecs, div, partials, st);
+    return sync_size<EBF16>(world, members, n, vecs, div, partials, st);
+}
+
+int64_t sync_norm_tiles(int world, const SyncMember& m, int vecs, int dtype) {
+    const int64_t t = (int64_t)kThreads * vecs * (16 / elem_bytes(dtype));
     return (std::max(lead_of(world, m, elem_bytes(dtype)), 0) + m.numel + t - 1) / t;
 }
 
