@@ -133,8 +133,7 @@ def lib() -> ctypes.CDLL:
                                                i32, vp, i64, P(vp)]
             L.ddp_sync_norm_run.argtypes = [vp, vp, vp]
             L.ddp_sync_norm_destroy.argtypes = [vp]
-            L.ddp_adamw_create.argtypes = [i32, i32, P(vp), P(vp), i32, P(vp), P(vp), P(vp), P(i64), P(u8), vp, vp, vp,
-                                           P(vp)]
+            L.ddp_adamw_create.argtypes = [i32, i32, P(vp), P(vp), i32, P(vp), P(vp), P(vp), P(i64), P(u8), vp, vp, P(vp)]
             L.ddp_adamw_step.argtypes = [vp, f64, f64, f64, f64, f64, vp, f64, vp]
             L.ddp_adamw_destroy.argtypes = [vp]
             for name in EXPORTS[4:]:   # every entry point from ddp_set_max_ctas on returns a status
@@ -783,7 +782,7 @@ class AdamW:
     true where weight decay does not apply.  steps: int32 [world], the steps
     taken so far (zeros if None)."""
 
-    def __init__(self, params, grads, exp_avg, exp_avg_sq, copies=None, no_decay=None, steps=None, stream=None):
+    def __init__(self, params, grads, exp_avg, exp_avg_sq, copies=None, no_decay=None, steps=None):
         torch = _torch()
         self.world = len(params)
         pp, numels, _ = _tensor_table(params, "params", (torch.float32,))
@@ -811,8 +810,7 @@ class AdamW:
         _check("ddp_adamw_create",
                lib().ddp_adamw_create(self.world, len(sizes), _vp_array(pp), _vp_array(gp),
                                       BF16 if gdt == torch.bfloat16 else F32, _vp_array(mp), _vp_array(vp), cp,
-                                      _i64_array(sizes), mask, word, self._workspace.data_ptr(), _stream(stream),
-                                      ctypes.byref(h)))
+                                      _i64_array(sizes), mask, word, self._workspace.data_ptr(), ctypes.byref(h)))
         self._h = h
 
     def step(self, lr: float, betas: Tuple[float, float] = (0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.0,

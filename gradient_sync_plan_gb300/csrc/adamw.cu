@@ -41,12 +41,13 @@ struct AdamWTab {
     uint8_t flags[CAP];        // 1: aligned groups of 4 line up in every array, 2: weight decay
 };
 constexpr int kAdamSmall = 32;
+constexpr int kAdamMedium = 176;
 constexpr int kAdamLarge = 560;
 static_assert(sizeof(AdamWTab<kAdamLarge>) + 128 <= kMaxParamBytes, "AdamW table exceeds the kernel parameter limit");
 
 static int64_t lead_of(const AdamWItem& it) { return (int64_t)(reinterpret_cast<uintptr_t>(it.p) % 128 / 4); }
 
-int64_t adamw_tiles(const AdamWItem& it, int) { return (lead_of(it) + it.numel + kAdamTile - 1) / kAdamTile; }
+int64_t adamw_tiles(const AdamWItem& it) { return (lead_of(it) + it.numel + kAdamTile - 1) / kAdamTile; }
 
 struct RankStep {
     float c, step, inv_root;   // clip factor, lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
@@ -107,16 +108,30 @@ __device__ __forceinline__ void update_one(const AdamWTab<CAP>& b, int i, int64_
     if (COPY) static_cast<uint16_t*>(b.copy[i])[e] = f32_to_bf16_rn(p);
 }
 
+__device__ __forceinline__ void advance_steps(const float* norms, int32_t* steps, int world, int from, int stride) {
+    for (int r = from; r < world; r += stride)
+        if (!norms || fabsf(norms[r]) <= 3.402823466e38f) ++steps[r];
+}
+
+// The counts advance when every block has read them.  In a launch of few
+// blocks the one that arrives last does it; a block that arrives waits for its
+// stores first, so a launch of many leaves it to a second kernel.
+__global__ void __launch_bounds__(kThreads) k_adamw_advance(const float* norms, int32_t* steps, int world) {
+    pdl_release();
+    pdl_acquire();
+    advance_steps(norms, steps, world, threadIdx.x, kThreads);
+}
+
 template <class G, bool COPY, int CAP>
-__global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ AdamWTab<CAP> b, const AdamWScalars s,
-                                                    const float* norms, int32_t* steps, int32_t* arrivals, int world,
-                                                    int advance) {
+__global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ AdamWTab<CAP> b,
+                                                    const __grid_constant__ AdamWScalars s, const float* norms,
+                                                    int32_t* steps, int32_t* arrivals, int world) {
     __shared__ RankStep shared_step;
-    __shared__ int last;
+    __shared__ int slot;
     pdl_release();
     pdl_acquire();
     for (int tile = blockIdx.x; tile < b.tiles; tile += gridDim.x) {
-        const int i = first_past(b.tile_end, b.n, tile);
+        const int i = block_first_past(b.tile_end, b.n, tile, &slot);
         const int64_t n = b.numel[i];
         const int64_t e0 = (int64_t)(tile - (i ? b.tile_end[i - 1] : 0)) * kAdamTile - b.lead[i];
         const bool vec = b.flags[i] & 1;
@@ -134,10 +149,13 @@ __global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Adam
                 }
             }
         }
-        if (threadIdx.x == 0) shared_step = rank_step(s, norms, steps, b.rank[i]);     // while the loads are under way
+        if (threadIdx.x < 32) {                  // while the loads are under way
+            const RankStep q = rank_step(s, norms, steps, b.rank[i]);
+            if (threadIdx.x == 0) shared_step = q;
+        }
         __syncthreads();
         const RankStep q = shared_step;
-        __syncthreads();                         // shared_step is free for the next tile
+        if (tile + (int)gridDim.x < b.tiles) __syncthreads();   // shared_step and slot are free for the next tile
         if (q.skip) continue;
         const float lr_decay = (b.flags[i] & 2) ? s.lr_decay : 0.f;
         if (vec) {
@@ -164,31 +182,38 @@ __global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Adam
                 if (k >= 0 && k < n) update_one<G, COPY>(b, i, k, s, q, lr_decay);
         }
     }
-    if (!advance) return;
-    // the block that arrives last, when every block has read the counts, advances them
-    __syncthreads();
+    if (!arrivals || threadIdx.x >= 32) return;
+    int last = 0;
     if (threadIdx.x == 0) {
         __threadfence();
         last = atomicAdd(arrivals, 1) == (int)gridDim.x - 1;
     }
-    __syncthreads();
-    if (!last) return;
+    if (!__shfl_sync(0xffffffffu, last, 0)) return;
+    __threadfence();
     if (threadIdx.x == 0) *arrivals = 0;
-    for (int r = threadIdx.x; r < world; r += kThreads)
-        if (!norms || fabsf(norms[r]) <= 3.402823466e38f) ++steps[r];
+    advance_steps(norms, steps, world, threadIdx.x, 32);
 }
 
-template <class G, bool COPY, int CAP>
-static cudaError_t adamw_cap(const AdamWItem* items, int64_t n, int world, AdamWScalars s, const float* norms,
-                             int32_t* steps, int32_t* arrivals, cudaStream_t st) {
-    AdamWTab<CAP> b;
+constexpr int kAdamArriveTiles = 608;            // a wave of four blocks an SM
+
+struct AdamWPlan {
+    std::vector<AdamWTab<kAdamSmall>> small;
+    std::vector<AdamWTab<kAdamMedium>> medium;
+    std::vector<AdamWTab<kAdamLarge>> large;
+};
+
+template <int CAP>
+static void fill_tables(const AdamWItem* items, int64_t n, int grad_dtype, bool copies, std::vector<AdamWTab<CAP>>* out) {
+    const uintptr_t gs = (uintptr_t)elem_bytes(grad_dtype);
     int64_t i = 0;
     do {                                         // a call without elements still counts as a step
+        out->emplace_back();
+        AdamWTab<CAP>& b = out->back();
         b.n = 0;
         b.tiles = 0;
         for (; i < n && b.n < CAP; ++i, ++b.n) {
             const AdamWItem& it = items[i];
-            b.tiles += (int32_t)adamw_tiles(it, 0);
+            b.tiles += (int32_t)adamw_tiles(it);
             b.p[b.n] = it.p;
             b.m[b.n] = it.m;
             b.v[b.n] = it.v;
@@ -198,35 +223,53 @@ static cudaError_t adamw_cap(const AdamWItem* items, int64_t n, int world, AdamW
             b.tile_end[b.n] = b.tiles;
             b.rank[b.n] = (int16_t)it.rank;
             const int64_t lead = lead_of(it);
-            const uintptr_t q = (uintptr_t)lead % 4, gs = sizeof(G);
+            const uintptr_t q = (uintptr_t)lead % 4;
             const bool vec = reinterpret_cast<uintptr_t>(it.m) % 16 == 4 * q &&
                              reinterpret_cast<uintptr_t>(it.v) % 16 == 4 * q &&
                              reinterpret_cast<uintptr_t>(it.g) % (4 * gs) == gs * q &&
-                             (!COPY || reinterpret_cast<uintptr_t>(it.copy) % 8 == 2 * q);
+                             (!copies || reinterpret_cast<uintptr_t>(it.copy) % 8 == 2 * q);
             b.lead[b.n] = (uint8_t)lead;
             b.flags[b.n] = (uint8_t)((vec ? 1 : 0) | (it.decay ? 2 : 0));
         }
-        const cudaError_t e = launch_dependent(k_adamw<G, COPY, CAP>, dim3(cap_ctas(b.tiles)), dim3(kThreads), 0, st, b,
-                                               s, norms, steps, arrivals, world, i >= n ? 1 : 0);
-        if (e != cudaSuccess) return e;
     } while (i < n);
-    return cudaSuccess;
+}
+
+std::shared_ptr<const AdamWPlan> make_adamw_plan(const AdamWItem* items, int64_t n, int grad_dtype, bool copies) {
+    auto plan = std::make_shared<AdamWPlan>();
+    if (n <= kAdamSmall) fill_tables(items, n, grad_dtype, copies, &plan->small);
+    else if (n <= kAdamMedium) fill_tables(items, n, grad_dtype, copies, &plan->medium);
+    else fill_tables(items, n, grad_dtype, copies, &plan->large);
+    return plan;
+}
+
+template <class G, bool COPY, int CAP>
+static cudaError_t adamw_tables(const std::vector<AdamWTab<CAP>>& tables, int world, const AdamWScalars& s,
+                                const float* norms, int32_t* steps, int32_t* arrivals, cudaStream_t st) {
+    const bool one = tables.size() == 1 && tables[0].tiles <= kAdamArriveTiles;
+    int32_t* const count = one ? arrivals : nullptr;
+    for (const AdamWTab<CAP>& b : tables) {
+        const cudaError_t e = launch_table(k_adamw<G, COPY, CAP>, dim3(cap_ctas(b.tiles)), dim3(kThreads), st, b, s, norms,
+                                           steps, count, world);
+        if (e != cudaSuccess) return e;
+    }
+    return one ? cudaSuccess : launch_table(k_adamw_advance, dim3(1), dim3(kThreads), st, norms, steps, world);
 }
 
 template <class G, bool COPY>
-static cudaError_t adamw_n(const AdamWItem* items, int64_t n, int world, AdamWScalars s, const float* norms,
-                           int32_t* steps, int32_t* arrivals, cudaStream_t st) {
-    if (n <= kAdamSmall) return adamw_cap<G, COPY, kAdamSmall>(items, n, world, s, norms, steps, arrivals, st);
-    return adamw_cap<G, COPY, kAdamLarge>(items, n, world, s, norms, steps, arrivals, st);
+static cudaError_t adamw(const AdamWPlan& p, int world, const AdamWScalars& s, const float* norms, int32_t* steps,
+                         int32_t* arrivals, cudaStream_t st) {
+    if (!p.small.empty()) return adamw_tables<G, COPY>(p.small, world, s, norms, steps, arrivals, st);
+    if (!p.medium.empty()) return adamw_tables<G, COPY>(p.medium, world, s, norms, steps, arrivals, st);
+    return adamw_tables<G, COPY>(p.large, world, s, norms, steps, arrivals, st);
 }
 
-cudaError_t launch_adamw(const AdamWItem* items, int64_t n, int world, int grad_dtype, bool copies, AdamWScalars s,
+cudaError_t launch_adamw(const AdamWPlan& p, int world, int grad_dtype, bool copies, const AdamWScalars& s,
                          const float* norms, int32_t* steps, int32_t* arrivals, cudaStream_t st) {
     if (grad_dtype == DDP_BF16)
-        return copies ? adamw_n<uint16_t, true>(items, n, world, s, norms, steps, arrivals, st)
-                      : adamw_n<uint16_t, false>(items, n, world, s, norms, steps, arrivals, st);
-    return copies ? adamw_n<float, true>(items, n, world, s, norms, steps, arrivals, st)
-                  : adamw_n<float, false>(items, n, world, s, norms, steps, arrivals, st);
+        return copies ? adamw<uint16_t, true>(p, world, s, norms, steps, arrivals, st)
+                      : adamw<uint16_t, false>(p, world, s, norms, steps, arrivals, st);
+    return copies ? adamw<float, true>(p, world, s, norms, steps, arrivals, st)
+                  : adamw<float, false>(p, world, s, norms, steps, arrivals, st);
 }
 
 }  // namespace ddpk

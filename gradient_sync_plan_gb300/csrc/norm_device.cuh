@@ -1,22 +1,30 @@
 // norm_device.cuh -- sums of squares, shared by the kernels that take a norm.
 //
-// A warp adds the squares of the values its lanes hold in binary32: at most a
-// few thousand terms, all positive, so the sum's relative error stays within a
-// few units of 2^-24 times the chain length, and far below that on average.
-// Everything beyond a warp is added in binary64.  A square leaves binary32's
-// range long before its value does (2^-75 squares to nothing, 2^64 to
-// infinity), so a warp whose sum falls outside [2^-90, 2^126] squares again in
-// binary64, from the registers that still hold the values.  Inside that range
-// what underflow took is below 2^-138 a warp, nothing next to 2^-90.
+// A block adds the squares of its tile in binary32: at most some ten thousand
+// terms, all positive and added as a tree over short chains, so the sum's
+// relative error stays within chain length + 8 units of 2^-24, and far below
+// that on average.  Everything beyond a tile is added in binary64.  A square
+// leaves binary32's range long before its value does (2^-75 squares to nothing,
+// 2^64 to infinity), so a tile with a warp whose sum falls outside
+// [2^-90, 2^112] squares again in binary64, from registers or memory that still
+// hold the values.  Inside that range what underflow took is below 2^-136 a
+// warp, nothing next to 2^-90, and 32 warps' sums stay finite.
 #pragma once
 
+#include <type_traits>
+
 #include "ddp_device.cuh"
+#include "optim_internal.h"
 
 namespace ddpk {
 
-// launch_dependent for a kernel whose blocks form clusters of C.
-template <int C, class... KArgs, class... Args>
-inline cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, cudaStream_t st, Args&&... args) {
+// launch_dependent for a kernel whose first parameter is a table the caller
+// keeps: its address goes to the launch, which copies it once.  C > 1: blocks
+// form clusters of C.
+template <int C = 1, class... KArgs, class... Args>
+inline cudaError_t launch_table(void (*kernel)(KArgs...), dim3 grid, dim3 block, cudaStream_t st, const Args&... args) {
+    static_assert(sizeof...(KArgs) == sizeof...(Args), "one argument a parameter");
+    static_assert((std::is_same<KArgs, Args>::value && ...), "arguments of the parameters' own types");
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
@@ -29,8 +37,9 @@ inline cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 bloc
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...);
+    cfg.numAttrs = C > 1 ? 2 : 1;
+    void* p[] = {const_cast<void*>(static_cast<const void*>(&args))...};
+    const cudaError_t e = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(kernel), p);
     const cudaError_t last = cudaGetLastError();
     return e != cudaSuccess ? e : last;
 }
@@ -54,42 +63,54 @@ __device__ __forceinline__ double warp_sum(double s) {
 
 // Whether a warp's sum of squares can be trusted in binary32 (so can a zero, if
 // every value is one).
-__device__ __forceinline__ bool in_square_range(float w) { return w >= 0x1p-90f && w <= 0x1p126f; }
+__device__ __forceinline__ bool in_square_range(float w) { return w >= 0x1p-90f && w <= 0x1p112f; }
 
-// The sum of squares of every value in the warp's U vectors a lane; all lanes
-// must call it, all get the sum.  Lanes without data pass zero vectors.
-template <class E, int U>
-__device__ __forceinline__ double warp_sum_squares(const typename E::V (&x)[U]) {
-    float s[4] = {0.f, 0.f, 0.f, 0.f};           // four chains: a quarter of the length, and they overlap
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int l = 0; l < E::L; ++l) {
-            const float f = f32_of(x[u], l);
-            s[l & 3] = fmaf(f, f, s[l & 3]);
-        }
-    const float w = warp_sum((s[0] + s[1]) + (s[2] + s[3]));
-    if (in_square_range(w)) return (double)w;
-    bool some = false;                           // zeros alone need no second pass
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int l = 0; l < E::L; ++l) some |= f32_of(x[u], l) != 0.f;
-    if (!__any_sync(0xffffffffu, some)) return 0.0;
-    double d = 0.0;
-#pragma unroll 1
-    for (int u = 0; u < U; ++u) {
-        typename E::V v = x[0];
-#pragma unroll
-        for (int k = 1; k < U; ++k)
-            if (k == u) v = x[k];
-#pragma unroll
-        for (int l = 0; l < E::L; ++l) {
-            const double f = (double)f32_of(v, l);
-            d = fma(f, f, d);
-        }
+// One value a warp -> their sum in every lane of warp 0 (undefined elsewhere).
+// `sh` has a slot a warp; the caller puts a barrier between two uses.
+template <class T>
+__device__ __forceinline__ T block_sum(T warp_total, T* sh) {
+    const int warps = blockDim.x >> 5;
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = warp_total;
+    __syncthreads();
+    T t = 0;
+    if (threadIdx.x < 32) t = warp_sum((int)threadIdx.x < warps ? sh[threadIdx.x] : T(0));
+    return t;
+}
+
+// Scratch of a block's sum of squares.
+struct SquareScratch {
+    float w[32];
+    double d[32];
+    int odd;                                     // some warp's sum is out of the safe range
+};
+__device__ __forceinline__ void init_squares(SquareScratch& sc) {
+    if (threadIdx.x == 0) sc.odd = 0;
+    __syncthreads();
+}
+
+// The block's sum of squares in warp 0's lanes, from each thread's own sum s in
+// binary32.  Where a warp's is out of range and not all of its values are
+// zeros (nonzero), every thread squares again: again() -> double.  Ends without
+// a barrier; the caller puts one before the next use.
+template <class Again>
+__device__ __forceinline__ double block_squares(float s, bool nonzero, SquareScratch& sc, Again again) {
+    const float w = warp_sum(s);
+    const bool odd = !in_square_range(w) && __any_sync(0xffffffffu, nonzero);
+    if ((threadIdx.x & 31) == 0) {
+        sc.w[threadIdx.x >> 5] = w;
+        if (odd) sc.odd = 1;
     }
-    return warp_sum(d);
+    __syncthreads();
+    if (!sc.odd) return threadIdx.x < 32 ? (double)warp_sum((int)threadIdx.x < (int)blockDim.x >> 5 ? sc.w[threadIdx.x] : 0.f) : 0.0;
+    const double t = block_sum(warp_sum(again()), sc.d);
+    if (threadIdx.x == 0) sc.odd = 0;
+    return t;
+}
+
+__device__ __forceinline__ float norm_of(double squares) {
+    // half a rounding more than from the binary64 root, which takes ten times as long
+    if (squares >= 0x1p-120 && squares <= 0x1p120) return __fsqrt_rn((float)squares);
+    return (float)sqrt(squares);
 }
 
 // The first of n ascending ends that lies past x (x is below the last end).
@@ -109,16 +130,57 @@ __device__ __forceinline__ int first_past(const int32_t* ends, int n, int x) {
     }
 }
 
-// One value a warp -> their sum in thread 0 (undefined elsewhere), added in
-// warp order.  `sh` has a slot a warp; the caller puts a barrier between two uses.
-__device__ __forceinline__ double block_sum(double warp_total, double* sh) {
-    const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    if ((threadIdx.x & 31) == 0) sh[warp] = warp_total;
+// first_past for a whole block: warp 0 looks, the others read what it found from
+// `slot` (a divergent load of the table keeps the constant cache busy for 32
+// accesses: one warp's is enough).  A barrier has to lie between two uses.
+__device__ __forceinline__ int block_first_past(const int32_t* ends, int n, int x, int* slot) {
+    if (n == 1) return 0;
+    if (threadIdx.x < 32) {
+        const int i = first_past(ends, n, x);
+        if (threadIdx.x == 0) *slot = i;
+    }
     __syncthreads();
-    double t = 0.0;
-    if (threadIdx.x == 0)
-        for (int w = 0; w < warps; ++w) t += sh[w];
-    return t;
+    return *slot;
+}
+
+// The end of a launch that has all the partials: the block that arrives last
+// adds each rank's in a fixed order and writes the norms.  atomicInc wraps the
+// counter back to zero for the next launch.  Every thread of the block calls
+// it, after its block's partials are written (by thread 0).
+template <int THREADS>
+__device__ __forceinline__ void finish_norms(const NormFinish& f, const double* partials, double* sh) {
+    __shared__ bool last;
+    if (!f.counter) return;
+    if (threadIdx.x == 0) {
+        __threadfence();
+        last = atomicInc(f.counter, gridDim.x - 1) == gridDim.x - 1;
+    }
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    int groups = 1;                              // ranks side by side, each by a whole number of warps
+    while (groups < f.ranks && groups < THREADS / 32) groups *= 2;
+    const int per = THREADS / groups, g = threadIdx.x / per, t = threadIdx.x % per;
+    for (int r0 = 0; r0 < f.ranks; r0 += groups) {
+        const int r = r0 + g;
+        const int end = r < f.ranks ? f.first[r + 1] : 0;
+        double d[4] = {0.0, 0.0, 0.0, 0.0};
+        int k = r < f.ranks ? f.first[r] + t : 0;
+        for (; k + 3 * per < end; k += 4 * per)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) d[u] += __ldcg(partials + k + u * per);
+        for (; k < end; k += per) d[0] += __ldcg(partials + k);
+        const double w = warp_sum((d[0] + d[1]) + (d[2] + d[3]));
+        if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = w;
+        __syncthreads();
+        if (t == 0 && r < f.ranks) {
+            double s = sh[threadIdx.x >> 5];
+            for (int q = 1; q < per / 32; ++q) s += sh[(threadIdx.x >> 5) + q];
+            const float norm = norm_of(s);
+            for (int q = 0; q < f.copies; ++q) f.norms[r * f.copies + q] = norm;
+        }
+        __syncthreads();
+    }
 }
 
 }  // namespace ddpk

@@ -23,10 +23,10 @@ using namespace ddpk;
 
 struct ddp_grad_set {
     int32_t world = 0, dtype = 0;
-    std::vector<GradRange> ranges;                             // by rank, then by address
-    std::vector<int32_t> rank_first;                           // first partial of each rank, and their end
+    std::shared_ptr<const RangePlan> plan;
     std::vector<std::pair<uintptr_t, uintptr_t>> spans;        // the memory of the tensors and the workspace, sorted
-    double* partials = nullptr;
+    NormSpace space{nullptr, nullptr};
+    bool cleared = false;                                      // the counter is known to be zero
 };
 
 struct ddp_sync_norm {
@@ -35,25 +35,22 @@ struct ddp_sync_norm {
     std::vector<void*> grads, buckets;
     std::vector<int64_t> numel, offset, bucket_numel;
     std::vector<int32_t> bucket_of;
-    // the view algorithms' members, those that continue one another joined
-    std::vector<SyncMember> members;
-    std::vector<void*> ptrs;
-    int32_t member_tiles = 0;
-    int vecs = 0;
+    std::shared_ptr<const SyncPlan> sync;                      // the view algorithms' tables
     // rank 0's gradients, for a norm pass after a sync without one
-    std::vector<GradRange> ranges;
-    int32_t range_tiles = 0;
+    std::shared_ptr<const RangePlan> plan;
     std::vector<std::pair<uintptr_t, uintptr_t>> spans;        // the gradients, buckets and the workspace, sorted
-    double* partials = nullptr;
+    NormSpace space{nullptr, nullptr};
+    bool cleared = false;                                      // the counter is known to be zero
 };
 
 struct ddp_adamw {
     int32_t world = 0, grad_dtype = 0;
     bool copies = false;
-    std::vector<AdamWItem> items;
+    std::shared_ptr<const AdamWPlan> plan;
     std::vector<std::pair<uintptr_t, uintptr_t>> spans;        // what a step writes, sorted
     int32_t* steps = nullptr;
     int32_t* arrivals = nullptr;
+    bool cleared = false;                                      // arrivals is known to be zero
 };
 
 namespace {
@@ -103,7 +100,8 @@ void add_range(std::vector<GradRange>* v, void* p, int64_t bytes, int32_t r) {
     else v->push_back(GradRange{c, bytes, r});
 }
 
-// The most tiles that tensors of these sizes can take, wherever they lie.
+// The most tiles that tensors of these sizes can take, wherever they lie; their
+// partials are fewer, but for the padding of a rank's or a table's last run.
 int64_t most_tiles(int32_t n_params, const int64_t* numel, int64_t es) {
     int64_t t = 0;
     for (int32_t i = 0; i < n_params; ++i)
@@ -118,6 +116,22 @@ int sync_vecs(int32_t world, int32_t n_params, const int64_t* numel, int32_t dty
     return sync_norm_vecs(world, n, dtype);
 }
 
+NormSpace space_of(void* workspace) {
+    char* w = static_cast<char*>(workspace);
+    return NormSpace{reinterpret_cast<uint32_t*>(w), reinterpret_cast<double*>(w + kNormSpaceHead)};
+}
+
+// Zeroes a handle's counter before the first launch that uses it.  A capture
+// records the clearing for its replays, and proves nothing for later calls.
+cudaError_t clear_word(void* word, bool* cleared, cudaStream_t stream) {
+    if (*cleared) return cudaSuccess;
+    cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
+    cudaError_t e = cudaStreamIsCapturing(stream, &capturing);
+    if (e == cudaSuccess) e = cudaMemsetAsync(word, 0, 4, stream);
+    if (e == cudaSuccess && capturing == cudaStreamCaptureStatusNone) *cleared = true;
+    return e;
+}
+
 bool bad_max_norm(double max_norm) { return !(max_norm > 0.0) || !((float)max_norm > 0.f); }
 
 }  // namespace
@@ -130,7 +144,7 @@ int32_t ddp_grad_set_workspace_bytes(int32_t world, int32_t n_params, const int6
     if (!bytes) return DDP_ERR_INVALID;
     const int32_t st = check_sizes(world, n_params, numel, dtype);
     if (st) return st;
-    *bytes = 8 * std::max<int64_t>(1, world * most_tiles(n_params, numel, elem_bytes(dtype)));
+    *bytes = kNormSpaceHead + 8 * world * most_tiles(n_params, numel, elem_bytes(dtype));
     return DDP_OK;
 } DDP_ABI_CATCH
 
@@ -145,14 +159,14 @@ int32_t ddp_grad_set_create(int32_t world, int32_t n_params, void* const* grads,
     if (n_params > 0 && !grads) return DDP_ERR_INVALID;
     if ((st = check_ptr(workspace, 8))) return st;
     if (workspace_bytes < need) return DDP_ERR_CAPACITY;
-    if (need / 8 > INT32_MAX) return DDP_ERR_CAPACITY;
+    if (need / 8 > INT32_MAX / 8) return DDP_ERR_CAPACITY;
     const int64_t es = elem_bytes(dtype);
     std::unique_ptr<ddp_grad_set> s(new ddp_grad_set());
     s->world = world;
     s->dtype = dtype;
-    s->partials = static_cast<double*>(workspace);
+    s->space = space_of(workspace);
     s->spans.push_back(span_of(workspace, need));
-    int64_t tiles = 0;
+    std::vector<GradRange> ranges;               // by rank, then by address
     std::vector<Span> rank;
     for (int32_t r = 0; r < world; ++r) {
         rank.clear();
@@ -164,13 +178,10 @@ int32_t ddp_grad_set_create(int32_t world, int32_t n_params, void* const* grads,
         }
         std::sort(rank.begin(), rank.end());
         s->spans.insert(s->spans.end(), rank.begin(), rank.end());
-        s->rank_first.push_back((int32_t)tiles);
-        const size_t from = s->ranges.size();
         for (const Span& g : rank)
-            add_range(&s->ranges, reinterpret_cast<void*>(g.first), (int64_t)(g.second - g.first), r);
-        for (size_t k = from; k < s->ranges.size(); ++k) tiles += range_tiles(s->ranges[k].ptr, s->ranges[k].bytes);
+            add_range(&ranges, reinterpret_cast<void*>(g.first), (int64_t)(g.second - g.first), r);
     }
-    s->rank_first.push_back((int32_t)tiles);
+    s->plan = make_range_plan(ranges.data(), (int64_t)ranges.size(), world);
     if (any_overlap(&s->spans)) return DDP_ERR_INVALID;
     *out = s.release();
     return DDP_OK;
@@ -183,9 +194,8 @@ int32_t ddp_grad_norm(ddp_grad_set* s, float* norms, void* stream) try {
     if (st) return st;
     if (hits_any(s->spans, span_of(norms, 4 * (int64_t)s->world))) return DDP_ERR_INVALID;
     cudaStream_t q = (cudaStream_t)stream;
-    st = cuda_status(launch_norm_partials(s->ranges.data(), (int64_t)s->ranges.size(), s->dtype, s->partials, q));
-    if (st) return st;
-    return cuda_status(launch_norm_final(s->partials, s->rank_first.data(), s->world, 1, norms, q));
+    if ((st = cuda_status(clear_word(s->space.counter, &s->cleared, q)))) return st;
+    return cuda_status(launch_norm(*s->plan, s->dtype, s->space, 1, norms, q));
 } DDP_ABI_CATCH
 
 int32_t ddp_grad_clip(ddp_grad_set* s, const float* norms, double max_norm, void* stream) try {
@@ -194,8 +204,7 @@ int32_t ddp_grad_clip(ddp_grad_set* s, const float* norms, double max_norm, void
     const int32_t st = check_ptr(norms, 4);
     if (st) return st;
     if (hits_any(s->spans, span_of(norms, 4 * (int64_t)s->world))) return DDP_ERR_INVALID;
-    return cuda_status(launch_clip(s->ranges.data(), (int64_t)s->ranges.size(), s->dtype, norms, (float)max_norm,
-                                   (cudaStream_t)stream));
+    return cuda_status(launch_clip(*s->plan, s->dtype, norms, (float)max_norm, (cudaStream_t)stream));
 } DDP_ABI_CATCH
 
 int32_t ddp_grad_norm_clip(ddp_grad_set* s, float* norms, double max_norm, void* stream) try {
@@ -221,7 +230,7 @@ int32_t ddp_sync_norm_workspace_bytes(int32_t world, int32_t n_params, const int
     int64_t tiles = 0;
     for (int32_t i = 0; i < n_params; ++i)
         if (numel[i] > 0) tiles += numel[i] / tile + 2;
-    *bytes = 8 * std::max<int64_t>({1, tiles, most_tiles(n_params, numel, elem_bytes(dtype))});
+    *bytes = kNormSpaceHead + 8 * std::max(tiles, most_tiles(n_params, numel, elem_bytes(dtype)));
     return DDP_OK;
 } DDP_ABI_CATCH
 
@@ -243,7 +252,7 @@ int32_t ddp_sync_norm_create(int32_t world, int32_t n_params, void* const* grads
     if (n_params > 0 && (!grads || !bucket_of_param || !offset_of_param)) return DDP_ERR_INVALID;
     if (n_buckets > 0 && (!bucket_numel || (needs_buckets && !buckets))) return DDP_ERR_INVALID;
     if ((st = check_ptr(workspace, 8))) return st;
-    if (workspace_bytes < need || need / 8 > INT32_MAX) return DDP_ERR_CAPACITY;
+    if (workspace_bytes < need || need / 8 > INT32_MAX / 8) return DDP_ERR_CAPACITY;
     for (int32_t k = 0; k < n_buckets; ++k)
         if ((st = common_checks(world, bucket_numel[k], dtype))) return st;
     std::unique_ptr<ddp_sync_norm> s(new ddp_sync_norm());
@@ -253,7 +262,7 @@ int32_t ddp_sync_norm_create(int32_t world, int32_t n_params, void* const* grads
     s->dtype = dtype;
     s->divisor = divisor;
     s->algo = algo;
-    s->partials = static_cast<double*>(workspace);
+    s->space = space_of(workspace);
     const int64_t all = (int64_t)world * n_params, es = elem_bytes(dtype);
     if (n_params > 0) {
         s->grads.assign(grads, grads + all);
@@ -299,11 +308,13 @@ int32_t ddp_sync_norm_create(int32_t world, int32_t n_params, void* const* grads
         }
     }
     // a member that continues the one before it, in its bucket and at every rank, joins it
-    s->ptrs.reserve(order.size() * (size_t)world);
+    std::vector<SyncMember> members;
+    std::vector<void*> ptrs;
+    ptrs.reserve(order.size() * (size_t)world);
     int32_t bucket = -1;
     for (int32_t p : order) {
         const int32_t k = bucket_of_param[p];
-        SyncMember* m = bucket == k ? &s->members.back() : nullptr;
+        SyncMember* m = bucket == k ? &members.back() : nullptr;
         bool joins = m && m->offset + m->numel == offset_of_param[p];
         for (int32_t r = 0; joins && r < world; ++r)
             joins = static_cast<char*>(m->ptrs[r]) + m->numel * es == grads[(int64_t)r * n_params + p];
@@ -312,16 +323,21 @@ int32_t ddp_sync_norm_create(int32_t world, int32_t n_params, void* const* grads
             m->numel += numel[p];
             continue;
         }
-        void* const* at = s->ptrs.data() + s->ptrs.size();
-        for (int32_t r = 0; r < world; ++r) s->ptrs.push_back(grads[(int64_t)r * n_params + p]);
-        s->members.push_back(SyncMember{numel[p], offset_of_param[p], chunk_len(bucket_numel[k], world), at});
+        void* const* at = ptrs.data() + ptrs.size();
+        for (int32_t r = 0; r < world; ++r) ptrs.push_back(grads[(int64_t)r * n_params + p]);
+        members.push_back(SyncMember{numel[p], offset_of_param[p], chunk_len(bucket_numel[k], world), at});
     }
-    s->vecs = sync_vecs(world, n_params, numel, dtype);
-    for (const SyncMember& m : s->members) s->member_tiles += (int32_t)sync_norm_tiles(world, m, s->vecs, dtype);
+    const int launch_dtype = algo == DDP_ALGO_BF16_HOOK_VIEW   ? kDtypeHook
+                             : algo == DDP_ALGO_FP16_HOOK_VIEW ? kDtypeHook16
+                                                               : dtype;
+    if (!needs_buckets)
+        s->sync = make_sync_plan(world, members.data(), (int64_t)members.size(), sync_vecs(world, n_params, numel, dtype),
+                                 launch_dtype, make_div(divisor));
     // every rank holds the same average after the sync: rank 0's norm is everybody's
+    std::vector<GradRange> ranges;
     for (int32_t p = 0; p < n_params; ++p)
-        if (numel[p] > 0) add_range(&s->ranges, grads[p], numel[p] * es, 0);
-    for (const GradRange& g : s->ranges) s->range_tiles += (int32_t)range_tiles(g.ptr, g.bytes);
+        if (numel[p] > 0) add_range(&ranges, grads[p], numel[p] * es, 0);
+    s->plan = make_range_plan(ranges.data(), (int64_t)ranges.size(), 1);
     *out = s.release();
     return DDP_OK;
 } DDP_ABI_CATCH
@@ -333,28 +349,17 @@ int32_t ddp_sync_norm_run(ddp_sync_norm* s, float* norms, void* stream) try {
     if (st) return st;
     if (hits_any(s->spans, span_of(norms, 4 * (int64_t)s->world))) return DDP_ERR_INVALID;
     cudaStream_t q = (cudaStream_t)stream;
-    const bool view = s->algo == DDP_ALGO_VIEW || s->algo == DDP_ALGO_BF16_HOOK_VIEW || s->algo == DDP_ALGO_FP16_HOOK_VIEW;
-    int32_t first[2] = {0, 0};
+    if ((st = cuda_status(clear_word(s->space.counter, &s->cleared, q)))) return st;
     // the kernel with the norm is a register kernel: where the TMA-staged view
     // kernel is asked for, or the CTA budget is one that it needs, the sync
     // runs as ddp_sync_buckets runs it and the norm takes a pass over rank 0
-    if (view && fused_kernel_override() != DDP_FUSED_TMA && !cta_cap_is_tight()) {
-        const int dtype = s->algo == DDP_ALGO_BF16_HOOK_VIEW   ? kDtypeHook
-                          : s->algo == DDP_ALGO_FP16_HOOK_VIEW ? kDtypeHook16
-                                                               : s->dtype;
-        first[1] = s->member_tiles;
-        st = cuda_status(launch_sync_norm(s->world, s->members.data(), (int64_t)s->members.size(), s->vecs, dtype,
-                                          make_div(s->divisor), s->partials, q));
-    } else {
-        st = ddp_sync_buckets(s->world, s->n_params, s->grads.data(), s->numel.data(), s->bucket_of.data(),
-                              s->offset.data(), s->n_buckets, s->bucket_numel.data(),
-                              s->buckets.empty() ? nullptr : s->buckets.data(), s->dtype, s->divisor, s->algo, stream);
-        if (st) return st;
-        first[1] = s->range_tiles;
-        st = cuda_status(launch_norm_partials(s->ranges.data(), (int64_t)s->ranges.size(), s->dtype, s->partials, q));
-    }
+    if (s->sync && fused_kernel_override() != DDP_FUSED_TMA && !cta_cap_is_tight())
+        return cuda_status(launch_sync_norm(*s->sync, s->space, norms, q));
+    st = ddp_sync_buckets(s->world, s->n_params, s->grads.data(), s->numel.data(), s->bucket_of.data(), s->offset.data(),
+                          s->n_buckets, s->bucket_numel.data(), s->buckets.empty() ? nullptr : s->buckets.data(), s->dtype,
+                          s->divisor, s->algo, stream);
     if (st) return st;
-    return cuda_status(launch_norm_final(s->partials, first, 1, s->world, norms, q));
+    return cuda_status(launch_norm(*s->plan, s->dtype, s->space, s->world, norms, q));
 } DDP_ABI_CATCH
 
 int32_t ddp_sync_norm_destroy(ddp_sync_norm* s) try {
@@ -365,7 +370,7 @@ int32_t ddp_sync_norm_destroy(ddp_sync_norm* s) try {
 
 int32_t ddp_adamw_create(int32_t world, int32_t n_params, void* const* params, const void* const* grads,
                          int32_t grad_dtype, void* const* exp_avg, void* const* exp_avg_sq, void* const* copies,
-                         const int64_t* numel, const uint8_t* no_decay, int32_t* steps, void* workspace, void* stream,
+                         const int64_t* numel, const uint8_t* no_decay, int32_t* steps, void* workspace,
                          ddp_adamw** out) try {
     DDP_TRACE_CALL();
     if (!out) return DDP_ERR_INVALID;
@@ -384,6 +389,7 @@ int32_t ddp_adamw_create(int32_t world, int32_t n_params, void* const* params, c
     a->spans.push_back(span_of(workspace, DDP_ADAMW_WORKSPACE_BYTES));
     std::vector<Span> read;
     const int64_t gs = elem_bytes(grad_dtype);
+    std::vector<AdamWItem> items;
     int64_t tiles = 0;
     for (int32_t r = 0; r < world; ++r)
         for (int32_t i = 0; i < n_params; ++i) {
@@ -405,20 +411,20 @@ int32_t ddp_adamw_create(int32_t world, int32_t n_params, void* const* params, c
             if (copies) a->spans.push_back(span_of(it.copy, 2 * it.numel));
             read.push_back(span_of(it.g, gs * it.numel));
             // a tensor that continues the one before it in every array joins it
-            AdamWItem* b = a->items.empty() ? nullptr : &a->items.back();
+            AdamWItem* b = items.empty() ? nullptr : &items.back();
             if (b && b->rank == r && b->decay == it.decay && b->p + b->numel == it.p && b->m + b->numel == it.m &&
                 b->v + b->numel == it.v && static_cast<const char*>(b->g) + gs * b->numel == it.g &&
                 (!copies || static_cast<char*>(b->copy) + 2 * b->numel == it.copy))
                 b->numel += it.numel;
             else
-                a->items.push_back(it);
+                items.push_back(it);
         }
-    for (const AdamWItem& it : a->items) tiles += adamw_tiles(it, grad_dtype);
-    if (tiles > INT32_MAX) return DDP_ERR_CAPACITY;
+    for (const AdamWItem& it : items) tiles += adamw_tiles(it);
+    if (tiles > INT32_MAX / 8) return DDP_ERR_CAPACITY;
     if (any_overlap(&a->spans)) return DDP_ERR_INVALID;
     for (const Span& g : read)
         if (hits_any(a->spans, g)) return DDP_ERR_INVALID;
-    if ((st = cuda_status(cudaMemsetAsync(workspace, 0, DDP_ADAMW_WORKSPACE_BYTES, (cudaStream_t)stream)))) return st;
+    a->plan = make_adamw_plan(items.data(), (int64_t)items.size(), grad_dtype, a->copies);
     *out = a.release();
     return DDP_OK;
 } DDP_ABI_CATCH
@@ -436,6 +442,8 @@ int32_t ddp_adamw_step(ddp_adamw* a, double lr, double beta1, double beta2, doub
         if (st) return st;
         if (hits_any(a->spans, span_of(norms, 4 * (int64_t)a->world))) return DDP_ERR_INVALID;
     }
+    const int32_t st = cuda_status(clear_word(a->arrivals, &a->cleared, (cudaStream_t)stream));
+    if (st) return st;
     const AdamWScalars s{(float)lr,
                          (float)beta1,
                          (float)(1.0 - beta1),
@@ -446,8 +454,8 @@ int32_t ddp_adamw_step(ddp_adamw* a, double lr, double beta1, double beta2, doub
                          (float)eps,
                          (float)(lr * weight_decay),
                          (float)max_norm};
-    return cuda_status(launch_adamw(a->items.data(), (int64_t)a->items.size(), a->world, a->grad_dtype, a->copies, s,
-                                    norms, a->steps, a->arrivals, (cudaStream_t)stream));
+    return cuda_status(launch_adamw(*a->plan, a->world, a->grad_dtype, a->copies, s, norms, a->steps, a->arrivals,
+                                    (cudaStream_t)stream));
 } DDP_ABI_CATCH
 
 int32_t ddp_adamw_destroy(ddp_adamw* a) try {

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <memory>
 #include <vector>
 
 #include "ddp_internal.h"
@@ -20,22 +21,46 @@ struct GradRange {
     int32_t rank;
 };
 
-// Bytes that one block of the norm and clip kernels takes.  Tiles start at
-// 128-byte boundaries of memory, so a range has at most one more than
-// bytes / kNormTile rounded up.
+// Bytes of a tile of the norm and clip kernels.  Tiles start at 128-byte
+// boundaries of memory, so a range has at most one more than bytes / kNormTile
+// rounded up.  A norm block takes up to kNormRun of them, as many as make
+// kNormBlocks blocks (eight on each of 152 SMs).
 constexpr int64_t kNormTile = 16384;
 constexpr int64_t kNormAlign = 128;
-int64_t range_tiles(const void* ptr, int64_t bytes);
+constexpr int64_t kNormRun = 4;
+constexpr int64_t kNormBlocks = 8 * 152;
 
-// Partial sums of squares (one double a tile, in the order of the ranges,
-// which are sorted by rank), then norms[r] = sqrt(sum of rank r's partials).
-// rank_first[r] .. rank_first[r + 1] are rank r's partials.
-cudaError_t launch_norm_partials(const GradRange* ranges, int64_t n, int dtype, double* partials, cudaStream_t stream);
-// Each of `ranks` norms is written `copies` times, norms[r * copies ..].
+// The kernels' tables, filled once for ranges sorted by rank.
+struct RangePlan;
+std::shared_ptr<const RangePlan> make_range_plan(const GradRange* ranges, int64_t n, int ranks);
+int64_t range_plan_partials(const RangePlan& plan);
+
+// How a launch of partials ends: where there are few, its last block adds them
+// itself (counter: a word that is zero between launches); NULL: it does not.
+constexpr int kFinishRanks = 16;
+constexpr int32_t kFinishPartials = 1280;
+struct NormFinish {
+    uint32_t* counter;
+    float* norms;
+    int32_t ranks, copies;                     // norms[r * copies ..] receive rank r's
+    int32_t first[kFinishRanks + 1];           // rank r's partials are first[r] .. first[r + 1]
+};
+
+// Where a norm's launches put things: the workspace's counter, which the first
+// launch finds zero, and its partials.
+struct NormSpace {
+    uint32_t* counter;
+    double* partials;
+};
+constexpr int64_t kNormSpaceHead = 16;         // bytes before the partials
+
+// norms[r * copies ..] = sqrt(sum of squares of rank r's ranges).
+cudaError_t launch_norm(const RangePlan& plan, int dtype, NormSpace ws, int copies, float* norms, cudaStream_t stream);
+cudaError_t launch_clip(const RangePlan& plan, int dtype, const float* norms, float max_norm, cudaStream_t stream);
+NormFinish norm_finish(NormSpace ws, const int32_t* rank_first, int ranks, int copies, float* norms, bool one_launch);
+// Partials that a launch left, into norms.
 cudaError_t launch_norm_final(const double* partials, const int32_t* rank_first, int ranks, int copies, float* norms,
                               cudaStream_t stream);
-cudaError_t launch_clip(const GradRange* ranges, int64_t n, int dtype, const float* norms, float max_norm,
-                        cudaStream_t stream);
 
 // ---- view sync with the norm in its epilogue (sync_norm.cu) ----------------
 // One bucket member: its elements, its place in its bucket, its bucket's chunk
@@ -44,13 +69,14 @@ struct SyncMember {
     int64_t numel, offset, clen;
     void* const* ptrs;
 };
-// Vectors a thread takes of a tile when a rank's members have numel elements,
-// and the tiles (one partial each) of one member.
+// Vectors a thread takes of a tile when a rank's members have numel elements.
 int sync_norm_vecs(int world, int64_t numel, int dtype);
-int64_t sync_norm_tiles(int world, const SyncMember& m, int vecs, int dtype);
-// dtype: a ddp_dtype or one of the hooks' (kDtypeHook, kDtypeHook16).
-cudaError_t launch_sync_norm(int world, const SyncMember* members, int64_t n, int vecs, int dtype, DivSpec div,
-                             double* partials, cudaStream_t stream);
+// The kernel's tables, filled once.  dtype: a ddp_dtype or one of the hooks'
+// (kDtypeHook, kDtypeHook16).
+struct SyncPlan;
+std::shared_ptr<const SyncPlan> make_sync_plan(int world, const SyncMember* members, int64_t n, int vecs, int dtype,
+                                               DivSpec div);
+cudaError_t launch_sync_norm(const SyncPlan& plan, NormSpace ws, float* norms, cudaStream_t stream);
 
 // ---- AdamW (adamw.cu) ------------------------------------------------------
 // One tensor of one rank.  g is float32 or bf16 (the call's grad dtype), copy
@@ -68,10 +94,13 @@ struct AdamWItem {
 struct AdamWScalars {
     float lr, beta1, one_minus_beta1, ln_beta1, beta2, one_minus_beta2, ln_beta2, eps, lr_decay, max_norm;
 };
-int64_t adamw_tiles(const AdamWItem& it, int grad_dtype);
+int64_t adamw_tiles(const AdamWItem& it);
+// The kernel's tables, filled once.
+struct AdamWPlan;
+std::shared_ptr<const AdamWPlan> make_adamw_plan(const AdamWItem* items, int64_t n, int grad_dtype, bool copies);
 // norms may be null (no clipping).  steps[world] is read, and advanced for the
 // ranks that were updated; arrivals is one word, zero between calls.
-cudaError_t launch_adamw(const AdamWItem* items, int64_t n, int world, int grad_dtype, bool copies, AdamWScalars s,
+cudaError_t launch_adamw(const AdamWPlan& plan, int world, int grad_dtype, bool copies, const AdamWScalars& s,
                          const float* norms, int32_t* steps, int32_t* arrivals, cudaStream_t stream);
 
 }  // namespace ddpk

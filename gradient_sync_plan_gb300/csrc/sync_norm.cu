@@ -41,6 +41,7 @@ struct SyncTab {
     char* ptr[PTRS];             // ptr[m * world + r]
 };
 using SyncSmall = SyncTab<32, 256>;
+using SyncMedium = SyncTab<176, 704>;
 using SyncLarge = SyncTab<336, 2624>;
 static_assert(sizeof(SyncLarge) + 16 <= kMaxParamBytes, "sync table exceeds the kernel parameter limit");
 
@@ -91,21 +92,20 @@ __device__ __forceinline__ uint32_t magnitude_bits(uint4 y) { return (y.x | y.y 
 // E: element type; G: ranks whose loads are in flight together; B: vectors a
 // thread folds side by side; MINB: blocks an SM has room for.
 template <class E, int G, int B, int MINB, class TAB>
-__global__ void __launch_bounds__(kThreads, MINB) k_sync_norm(const __grid_constant__ TAB b, double* partials) {
+__global__ void __launch_bounds__(kThreads, MINB) k_sync_norm(const __grid_constant__ TAB b, double* partials,
+                                                              const __grid_constant__ NormFinish finish) {
     using V = typename E::V;
     using S = typename E::S;
     constexpr int L = E::L;
     constexpr int kRow = kThreads * L;           // elements the block takes with one vector a thread
-    __shared__ float sh[kThreads / 32];
-    __shared__ double sh64[kThreads / 32];
-    __shared__ int odd;                          // a warp's sum is out of binary32's safe range
-    if (threadIdx.x == 0) odd = 0;
-    __syncthreads();
+    __shared__ SquareScratch scratch;
+    __shared__ int slot;
+    init_squares(scratch);
     pdl_release();
     pdl_acquire();
     const int world = b.world;
     for (int tile = blockIdx.x; tile < b.tiles; tile += gridDim.x) {
-        const int i = first_past(b.tile_end, b.n, tile);
+        const int i = block_first_past(b.tile_end, b.n, tile, &slot);
         // pieces: vectors at 16-byte boundaries, or elements where the ranks'
         // pointers do not line up; positions count from e0, [head, tail) are the member's
         const int tile_len = kRow * b.vecs;
@@ -164,29 +164,17 @@ __global__ void __launch_bounds__(kThreads, MINB) k_sync_norm(const __grid_const
                 bits |= magnitude_bits(y);
             }
         }
-        const float w = warp_sum(s);
-        const bool again = !in_square_range(w) && __any_sync(0xffffffffu, bits != 0);     // zeros are exact
-        if ((threadIdx.x & 31) == 0) {
-            sh[threadIdx.x >> 5] = w;
-            if (again) odd = 1;
-        }
-        __syncthreads();
-        if (odd) {
-            // squared again in binary64, from what the block wrote to rank 0
+        const double t = block_squares(s, bits != 0, scratch, [&] {          // from what the block wrote to rank 0
             const S* mine = reinterpret_cast<const S*>(pp[0]) + e0;
             double d = 0.0;
 #pragma unroll 1
             for (int e = head + (int)threadIdx.x; e < tail; e += kThreads) d += square(mine[e]);
-            const double t = block_sum(warp_sum(d), sh64);
-            if (threadIdx.x == 0) partials[tile] = t, odd = 0;
-        } else if (threadIdx.x < kThreads / 32) {
-            float t = sh[threadIdx.x];
-#pragma unroll
-            for (int d = kThreads / 64; d; d >>= 1) t += __shfl_xor_sync((1u << (kThreads / 32)) - 1, t, d);
-            if (threadIdx.x == 0) partials[tile] = (double)t;
-        }
-        __syncthreads();                         // sh is free for the next tile
+            return d;
+        });
+        if (threadIdx.x == 0) partials[tile] = t;
+        __syncthreads();                         // scratch and slot are free for the next tile
     }
+    finish_norms<kThreads>(finish, partials, scratch.d);
 }
 
 // Vectors a thread takes of a tile: more of them share a block's fixed costs
@@ -209,23 +197,34 @@ static int lead_of(int world, const SyncMember& m, int64_t es) {
     return (int)((int64_t)q / es);
 }
 
-template <class E, int G, int B, int MINB, class TAB>
-static cudaError_t sync_tables(int world, const SyncMember* members, int64_t n, int vecs, DivSpec div, double* partials,
-                               cudaStream_t st) {
-    const int64_t tile = (int64_t)kThreads * vecs * E::L;
+// Launches to make, each with its table: of the smallest capacity that takes
+// them all, since a launch's parameters are copied for every eager launch.
+struct SyncPlan {
+    int world = 0, dtype = 0;
+    int32_t tiles = 0;
+    std::vector<SyncSmall> small;
+    std::vector<SyncMedium> medium;
+    std::vector<SyncLarge> large;
+};
+
+template <class TAB>
+static void fill_tables(SyncPlan* plan, const SyncMember* members, int64_t n, int vecs, DivSpec div,
+                        std::vector<TAB>* out) {
+    const int world = plan->world;
+    const int64_t es = elem_bytes(plan->dtype), tile = (int64_t)kThreads * vecs * (16 / es);
     const int most = std::min(TAB::kMembers, TAB::kPtrs / world);
-    TAB b;
-    b.world = world;
-    b.vecs = vecs;
-    b.div_mode = div.mode;
-    b.div_operand = div.operand;
-    int64_t i = 0;
-    while (i < n) {
+    for (int64_t i = 0; i < n;) {
+        out->emplace_back();
+        TAB& b = out->back();
+        b.world = world;
+        b.vecs = vecs;
+        b.div_mode = div.mode;
+        b.div_operand = div.operand;
         b.n = 0;
         b.tiles = 0;
         for (; i < n && b.n < most; ++i, ++b.n) {
             const SyncMember& m = members[i];
-            const int lead = lead_of(world, m, (int64_t)sizeof(typename E::S));
+            const int lead = lead_of(world, m, es);
             b.tiles += (int32_t)((std::max(lead, 0) + m.numel + tile - 1) / tile);
             b.numel[b.n] = m.numel;
             b.offset[b.n] = m.offset;
@@ -235,8 +234,30 @@ static cudaError_t sync_tables(int world, const SyncMember* members, int64_t n, 
             b.lead[b.n] = (int8_t)lead;
             for (int r = 0; r < world; ++r) b.ptr[(size_t)b.n * world + r] = static_cast<char*>(m.ptrs[r]);
         }
-        const cudaError_t e = launch_dependent(k_sync_norm<E, G, B, MINB, TAB>, dim3(cap_ctas(b.tiles)), dim3(kThreads), 0, st,
-                                               b, partials);
+        plan->tiles += b.tiles;
+    }
+}
+
+template <class TAB>
+static bool fits(int world, int64_t n) { return n <= std::min(TAB::kMembers, TAB::kPtrs / world); }
+
+std::shared_ptr<const SyncPlan> make_sync_plan(int world, const SyncMember* members, int64_t n, int vecs, int dtype,
+                                               DivSpec div) {
+    auto plan = std::make_shared<SyncPlan>();
+    plan->world = world;
+    plan->dtype = dtype;
+    if (fits<SyncSmall>(world, n)) fill_tables(plan.get(), members, n, vecs, div, &plan->small);
+    else if (fits<SyncMedium>(world, n)) fill_tables(plan.get(), members, n, vecs, div, &plan->medium);
+    else fill_tables(plan.get(), members, n, vecs, div, &plan->large);
+    return plan;
+}
+
+template <class E, int G, int B, int MINB, class TAB>
+static cudaError_t sync_tables(const std::vector<TAB>& tables, double* partials, const NormFinish& finish,
+                               cudaStream_t st) {
+    for (const TAB& b : tables) {
+        const cudaError_t e = launch_table(k_sync_norm<E, G, B, MINB, TAB>, dim3(cap_ctas(b.tiles)), dim3(kThreads), st, b,
+                                           partials, finish);
         if (e != cudaSuccess) return e;
         partials += b.tiles;
     }
@@ -244,34 +265,38 @@ static cudaError_t sync_tables(int world, const SyncMember* members, int64_t n, 
 }
 
 template <class E, class TAB>
-static cudaError_t sync_world(int world, const SyncMember* m, int64_t n, int vecs, DivSpec div, double* partials,
+static cudaError_t sync_world(int world, const std::vector<TAB>& tables, double* partials, const NormFinish& finish,
                               cudaStream_t st) {
     // 6.9 TB/s each on the 355M decoder; without side-by-side vectors 6.2 on 2
     // ranks, with four blocks of 8 ranks' loads 6.7 on 8
-    if (world <= 2) return sync_tables<E, 2, 2, 4, TAB>(world, m, n, vecs, div, partials, st);
-    if (world <= 4) return sync_tables<E, 4, 1, 4, TAB>(world, m, n, vecs, div, partials, st);
-    return sync_tables<E, 4, 1, 5, TAB>(world, m, n, vecs, div, partials, st);
+    if (world <= 2) return sync_tables<E, 2, 2, 4>(tables, partials, finish, st);
+    if (world <= 4) return sync_tables<E, 4, 1, 4>(tables, partials, finish, st);
+    return sync_tables<E, 4, 1, 5>(tables, partials, finish, st);
 }
 
 template <class E>
-static cudaError_t sync_size(int world, const SyncMember* m, int64_t n, int vecs, DivSpec div, double* partials,
-                             cudaStream_t st) {
-    if (n <= SyncSmall::kMembers && n * world <= SyncSmall::kPtrs)
-        return sync_world<E, SyncSmall>(world, m, n, vecs, div, partials, st);
-    return sync_world<E, SyncLarge>(world, m, n, vecs, div, partials, st);
+static cudaError_t sync_size(const SyncPlan& p, double* partials, const NormFinish& f, cudaStream_t st) {
+    if (!p.small.empty()) return sync_world<E>(p.world, p.small, partials, f, st);
+    if (!p.medium.empty()) return sync_world<E>(p.world, p.medium, partials, f, st);
+    return sync_world<E>(p.world, p.large, partials, f, st);
 }
 
-cudaError_t launch_sync_norm(int world, const SyncMember* members, int64_t n, int vecs, int dtype, DivSpec div,
-                             double* partials, cudaStream_t st) {
-    if (dtype == DDP_F32) return sync_size<EF32>(world, members, n, vecs, div, partials, st);
-    if (dtype == kDtypeHook) return sync_size<EHOOK>(world, members, n, vecs, div, partials, st);
-    if (dtype == kDtypeHook16) return sync_size<EHOOK16>(world, members, n, vecs, div, partials, st);
-    return sync_size<EBF16>(world, members, n, vecs, div, partials, st);
-}
+// Tiles up to which a launch adds its partials itself: a block that arrives
+// waits for its stores first, which costs more than a second launch where there
+// are waves of blocks (3M elements on 3 ranks, 3100 tiles: 29 against 26 us).
+constexpr int32_t kSyncFinishTiles = 608;
 
-int64_t sync_norm_tiles(int world, const SyncMember& m, int vecs, int dtype) {
-    const int64_t t = (int64_t)kThreads * vecs * (16 / elem_bytes(dtype));
-    return (std::max(lead_of(world, m, elem_bytes(dtype)), 0) + m.numel + t - 1) / t;
+cudaError_t launch_sync_norm(const SyncPlan& p, NormSpace ws, float* norms, cudaStream_t st) {
+    const int32_t first[2] = {0, p.tiles};
+    const size_t launches = p.small.size() + p.medium.size() + p.large.size();
+    const NormFinish f = norm_finish(ws, first, 1, p.world, norms, launches == 1 && p.tiles <= kSyncFinishTiles);
+    cudaError_t e;
+    if (p.dtype == DDP_F32) e = sync_size<EF32>(p, ws.partials, f, st);
+    else if (p.dtype == kDtypeHook) e = sync_size<EHOOK>(p, ws.partials, f, st);
+    else if (p.dtype == kDtypeHook16) e = sync_size<EHOOK16>(p, ws.partials, f, st);
+    else e = sync_size<EBF16>(p, ws.partials, f, st);
+    if (e != cudaSuccess || f.counter) return e;
+    return launch_norm_final(ws.partials, first, 1, p.world, norms, st);
 }
 
 }  // namespace ddpk

@@ -653,8 +653,10 @@ int32_t ddp_bucket_allreduce_view_fp16(int32_t world, int32_t n_in_bucket, void*
  *   dtype                 a ddp_dtype
  *   workspace             device memory, 8-byte aligned, of at least
  *                         ddp_grad_set_workspace_bytes (DDP_ERR_CAPACITY if
- *                         smaller); the set keeps it, the caller owns it.  Calls
- *                         on one set share it: order them (one stream, or events)
+ *                         smaller), for the set alone (its first norm clears
+ *                         what has to start at zero); the set keeps it, the caller
+ *                         owns it.  Calls on one set share it: order them (one
+ *                         stream, or events)
  *   norms[world]          device float32, outside the tensors and the workspace
  *   max_norm              > 0 (may be infinite)
  * The set keeps these pointers until it is destroyed, the caller keeps the
@@ -686,9 +688,9 @@ int32_t ddp_grad_set_destroy(ddp_grad_set* set);
  * The handle checks its arguments and lays out its tables once; a run then
  * costs its launches.
  *   workspace     device memory, 8-byte aligned, of at least
- *                 ddp_sync_norm_workspace_bytes (DDP_ERR_CAPACITY if smaller);
- *                 its contents need not be set.  Runs of one handle share it:
- *                 order them
+ *                 ddp_sync_norm_workspace_bytes (DDP_ERR_CAPACITY if smaller),
+ *                 for the handle alone (its first run clears what has to start
+ *                 at zero).  Runs of one handle share it: order them
  *   norms[world]  device float32, outside the gradients and the workspace
  * Other arguments as for ddp_sync_buckets (any algo it takes).  The handle keeps
  * the pointers until it is destroyed, the caller keeps the memory.
@@ -733,9 +735,8 @@ int32_t ddp_sync_norm_destroy(ddp_sync_norm* sync);
  *                        norms' weights); NULL: all decay
  *   steps[world]         device int32: steps taken so far, 0 at the start
  *   workspace            DDP_ADAMW_WORKSPACE_BYTES of device memory, 8-byte
- *                        aligned; create clears it on `stream`, and steps must
- *                        come after that.  Steps of one handle must not overlap
- *                        on the GPU
+ *                        aligned, for the handle alone (its first step clears
+ *                        it).  Steps of one handle must not overlap on the GPU
  *   lr >= 0, 0 <= beta < 1, eps > 0, weight_decay >= 0, max_norm > 0 with norms
  * Nothing that a step writes may overlap anything else of the handle;
  * gradients may overlap each other (ranks may share one).  The handle keeps the
@@ -745,7 +746,7 @@ int32_t ddp_sync_norm_destroy(ddp_sync_norm* sync);
 typedef struct ddp_adamw ddp_adamw;
 int32_t ddp_adamw_create(int32_t world, int32_t n_params, void* const* params, const void* const* grads,
                          int32_t grad_dtype, void* const* exp_avg, void* const* exp_avg_sq, void* const* copies,
-                         const int64_t* numel, const uint8_t* no_decay, int32_t* steps, void* workspace, void* stream,
+                         const int64_t* numel, const uint8_t* no_decay, int32_t* steps, void* workspace,
                          ddp_adamw** out);
 int32_t ddp_adamw_step(ddp_adamw* adamw, double lr, double beta1, double beta2, double eps, double weight_decay,
                        const float* norms, double max_norm, void* stream);

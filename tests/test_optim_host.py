@@ -123,9 +123,9 @@ def _adamw(world=1, n=1, p=(H,), g=(H + (1 << 20),), m=(H + (2 << 20),), v=(H + 
     h = ctypes.c_void_p(1)
     tab = [None if t is None else _vp(*t) for t in (p, g, m, v, c)]
     st = ddp.lib().ddp_adamw_create(world, n, tab[0], tab[1], dtype, tab[2], tab[3], tab[4], _i64(*sizes), None, steps,
-                                    ws, None, ctypes.byref(h) if out else None)
-    assert not out or h.value is None
-    return st
+                                    ws, ctypes.byref(h) if out else None)
+    assert not out or st == 0 or h.value is None
+    return st, h
 
 
 @pytest.mark.parametrize("want,kw", [
@@ -139,7 +139,22 @@ def _adamw(world=1, n=1, p=(H,), g=(H + (1 << 20),), m=(H + (2 << 20),), v=(H + 
     (-1, dict(steps=H)), (-1, dict(ws=H + 16)),
 ])
 def test_adamw_refusals(want, kw):
-    assert _adamw(**kw) == want
+    assert _adamw(**kw)[0] == want
+
+
+def test_adamw_step_refusals():
+    L = ddp.lib()
+    st, h = _adamw()
+    assert st == 0
+    good = dict(lr=1e-3, b1=0.9, b2=0.999, eps=1e-8, wd=0.1, norms=None, max_norm=0.0)
+    for kw in (dict(lr=-1.0), dict(lr=NAN), dict(lr=INF), dict(b1=1.0), dict(b2=1.0), dict(b1=-0.1), dict(b1=NAN),
+               dict(eps=0.0), dict(eps=-1.0), dict(eps=1e-60), dict(eps=NAN), dict(wd=-0.1), dict(wd=INF),
+               dict(norms=WS + 4096), dict(norms=WS + 4096, max_norm=-1.0), dict(norms=WS + 4096, max_norm=NAN),
+               dict(norms=H, max_norm=1.0), dict(norms=NORMS, max_norm=1.0)):
+        a = {**good, **kw}
+        assert L.ddp_adamw_step(h, a["lr"], a["b1"], a["b2"], a["eps"], a["wd"], a["norms"], a["max_norm"], None) == -1, kw
+    assert L.ddp_adamw_step(h, 1e-3, 0.9, 0.999, 1e-8, 0.0, WS + 4098, 1.0, None) == -2
+    L.ddp_adamw_destroy(h)
 
 
 def test_adamw_step_and_destroy_without_a_handle():
