@@ -705,22 +705,24 @@ class GradSet:
                lib().ddp_grad_set_create(self.world, n, _vp_array(ptrs), sizes, code, self._workspace.data_ptr(),
                                          need.value, ctypes.byref(h)))
         self._h = h
+        self._lib = lib()
+        self._own = self.norms.data_ptr()
 
     def _norms(self, t):
-        return self.norms.data_ptr() if t is None or t is self.norms else _rank_words(t, self.world, _torch().float32, "norms")
+        return self._own if t is None else _rank_words(t, self.world, _torch().float32, "norms")
 
     def norm(self, out=None, stream=None):
         """norms[r] of every rank, into `out` or self.norms; returns that tensor."""
-        _check("ddp_grad_norm", lib().ddp_grad_norm(self._h, self._norms(out), _stream(stream)))
+        _check("ddp_grad_norm", self._lib.ddp_grad_norm(self._h, self._norms(out), _stream(stream)))
         return self.norms if out is None else out
 
     def clip(self, max_norm: float, norms=None, stream=None) -> None:
         """Scale each rank's gradients by min(1, max_norm / (norms[r] + 1e-6)), in place."""
-        _check("ddp_grad_clip", lib().ddp_grad_clip(self._h, self._norms(norms), max_norm, _stream(stream)))
+        _check("ddp_grad_clip", self._lib.ddp_grad_clip(self._h, self._norms(norms), max_norm, _stream(stream)))
 
     def norm_clip(self, max_norm: float, out=None, stream=None):
         """norm() and clip() by it; returns the norms before clipping."""
-        _check("ddp_grad_norm_clip", lib().ddp_grad_norm_clip(self._h, self._norms(out), max_norm, _stream(stream)))
+        _check("ddp_grad_norm_clip", self._lib.ddp_grad_norm_clip(self._h, self._norms(out), max_norm, _stream(stream)))
         return self.norms if out is None else out
 
     def close(self):
@@ -756,9 +758,11 @@ class SyncNormCall(SyncCall):
                                           self.K, self._bn, self._buckets, self.dtype, self.divisor, self.algo,
                                           self._workspace.data_ptr(), need.value, ctypes.byref(h)))
         self._h = h
+        self._lib = lib()
+        self._own = self.norms.data_ptr()
 
     def __call__(self, stream=None):
-        _check("ddp_sync_norm_run", lib().ddp_sync_norm_run(self._h, self.norms.data_ptr(), _stream(stream)))
+        _check("ddp_sync_norm_run", self._lib.ddp_sync_norm_run(self._h, self._own, _stream(stream)))
         return self.norms
 
     def close(self):
@@ -812,6 +816,7 @@ class AdamW:
                                       BF16 if gdt == torch.bfloat16 else F32, _vp_array(mp), _vp_array(vp), cp,
                                       _i64_array(sizes), mask, word, self._workspace.data_ptr(), ctypes.byref(h)))
         self._h = h
+        self._lib = lib()
 
     def step(self, lr: float, betas: Tuple[float, float] = (0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.0,
              norms=None, max_norm: float = 0.0, stream=None) -> None:
@@ -819,7 +824,7 @@ class AdamW:
         clip to max_norm, and skip a rank whose norm is not finite."""
         n = None if norms is None else _rank_words(norms, self.world, _torch().float32, "norms")
         _check("ddp_adamw_step",
-               lib().ddp_adamw_step(self._h, lr, betas[0], betas[1], eps, weight_decay, n, max_norm, _stream(stream)))
+               self._lib.ddp_adamw_step(self._h, lr, betas[0], betas[1], eps, weight_decay, n, max_norm, _stream(stream)))
 
     def close(self):
         if getattr(self, "_h", None):

@@ -25,15 +25,21 @@ struct RangeTab {
     int32_t n;
     int32_t tiles;             // a multiple of `run`
     int32_t run;               // tiles a norm block takes: never of two ranks
-    char* ptr[CAP];
-    int64_t bytes[CAP];
     int32_t tile_end[CAP];     // inclusive prefix of tiles; a rank's last range has the padding to a whole run
-    int32_t rank[CAP];
+    struct Range {             // side by side: a block finds one line of a cold constant cache, not one a field
+        char* ptr;
+        int64_t bytes;
+        int32_t first;         // its first tile
+        int32_t rank;
+    } range[CAP];
 };
 // Capacities: a launch's parameters are copied for every eager launch.
+constexpr int kNormVecs = (int)(kNormTile / 16 / kThreads);      // vectors a thread takes of a tile
+constexpr int64_t kWarpTile = 32 * kNormVecs * 16;               // bytes of a warp's tile
+constexpr int kSmallTiles = 128;                                 // warp tiles a rank that k_norm_small takes
 constexpr int kRangesSmall = 32;
 constexpr int kRangesMedium = 320;
-constexpr int kRangesLarge = 1280;
+constexpr int kRangesLarge = 1152;
 static_assert(sizeof(RangeTab<kRangesLarge>) + sizeof(NormFinish) + 64 <= kMaxParamBytes,
               "range table exceeds the kernel parameter limit");
 
@@ -44,60 +50,75 @@ struct RangePlan {
     std::vector<RangeTab<kRangesLarge>> large;
     int32_t run = 1;
     std::vector<int32_t> rank_first;             // first partial of each rank, and their end
+    // a few warp tiles a rank: what k_norm_small walks, and each rank's first
+    std::vector<RangeTab<kRangesSmall>> tiny_small;
+    std::vector<RangeTab<kRangesMedium>> tiny_medium;
+    std::vector<int32_t> tiny_first;
 };
 
-static int64_t range_tiles(const GradRange& g) {
+static int64_t range_tiles(const GradRange& g, int64_t tile) {
     const int64_t lead = (int64_t)(reinterpret_cast<uintptr_t>(g.ptr) % kNormAlign);
-    return (lead + g.bytes + kNormTile - 1) / kNormTile;
+    return (lead + g.bytes + tile - 1) / tile;
 }
 
 template <int CAP>
-static void fill_tables(const GradRange* ranges, int64_t n, int ranks, RangePlan* plan, std::vector<RangeTab<CAP>>* out) {
-    plan->cap = CAP;
-    plan->rank_first.assign(ranks + 1, 0);
+static void fill_tables(const GradRange* ranges, int64_t n, int ranks, int64_t tile, int run,
+                        std::vector<RangeTab<CAP>>* out, std::vector<int32_t>* rank_first) {
+    rank_first->assign(ranks + 1, 0);
     int64_t partials = 0;
     int rank = 0;                                // ranks below it have their rank_first
     for (int64_t i = 0; i < n;) {
         out->emplace_back();
         RangeTab<CAP>& b = out->back();
         b.n = 0;
-        b.run = plan->run;
+        b.run = run;
         int64_t tiles = 0;
         for (; i < n && b.n < CAP; ++i, ++b.n) {
-            while (rank < ranges[i].rank) plan->rank_first[++rank] = (int32_t)(partials + tiles / plan->run);
-            tiles += range_tiles(ranges[i]);
+            while (rank < ranges[i].rank) (*rank_first)[++rank] = (int32_t)(partials + tiles / run);
+            tiles += range_tiles(ranges[i], tile);
             if (b.n + 1 == CAP || i + 1 == n || ranges[i + 1].rank != ranges[i].rank)
-                tiles = (tiles + plan->run - 1) / plan->run * plan->run;
-            b.ptr[b.n] = ranges[i].ptr;
-            b.bytes[b.n] = ranges[i].bytes;
+                tiles = (tiles + run - 1) / run * run;
             b.tile_end[b.n] = (int32_t)tiles;
-            b.rank[b.n] = ranges[i].rank;
+            b.range[b.n] = {ranges[i].ptr, ranges[i].bytes, b.n ? b.tile_end[b.n - 1] : 0, ranges[i].rank};
         }
         b.tiles = (int32_t)tiles;
-        partials += tiles / plan->run;
+        partials += tiles / run;
     }
-    while (rank < ranks) plan->rank_first[++rank] = (int32_t)partials;
+    while (rank < ranks) (*rank_first)[++rank] = (int32_t)partials;
 }
 
 std::shared_ptr<const RangePlan> make_range_plan(const GradRange* ranges, int64_t n, int ranks) {
     auto plan = std::make_shared<RangePlan>();
     int64_t tiles = 0;
-    for (int64_t i = 0; i < n; ++i) tiles += range_tiles(ranges[i]);
-    // one wave of eight blocks an SM while a run of four is enough for that
-    plan->run = (int32_t)std::min<int64_t>(kNormRun, std::max<int64_t>(1, (tiles + kNormBlocks - 1) / kNormBlocks));
-    if (n <= kRangesSmall) fill_tables(ranges, n, ranks, plan.get(), &plan->small);
-    else if (n <= kRangesMedium) fill_tables(ranges, n, ranks, plan.get(), &plan->medium);
-    else fill_tables(ranges, n, ranks, plan.get(), &plan->large);
+    std::vector<int64_t> warp_tiles(ranks, 0);
+    for (int64_t i = 0; i < n; ++i) {
+        tiles += range_tiles(ranges[i], kNormTile);
+        warp_tiles[ranges[i].rank] += range_tiles(ranges[i], kWarpTile);
+    }
+    // One wave of eight blocks an SM while a run of kNormOneWave makes it; then
+    // runs of four, whose blocks the SMs take as they get free.
+    const int64_t wave = std::max<int64_t>(1, (tiles + kNormBlocks - 1) / kNormBlocks);
+    plan->run = (int32_t)(wave <= kNormOneWave ? wave : kNormRun);
+    plan->cap = n <= kRangesSmall ? kRangesSmall : n <= kRangesMedium ? kRangesMedium : kRangesLarge;
+    if (plan->cap == kRangesSmall) fill_tables(ranges, n, ranks, kNormTile, plan->run, &plan->small, &plan->rank_first);
+    else if (plan->cap == kRangesMedium)
+        fill_tables(ranges, n, ranks, kNormTile, plan->run, &plan->medium, &plan->rank_first);
+    else fill_tables(ranges, n, ranks, kNormTile, plan->run, &plan->large, &plan->rank_first);
+    if (n > 0 && plan->cap != kRangesLarge && ranks <= kFinishRanks &&
+        *std::max_element(warp_tiles.begin(), warp_tiles.end()) <= kSmallTiles) {
+        if (plan->cap == kRangesSmall) fill_tables(ranges, n, ranks, kWarpTile, 1, &plan->tiny_small, &plan->tiny_first);
+        else fill_tables(ranges, n, ranks, kWarpTile, 1, &plan->tiny_medium, &plan->tiny_first);
+    }
     return plan;
 }
 
 int64_t range_plan_partials(const RangePlan& plan) { return plan.rank_first.back(); }
 
 // Where `tile`, which belongs to range i, starts in memory.
-template <int CAP>
+template <int64_t TILE = kNormTile, int CAP>
 __device__ __forceinline__ uintptr_t tile_base(const RangeTab<CAP>& b, int i, int tile) {
-    const int first = i ? b.tile_end[i - 1] : 0;
-    return (reinterpret_cast<uintptr_t>(b.ptr[i]) & ~(uintptr_t)(kNormAlign - 1)) + (uintptr_t)(tile - first) * kNormTile;
+    return (reinterpret_cast<uintptr_t>(b.range[i].ptr) & ~(uintptr_t)(kNormAlign - 1)) +
+           (uintptr_t)(tile - b.range[i].first) * TILE;
 }
 
 // The vector at address a, zeros where it lies outside [p, end).
@@ -118,10 +139,8 @@ __device__ __forceinline__ typename E::V load_inside(uintptr_t a, uintptr_t p, u
     return v;
 }
 
-constexpr int kNormVecs = (int)(kNormTile / 16 / kThreads);      // vectors a thread takes of a tile
-
-// The sum of squares of a thread's vectors: in binary32 as four chains, which
-// are a quarter as long and overlap; in binary64 where that leaves its range.
+// The sum of squares of a thread's vectors, as four chains, which are a quarter
+// as long and overlap.
 template <class E, int U>
 __device__ __forceinline__ float sum_squares(const typename E::V (&x)[U]) {
     float s[4] = {0.f, 0.f, 0.f, 0.f};
@@ -131,37 +150,55 @@ __device__ __forceinline__ float sum_squares(const typename E::V (&x)[U]) {
         for (int l = 0; l < E::L; ++l) s[l & 3] = fmaf(f32_of(x[u], l), f32_of(x[u], l), s[l & 3]);
     return (s[0] + s[1]) + (s[2] + s[3]);
 }
+// Zero if all of them are zeros of either sign.
 template <class E, int U>
-__device__ __forceinline__ double sum_squares64(const typename E::V (&x)[U]) {
-    double d = 0.0;
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int l = 0; l < E::L; ++l) d = fma((double)f32_of(x[u], l), (double)f32_of(x[u], l), d);
-    return d;
-}
-// Whether any of them is not a zero of either sign.
-template <class E, int U>
-__device__ __forceinline__ bool any_nonzero(const typename E::V (&x)[U]) {
+__device__ __forceinline__ uint32_t magnitude_bits(const typename E::V (&x)[U]) {
     uint32_t bits = 0;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const uint4 w = *reinterpret_cast<const uint4*>(&x[u]);
         bits |= w.x | w.y | w.z | w.w;
     }
-    return (bits & (E::L == 8 ? 0x7FFF7FFFu : 0x7FFFFFFFu)) != 0;
+    return bits & (E::L == 8 ? 0x7FFF7FFFu : 0x7FFFFFFFu);
+}
+
+// Thread t's vectors of a tile that T threads share.
+template <class E, int T>
+__device__ __forceinline__ void load_tile(typename E::V (&x)[kNormVecs], int t, uintptr_t base, uintptr_t p, uintptr_t end) {
+#pragma unroll
+    for (int u = 0; u < kNormVecs; ++u) x[u] = load_inside<E>(base + (u * T + t) * 16, p, end);
+}
+
+// A thread's part of a tile's sum of squares.  Where it leaves binary32's range
+// and the values are not all zeros, they are loaded once more and squared in
+// binary64: keeping them would cost every tile the registers.
+template <class E, int T>
+__device__ __forceinline__ double tile_squares(const typename E::V (&x)[kNormVecs], int t, uintptr_t base, uintptr_t p,
+                                               uintptr_t end) {
+    const float s = sum_squares<E>(x);
+    if (in_square_range(s)) return (double)s;
+    double d = 0.0;
+    if (magnitude_bits<E>(x) != 0) {
+#pragma unroll 1
+        for (int u = 0; u < kNormVecs; ++u) {
+            const typename E::V v = load_inside<E>(base + (u * T + t) * 16, p, end);
+#pragma unroll
+            for (int l = 0; l < E::L; ++l) d = fma((double)f32_of(v, l), (double)f32_of(v, l), d);
+        }
+    }
+    return d;
 }
 
 // HBM bounds it: one read of every gradient.  A thread adds a tile's squares in
 // binary32 and the tiles in binary64; the block joins its threads once a run.
 template <class E, int CAP>
-__global__ void __launch_bounds__(kThreads) k_norm_partials(const __grid_constant__ RangeTab<CAP> b, double* partials,
+__global__ void __launch_bounds__(kThreads, 8) k_norm_partials(const __grid_constant__ RangeTab<CAP> b, double* partials,
                                                             const __grid_constant__ NormFinish finish) {
     __shared__ SquareScratch scratch;
     __shared__ int slot;
     init_squares(scratch);
+    AcquireOnce acquire;
     pdl_release();
-    pdl_acquire();
     const int runs = b.tiles / b.run;
     for (int r = blockIdx.x; r < runs; r += gridDim.x) {
         int tile = r * b.run;
@@ -171,13 +208,11 @@ __global__ void __launch_bounds__(kThreads) k_norm_partials(const __grid_constan
         for (const int stop = tile + b.run; tile < stop; ++tile) {
             while (tile >= b.tile_end[i]) ++i;
             const uintptr_t base = tile_base(b, i, tile);
-            const uintptr_t p = reinterpret_cast<uintptr_t>(b.ptr[i]), end = p + (uintptr_t)b.bytes[i];
+            const uintptr_t p = reinterpret_cast<uintptr_t>(b.range[i].ptr), end = p + (uintptr_t)b.range[i].bytes;
+            acquire();
             typename E::V x[kNormVecs];
-#pragma unroll
-            for (int u = 0; u < kNormVecs; ++u) x[u] = load_inside<E>(base + (u * kThreads + threadIdx.x) * 16, p, end);
-            const float s = sum_squares<E>(x);
-            if (in_square_range(s)) d += (double)s;
-            else if (any_nonzero<E>(x)) d += sum_squares64<E>(x);
+            load_tile<E, kThreads>(x, threadIdx.x, base, p, end);
+            d += tile_squares<E, kThreads>(x, threadIdx.x, base, p, end);
         }
         const double t = block_squares((float)d, d != 0.0, scratch, [&] { return d; });
         if (threadIdx.x == 0) partials[r] = t;
@@ -186,44 +221,110 @@ __global__ void __launch_bounds__(kThreads) k_norm_partials(const __grid_constan
     finish_norms<kThreads>(finish, partials, scratch.d);
 }
 
+// The norm of little data in one launch without partials: a cluster of
+// kSmallParts blocks a rank, each warp of it a 2 KB tile (or a few).  What a
+// call takes here is latency: the table's lines come from a cold constant cache
+// and the data from L2, one after the other, so every warp does it once and at
+// the same time, and the sums meet in shared memory.  (A launch of partials and
+// its last block exchange theirs through L2, twice 0.7 us away.)  Under a CTA
+// cap that has no room for the clusters one block takes the parts in turn.
+constexpr int kSmallParts = 8;
+template <class E, int CAP, bool CLUSTER>
+__global__ void __launch_bounds__(kThreads) k_norm_small(const __grid_constant__ RangeTab<CAP> b,
+                                                         const __grid_constant__ NormFinish f) {
+    __shared__ SquareScratch scratch;
+    __shared__ double part[kSmallParts];
+    init_squares(scratch);
+    AcquireOnce acquire;
+    pdl_release();
+    constexpr int kPer = CLUSTER ? kSmallParts : 1;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int r = blockIdx.x / kPer; r < f.ranks; r += gridDim.x / kPer) {
+        const int stop = f.first[r + 1];
+        for (int c = blockIdx.x % kPer; c < kSmallParts; c += kPer) {
+            double d = 0.0;
+            constexpr int kStep = kSmallParts * (kThreads / 32);
+#pragma unroll 1
+            for (int tile = f.first[r] + warp * kSmallParts + c; tile < stop; tile += 2 * kStep) {
+                uintptr_t base[2], p[2], end[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {    // two tiles' table lines and data at a time; none past the rank's
+                    const int t = tile + k * kStep < stop ? tile + k * kStep : tile;
+                    const int i = first_past(b.tile_end, b.n, t);
+                    base[k] = tile_base<kWarpTile>(b, i, t);
+                    p[k] = reinterpret_cast<uintptr_t>(b.range[i].ptr);
+                    end[k] = tile + k * kStep < stop ? p[k] + (uintptr_t)b.range[i].bytes : p[k];
+                }
+                acquire();
+                typename E::V x[2][kNormVecs];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) load_tile<E, 32>(x[k], lane, base[k], p[k], end[k]);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) d += tile_squares<E, 32>(x[k], lane, base[k], p[k], end[k]);
+            }
+            acquire();
+            const double t = block_squares((float)d, d != 0.0, scratch, [&] { return d; });
+            if (threadIdx.x == 0) {
+                if constexpr (CLUSTER) cooperative_groups::this_cluster().map_shared_rank(part, 0)[c] = t;
+                else part[c] = t;
+            }
+            __syncthreads();
+        }
+        if constexpr (CLUSTER) cooperative_groups::this_cluster().sync();
+        if (threadIdx.x == 0 && blockIdx.x % kPer == 0) {
+            double t = part[0];
+            for (int q = 1; q < kSmallParts; ++q) t += part[q];
+            const float norm = norm_of(t);
+            for (int q = 0; q < f.copies; ++q) f.norms[r * f.copies + q] = norm;
+        }
+        __syncthreads();
+    }
+}
+
 struct RankFirst {
     int32_t first[DDP_MAX_WORLD + 1];
 };
 
-// A cluster of C blocks a rank: its partials added in binary64, each thread's
-// in order, then the threads' sums, then the blocks'.  One block reads some
-// 100 GB/s, so that the 350 thousand partials of a 355M-parameter sync would
-// take it 30 us; eight share them.
+// Partials to norms.  Each rank's are added in `parts` parts in binary64: each
+// thread's in order, then the threads' sums, then the parts'.  One block reads
+// some 100 GB/s, so that the 350 thousand partials of a 355M-parameter sync
+// would take it 30 us: there the parts are a cluster's blocks.  Under a CTA cap
+// that has no room for them one block takes the parts in turn.
 constexpr int kFinalThreads = 512;
-constexpr int kFinalBlocks = 8;
-template <int C>
+constexpr int kFinalParts = 8;
+template <bool CLUSTER>
 __global__ void __launch_bounds__(kFinalThreads) k_norm_final(const double* partials, const __grid_constant__ RankFirst rf,
-                                                              float* norms, int copies) {
+                                                              float* norms, int ranks, int copies, int parts) {
     __shared__ double sh[kFinalThreads / 32];
-    __shared__ double block[C];
+    __shared__ double part[kFinalParts];
     pdl_release();
     pdl_acquire();
-    const int r = blockIdx.x / C, c = blockIdx.x % C;
-    const int end = rf.first[r + 1];
-    constexpr int kStep = C * kFinalThreads;
-    double d[4] = {0.0, 0.0, 0.0, 0.0};          // four loads in flight
-    int k = rf.first[r] + c * kFinalThreads + (int)threadIdx.x;
-    for (; k + 3 * kStep < end; k += 4 * kStep)
+    const int per = CLUSTER ? parts : 1;
+    const int step = parts * kFinalThreads;
+    for (int r = blockIdx.x / per; r < ranks; r += gridDim.x / per) {
+        const int end = rf.first[r + 1];
+        for (int c = blockIdx.x % per; c < parts; c += per) {
+            double d[4] = {0.0, 0.0, 0.0, 0.0};  // four loads in flight
+            int k = rf.first[r] + c * kFinalThreads + (int)threadIdx.x;
+            for (; k + 3 * step < end; k += 4 * step)
 #pragma unroll
-        for (int u = 0; u < 4; ++u) d[u] += partials[k + u * kStep];
-    for (; k < end; k += kStep) d[0] += partials[k];
-    double t = block_sum(warp_sum((d[0] + d[1]) + (d[2] + d[3])), sh);
-    if constexpr (C > 1) {
-        auto cluster = cooperative_groups::this_cluster();
-        if (threadIdx.x == 0) cluster.map_shared_rank(block, 0)[c] = t;
-        cluster.sync();
-        if (threadIdx.x == 0 && c == 0) {
-            t = block[0];
-            for (int q = 1; q < C; ++q) t += block[q];
+                for (int u = 0; u < 4; ++u) d[u] += partials[k + u * step];
+            for (; k < end; k += step) d[0] += partials[k];
+            const double t = block_sum(warp_sum((d[0] + d[1]) + (d[2] + d[3])), sh);
+            if (threadIdx.x == 0) {
+                if constexpr (CLUSTER) cooperative_groups::this_cluster().map_shared_rank(part, 0)[c] = t;
+                else part[c] = t;
+            }
+            __syncthreads();
         }
+        if constexpr (CLUSTER) cooperative_groups::this_cluster().sync();
+        if (threadIdx.x == 0 && blockIdx.x % per == 0) {
+            double t = part[0];
+            for (int q = 1; q < parts; ++q) t += part[q];
+            for (int q = 0; q < copies; ++q) norms[r * copies + q] = norm_of(t);
+        }
+        __syncthreads();
     }
-    if (threadIdx.x == 0 && c == 0)
-        for (int q = 0; q < copies; ++q) norms[r * copies + q] = norm_of(t);
 }
 
 // min(1, max_norm / (norm + 1e-6)); a NaN stays one.
@@ -249,15 +350,16 @@ __global__ void __launch_bounds__(kThreads) k_clip(const __grid_constant__ Range
     using V = typename E::V;
     using S = typename E::S;
     __shared__ int slot;
+    AcquireOnce acquire;
     pdl_release();
-    pdl_acquire();
     for (int tile = blockIdx.x; tile < b.tiles; tile += gridDim.x) {
         if (tile != (int)blockIdx.x) __syncthreads();          // slot is free for this tile
         const int i = block_first_past(b.tile_end, b.n, tile, &slot);
         const uintptr_t base = tile_base(b, i, tile);
-        const float c = clip_factor(norms[b.rank[i]], max_norm);
+        acquire();
+        const float c = clip_factor(norms[b.range[i].rank], max_norm);
         if (c == 1.f) continue;                  // the gradients keep their bits
-        const uintptr_t p = reinterpret_cast<uintptr_t>(b.ptr[i]), end = p + (uintptr_t)b.bytes[i];
+        const uintptr_t p = reinterpret_cast<uintptr_t>(b.range[i].ptr), end = p + (uintptr_t)b.range[i].bytes;
         V x[kNormVecs];
 #pragma unroll
         for (int u = 0; u < kNormVecs; ++u) {
@@ -279,15 +381,28 @@ __global__ void __launch_bounds__(kThreads) k_clip(const __grid_constant__ Range
     }
 }
 
-NormFinish norm_finish(NormSpace ws, const int32_t* rank_first, int ranks, int copies, float* norms, bool one_launch) {
+static NormFinish finish_of(NormSpace ws, const int32_t* rank_first, int ranks, int copies, float* norms) {
     NormFinish f{};
-    if (!one_launch || ranks > kFinishRanks || rank_first[ranks] > kFinishPartials) return f;
     f.counter = ws.counter;
     f.norms = norms;
     f.ranks = ranks;
     f.copies = copies;
     std::copy(rank_first, rank_first + ranks + 1, f.first);
     return f;
+}
+
+NormFinish norm_finish(NormSpace ws, const int32_t* rank_first, int ranks, int copies, float* norms, bool one_launch) {
+    if (!one_launch || ranks > kFinishRanks || rank_first[ranks] > kFinishPartials) return NormFinish{};
+    return finish_of(ws, rank_first, ranks, copies, norms);
+}
+
+static bool room_for(int64_t blocks) { return cap_ctas(blocks) == blocks; }
+
+template <class E, int CAP>
+static cudaError_t norm_small(const RangeTab<CAP>& b, const NormFinish& f, cudaStream_t st) {
+    if (room_for(f.ranks * kSmallParts))
+        return launch_table<kSmallParts>(k_norm_small<E, CAP, true>, dim3(f.ranks * kSmallParts), dim3(kThreads), st, b, f);
+    return launch_table(k_norm_small<E, CAP, false>, dim3(cap_ctas(f.ranks)), dim3(kThreads), st, b, f);
 }
 
 template <class E, int CAP>
@@ -304,20 +419,27 @@ static cudaError_t norm_tables(const std::vector<RangeTab<CAP>>& tables, double*
 }
 
 template <class E>
-static cudaError_t norm_partials(const RangePlan& plan, double* partials, const NormFinish& f, cudaStream_t st) {
-    if (plan.cap == kRangesSmall) return norm_tables<E>(plan.small, partials, f, st);
-    if (plan.cap == kRangesMedium) return norm_tables<E>(plan.medium, partials, f, st);
-    return norm_tables<E>(plan.large, partials, f, st);
+static cudaError_t norm_kernels(const RangePlan& plan, NormSpace ws, int copies, float* norms, cudaStream_t st) {
+    const int ranks = (int)plan.rank_first.size() - 1;
+    const int32_t* first = plan.rank_first.data();
+    if (!plan.tiny_first.empty()) {
+        const NormFinish f = finish_of(ws, plan.tiny_first.data(), ranks, copies, norms);
+        if (plan.cap == kRangesSmall) return norm_small<E>(plan.tiny_small[0], f, st);
+        return norm_small<E>(plan.tiny_medium[0], f, st);
+    }
+    const size_t launches = plan.small.size() + plan.medium.size() + plan.large.size();
+    const NormFinish f = norm_finish(ws, first, ranks, copies, norms, launches == 1);
+    cudaError_t e;
+    if (plan.cap == kRangesSmall) e = norm_tables<E>(plan.small, ws.partials, f, st);
+    else if (plan.cap == kRangesMedium) e = norm_tables<E>(plan.medium, ws.partials, f, st);
+    else e = norm_tables<E>(plan.large, ws.partials, f, st);
+    if (e != cudaSuccess || f.counter) return e;
+    return launch_norm_final(ws.partials, first, ranks, copies, norms, st);
 }
 
 cudaError_t launch_norm(const RangePlan& plan, int dtype, NormSpace ws, int copies, float* norms, cudaStream_t st) {
-    const int ranks = (int)plan.rank_first.size() - 1;
-    const size_t launches = plan.small.size() + plan.medium.size() + plan.large.size();
-    const NormFinish f = norm_finish(ws, plan.rank_first.data(), ranks, copies, norms, launches == 1);
-    const cudaError_t e = dtype == DDP_BF16 ? norm_partials<EBF16>(plan, ws.partials, f, st)
-                                            : norm_partials<EF32>(plan, ws.partials, f, st);
-    if (e != cudaSuccess || f.counter) return e;
-    return launch_norm_final(ws.partials, plan.rank_first.data(), ranks, copies, norms, st);
+    return dtype == DDP_BF16 ? norm_kernels<EBF16>(plan, ws, copies, norms, st)
+                             : norm_kernels<EF32>(plan, ws, copies, norms, st);
 }
 
 cudaError_t launch_norm_final(const double* partials, const int32_t* rank_first, int ranks, int copies, float* norms,
@@ -326,10 +448,12 @@ cudaError_t launch_norm_final(const double* partials, const int32_t* rank_first,
     std::copy(rank_first, rank_first + ranks + 1, rf.first);
     int32_t most = 0;
     for (int r = 0; r < ranks; ++r) most = std::max(most, rank_first[r + 1] - rank_first[r]);
-    if (most <= 8 * kFinalThreads)
-        return launch_table(k_norm_final<1>, dim3(ranks), dim3(kFinalThreads), st, partials, rf, norms, copies);
-    return launch_table<kFinalBlocks>(k_norm_final<kFinalBlocks>, dim3(ranks * kFinalBlocks), dim3(kFinalThreads), st,
-                                      partials, rf, norms, copies);
+    const int parts = most <= 8 * kFinalThreads ? 1 : kFinalParts;
+    if (parts > 1 && room_for((int64_t)ranks * parts))
+        return launch_table<kFinalParts>(k_norm_final<true>, dim3(ranks * parts), dim3(kFinalThreads), st, partials, rf,
+                                         norms, ranks, copies, parts);
+    return launch_table(k_norm_final<false>, dim3(cap_ctas(ranks)), dim3(kFinalThreads), st, partials, rf, norms, ranks,
+                        copies, parts);
 }
 
 template <class E, int CAP>

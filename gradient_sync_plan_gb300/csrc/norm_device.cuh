@@ -65,6 +65,18 @@ __device__ __forceinline__ double warp_sum(double s) {
 // every value is one).
 __device__ __forceinline__ bool in_square_range(float w) { return w >= 0x1p-90f && w <= 0x1p112f; }
 
+// pdl_acquire at its first call: after a block has found its place in the table,
+// which is a parameter and waits for nobody, and before it touches memory.  The
+// search (1 to 2 us from a cold constant cache) then overlaps the tail of the
+// kernel before.
+struct AcquireOnce {
+    bool done = false;
+    __device__ __forceinline__ void operator()() {
+        if (!done) pdl_acquire();
+        done = true;
+    }
+};
+
 // One value a warp -> their sum in every lane of warp 0 (undefined elsewhere).
 // `sh` has a slot a warp; the caller puts a barrier between two uses.
 template <class T>

@@ -23,11 +23,13 @@ struct GradRange {
 
 // Bytes of a tile of the norm and clip kernels.  Tiles start at 128-byte
 // boundaries of memory, so a range has at most one more than bytes / kNormTile
-// rounded up.  A norm block takes up to kNormRun of them, as many as make
-// kNormBlocks blocks (eight on each of 152 SMs).
+// rounded up.  A norm block takes a run of them: as many as make kNormBlocks
+// blocks (eight on each of 152 SMs) while kNormOneWave are enough for that, else
+// kNormRun.
 constexpr int64_t kNormTile = 16384;
 constexpr int64_t kNormAlign = 128;
 constexpr int64_t kNormRun = 4;
+constexpr int64_t kNormOneWave = 16;
 constexpr int64_t kNormBlocks = 8 * 152;
 
 // The kernels' tables, filled once for ranges sorted by rank.

@@ -23,6 +23,8 @@
 
 namespace ddpk {
 
+constexpr uint32_t kRanksDiffer = 15;
+
 template <int MEMBERS, int PTRS>
 struct SyncTab {
     static constexpr int kMembers = MEMBERS, kPtrs = PTRS;
@@ -32,17 +34,20 @@ struct SyncTab {
     int32_t vecs;                // vectors a thread takes of a tile
     int32_t div_mode;
     float div_operand;
-    int64_t numel[MEMBERS];
-    int64_t offset[MEMBERS];     // bucket position of element 0
-    int64_t clen[MEMBERS];       // chunk length of the member's bucket
-    float inv_clen[MEMBERS];
     int32_t tile_end[MEMBERS];   // inclusive prefix of tiles
-    int8_t lead[MEMBERS];        // elements past a 16-byte boundary, at every rank; -1: ranks differ
+    struct Member {              // side by side: a block finds one line of a cold constant cache, not one a field
+        int64_t numel;
+        int64_t offset;          // bucket position of element 0
+        int64_t clen;            // chunk length of the member's bucket
+        float inv_clen;
+        uint32_t first : 28;     // its first tile
+        uint32_t lead : 4;       // elements past a 16-byte boundary, at every rank; kRanksDiffer
+    } member[MEMBERS];
     char* ptr[PTRS];             // ptr[m * world + r]
 };
 using SyncSmall = SyncTab<32, 256>;
 using SyncMedium = SyncTab<176, 704>;
-using SyncLarge = SyncTab<336, 2624>;
+using SyncLarge = SyncTab<304, 2688>;
 static_assert(sizeof(SyncLarge) + 16 <= kMaxParamBytes, "sync table exceeds the kernel parameter limit");
 
 // Ring chunk of bucket position q: the quotient from a binary32 estimate, off
@@ -101,24 +106,26 @@ __global__ void __launch_bounds__(kThreads, MINB) k_sync_norm(const __grid_const
     __shared__ SquareScratch scratch;
     __shared__ int slot;
     init_squares(scratch);
+    AcquireOnce acquire;
     pdl_release();
-    pdl_acquire();
     const int world = b.world;
     for (int tile = blockIdx.x; tile < b.tiles; tile += gridDim.x) {
         const int i = block_first_past(b.tile_end, b.n, tile, &slot);
         // pieces: vectors at 16-byte boundaries, or elements where the ranks'
         // pointers do not line up; positions count from e0, [head, tail) are the member's
         const int tile_len = kRow * b.vecs;
-        const int step = b.lead[i] >= 0 ? L : 1;
-        const int64_t e0 = (int64_t)(tile - (i ? b.tile_end[i - 1] : 0)) * tile_len - max((int)b.lead[i], 0);
+        const int step = b.member[i].lead != kRanksDiffer ? L : 1;
+        const int lead = b.member[i].lead != kRanksDiffer ? (int)b.member[i].lead : 0;
+        const int64_t e0 = (int64_t)(tile - (int)b.member[i].first) * tile_len - lead;
         const int head = e0 < 0 ? (int)-e0 : 0;
-        const int tail = (int)min((int64_t)tile_len, b.numel[i] - e0);
-        const int64_t q0 = b.offset[i] + e0;
-        const int j0 = chunk_of(q0 + head, b.clen[i], b.inv_clen[i]);
-        const int near = (int)min((int64_t)tile_len, (int64_t)(j0 + 1) * b.clen[i] - q0);     // where chunk j0 ends
+        const int tail = (int)min((int64_t)tile_len, b.member[i].numel - e0);
+        const int64_t q0 = b.member[i].offset + e0;
+        const int j0 = chunk_of(q0 + head, b.member[i].clen, b.member[i].inv_clen);
+        const int near = (int)min((int64_t)tile_len, (int64_t)(j0 + 1) * b.member[i].clen - q0);     // where chunk j0 ends
         char* const* pp = b.ptr + (size_t)i * world;
         auto at = [&](int r) -> const char* { return pp[r]; };
         auto start_of = [&](int j) { return j + 1 == world ? 0 : j + 1; };
+        acquire();
         float s = 0.f;
         uint32_t bits = 0;                       // of every value's, but the sign
         int a = 0;
@@ -144,8 +151,8 @@ __global__ void __launch_bounds__(kThreads, MINB) k_sync_norm(const __grid_const
             int j = j0;
             bool whole = end - first == L;
             if (whole && end > near) {
-                j = chunk_of(q0 + first, b.clen[i], b.inv_clen[i]);
-                whole = q0 + end <= (int64_t)(j + 1) * b.clen[i];
+                j = chunk_of(q0 + first, b.member[i].clen, b.member[i].inv_clen);
+                whole = q0 + end <= (int64_t)(j + 1) * b.member[i].clen;
             }
             if (whole) {
                 const int64_t byte = (e0 + first) * (int64_t)sizeof(S);
@@ -157,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, MINB) k_sync_norm(const __grid_const
             }
 #pragma unroll 1
             for (int e = first; e < end; ++e) {
-                j = chunk_of(q0 + e, b.clen[i], b.inv_clen[i]);
+                j = chunk_of(q0 + e, b.member[i].clen, b.member[i].inv_clen);
                 const S y = average_s<E>(fold_ring_scalar<E>(at, world, start_of(j), e0 + e), b.div_mode, b.div_operand);
                 for (int r = 0; r < world; ++r) reinterpret_cast<S*>(pp[r])[e0 + e] = y;
                 s += sum_squares(y);
@@ -185,7 +192,7 @@ constexpr int kSms = 152;
 int sync_norm_vecs(int world, int64_t numel, int dtype) {
     const int64_t vectors = numel / (16 / elem_bytes(dtype));
     int v = world <= 4 ? 4 : 1;
-    while (v > 1 && vectors < (int64_t)v * kThreads * kSms * 16) v /= 2;
+    while (v > 1 && vectors < (int64_t)v * kThreads * kSms * 8) v /= 2;
     return v;
 }
 
@@ -225,13 +232,10 @@ static void fill_tables(SyncPlan* plan, const SyncMember* members, int64_t n, in
         for (; i < n && b.n < most; ++i, ++b.n) {
             const SyncMember& m = members[i];
             const int lead = lead_of(world, m, es);
+            const int32_t first = b.tiles;
             b.tiles += (int32_t)((std::max(lead, 0) + m.numel + tile - 1) / tile);
-            b.numel[b.n] = m.numel;
-            b.offset[b.n] = m.offset;
-            b.clen[b.n] = m.clen;
-            b.inv_clen[b.n] = 1.0f / (float)m.clen;
             b.tile_end[b.n] = b.tiles;
-            b.lead[b.n] = (int8_t)lead;
+            b.member[b.n] = {m.numel, m.offset, m.clen, 1.0f / (float)m.clen, (uint32_t)first, lead < 0 ? kRanksDiffer : (uint32_t)lead};
             for (int r = 0; r < world; ++r) b.ptr[(size_t)b.n * world + r] = static_cast<char*>(m.ptrs[r]);
         }
         plan->tiles += b.tiles;
