@@ -76,14 +76,18 @@ bool hits_any(const std::vector<Span>& sorted, Span s) {
     return it != sorted.begin() && std::prev(it)->second > s.first;
 }
 
-// World, tensor count and sizes shared by the three creating calls.
+// World, tensor count and sizes shared by the creating calls.  A rank's
+// elements are capped as one buffer's are, so that sums of bytes and tiles fit.
 int32_t check_sizes(int32_t world, int32_t n_params, const int64_t* numel, int32_t dtype) {
     const int32_t st = common_checks(world, 0, dtype);
     if (st) return st;
     if (n_params < 0 || (n_params > 0 && !numel)) return DDP_ERR_INVALID;
+    int64_t total = 0;
     for (int32_t i = 0; i < n_params; ++i) {
         const int32_t s = common_checks(world, numel[i], dtype);
         if (s) return s;
+        total += numel[i];
+        if (total > DDP_MAX_NUMEL) return DDP_ERR_CAPACITY;
     }
     return DDP_OK;
 }

@@ -649,7 +649,8 @@ int32_t ddp_bucket_allreduce_view_fp16(int32_t world, int32_t n_in_bucket, void*
  *   grads[world*n_params] host table of device pointers, rank-major; no two
  *                         tensors may overlap.  Entries of empty tensors may be
  *                         NULL
- *   numel[n_params]       elements of each tensor (>= 0)
+ *   numel[n_params]       elements of each tensor (>= 0; their sum at most
+ *                         DDP_MAX_NUMEL)
  *   dtype                 a ddp_dtype
  *   workspace             device memory, 8-byte aligned, of at least
  *                         ddp_grad_set_workspace_bytes (DDP_ERR_CAPACITY if

@@ -161,11 +161,19 @@ def test_zero_gradients_and_a_limit_that_is_not_reached():
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-def test_norm_does_not_depend_on_the_grid(dtype):
-    views, _ = _place(_values(2, [700_001, 40_000, 5], 11), "packed", DT[dtype])
+@pytest.mark.parametrize("sizes", [[3000, 500, 5], [700_001, 40_000, 5], [60_000_001]],
+                         ids=["cluster", "one_launch", "two_launches"])
+def test_norm_does_not_depend_on_the_grid(sizes, dtype):
+    if sizes[0] > 10_000_000:
+        views = [[torch.randn(n, device="cuda").to(DT[dtype]) for n in sizes] for _ in range(2)]
+    else:
+        views, _ = _place(_values(2, sizes, 11), "packed", DT[dtype])
     s = ddp.GradSet(views)
     want = s.norm().clone()
-    for cap in (1, 3, 150):
+    for r in range(2):
+        ref = _norm64(views[r])
+        assert abs(float(want[r]) - ref) <= 16 * U * ref
+    for cap in (1, 3, 15, 150):
         prev = ddp.ddp_set_max_ctas(cap)
         try:
             got = s.norm(out=torch.empty(2, device="cuda"))
@@ -176,8 +184,9 @@ def test_norm_does_not_depend_on_the_grid(dtype):
 
 
 @pytest.mark.parametrize("limit", [0.5, 0.1])
-def test_set_on_another_stream_and_in_a_graph(limit):
-    views, _ = _place(_values(2, [100_000, 333], 2), "apart", torch.float32)
+@pytest.mark.parametrize("sizes", [[100_000, 333], [3000, 33]])
+def test_set_on_another_stream_and_in_a_graph(sizes, limit):
+    views, _ = _place(_values(2, sizes, 2), "apart", torch.float32)
     s = ddp.GradSet(views)
     want = s.norm().clone()
     torch.cuda.synchronize()
@@ -198,6 +207,34 @@ def test_set_on_another_stream_and_in_a_graph(limit):
         assert k or torch.equal(out, want)
     for r in range(2):
         assert abs(_norm64(views[r]) - min(limit, float(want[r]))) < 1e-5
+
+
+def test_first_norm_inside_a_capture_then_eager_ones():
+    views, _ = _place(_values(2, [100_000, 333], 2), "apart", torch.float32)
+    want = ddp.GradSet(views).norm().clone()
+    s = ddp.GradSet(views)
+    out = torch.zeros(2, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):                # the set's first call: its counter is cleared by every replay
+        s.norm(out=out)
+    assert torch.equal(s.norm(), want)           # and by the first eager call, replayed or not
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(s.norm(), want)
+
+
+@pytest.mark.parametrize("world,sizes", [(40, [3000, 7]), (17, [200_003]), (300, [50])])
+def test_norm_and_clip_of_many_ranks(world, sizes):
+    views, held = _place(_values(world, sizes, 13, 1e-2), "apart", torch.float32)
+    want = [_norm64(row) for row in views]
+    s = ddp.GradSet(views)
+    norms = s.norm_clip(want[0]).cpu()
+    _check_held(held, "many ranks")
+    for r in range(world):
+        assert abs(float(norms[r]) - want[r]) <= 16 * U * want[r]
+        got, limit = _norm64(views[r]), min(want[r], want[0])
+        assert abs(got - limit) <= 16 * U * limit + 2e-6
 
 
 def test_elements_past_32_bits():
@@ -227,7 +264,8 @@ def _sync_views(world, sizes, dtype, seed, layout):
 @pytest.mark.parametrize("world,sizes,layout", [
     (1, [1000, 3], "apart"), (2, [300_001, 7, 0, 40_000], "packed"), (3, [700_001, 1, 5, 900_000], "apart"),
     (5, [1, 2, 3], "odd"), (8, [400_003, 100_000, 999], "odd"), (8, [400_003, 100_000, 999], "apart"),
-    (16, [260_000, 9], "apart"), (2, [6_000_001, 100], "apart"), (33, [50_001], "apart"),
+    (16, [260_000, 9], "apart"), (2, [6_000_001, 100], "apart"), (33, [50_001], "apart"), (4, [800_001, 5], "packed"),
+    (150, [3001, 40], "apart"), (2, [1 + (37 * i) % 911 for i in range(700)], "packed"),
 ])
 def test_sync_norm_keeps_the_syncs_bits(world, sizes, layout, dtype, algo):
     hook = algo in (ddp.DDP_ALGO_BF16_HOOK, ddp.DDP_ALGO_BF16_HOOK_VIEW, ddp.DDP_ALGO_FP16_HOOK_VIEW)

@@ -50,6 +50,9 @@ def test_grad_set_sizes_that_overflow_are_refused():
     for n in ((1 << 62) + 16, (1 << 63) - 1, ddp.MAX_NUMEL + 1):
         assert L.ddp_grad_set_workspace_bytes(1, 1, _i64(n), 0, ctypes.byref(out)) == -5
         assert L.ddp_sync_norm_workspace_bytes(1, 1, _i64(n), 0, ctypes.byref(out)) == -5
+    for sizes in ([ddp.MAX_NUMEL, 1], [ddp.MAX_NUMEL] * 3):      # one rank's elements together
+        assert L.ddp_grad_set_workspace_bytes(1, len(sizes), _i64(*sizes), 0, ctypes.byref(out)) == -5
+        assert L.ddp_sync_norm_workspace_bytes(1, len(sizes), _i64(*sizes), 0, ctypes.byref(out)) == -5
     assert out.value == -1
     assert L.ddp_grad_set_workspace_bytes(1, 1, None, 0, ctypes.byref(out)) == -1
     assert L.ddp_grad_set_workspace_bytes(1, -1, _i64(1), 0, ctypes.byref(out)) == -1
