@@ -168,15 +168,21 @@ def dtype_code(t) -> int:
     raise TypeError(f"unsupported dtype {t.dtype}: float32 or bfloat16")
 
 
+_raw_stream = None          # () -> the current stream's handle, once CUDA is initialised
+
+
 def _stream(stream) -> int:
-    torch = _torch()
+    global _raw_stream
     if stream is None:
-        # the same handle as current_stream().cuda_stream, without making a
-        # Stream object (2.9 us of a call on a Grace host)
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if raw is not None and torch.cuda.is_initialized():
-            return raw(torch.cuda.current_device())
-        return torch.cuda.current_stream().cuda_stream
+        if _raw_stream is not None:
+            return _raw_stream()
+        torch = _torch()
+        handle = torch.cuda.current_stream().cuda_stream
+        # the same handle without making a Stream object (2.9 us of a call on a Grace host)
+        raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+        if raw is not None and device is not None:
+            _raw_stream = lambda: raw(device())
+        return handle
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -709,7 +715,7 @@ class GradSet:
         self._own = self.norms.data_ptr()
 
     def _norms(self, t):
-        return self._own if t is None else _rank_words(t, self.world, _torch().float32, "norms")
+        return self._own if t is None else _rank_words(t, self.world, self.norms.dtype, "norms")
 
     def norm(self, out=None, stream=None):
         """norms[r] of every rank, into `out` or self.norms; returns that tensor."""
@@ -817,12 +823,13 @@ class AdamW:
                                       _i64_array(sizes), mask, word, self._workspace.data_ptr(), ctypes.byref(h)))
         self._h = h
         self._lib = lib()
+        self._f32 = torch.float32
 
     def step(self, lr: float, betas: Tuple[float, float] = (0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.0,
              norms=None, max_norm: float = 0.0, stream=None) -> None:
         """One step.  norms ([world], as GradSet.norm or SyncNormCall return):
         clip to max_norm, and skip a rank whose norm is not finite."""
-        n = None if norms is None else _rank_words(norms, self.world, _torch().float32, "norms")
+        n = None if norms is None else _rank_words(norms, self.world, self._f32, "norms")
         _check("ddp_adamw_step",
                self._lib.ddp_adamw_step(self._h, lr, betas[0], betas[1], eps, weight_decay, n, max_norm, _stream(stream)))
 

@@ -121,12 +121,13 @@ __device__ __forceinline__ uintptr_t tile_base(const RangeTab<CAP>& b, int i, in
            (uintptr_t)(tile - b.range[i].first) * TILE;
 }
 
-// The vector at address a, zeros where it lies outside [p, end).
+// The vector at address a, zeros where it lies outside [p, end).  A plain load,
+// not a streaming one: a clip that follows finds the gradients' end in L2.
 template <class E>
 __device__ __forceinline__ typename E::V load_inside(uintptr_t a, uintptr_t p, uintptr_t end) {
     using V = typename E::V;
     using S = typename E::S;
-    if (a >= p && a + 16 <= end) return ld_stream<V>(reinterpret_cast<const void*>(a));
+    if (a >= p && a + 16 <= end) return *reinterpret_cast<const V*>(a);
     V v = make_zero<V>();
     if (a < end && a + 16 > p) {
         S* s = reinterpret_cast<S*>(&v);
@@ -169,24 +170,23 @@ __device__ __forceinline__ void load_tile(typename E::V (&x)[kNormVecs], int t, 
     for (int u = 0; u < kNormVecs; ++u) x[u] = load_inside<E>(base + (u * T + t) * 16, p, end);
 }
 
-// A thread's part of a tile's sum of squares.  Where it leaves binary32's range
-// and the values are not all zeros, they are loaded once more and squared in
-// binary64: keeping them would cost every tile the registers.
+// Thread t's part of a tile's sum of squares.  Where it leaves binary32's range
+// and the values are not all zeros, they are loaded once more and squared
+// scaled: keeping them for that would cost every tile registers.
 template <class E, int T>
 __device__ __forceinline__ double tile_squares(const typename E::V (&x)[kNormVecs], int t, uintptr_t base, uintptr_t p,
                                                uintptr_t end) {
     const float s = sum_squares<E>(x);
     if (in_square_range(s)) return (double)s;
-    double d = 0.0;
-    if (magnitude_bits<E>(x) != 0) {
+    if (magnitude_bits<E>(x) == 0) return 0.0;
+    WideSquares w[2];
 #pragma unroll 1
-        for (int u = 0; u < kNormVecs; ++u) {
-            const typename E::V v = load_inside<E>(base + (u * T + t) * 16, p, end);
+    for (int u = 0; u < kNormVecs; ++u) {
+        const typename E::V v = load_inside<E>(base + (u * T + t) * 16, p, end);
 #pragma unroll
-            for (int l = 0; l < E::L; ++l) d = fma((double)f32_of(v, l), (double)f32_of(v, l), d);
-        }
+        for (int l = 0; l < E::L; ++l) w[l & 1].add(f32_of(v, l));
     }
-    return d;
+    return total(w[0], w[1]);
 }
 
 // HBM bounds it: one read of every gradient.  A thread adds a tile's squares in
@@ -221,6 +221,32 @@ __global__ void __launch_bounds__(kThreads, 8) k_norm_partials(const __grid_cons
     finish_norms<kThreads>(finish, partials, scratch.d);
 }
 
+// The first block of a cluster takes the others' values in its shared memory:
+// once it runs (each block arrives when it starts, and waits for all before it
+// writes), and it reads them, or ends, after sync().  Without a cluster a block
+// writes to its own.
+template <bool CLUSTER>
+struct ClusterStart {
+    bool waited = false;
+    __device__ __forceinline__ ClusterStart() {
+        if constexpr (CLUSTER) asm volatile("barrier.cluster.arrive;" ::: "memory");
+    }
+    __device__ __forceinline__ void wait() {
+        if constexpr (CLUSTER) {
+            if (!waited) asm volatile("barrier.cluster.wait;" ::: "memory");
+            waited = true;
+        }
+    }
+    template <class T>
+    __device__ __forceinline__ T* in_first_block(T* p) const {
+        if constexpr (CLUSTER) return cooperative_groups::this_cluster().map_shared_rank(p, 0);
+        return p;
+    }
+    __device__ __forceinline__ void sync() const {
+        if constexpr (CLUSTER) cooperative_groups::this_cluster().sync();
+    }
+};
+
 // The norm of little data in one launch without partials: a cluster of
 // kSmallParts blocks a rank, each warp of it a 2 KB tile (or a few).  What a
 // call takes here is latency: the table's lines come from a cold constant cache
@@ -234,6 +260,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_small(const __grid_constant__
                                                          const __grid_constant__ NormFinish f) {
     __shared__ SquareScratch scratch;
     __shared__ double part[kSmallParts];
+    ClusterStart<CLUSTER> cluster;
     init_squares(scratch);
     AcquireOnce acquire;
     pdl_release();
@@ -264,13 +291,11 @@ __global__ void __launch_bounds__(kThreads) k_norm_small(const __grid_constant__
             }
             acquire();
             const double t = block_squares((float)d, d != 0.0, scratch, [&] { return d; });
-            if (threadIdx.x == 0) {
-                if constexpr (CLUSTER) cooperative_groups::this_cluster().map_shared_rank(part, 0)[c] = t;
-                else part[c] = t;
-            }
+            cluster.wait();
+            if (threadIdx.x == 0) *cluster.in_first_block(&part[c]) = t;
             __syncthreads();
         }
-        if constexpr (CLUSTER) cooperative_groups::this_cluster().sync();
+        cluster.sync();
         if (threadIdx.x == 0 && blockIdx.x % kPer == 0) {
             double t = part[0];
             for (int q = 1; q < kSmallParts; ++q) t += part[q];
@@ -297,6 +322,7 @@ __global__ void __launch_bounds__(kFinalThreads) k_norm_final(const double* part
                                                               float* norms, int ranks, int copies, int parts) {
     __shared__ double sh[kFinalThreads / 32];
     __shared__ double part[kFinalParts];
+    ClusterStart<CLUSTER> cluster;
     pdl_release();
     pdl_acquire();
     const int per = CLUSTER ? parts : 1;
@@ -311,13 +337,11 @@ __global__ void __launch_bounds__(kFinalThreads) k_norm_final(const double* part
                 for (int u = 0; u < 4; ++u) d[u] += partials[k + u * step];
             for (; k < end; k += step) d[0] += partials[k];
             const double t = block_sum(warp_sum((d[0] + d[1]) + (d[2] + d[3])), sh);
-            if (threadIdx.x == 0) {
-                if constexpr (CLUSTER) cooperative_groups::this_cluster().map_shared_rank(part, 0)[c] = t;
-                else part[c] = t;
-            }
+            cluster.wait();
+            if (threadIdx.x == 0) *cluster.in_first_block(&part[c]) = t;
             __syncthreads();
         }
-        if constexpr (CLUSTER) cooperative_groups::this_cluster().sync();
+        cluster.sync();
         if (threadIdx.x == 0 && blockIdx.x % per == 0) {
             double t = part[0];
             for (int q = 1; q < parts; ++q) t += part[q];
@@ -345,6 +369,9 @@ __device__ __forceinline__ uint4 scale_v(uint4 x, float c) {
     return make_uint4(scale_2(x.x, c), scale_2(x.y, c), scale_2(x.z, c), scale_2(x.w, c));
 }
 
+// HBM bounds it: one read and one write of every gradient.  From the last tile
+// to the first, so that the tiles a norm read last are taken from L2 (norm and
+// clip of 400 MB: 181 against 186 us).
 template <class E, int CAP>
 __global__ void __launch_bounds__(kThreads) k_clip(const __grid_constant__ RangeTab<CAP> b, const float* norms, float max_norm) {
     using V = typename E::V;
@@ -352,8 +379,9 @@ __global__ void __launch_bounds__(kThreads) k_clip(const __grid_constant__ Range
     __shared__ int slot;
     AcquireOnce acquire;
     pdl_release();
-    for (int tile = blockIdx.x; tile < b.tiles; tile += gridDim.x) {
-        if (tile != (int)blockIdx.x) __syncthreads();          // slot is free for this tile
+    for (int k = blockIdx.x; k < b.tiles; k += gridDim.x) {
+        if (k != (int)blockIdx.x) __syncthreads();             // slot is free for this tile
+        const int tile = b.tiles - 1 - k;
         const int i = block_first_past(b.tile_end, b.n, tile, &slot);
         const uintptr_t base = tile_base(b, i, tile);
         acquire();

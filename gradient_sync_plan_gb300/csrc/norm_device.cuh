@@ -6,8 +6,8 @@
 // that on average.  Everything beyond a tile is added in binary64.  A square
 // leaves binary32's range long before its value does (2^-75 squares to nothing,
 // 2^64 to infinity), so a tile with a warp whose sum falls outside
-// [2^-90, 2^112] squares again in binary64, from registers or memory that still
-// hold the values.  Inside that range what underflow took is below 2^-136 a
+// [2^-90, 2^112] squares again with scaled values, from registers or memory that
+// still hold them.  Inside that range what underflow took is below 2^-136 a
 // warp, nothing next to 2^-90, and 32 warps' sums stay finite.
 #pragma once
 
@@ -76,6 +76,24 @@ struct AcquireOnce {
         done = true;
     }
 };
+
+// A sum of squares of any binary32 values, in binary32 but for its end: the
+// large and the small ones are scaled by a power of two before they are squared
+// (2^-100 and 2^100: every finite value's square is then in range) and added
+// apart.  An infinity or a NaN comes out as one.
+struct WideSquares {
+    float low = 0.f, mid = 0.f, high = 0.f;
+    __device__ __forceinline__ void add(float f) {
+        const float a = fabsf(f);
+        if (a > 0x1p40f) high = fmaf(f * 0x1p-100f, f * 0x1p-100f, high);
+        else if (a < 0x1p-40f) low = fmaf(f * 0x1p100f, f * 0x1p100f, low);
+        else mid = fmaf(f, f, mid);
+    }
+};
+// Two of them (half the chain each) together.
+__device__ __forceinline__ double total(const WideSquares& a, const WideSquares& b) {
+    return (double)(a.low + b.low) * 0x1p-200 + ((double)(a.mid + b.mid) + (double)(a.high + b.high) * 0x1p200);
+}
 
 // One value a warp -> their sum in every lane of warp 0 (undefined elsewhere).
 // `sh` has a slot a warp; the caller puts a barrier between two uses.

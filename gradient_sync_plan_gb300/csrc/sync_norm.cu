@@ -71,8 +71,8 @@ __device__ __forceinline__ typename E::S average_s(typename E::S y, int mode, fl
     if (mode == kDivIeee) return E::template sdiv<kDivIeee>(y, op);
     return E::template sdiv<kDivNone>(y, op);
 }
-__device__ __forceinline__ double square(float f) { return (double)f * (double)f; }
-__device__ __forceinline__ double square(uint16_t h) { return square(bf16_to_f32(h)); }
+__device__ __forceinline__ float f32_of(float f) { return f; }
+__device__ __forceinline__ float f32_of(uint16_t h) { return bf16_to_f32(h); }
 
 __device__ __forceinline__ float sum_squares(float4 y) {
     return fmaf(y.x, y.x, y.y * y.y) + fmaf(y.z, y.z, y.w * y.w);
@@ -173,10 +173,13 @@ __global__ void __launch_bounds__(kThreads, MINB) k_sync_norm(const __grid_const
         }
         const double t = block_squares(s, bits != 0, scratch, [&] {          // from what the block wrote to rank 0
             const S* mine = reinterpret_cast<const S*>(pp[0]) + e0;
-            double d = 0.0;
+            WideSquares w[2];
 #pragma unroll 1
-            for (int e = head + (int)threadIdx.x; e < tail; e += kThreads) d += square(mine[e]);
-            return d;
+            for (int e = head + (int)threadIdx.x; e < tail; e += 2 * kThreads) {
+                w[0].add(f32_of(mine[e]));
+                if (e + kThreads < tail) w[1].add(f32_of(mine[e + kThreads]));
+            }
+            return total(w[0], w[1]);
         });
         if (threadIdx.x == 0) partials[tile] = t;
         __syncthreads();                         // scratch and slot are free for the next tile

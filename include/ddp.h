@@ -631,10 +631,10 @@ int32_t ddp_bucket_allreduce_view_fp16(int32_t world, int32_t n_in_bucket, void*
  *
  *   ddp_grad_norm       norms[r] = sqrt(sum of g^2 over every element of rank
  *                       r's tensors).  Squares are added in binary32 within a
- *                       warp's few thousand and in binary64 beyond it; where a
- *                       square would leave binary32's range it is taken in
- *                       binary64, so that a norm is right whenever it is itself
- *                       a binary32 number.  An infinity or NaN among the
+ *                       tile of a few thousand and in binary64 beyond it; values
+ *                       whose squares would leave binary32's range are scaled
+ *                       first, so that a norm is right whenever it is itself a
+ *                       binary32 number.  An infinity or NaN among the
  *                       gradients makes the norm one.  No elements: 0.
  *                       The additions' order depends on the tensors' sizes and
  *                       addresses only: neither ddp_set_max_ctas nor a repeat

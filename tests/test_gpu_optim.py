@@ -1,9 +1,10 @@
 """Gradient norm, clipping, norm-in-sync and AdamW on the GPU against float64.
 
 Tolerances, from the roundings on the way (u = 2^-24, binary32's unit roundoff):
-  norm    a chain of at most 8 squares, 2 adds and 5 shuffles a warp, all terms
-          positive: 15 u on the sum, half on its root, one rounding to binary32:
-          below 9 u.  16 u allowed.
+  norm    positive terms, added as a tree: a thread's chains of at most 12
+          squares (16 of scaled ones, where squares leave binary32's range), 3
+          additions of its own and 10 in the block: below 30 u on the sum, half
+          on its root, one rounding to binary32.  16 u allowed.
   clip    c: one add, one quotient; the product: 3 u, and the constant 1e-6's
           own rounding; 4 u allowed, for bf16 one rounding of 2^-8 on top.
   AdamW   m: 6 u of the sum of its two terms' sizes (they may cancel); v: 16 u
