@@ -544,3 +544,16 @@ def test_a_training_step_end_to_end():
         for i in range(len(numels)):
             assert torch.equal(p[r][i], p[0][i])
             assert float((p[r][i].double() - ref[0][i]).abs().max()) < 1e-6
+
+
+def test_the_example_trains_and_its_ranks_agree():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "train_step.py")
+    spec = importlib.util.spec_from_file_location("train_step", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    losses, norms, params = example.train(ranks=3, steps=60)
+    assert losses[-1] < 0.5 * losses[0] and all(math.isfinite(n) and n > 0 for n in norms)
+    for row in params[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(row, params[0]))
