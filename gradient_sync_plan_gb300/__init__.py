@@ -52,7 +52,7 @@ EXPORTS = ["ddp_status_string", "ddp_abi_version", "ddp_last_cuda_error", "ddp_d
            "ddp_reducer_launch_order", "ddp_reducer_bucket_times", "ddp_reducer_destroy",
            "ddp_grad_set_workspace_bytes", "ddp_grad_set_create", "ddp_grad_norm", "ddp_grad_clip", "ddp_grad_norm_clip",
            "ddp_grad_set_destroy", "ddp_sync_norm_workspace_bytes", "ddp_sync_norm_create", "ddp_sync_norm_run",
-           "ddp_sync_norm_destroy", "ddp_adamw_create", "ddp_adamw_step", "ddp_adamw_destroy"]
+           "ddp_sync_norm_destroy", "ddp_adamw_workspace_bytes", "ddp_adamw_create", "ddp_adamw_step", "ddp_adamw_destroy"]
 
 
 class DDPError(RuntimeError):
@@ -133,7 +133,9 @@ def lib() -> ctypes.CDLL:
                                                i32, vp, i64, P(vp)]
             L.ddp_sync_norm_run.argtypes = [vp, vp, vp]
             L.ddp_sync_norm_destroy.argtypes = [vp]
-            L.ddp_adamw_create.argtypes = [i32, i32, P(vp), P(vp), i32, P(vp), P(vp), P(vp), P(i64), P(u8), vp, vp, P(vp)]
+            L.ddp_adamw_workspace_bytes.argtypes = [i32, i32, P(i64)]
+            L.ddp_adamw_create.argtypes = [i32, i32, P(vp), P(vp), i32, P(vp), P(vp), P(vp), P(i64), P(u8), vp, vp, i64,
+                                           P(vp)]
             L.ddp_adamw_step.argtypes = [vp, f64, f64, f64, f64, f64, vp, f64, vp]
             L.ddp_adamw_destroy.argtypes = [vp]
             for name in EXPORTS[4:]:   # every entry point from ddp_set_max_ctas on returns a status
@@ -749,6 +751,7 @@ class SyncNormCall(SyncCall):
     arguments are checked and laid out once; each call is one ctypes call."""
 
     def __init__(self, grads, plan, buckets=None, divisor=None, algo=DDP_ALGO_VIEW):
+        _tensor_table(grads, "gradients", (_torch().float32, _torch().bfloat16))     # one size a tensor at every rank
         super().__init__(grads, plan, buckets, divisor, algo)
         torch = _torch()
         need = ctypes.c_int64(0)
@@ -814,13 +817,17 @@ class AdamW:
         device = params[0][0].device if sizes else "cuda"
         self.steps = torch.zeros(self.world, dtype=torch.int32, device=device) if steps is None else steps
         word = _rank_words(self.steps, self.world, torch.int32, "steps")
-        self._workspace = torch.empty(2, dtype=torch.float64, device=device)       # DDP_ADAMW_WORKSPACE_BYTES
+        need = ctypes.c_int64(0)
+        _check("ddp_adamw_workspace_bytes",
+               lib().ddp_adamw_workspace_bytes(self.world, len(sizes), ctypes.byref(need)))
+        self._workspace = torch.empty(need.value // 8, dtype=torch.float64, device=device)
         self._keep = (params, grads, exp_avg, exp_avg_sq, copies)
         h = ctypes.c_void_p()
         _check("ddp_adamw_create",
                lib().ddp_adamw_create(self.world, len(sizes), _vp_array(pp), _vp_array(gp),
                                       BF16 if gdt == torch.bfloat16 else F32, _vp_array(mp), _vp_array(vp), cp,
-                                      _i64_array(sizes), mask, word, self._workspace.data_ptr(), ctypes.byref(h)))
+                                      _i64_array(sizes), mask, word, self._workspace.data_ptr(), need.value,
+                                      ctypes.byref(h)))
         self._h = h
         self._lib = lib()
         self._f32 = torch.float32

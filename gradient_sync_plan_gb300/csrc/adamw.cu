@@ -25,23 +25,33 @@ namespace ddpk {
 // Elements of a tile in which a thread takes `vecs` groups of 4.
 constexpr int64_t adamw_tile(int vecs) { return (int64_t)kThreads * 4 * vecs; }
 
+struct Item {                  // side by side: a block finds one line of a cold constant cache, not one a field
+    float* p;
+    float* m;
+    float* v;
+    const void* g;
+    void* copy;
+    int64_t numel;
+    int32_t first;             // its first tile
+    int16_t rank;
+    uint8_t lead;              // elements between the 128-byte boundary before p and p: where tiles are cut
+    uint8_t flags;             // 1: aligned groups of 4 line up in every array, 2: weight decay
+};
+static_assert(sizeof(Item) == kAdamWEntry, "the workspace counts on it");
+
 template <int CAP>
 struct AdamWTab {
+    static constexpr bool kDevice = false;
     int32_t n;
     int32_t tiles;
     int32_t tile_end[CAP];     // inclusive prefix of tiles
-    struct Item {              // side by side: a block finds one line of a cold constant cache, not one a field
-        float* p;
-        float* m;
-        float* v;
-        const void* g;
-        void* copy;
-        int64_t numel;
-        int32_t first;         // its first tile
-        int16_t rank;
-        uint8_t lead;          // elements between the 128-byte boundary before p and p: where tiles are cut
-        uint8_t flags;         // 1: aligned groups of 4 line up in every array, 2: weight decay
-    } item[CAP];
+    Item item[CAP];
+};
+struct AdamWDev {              // the same in device memory
+    static constexpr bool kDevice = true;
+    int32_t n, tiles;
+    const int32_t* tile_end;
+    const Item* item;
 };
 constexpr int kAdamSmall = 32;
 constexpr int kAdamMedium = 176;
@@ -101,8 +111,8 @@ template <> struct GradVec<uint16_t> {
 };
 
 // One element, through memory.
-template <class G, bool COPY, int CAP>
-__device__ __forceinline__ void update_one(const AdamWTab<CAP>& b, int i, int64_t e, const AdamWScalars& s,
+template <class G, bool COPY, class TAB>
+__device__ __forceinline__ void update_one(const TAB& b, int i, int64_t e, const AdamWScalars& s,
                                            const RankStep& q, float lr_decay) {
     float p = b.item[i].p[e], m = b.item[i].m[e], v = b.item[i].v[e];
     update(p, m, v, GradVec<G>::one(b.item[i].g, e), s, q, lr_decay);
@@ -127,8 +137,8 @@ __global__ void __launch_bounds__(kThreads) k_adamw_advance(const float* norms, 
 }
 
 // V: groups of 4 elements a thread takes.
-template <class G, bool COPY, int V, int CAP>
-__global__ void __launch_bounds__(kThreads, V == 1 ? 4 : 3) k_adamw(const __grid_constant__ AdamWTab<CAP> b,
+template <class G, bool COPY, int V, class TAB>
+__global__ void __launch_bounds__(kThreads, V == 1 ? 4 : 3) k_adamw(const __grid_constant__ TAB b,
                                                     const __grid_constant__ AdamWScalars s, const float* norms,
                                                     int32_t* steps, int32_t* arrivals, int world) {
     constexpr int64_t kTile = adamw_tile(V);
@@ -136,6 +146,7 @@ __global__ void __launch_bounds__(kThreads, V == 1 ? 4 : 3) k_adamw(const __grid
     __shared__ int slot;
     AcquireOnce acquire;
     pdl_release();
+    if constexpr (TAB::kDevice) acquire();
     for (int tile = blockIdx.x; tile < b.tiles; tile += gridDim.x) {
         const int i = block_first_past(b.tile_end, b.n, tile, &slot);
         const int64_t n = b.item[i].numel;
@@ -210,32 +221,45 @@ struct AdamWPlan {
     std::vector<AdamWTab<kAdamSmall>> small;
     std::vector<AdamWTab<kAdamMedium>> medium;
     std::vector<AdamWTab<kAdamLarge>> large;
+    DeviceTable device;                          // more items than one launch's table takes, for little data
+    AdamWDev dev{};                              // with offsets for addresses
 };
 
-template <int CAP>
-static void fill_tables(const AdamWItem* items, int64_t n, int64_t plan_tile, int grad_dtype, bool copies,
-                        std::vector<AdamWTab<CAP>>* out) {
+const DeviceTable* adamw_plan_table(const AdamWPlan& plan) { return plan.device.image.empty() ? nullptr : &plan.device; }
+
+static Item item_of(const AdamWItem& it, int32_t first, int grad_dtype, bool copies) {
     const uintptr_t gs = (uintptr_t)elem_bytes(grad_dtype);
+    const int64_t lead = lead_of(it);
+    const uintptr_t q = (uintptr_t)lead % 4;
+    const bool vec = reinterpret_cast<uintptr_t>(it.m) % 16 == 4 * q && reinterpret_cast<uintptr_t>(it.v) % 16 == 4 * q &&
+                     reinterpret_cast<uintptr_t>(it.g) % (4 * gs) == gs * q &&
+                     (!copies || reinterpret_cast<uintptr_t>(it.copy) % 8 == 2 * q);
+    return Item{it.p, it.m, it.v, it.g, it.copy, it.numel, first, (int16_t)it.rank, (uint8_t)lead,
+                (uint8_t)((vec ? 1 : 0) | (it.decay ? 2 : 0))};
+}
+
+// Items [i, n) as far as `most` goes into one table; returns where it stopped.
+template <class Ends, class Entries>
+static int64_t fill_table(const AdamWItem* items, int64_t i, int64_t n, int64_t most, int64_t tile, int grad_dtype,
+                          bool copies, Ends ends, Entries entries, int32_t* count, int32_t* tiles) {
+    *count = 0;
+    *tiles = 0;
+    for (; i < n && *count < most; ++i, ++*count) {
+        entries[*count] = item_of(items[i], *tiles, grad_dtype, copies);
+        *tiles += (int32_t)adamw_tiles(items[i], tile);
+        ends[*count] = *tiles;
+    }
+    return i;
+}
+
+template <int CAP>
+static void fill_tables(const AdamWItem* items, int64_t n, int64_t tile, int grad_dtype, bool copies,
+                        std::vector<AdamWTab<CAP>>* out) {
     int64_t i = 0;
     do {                                         // a call without elements still counts as a step
         out->emplace_back();
         AdamWTab<CAP>& b = out->back();
-        b.n = 0;
-        b.tiles = 0;
-        for (; i < n && b.n < CAP; ++i, ++b.n) {
-            const AdamWItem& it = items[i];
-            const int32_t first = b.tiles;
-            b.tiles += (int32_t)adamw_tiles(it, plan_tile);
-            b.tile_end[b.n] = b.tiles;
-            const int64_t lead = lead_of(it);
-            const uintptr_t q = (uintptr_t)lead % 4;
-            const bool vec = reinterpret_cast<uintptr_t>(it.m) % 16 == 4 * q &&
-                             reinterpret_cast<uintptr_t>(it.v) % 16 == 4 * q &&
-                             reinterpret_cast<uintptr_t>(it.g) % (4 * gs) == gs * q &&
-                             (!copies || reinterpret_cast<uintptr_t>(it.copy) % 8 == 2 * q);
-            b.item[b.n] = {it.p, it.m, it.v, it.g, it.copy, it.numel, first, (int16_t)it.rank, (uint8_t)lead,
-                           (uint8_t)((vec ? 1 : 0) | (it.decay ? 2 : 0))};
-        }
+        i = fill_table(items, i, n, CAP, tile, grad_dtype, copies, b.tile_end, b.item, &b.n, &b.tiles);
     } while (i < n);
 }
 
@@ -249,45 +273,65 @@ std::shared_ptr<const AdamWPlan> make_adamw_plan(const AdamWItem* items, int64_t
     const int64_t tile = adamw_tile(plan->vecs);
     if (n <= kAdamSmall) fill_tables(items, n, tile, grad_dtype, copies, &plan->small);
     else if (n <= kAdamMedium) fill_tables(items, n, tile, grad_dtype, copies, &plan->medium);
-    else fill_tables(items, n, tile, grad_dtype, copies, &plan->large);
+    else if (table_on_device((n + kAdamLarge - 1) / kAdamLarge, numel * (24 + elem_bytes(grad_dtype) + (copies ? 2 : 0)))) {
+        DeviceTable& t = plan->device;
+        t.entries_at = (4 * n + 15) / 16 * 16;
+        t.image.assign((size_t)(t.entries_at + (n * kAdamWEntry + 15) / 16 * 16), 0);
+        fill_table(items, 0, n, n, tile, grad_dtype, copies, reinterpret_cast<int32_t*>(t.image.data()),
+                   reinterpret_cast<Item*>(t.image.data() + t.entries_at), &plan->dev.n, &plan->dev.tiles);
+    } else fill_tables(items, n, tile, grad_dtype, copies, &plan->large);
     return plan;
 }
 
-template <class G, bool COPY, int V, int CAP>
-static cudaError_t adamw_tables(const std::vector<AdamWTab<CAP>>& tables, int world, const AdamWScalars& s,
-                                const float* norms, int32_t* steps, int32_t* arrivals, cudaStream_t st) {
-    const bool one = tables.size() == 1 && tables[0].tiles <= kAdamArriveTiles;
+template <class G, bool COPY, int V, class TAB>
+static cudaError_t adamw_table(const TAB& b, int world, const AdamWScalars& s, const float* norms, int32_t* steps,
+                               int32_t* arrivals, cudaStream_t st) {
+    return launch_table(k_adamw<G, COPY, V, TAB>, dim3(cap_ctas(b.tiles)), dim3(kThreads), st, b, s, norms, steps, arrivals,
+                        world);
+}
+
+// `one` launch of few tiles advances the counts itself.
+template <class G, bool COPY, int V, class TAB>
+static cudaError_t adamw_tables(const TAB* tables, size_t n, int world, const AdamWScalars& s, const float* norms,
+                                int32_t* steps, int32_t* arrivals, cudaStream_t st) {
+    const bool one = n == 1 && tables[0].tiles <= kAdamArriveTiles;
     int32_t* const count = one ? arrivals : nullptr;
-    for (const AdamWTab<CAP>& b : tables) {
-        const cudaError_t e = launch_table(k_adamw<G, COPY, V, CAP>, dim3(cap_ctas(b.tiles)), dim3(kThreads), st, b, s, norms,
-                                           steps, count, world);
+    for (size_t k = 0; k < n; ++k) {
+        const cudaError_t e = adamw_table<G, COPY, V>(tables[k], world, s, norms, steps, count, st);
         if (e != cudaSuccess) return e;
     }
     return one ? cudaSuccess : launch_table(k_adamw_advance, dim3(1), dim3(kThreads), st, norms, steps, world);
 }
 
 template <class G, bool COPY, int V>
-static cudaError_t adamw_size(const AdamWPlan& p, int world, const AdamWScalars& s, const float* norms, int32_t* steps,
-                         int32_t* arrivals, cudaStream_t st) {
-    if (!p.small.empty()) return adamw_tables<G, COPY, V>(p.small, world, s, norms, steps, arrivals, st);
-    if (!p.medium.empty()) return adamw_tables<G, COPY, V>(p.medium, world, s, norms, steps, arrivals, st);
-    return adamw_tables<G, COPY, V>(p.large, world, s, norms, steps, arrivals, st);
+static cudaError_t adamw_size(const AdamWPlan& p, const char* table, int world, const AdamWScalars& s, const float* norms,
+                              int32_t* steps, int32_t* arrivals, cudaStream_t st) {
+    auto run = [&](const auto& t) {
+        return adamw_tables<G, COPY, V>(t.data(), t.size(), world, s, norms, steps, arrivals, st);
+    };
+    if (!p.small.empty()) return run(p.small);
+    if (!p.medium.empty()) return run(p.medium);
+    if (!p.large.empty()) return run(p.large);
+    AdamWDev d = p.dev;
+    d.tile_end = reinterpret_cast<const int32_t*>(table);
+    d.item = reinterpret_cast<const Item*>(table + p.device.entries_at);
+    return adamw_tables<G, COPY, V>(&d, 1, world, s, norms, steps, arrivals, st);
 }
 
 template <class G, bool COPY>
-static cudaError_t adamw(const AdamWPlan& p, int world, const AdamWScalars& s, const float* norms, int32_t* steps,
-                         int32_t* arrivals, cudaStream_t st) {
-    return p.vecs == 1 ? adamw_size<G, COPY, 1>(p, world, s, norms, steps, arrivals, st)
-                       : adamw_size<G, COPY, 2>(p, world, s, norms, steps, arrivals, st);
+static cudaError_t adamw(const AdamWPlan& p, const char* table, int world, const AdamWScalars& s, const float* norms,
+                         int32_t* steps, int32_t* arrivals, cudaStream_t st) {
+    return p.vecs == 1 ? adamw_size<G, COPY, 1>(p, table, world, s, norms, steps, arrivals, st)
+                       : adamw_size<G, COPY, 2>(p, table, world, s, norms, steps, arrivals, st);
 }
 
-cudaError_t launch_adamw(const AdamWPlan& p, int world, int grad_dtype, bool copies, const AdamWScalars& s,
-                         const float* norms, int32_t* steps, int32_t* arrivals, cudaStream_t st) {
+cudaError_t launch_adamw(const AdamWPlan& p, const char* table, int world, int grad_dtype, bool copies,
+                         const AdamWScalars& s, const float* norms, int32_t* steps, int32_t* arrivals, cudaStream_t st) {
     if (grad_dtype == DDP_BF16)
-        return copies ? adamw<uint16_t, true>(p, world, s, norms, steps, arrivals, st)
-                      : adamw<uint16_t, false>(p, world, s, norms, steps, arrivals, st);
-    return copies ? adamw<float, true>(p, world, s, norms, steps, arrivals, st)
-                  : adamw<float, false>(p, world, s, norms, steps, arrivals, st);
+        return copies ? adamw<uint16_t, true>(p, table, world, s, norms, steps, arrivals, st)
+                      : adamw<uint16_t, false>(p, table, world, s, norms, steps, arrivals, st);
+    return copies ? adamw<float, true>(p, table, world, s, norms, steps, arrivals, st)
+                  : adamw<float, false>(p, table, world, s, norms, steps, arrivals, st);
 }
 
 }  // namespace ddpk

@@ -20,18 +20,28 @@
 
 namespace ddpk {
 
+struct Range {                 // side by side: a block finds one line of a cold constant cache, not one a field
+    char* ptr;
+    int64_t bytes;
+    int32_t first;             // its first tile
+    int32_t rank;
+};
+static_assert(sizeof(Range) == kRangeEntry, "the workspace counts on it");
+
 template <int CAP>
 struct RangeTab {
+    static constexpr bool kDevice = false;
     int32_t n;
     int32_t tiles;             // a multiple of `run`
     int32_t run;               // tiles a norm block takes: never of two ranks
     int32_t tile_end[CAP];     // inclusive prefix of tiles; a rank's last range has the padding to a whole run
-    struct Range {             // side by side: a block finds one line of a cold constant cache, not one a field
-        char* ptr;
-        int64_t bytes;
-        int32_t first;         // its first tile
-        int32_t rank;
-    } range[CAP];
+    Range range[CAP];
+};
+struct RangeDev {              // the same in device memory
+    static constexpr bool kDevice = true;
+    int32_t n, tiles, run;
+    const int32_t* tile_end;
+    const Range* range;
 };
 // Capacities: a launch's parameters are copied for every eager launch.
 constexpr int kNormVecs = (int)(kNormTile / 16 / kThreads);      // vectors a thread takes of a tile
@@ -50,6 +60,9 @@ struct RangePlan {
     std::vector<RangeTab<kRangesLarge>> large;
     int32_t run = 1;
     std::vector<int32_t> rank_first;             // first partial of each rank, and their end
+    // more ranges than one launch's table takes, for little data
+    DeviceTable device;
+    RangeDev dev{};                              // with offsets for addresses
     // a few warp tiles a rank: what k_norm_small walks, and each rank's first
     std::vector<RangeTab<kRangesSmall>> tiny_small;
     std::vector<RangeTab<kRangesMedium>> tiny_medium;
@@ -61,30 +74,64 @@ static int64_t range_tiles(const GradRange& g, int64_t tile) {
     return (lead + g.bytes + tile - 1) / tile;
 }
 
+// Fills one table with ranges [i, n) as far as `most` goes; returns where it
+// stopped.  `rank` counts the ranks whose first partial is known.
+template <class Ends, class Entries>
+static int64_t fill_table(const GradRange* ranges, int64_t i, int64_t n, int64_t most, int64_t tile, int run,
+                          int64_t partials, int* rank, std::vector<int32_t>* rank_first, Ends ends, Entries entries,
+                          int32_t* count, int32_t* all_tiles) {
+    int64_t tiles = 0, k = 0;
+    for (; i < n && k < most; ++i, ++k) {
+        while (*rank < ranges[i].rank) (*rank_first)[++*rank] = (int32_t)(partials + tiles / run);
+        const int64_t first = tiles;
+        tiles += range_tiles(ranges[i], tile);
+        if (k + 1 == most || i + 1 == n || ranges[i + 1].rank != ranges[i].rank) tiles = (tiles + run - 1) / run * run;
+        ends[k] = (int32_t)tiles;
+        entries[k] = Range{ranges[i].ptr, ranges[i].bytes, (int32_t)first, ranges[i].rank};
+    }
+    *count = (int32_t)k;
+    *all_tiles = (int32_t)tiles;
+    return i;
+}
+
 template <int CAP>
 static void fill_tables(const GradRange* ranges, int64_t n, int ranks, int64_t tile, int run,
                         std::vector<RangeTab<CAP>>* out, std::vector<int32_t>* rank_first) {
     rank_first->assign(ranks + 1, 0);
     int64_t partials = 0;
-    int rank = 0;                                // ranks below it have their rank_first
+    int rank = 0;
     for (int64_t i = 0; i < n;) {
         out->emplace_back();
         RangeTab<CAP>& b = out->back();
-        b.n = 0;
         b.run = run;
-        int64_t tiles = 0;
-        for (; i < n && b.n < CAP; ++i, ++b.n) {
-            while (rank < ranges[i].rank) (*rank_first)[++rank] = (int32_t)(partials + tiles / run);
-            tiles += range_tiles(ranges[i], tile);
-            if (b.n + 1 == CAP || i + 1 == n || ranges[i + 1].rank != ranges[i].rank)
-                tiles = (tiles + run - 1) / run * run;
-            b.tile_end[b.n] = (int32_t)tiles;
-            b.range[b.n] = {ranges[i].ptr, ranges[i].bytes, b.n ? b.tile_end[b.n - 1] : 0, ranges[i].rank};
-        }
-        b.tiles = (int32_t)tiles;
-        partials += tiles / run;
+        i = fill_table(ranges, i, n, CAP, tile, run, partials, &rank, rank_first, b.tile_end, b.range, &b.n, &b.tiles);
+        partials += b.tiles / run;
     }
     while (rank < ranks) (*rank_first)[++rank] = (int32_t)partials;
+}
+
+static void fill_device(const GradRange* ranges, int64_t n, int ranks, RangePlan* plan) {
+    DeviceTable& t = plan->device;
+    t.entries_at = (4 * n + 15) / 16 * 16;
+    t.image.assign((size_t)(t.entries_at + (n * kRangeEntry + 15) / 16 * 16), 0);
+    plan->rank_first.assign(ranks + 1, 0);
+    int rank = 0;
+    plan->dev.run = plan->run;
+    fill_table(ranges, 0, n, n, kNormTile, plan->run, 0, &rank, &plan->rank_first,
+               reinterpret_cast<int32_t*>(t.image.data()), reinterpret_cast<Range*>(t.image.data() + t.entries_at),
+               &plan->dev.n, &plan->dev.tiles);
+    while (rank < ranks) plan->rank_first[++rank] = plan->dev.tiles / plan->run;
+}
+
+const DeviceTable* range_plan_table(const RangePlan& plan) {
+    return plan.device.image.empty() ? nullptr : &plan.device;
+}
+
+static RangeDev device_ranges(const RangePlan& plan, const char* table) {
+    RangeDev d = plan.dev;
+    d.tile_end = reinterpret_cast<const int32_t*>(table);
+    d.range = reinterpret_cast<const Range*>(table + plan.device.entries_at);
+    return d;
 }
 
 std::shared_ptr<const RangePlan> make_range_plan(const GradRange* ranges, int64_t n, int ranks) {
@@ -103,7 +150,12 @@ std::shared_ptr<const RangePlan> make_range_plan(const GradRange* ranges, int64_
     if (plan->cap == kRangesSmall) fill_tables(ranges, n, ranks, kNormTile, plan->run, &plan->small, &plan->rank_first);
     else if (plan->cap == kRangesMedium)
         fill_tables(ranges, n, ranks, kNormTile, plan->run, &plan->medium, &plan->rank_first);
-    else fill_tables(ranges, n, ranks, kNormTile, plan->run, &plan->large, &plan->rank_first);
+    else {
+        int64_t bytes = 0;
+        for (int64_t i = 0; i < n; ++i) bytes += ranges[i].bytes;
+        if (table_on_device((n + kRangesLarge - 1) / kRangesLarge, bytes)) fill_device(ranges, n, ranks, plan.get());
+        else fill_tables(ranges, n, ranks, kNormTile, plan->run, &plan->large, &plan->rank_first);
+    }
     if (n > 0 && plan->cap != kRangesLarge && ranks <= kFinishRanks &&
         *std::max_element(warp_tiles.begin(), warp_tiles.end()) <= kSmallTiles) {
         if (plan->cap == kRangesSmall) fill_tables(ranges, n, ranks, kWarpTile, 1, &plan->tiny_small, &plan->tiny_first);
@@ -112,11 +164,37 @@ std::shared_ptr<const RangePlan> make_range_plan(const GradRange* ranges, int64_
     return plan;
 }
 
-int64_t range_plan_partials(const RangePlan& plan) { return plan.rank_first.back(); }
+// Writes a chunk of a table, which is a parameter, to device memory: unlike a
+// copy from host memory it can be captured, and nothing of the host has to
+// outlive the call.
+struct TableChunk {
+    int32_t vectors;
+    uint4 data[2040];
+};
+static_assert(sizeof(TableChunk) + 16 <= kMaxParamBytes, "table chunk exceeds the kernel parameter limit");
+__global__ void __launch_bounds__(kThreads) k_upload_table(const __grid_constant__ TableChunk c, uint4* to) {
+    pdl_release();
+    pdl_acquire();
+    for (int i = threadIdx.x; i < c.vectors; i += kThreads) to[i] = c.data[i];
+}
+
+cudaError_t upload_table(const DeviceTable& t, void* device, cudaStream_t st) {
+    const int64_t all = (int64_t)t.image.size() / 16;
+    uint4* to = static_cast<uint4*>(device);
+    TableChunk c;
+    for (int64_t i = 0; i < all; i += 2040) {
+        c.vectors = (int32_t)std::min<int64_t>(2040, all - i);
+        std::copy_n(t.image.data() + 16 * i, 16 * (size_t)c.vectors, reinterpret_cast<char*>(c.data));
+        uint4* const at = to + i;
+        const cudaError_t e = launch_table(k_upload_table, dim3(1), dim3(kThreads), st, c, at);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
 
 // Where `tile`, which belongs to range i, starts in memory.
-template <int64_t TILE = kNormTile, int CAP>
-__device__ __forceinline__ uintptr_t tile_base(const RangeTab<CAP>& b, int i, int tile) {
+template <int64_t TILE = kNormTile, class TAB>
+__device__ __forceinline__ uintptr_t tile_base(const TAB& b, int i, int tile) {
     return (reinterpret_cast<uintptr_t>(b.range[i].ptr) & ~(uintptr_t)(kNormAlign - 1)) +
            (uintptr_t)(tile - b.range[i].first) * TILE;
 }
@@ -191,14 +269,15 @@ __device__ __forceinline__ double tile_squares(const typename E::V (&x)[kNormVec
 
 // HBM bounds it: one read of every gradient.  A thread adds a tile's squares in
 // binary32 and the tiles in binary64; the block joins its threads once a run.
-template <class E, int CAP>
-__global__ void __launch_bounds__(kThreads, 8) k_norm_partials(const __grid_constant__ RangeTab<CAP> b, double* partials,
+template <class E, class TAB>
+__global__ void __launch_bounds__(kThreads, 8) k_norm_partials(const __grid_constant__ TAB b, double* partials,
                                                             const __grid_constant__ NormFinish finish) {
     __shared__ SquareScratch scratch;
     __shared__ int slot;
     init_squares(scratch);
     AcquireOnce acquire;
     pdl_release();
+    if constexpr (TAB::kDevice) acquire();
     const int runs = b.tiles / b.run;
     for (int r = blockIdx.x; r < runs; r += gridDim.x) {
         int tile = r * b.run;
@@ -372,13 +451,14 @@ __device__ __forceinline__ uint4 scale_v(uint4 x, float c) {
 // HBM bounds it: one read and one write of every gradient.  From the last tile
 // to the first, so that the tiles a norm read last are taken from L2 (norm and
 // clip of 400 MB: 181 against 186 us).
-template <class E, int CAP>
-__global__ void __launch_bounds__(kThreads) k_clip(const __grid_constant__ RangeTab<CAP> b, const float* norms, float max_norm) {
+template <class E, class TAB>
+__global__ void __launch_bounds__(kThreads) k_clip(const __grid_constant__ TAB b, const float* norms, float max_norm) {
     using V = typename E::V;
     using S = typename E::S;
     __shared__ int slot;
     AcquireOnce acquire;
     pdl_release();
+    if constexpr (TAB::kDevice) acquire();
     for (int k = blockIdx.x; k < b.tiles; k += gridDim.x) {
         if (k != (int)blockIdx.x) __syncthreads();             // slot is free for this tile
         const int tile = b.tiles - 1 - k;
@@ -433,15 +513,18 @@ static cudaError_t norm_small(const RangeTab<CAP>& b, const NormFinish& f, cudaS
     return launch_table(k_norm_small<E, CAP, false>, dim3(cap_ctas(f.ranks)), dim3(kThreads), st, b, f);
 }
 
-template <class E, int CAP>
-static cudaError_t norm_tables(const std::vector<RangeTab<CAP>>& tables, double* partials, const NormFinish& finish,
+template <class E, class TAB>
+static cudaError_t norm_table(const TAB& b, double* partials, const NormFinish& finish, cudaStream_t st) {
+    return launch_table(k_norm_partials<E, TAB>, dim3(cap_ctas(b.tiles / b.run)), dim3(kThreads), st, b, partials, finish);
+}
+
+template <class E, class TAB>
+static cudaError_t norm_tables(const std::vector<TAB>& tables, double* partials, const NormFinish& finish,
                                cudaStream_t st) {
-    for (const RangeTab<CAP>& b : tables) {
-        const int runs = b.tiles / b.run;
-        const cudaError_t e = launch_table(k_norm_partials<E, CAP>, dim3(cap_ctas(runs)), dim3(kThreads), st, b, partials,
-                                           finish);
+    for (const TAB& b : tables) {
+        const cudaError_t e = norm_table<E>(b, partials, finish, st);
         if (e != cudaSuccess) return e;
-        partials += runs;
+        partials += b.tiles / b.run;
     }
     return cudaSuccess;
 }
@@ -455,10 +538,12 @@ static cudaError_t norm_kernels(const RangePlan& plan, NormSpace ws, int copies,
         if (plan.cap == kRangesSmall) return norm_small<E>(plan.tiny_small[0], f, st);
         return norm_small<E>(plan.tiny_medium[0], f, st);
     }
-    const size_t launches = plan.small.size() + plan.medium.size() + plan.large.size();
+    const bool device = !plan.device.image.empty();
+    const size_t launches = plan.small.size() + plan.medium.size() + plan.large.size() + (device ? 1 : 0);
     const NormFinish f = norm_finish(ws, first, ranks, copies, norms, launches == 1);
     cudaError_t e;
-    if (plan.cap == kRangesSmall) e = norm_tables<E>(plan.small, ws.partials, f, st);
+    if (device) e = norm_table<E>(device_ranges(plan, ws.table), ws.partials, f, st);
+    else if (plan.cap == kRangesSmall) e = norm_tables<E>(plan.small, ws.partials, f, st);
     else if (plan.cap == kRangesMedium) e = norm_tables<E>(plan.medium, ws.partials, f, st);
     else e = norm_tables<E>(plan.large, ws.partials, f, st);
     if (e != cudaSuccess || f.counter) return e;
@@ -484,25 +569,31 @@ cudaError_t launch_norm_final(const double* partials, const int32_t* rank_first,
                         copies, parts);
 }
 
-template <class E, int CAP>
-static cudaError_t clip_tables(const std::vector<RangeTab<CAP>>& tables, const float* norms, float max_norm,
-                               cudaStream_t st) {
-    for (const RangeTab<CAP>& b : tables) {
-        const cudaError_t e = launch_table(k_clip<E, CAP>, dim3(cap_ctas(b.tiles)), dim3(kThreads), st, b, norms, max_norm);
+template <class E, class TAB>
+static cudaError_t clip_table(const TAB& b, const float* norms, float max_norm, cudaStream_t st) {
+    return launch_table(k_clip<E, TAB>, dim3(cap_ctas(b.tiles)), dim3(kThreads), st, b, norms, max_norm);
+}
+
+template <class E, class TAB>
+static cudaError_t clip_tables(const std::vector<TAB>& tables, const float* norms, float max_norm, cudaStream_t st) {
+    for (const TAB& b : tables) {
+        const cudaError_t e = clip_table<E>(b, norms, max_norm, st);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
 }
 
 template <class E>
-static cudaError_t clip(const RangePlan& plan, const float* norms, float max_norm, cudaStream_t st) {
+static cudaError_t clip(const RangePlan& plan, NormSpace ws, const float* norms, float max_norm, cudaStream_t st) {
+    if (!plan.device.image.empty()) return clip_table<E>(device_ranges(plan, ws.table), norms, max_norm, st);
     if (plan.cap == kRangesSmall) return clip_tables<E>(plan.small, norms, max_norm, st);
     if (plan.cap == kRangesMedium) return clip_tables<E>(plan.medium, norms, max_norm, st);
     return clip_tables<E>(plan.large, norms, max_norm, st);
 }
 
-cudaError_t launch_clip(const RangePlan& plan, int dtype, const float* norms, float max_norm, cudaStream_t st) {
-    return dtype == DDP_BF16 ? clip<EBF16>(plan, norms, max_norm, st) : clip<EF32>(plan, norms, max_norm, st);
+cudaError_t launch_clip(const RangePlan& plan, int dtype, NormSpace ws, const float* norms, float max_norm,
+                        cudaStream_t st) {
+    return dtype == DDP_BF16 ? clip<EBF16>(plan, ws, norms, max_norm, st) : clip<EF32>(plan, ws, norms, max_norm, st);
 }
 
 }  // namespace ddpk

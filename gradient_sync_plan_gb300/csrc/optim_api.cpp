@@ -25,8 +25,8 @@ struct ddp_grad_set {
     int32_t world = 0, dtype = 0;
     std::shared_ptr<const RangePlan> plan;
     std::vector<std::pair<uintptr_t, uintptr_t>> spans;        // the memory of the tensors and the workspace, sorted
-    NormSpace space{nullptr, nullptr};
-    bool cleared = false;                                      // the counter is known to be zero
+    NormSpace space{nullptr, nullptr, nullptr};
+    bool ready = false;                                        // the workspace is set up
 };
 
 struct ddp_sync_norm {
@@ -36,11 +36,13 @@ struct ddp_sync_norm {
     std::vector<int64_t> numel, offset, bucket_numel;
     std::vector<int32_t> bucket_of;
     std::shared_ptr<const SyncPlan> sync;                      // the view algorithms' tables
+    char* sync_table = nullptr;
+    bool sync_ready = false;                                   // the workspace is set up for `sync`
     // rank 0's gradients, for a norm pass after a sync without one
     std::shared_ptr<const RangePlan> plan;
     std::vector<std::pair<uintptr_t, uintptr_t>> spans;        // the gradients, buckets and the workspace, sorted
-    NormSpace space{nullptr, nullptr};
-    bool cleared = false;                                      // the counter is known to be zero
+    NormSpace space{nullptr, nullptr, nullptr};
+    bool ready = false;                                        // the workspace is set up
 };
 
 struct ddp_adamw {
@@ -50,7 +52,8 @@ struct ddp_adamw {
     std::vector<std::pair<uintptr_t, uintptr_t>> spans;        // what a step writes, sorted
     int32_t* steps = nullptr;
     int32_t* arrivals = nullptr;
-    bool cleared = false;                                      // arrivals is known to be zero
+    char* table = nullptr;
+    bool ready = false;                                        // the workspace is set up
 };
 
 namespace {
@@ -120,20 +123,49 @@ int sync_vecs(int32_t world, int32_t n_params, const int64_t* numel, int32_t dty
     return sync_norm_vecs(world, n, dtype);
 }
 
-NormSpace space_of(void* workspace) {
+// `partials` is how many the workspace has room for; the table comes after them.
+NormSpace space_of(void* workspace, int64_t partials) {
     char* w = static_cast<char*>(workspace);
-    return NormSpace{reinterpret_cast<uint32_t*>(w), reinterpret_cast<double*>(w + kNormSpaceHead)};
+    return NormSpace{reinterpret_cast<uint32_t*>(w), reinterpret_cast<double*>(w + kNormSpaceHead),
+                     w + table_offset(kNormSpaceHead + 8 * partials)};
 }
 
-// Zeroes a handle's counter before the first launch that uses it.  A capture
-// records the clearing for its replays, and proves nothing for later calls.
-cudaError_t clear_word(void* word, bool* cleared, cudaStream_t stream) {
-    if (*cleared) return cudaSuccess;
+// Before the first launch that uses them: a handle's counter is zeroed and its
+// table, if it is in device memory, written.  A capture records both for its
+// replays, and proves nothing for later calls.
+cudaError_t make_ready(void* counter, const DeviceTable* table, void* at, bool* ready, cudaStream_t stream) {
+    if (*ready) return cudaSuccess;
     cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
     cudaError_t e = cudaStreamIsCapturing(stream, &capturing);
-    if (e == cudaSuccess) e = cudaMemsetAsync(word, 0, 4, stream);
-    if (e == cudaSuccess && capturing == cudaStreamCaptureStatusNone) *cleared = true;
+    if (e == cudaSuccess) e = cudaMemsetAsync(counter, 0, 4, stream);
+    if (e == cudaSuccess && table) e = upload_table(*table, at, stream);
+    if (e == cudaSuccess && capturing == cudaStreamCaptureStatusNone) *ready = true;
     return e;
+}
+
+int32_t ready(ddp_grad_set* s, cudaStream_t q) {
+    return cuda_status(make_ready(s->space.counter, range_plan_table(*s->plan), s->space.table, &s->ready, q));
+}
+
+// The workspace of a sync with norm, the partials it has room for, and where the
+// members' table goes (the ranges' comes right after the partials).
+int32_t sync_norm_space(int32_t world, int32_t n_params, const int64_t* numel, int32_t dtype, int64_t* bytes,
+                        int64_t* partials, int64_t* sync_table) {
+    if (!bytes) return DDP_ERR_INVALID;
+    const int32_t st = check_sizes(world, n_params, numel, dtype);
+    if (st) return st;
+    const int64_t tile = (int64_t)kThreads * sync_vecs(world, n_params, numel, dtype) * (16 / elem_bytes(dtype));
+    int64_t tiles = 0;
+    for (int32_t i = 0; i < n_params; ++i)
+        if (numel[i] > 0) tiles += numel[i] / tile + 2;
+    tiles = std::max(tiles, most_tiles(n_params, numel, elem_bytes(dtype)));
+    if (partials) *partials = tiles;
+    // members with their pointers, and ranges for a norm pass: which of them a run
+    // needs can change from run to run, and a captured graph keeps its own
+    const int64_t ranges = table_space(kNormSpaceHead + 8 * tiles, n_params, kRangeEntry);
+    if (sync_table) *sync_table = table_offset(ranges);
+    *bytes = table_space(ranges, n_params, kSyncEntry + 8 * (int64_t)world);
+    return DDP_OK;
 }
 
 bool bad_max_norm(double max_norm) { return !(max_norm > 0.0) || !((float)max_norm > 0.f); }
@@ -148,7 +180,8 @@ int32_t ddp_grad_set_workspace_bytes(int32_t world, int32_t n_params, const int6
     if (!bytes) return DDP_ERR_INVALID;
     const int32_t st = check_sizes(world, n_params, numel, dtype);
     if (st) return st;
-    *bytes = kNormSpaceHead + 8 * world * most_tiles(n_params, numel, elem_bytes(dtype));
+    *bytes = table_space(kNormSpaceHead + 8 * world * most_tiles(n_params, numel, elem_bytes(dtype)),
+                         (int64_t)world * n_params, kRangeEntry);
     return DDP_OK;
 } DDP_ABI_CATCH
 
@@ -161,14 +194,14 @@ int32_t ddp_grad_set_create(int32_t world, int32_t n_params, void* const* grads,
     int32_t st = ddp_grad_set_workspace_bytes(world, n_params, numel, dtype, &need);
     if (st) return st;
     if (n_params > 0 && !grads) return DDP_ERR_INVALID;
-    if ((st = check_ptr(workspace, 8))) return st;
+    if ((st = check_ptr(workspace, 16))) return st;
     if (workspace_bytes < need) return DDP_ERR_CAPACITY;
     if (need / 8 > INT32_MAX / 8) return DDP_ERR_CAPACITY;
     const int64_t es = elem_bytes(dtype);
     std::unique_ptr<ddp_grad_set> s(new ddp_grad_set());
     s->world = world;
     s->dtype = dtype;
-    s->space = space_of(workspace);
+    s->space = space_of(workspace, world * most_tiles(n_params, numel, es));
     s->spans.push_back(span_of(workspace, need));
     std::vector<GradRange> ranges;               // by rank, then by address
     std::vector<Span> rank;
@@ -198,17 +231,18 @@ int32_t ddp_grad_norm(ddp_grad_set* s, float* norms, void* stream) try {
     if (st) return st;
     if (hits_any(s->spans, span_of(norms, 4 * (int64_t)s->world))) return DDP_ERR_INVALID;
     cudaStream_t q = (cudaStream_t)stream;
-    if ((st = cuda_status(clear_word(s->space.counter, &s->cleared, q)))) return st;
+    if ((st = ready(s, q))) return st;
     return cuda_status(launch_norm(*s->plan, s->dtype, s->space, 1, norms, q));
 } DDP_ABI_CATCH
 
 int32_t ddp_grad_clip(ddp_grad_set* s, const float* norms, double max_norm, void* stream) try {
     DDP_TRACE_CALL();
     if (!s || bad_max_norm(max_norm)) return DDP_ERR_INVALID;
-    const int32_t st = check_ptr(norms, 4);
+    int32_t st = check_ptr(norms, 4);
     if (st) return st;
     if (hits_any(s->spans, span_of(norms, 4 * (int64_t)s->world))) return DDP_ERR_INVALID;
-    return cuda_status(launch_clip(*s->plan, s->dtype, norms, (float)max_norm, (cudaStream_t)stream));
+    if ((st = ready(s, (cudaStream_t)stream))) return st;
+    return cuda_status(launch_clip(*s->plan, s->dtype, s->space, norms, (float)max_norm, (cudaStream_t)stream));
 } DDP_ABI_CATCH
 
 int32_t ddp_grad_norm_clip(ddp_grad_set* s, float* norms, double max_norm, void* stream) try {
@@ -227,15 +261,7 @@ int32_t ddp_grad_set_destroy(ddp_grad_set* s) try {
 int32_t ddp_sync_norm_workspace_bytes(int32_t world, int32_t n_params, const int64_t* numel, int32_t dtype,
                                       int64_t* bytes) try {
     DDP_TRACE_CALL();
-    if (!bytes) return DDP_ERR_INVALID;
-    const int32_t st = check_sizes(world, n_params, numel, dtype);
-    if (st) return st;
-    const int64_t tile = (int64_t)kThreads * sync_vecs(world, n_params, numel, dtype) * (16 / elem_bytes(dtype));
-    int64_t tiles = 0;
-    for (int32_t i = 0; i < n_params; ++i)
-        if (numel[i] > 0) tiles += numel[i] / tile + 2;
-    *bytes = kNormSpaceHead + 8 * std::max(tiles, most_tiles(n_params, numel, elem_bytes(dtype)));
-    return DDP_OK;
+    return sync_norm_space(world, n_params, numel, dtype, bytes, nullptr, nullptr);
 } DDP_ABI_CATCH
 
 int32_t ddp_sync_norm_create(int32_t world, int32_t n_params, void* const* grads, const int64_t* numel,
@@ -245,8 +271,8 @@ int32_t ddp_sync_norm_create(int32_t world, int32_t n_params, void* const* grads
     DDP_TRACE_CALL();
     if (!out) return DDP_ERR_INVALID;
     *out = nullptr;
-    int64_t need = 0;
-    int32_t st = ddp_sync_norm_workspace_bytes(world, n_params, numel, dtype, &need);
+    int64_t need = 0, partials = 0, sync_table = 0;
+    int32_t st = sync_norm_space(world, n_params, numel, dtype, &need, &partials, &sync_table);
     if (st) return st;
     if (n_buckets < 0 || divisor < 0) return DDP_ERR_INVALID;
     const bool hook = algo == DDP_ALGO_BF16_HOOK || algo == DDP_ALGO_BF16_HOOK_VIEW || algo == DDP_ALGO_FP16_HOOK_VIEW;
@@ -255,7 +281,7 @@ int32_t ddp_sync_norm_create(int32_t world, int32_t n_params, void* const* grads
     if (hook && dtype != DDP_F32) return DDP_ERR_INVALID;
     if (n_params > 0 && (!grads || !bucket_of_param || !offset_of_param)) return DDP_ERR_INVALID;
     if (n_buckets > 0 && (!bucket_numel || (needs_buckets && !buckets))) return DDP_ERR_INVALID;
-    if ((st = check_ptr(workspace, 8))) return st;
+    if ((st = check_ptr(workspace, 16))) return st;
     if (workspace_bytes < need || need / 8 > INT32_MAX / 8) return DDP_ERR_CAPACITY;
     for (int32_t k = 0; k < n_buckets; ++k)
         if ((st = common_checks(world, bucket_numel[k], dtype))) return st;
@@ -266,7 +292,8 @@ int32_t ddp_sync_norm_create(int32_t world, int32_t n_params, void* const* grads
     s->dtype = dtype;
     s->divisor = divisor;
     s->algo = algo;
-    s->space = space_of(workspace);
+    s->space = space_of(workspace, partials);
+    s->sync_table = static_cast<char*>(workspace) + sync_table;
     const int64_t all = (int64_t)world * n_params, es = elem_bytes(dtype);
     if (n_params > 0) {
         s->grads.assign(grads, grads + all);
@@ -353,12 +380,17 @@ int32_t ddp_sync_norm_run(ddp_sync_norm* s, float* norms, void* stream) try {
     if (st) return st;
     if (hits_any(s->spans, span_of(norms, 4 * (int64_t)s->world))) return DDP_ERR_INVALID;
     cudaStream_t q = (cudaStream_t)stream;
-    if ((st = cuda_status(clear_word(s->space.counter, &s->cleared, q)))) return st;
     // the kernel with the norm is a register kernel: where the TMA-staged view
     // kernel is asked for, or the CTA budget is one that it needs, the sync
     // runs as ddp_sync_buckets runs it and the norm takes a pass over rank 0
-    if (s->sync && fused_kernel_override() != DDP_FUSED_TMA && !cta_cap_is_tight())
-        return cuda_status(launch_sync_norm(*s->sync, s->space, norms, q));
+    const bool fused = s->sync && fused_kernel_override() != DDP_FUSED_TMA && !cta_cap_is_tight();
+    if (fused) {
+        NormSpace ws = s->space;
+        ws.table = s->sync_table;
+        if ((st = cuda_status(make_ready(ws.counter, sync_plan_table(*s->sync), ws.table, &s->sync_ready, q)))) return st;
+        return cuda_status(launch_sync_norm(*s->sync, ws, norms, q));
+    }
+    if ((st = cuda_status(make_ready(s->space.counter, range_plan_table(*s->plan), s->space.table, &s->ready, q)))) return st;
     st = ddp_sync_buckets(s->world, s->n_params, s->grads.data(), s->numel.data(), s->bucket_of.data(), s->offset.data(),
                           s->n_buckets, s->bucket_numel.data(), s->buckets.empty() ? nullptr : s->buckets.data(), s->dtype,
                           s->divisor, s->algo, stream);
@@ -372,25 +404,38 @@ int32_t ddp_sync_norm_destroy(ddp_sync_norm* s) try {
     return DDP_OK;
 } DDP_ABI_CATCH
 
+int32_t ddp_adamw_workspace_bytes(int32_t world, int32_t n_params, int64_t* bytes) try {
+    DDP_TRACE_CALL();
+    const int32_t st = common_checks(world, 0, DDP_F32);
+    if (st) return st;
+    if (!bytes || n_params < 0) return DDP_ERR_INVALID;
+    *bytes = table_space(kNormSpaceHead, (int64_t)world * n_params, kAdamWEntry);
+    return DDP_OK;
+} DDP_ABI_CATCH
+
 int32_t ddp_adamw_create(int32_t world, int32_t n_params, void* const* params, const void* const* grads,
                          int32_t grad_dtype, void* const* exp_avg, void* const* exp_avg_sq, void* const* copies,
                          const int64_t* numel, const uint8_t* no_decay, int32_t* steps, void* workspace,
-                         ddp_adamw** out) try {
+                         int64_t workspace_bytes, ddp_adamw** out) try {
     DDP_TRACE_CALL();
     if (!out) return DDP_ERR_INVALID;
     *out = nullptr;
     int32_t st = check_sizes(world, n_params, numel, grad_dtype);
     if (st) return st;
     if (n_params > 0 && (!params || !grads || !exp_avg || !exp_avg_sq)) return DDP_ERR_INVALID;
-    if ((st = check_ptr(steps, 4)) || (st = check_ptr(workspace, 8))) return st;
+    if ((st = check_ptr(steps, 4)) || (st = check_ptr(workspace, 16))) return st;
+    int64_t need = 0;
+    if ((st = ddp_adamw_workspace_bytes(world, n_params, &need))) return st;
+    if (workspace_bytes < need) return DDP_ERR_CAPACITY;
     std::unique_ptr<ddp_adamw> a(new ddp_adamw());
     a->world = world;
     a->grad_dtype = grad_dtype;
     a->copies = copies != nullptr;
     a->steps = steps;
     a->arrivals = static_cast<int32_t*>(workspace);
+    a->table = static_cast<char*>(workspace) + table_offset(kNormSpaceHead);
     a->spans.push_back(span_of(steps, 4 * (int64_t)world));
-    a->spans.push_back(span_of(workspace, DDP_ADAMW_WORKSPACE_BYTES));
+    a->spans.push_back(span_of(workspace, need));
     std::vector<Span> read;
     const int64_t gs = elem_bytes(grad_dtype);
     std::vector<AdamWItem> items;
@@ -446,7 +491,8 @@ int32_t ddp_adamw_step(ddp_adamw* a, double lr, double beta1, double beta2, doub
         if (st) return st;
         if (hits_any(a->spans, span_of(norms, 4 * (int64_t)a->world))) return DDP_ERR_INVALID;
     }
-    const int32_t st = cuda_status(clear_word(a->arrivals, &a->cleared, (cudaStream_t)stream));
+    const int32_t st = cuda_status(make_ready(a->arrivals, adamw_plan_table(*a->plan), a->table, &a->ready,
+                                              (cudaStream_t)stream));
     if (st) return st;
     const AdamWScalars s{(float)lr,
                          (float)beta1,
@@ -458,7 +504,7 @@ int32_t ddp_adamw_step(ddp_adamw* a, double lr, double beta1, double beta2, doub
                          (float)eps,
                          (float)(lr * weight_decay),
                          (float)max_norm};
-    return cuda_status(launch_adamw(*a->plan, a->world, a->grad_dtype, a->copies, s, norms, a->steps, a->arrivals,
+    return cuda_status(launch_adamw(*a->plan, a->table, a->world, a->grad_dtype, a->copies, s, norms, a->steps, a->arrivals,
                                     (cudaStream_t)stream));
 } DDP_ABI_CATCH
 

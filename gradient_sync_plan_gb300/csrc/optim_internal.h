@@ -12,6 +12,29 @@
 
 namespace ddpk {
 
+// ---- tables in device memory (grad_norm.cu) ----------------------------------
+// A kernel's table travels in its parameters while one launch takes it.  Where
+// it would take several launches for little data, a handle keeps it in its
+// workspace instead, written there by launches of its own before the first use.
+struct DeviceTable {
+    std::vector<char> image;                   // tile ends, then entries
+    int64_t entries_at = 0;                    // byte offset of the entries
+    int64_t more_at = 0;                       // and of what follows them
+};
+// Whether entries that take `launches` launches, moving `bytes`, do better as one
+// from a table in device memory: another launch costs some 5 us, the table's
+// loads some 5 % of a large launch.
+inline bool table_on_device(int64_t launches, int64_t bytes) {
+    return launches > 1 && bytes < (launches - 1) * ((int64_t)512 << 20);
+}
+// Workspace for the table of `entries` entries of `entry` bytes, and its start
+// behind the `used` bytes before it.
+inline int64_t table_offset(int64_t used) { return (used + 255) / 256 * 256; }
+inline int64_t table_space(int64_t used, int64_t entries, int64_t entry) {
+    return table_offset(used) + (4 * entries + 15) / 16 * 16 + (entries * entry + 15) / 16 * 16;
+}
+cudaError_t upload_table(const DeviceTable& t, void* device, cudaStream_t stream);
+
 // ---- norm and clip (grad_norm.cu) ---------------------------------------
 // A run of contiguous gradient bytes of one rank: what the norm and clip
 // kernels walk.  Tensors that lie back to back in memory are one range.
@@ -35,7 +58,7 @@ constexpr int64_t kNormBlocks = 8 * 152;
 // The kernels' tables, filled once for ranges sorted by rank.
 struct RangePlan;
 std::shared_ptr<const RangePlan> make_range_plan(const GradRange* ranges, int64_t n, int ranks);
-int64_t range_plan_partials(const RangePlan& plan);
+constexpr int64_t kRangeEntry = 24;
 
 // How a launch of partials ends: where there are few, its last block adds them
 // itself (counter: a word that is zero between launches); NULL: it does not.
@@ -53,12 +76,17 @@ struct NormFinish {
 struct NormSpace {
     uint32_t* counter;
     double* partials;
+    char* table;                               // for a DeviceTable
 };
 constexpr int64_t kNormSpaceHead = 16;         // bytes before the partials
 
 // norms[r * copies ..] = sqrt(sum of squares of rank r's ranges).
 cudaError_t launch_norm(const RangePlan& plan, int dtype, NormSpace ws, int copies, float* norms, cudaStream_t stream);
-cudaError_t launch_clip(const RangePlan& plan, int dtype, const float* norms, float max_norm, cudaStream_t stream);
+cudaError_t launch_clip(const RangePlan& plan, int dtype, NormSpace ws, const float* norms, float max_norm,
+                        cudaStream_t stream);
+// The plan's table, if it belongs in device memory (else null): to be uploaded
+// to ws.table before the first launch.
+const DeviceTable* range_plan_table(const RangePlan& plan);
 NormFinish norm_finish(NormSpace ws, const int32_t* rank_first, int ranks, int copies, float* norms, bool one_launch);
 // Partials that a launch left, into norms.
 cudaError_t launch_norm_final(const double* partials, const int32_t* rank_first, int ranks, int copies, float* norms,
@@ -78,6 +106,8 @@ int sync_norm_vecs(int world, int64_t numel, int dtype);
 struct SyncPlan;
 std::shared_ptr<const SyncPlan> make_sync_plan(int world, const SyncMember* members, int64_t n, int vecs, int dtype,
                                                DivSpec div);
+const DeviceTable* sync_plan_table(const SyncPlan& plan);
+constexpr int64_t kSyncEntry = 32;             // and 8 a rank
 cudaError_t launch_sync_norm(const SyncPlan& plan, NormSpace ws, float* norms, cudaStream_t stream);
 
 // ---- AdamW (adamw.cu) ------------------------------------------------------
@@ -102,7 +132,9 @@ struct AdamWPlan;
 std::shared_ptr<const AdamWPlan> make_adamw_plan(const AdamWItem* items, int64_t n, int grad_dtype, bool copies);
 // norms may be null (no clipping).  steps[world] is read, and advanced for the
 // ranks that were updated; arrivals is one word, zero between calls.
-cudaError_t launch_adamw(const AdamWPlan& plan, int world, int grad_dtype, bool copies, const AdamWScalars& s,
+const DeviceTable* adamw_plan_table(const AdamWPlan& plan);
+constexpr int64_t kAdamWEntry = 56;
+cudaError_t launch_adamw(const AdamWPlan& plan, const char* table, int world, int grad_dtype, bool copies, const AdamWScalars& s,
                          const float* norms, int32_t* steps, int32_t* arrivals, cudaStream_t stream);
 
 }  // namespace ddpk

@@ -25,25 +25,37 @@ namespace ddpk {
 
 constexpr uint32_t kRanksDiffer = 15;
 
-template <int MEMBERS, int PTRS>
-struct SyncTab {
-    static constexpr int kMembers = MEMBERS, kPtrs = PTRS;
+struct Member {                  // side by side: a block finds one line of a cold constant cache, not one a field
+    int64_t numel;
+    int64_t offset;              // bucket position of element 0
+    int64_t clen;                // chunk length of the member's bucket
+    float inv_clen;
+    uint32_t first : 28;         // its first tile
+    uint32_t lead : 4;           // elements past a 16-byte boundary, at every rank; kRanksDiffer
+};
+static_assert(sizeof(Member) == kSyncEntry, "the workspace counts on it");
+
+struct SyncHead {
     int32_t n;
     int32_t tiles;
     int32_t world;
     int32_t vecs;                // vectors a thread takes of a tile
     int32_t div_mode;
     float div_operand;
+};
+template <int MEMBERS, int PTRS>
+struct SyncTab : SyncHead {
+    static constexpr bool kDevice = false;
+    static constexpr int kMembers = MEMBERS, kPtrs = PTRS;
     int32_t tile_end[MEMBERS];   // inclusive prefix of tiles
-    struct Member {              // side by side: a block finds one line of a cold constant cache, not one a field
-        int64_t numel;
-        int64_t offset;          // bucket position of element 0
-        int64_t clen;            // chunk length of the member's bucket
-        float inv_clen;
-        uint32_t first : 28;     // its first tile
-        uint32_t lead : 4;       // elements past a 16-byte boundary, at every rank; kRanksDiffer
-    } member[MEMBERS];
+    Member member[MEMBERS];
     char* ptr[PTRS];             // ptr[m * world + r]
+};
+struct SyncDev : SyncHead {      // the same in device memory
+    static constexpr bool kDevice = true;
+    const int32_t* tile_end;
+    const Member* member;
+    char* const* ptr;
 };
 using SyncSmall = SyncTab<32, 256>;
 using SyncMedium = SyncTab<176, 704>;
@@ -108,6 +120,7 @@ __global__ void __launch_bounds__(kThreads, MINB) k_sync_norm(const __grid_const
     init_squares(scratch);
     AcquireOnce acquire;
     pdl_release();
+    if constexpr (TAB::kDevice) acquire();
     const int world = b.world;
     for (int tile = blockIdx.x; tile < b.tiles; tile += gridDim.x) {
         const int i = block_first_past(b.tile_end, b.n, tile, &slot);
@@ -215,34 +228,51 @@ struct SyncPlan {
     std::vector<SyncSmall> small;
     std::vector<SyncMedium> medium;
     std::vector<SyncLarge> large;
+    DeviceTable device;                          // more members than one launch's table takes, for little data
+    SyncDev dev{};                               // with offsets for addresses
 };
+
+const DeviceTable* sync_plan_table(const SyncPlan& plan) { return plan.device.image.empty() ? nullptr : &plan.device; }
+
+// Members [i, n) as far as `most` goes into one table; returns where it stopped.
+template <class Ends, class Entries, class Ptrs>
+static int64_t fill_table(const SyncMember* members, int64_t i, int64_t n, int64_t most, int world, int dtype, int vecs,
+                          DivSpec div, SyncHead* b, Ends ends, Entries entries, Ptrs ptrs) {
+    const int64_t es = elem_bytes(dtype), tile = (int64_t)kThreads * vecs * (16 / es);
+    *b = SyncHead{0, 0, world, vecs, div.mode, div.operand};
+    for (; i < n && b->n < most; ++i, ++b->n) {
+        const SyncMember& m = members[i];
+        const int lead = lead_of(world, m, es);
+        entries[b->n] = Member{m.numel, m.offset, m.clen, 1.0f / (float)m.clen, (uint32_t)b->tiles,
+                               lead < 0 ? kRanksDiffer : (uint32_t)lead};
+        b->tiles += (int32_t)((std::max(lead, 0) + m.numel + tile - 1) / tile);
+        ends[b->n] = b->tiles;
+        for (int r = 0; r < world; ++r) ptrs[(size_t)b->n * world + r] = static_cast<char*>(m.ptrs[r]);
+    }
+    return i;
+}
 
 template <class TAB>
 static void fill_tables(SyncPlan* plan, const SyncMember* members, int64_t n, int vecs, DivSpec div,
                         std::vector<TAB>* out) {
-    const int world = plan->world;
-    const int64_t es = elem_bytes(plan->dtype), tile = (int64_t)kThreads * vecs * (16 / es);
-    const int most = std::min(TAB::kMembers, TAB::kPtrs / world);
+    const int most = std::min(TAB::kMembers, TAB::kPtrs / plan->world);
     for (int64_t i = 0; i < n;) {
         out->emplace_back();
         TAB& b = out->back();
-        b.world = world;
-        b.vecs = vecs;
-        b.div_mode = div.mode;
-        b.div_operand = div.operand;
-        b.n = 0;
-        b.tiles = 0;
-        for (; i < n && b.n < most; ++i, ++b.n) {
-            const SyncMember& m = members[i];
-            const int lead = lead_of(world, m, es);
-            const int32_t first = b.tiles;
-            b.tiles += (int32_t)((std::max(lead, 0) + m.numel + tile - 1) / tile);
-            b.tile_end[b.n] = b.tiles;
-            b.member[b.n] = {m.numel, m.offset, m.clen, 1.0f / (float)m.clen, (uint32_t)first, lead < 0 ? kRanksDiffer : (uint32_t)lead};
-            for (int r = 0; r < world; ++r) b.ptr[(size_t)b.n * world + r] = static_cast<char*>(m.ptrs[r]);
-        }
+        i = fill_table(members, i, n, most, plan->world, plan->dtype, vecs, div, &b, b.tile_end, b.member, b.ptr);
         plan->tiles += b.tiles;
     }
+}
+
+static void fill_device(SyncPlan* plan, const SyncMember* members, int64_t n, int vecs, DivSpec div) {
+    DeviceTable& t = plan->device;
+    t.entries_at = (4 * n + 15) / 16 * 16;
+    t.more_at = t.entries_at + n * kSyncEntry;
+    t.image.assign((size_t)(t.more_at + (8 * n * plan->world + 15) / 16 * 16), 0);
+    fill_table(members, 0, n, n, plan->world, plan->dtype, vecs, div, &plan->dev,
+               reinterpret_cast<int32_t*>(t.image.data()), reinterpret_cast<Member*>(t.image.data() + t.entries_at),
+               reinterpret_cast<char**>(t.image.data() + t.more_at));
+    plan->tiles = plan->dev.tiles;
 }
 
 template <class TAB>
@@ -255,37 +285,48 @@ std::shared_ptr<const SyncPlan> make_sync_plan(int world, const SyncMember* memb
     plan->dtype = dtype;
     if (fits<SyncSmall>(world, n)) fill_tables(plan.get(), members, n, vecs, div, &plan->small);
     else if (fits<SyncMedium>(world, n)) fill_tables(plan.get(), members, n, vecs, div, &plan->medium);
-    else fill_tables(plan.get(), members, n, vecs, div, &plan->large);
+    else {
+        int64_t bytes = 0;
+        for (int64_t i = 0; i < n; ++i) bytes += 2 * members[i].numel * elem_bytes(dtype) * world;
+        const int64_t most = std::min(SyncLarge::kMembers, SyncLarge::kPtrs / world);
+        if (table_on_device((n + most - 1) / most, bytes)) fill_device(plan.get(), members, n, vecs, div);
+        else fill_tables(plan.get(), members, n, vecs, div, &plan->large);
+    }
     return plan;
 }
 
 template <class E, int G, int B, int MINB, class TAB>
-static cudaError_t sync_tables(const std::vector<TAB>& tables, double* partials, const NormFinish& finish,
-                               cudaStream_t st) {
-    for (const TAB& b : tables) {
-        const cudaError_t e = launch_table(k_sync_norm<E, G, B, MINB, TAB>, dim3(cap_ctas(b.tiles)), dim3(kThreads), st, b,
-                                           partials, finish);
+static cudaError_t sync_tables(const TAB* tables, size_t n, double* partials, const NormFinish& finish, cudaStream_t st) {
+    for (size_t k = 0; k < n; ++k) {
+        const cudaError_t e = launch_table(k_sync_norm<E, G, B, MINB, TAB>, dim3(cap_ctas(tables[k].tiles)),
+                                           dim3(kThreads), st, tables[k], partials, finish);
         if (e != cudaSuccess) return e;
-        partials += b.tiles;
+        partials += tables[k].tiles;
     }
     return cudaSuccess;
 }
 
 template <class E, class TAB>
-static cudaError_t sync_world(int world, const std::vector<TAB>& tables, double* partials, const NormFinish& finish,
+static cudaError_t sync_world(int world, const TAB* tables, size_t n, double* partials, const NormFinish& finish,
                               cudaStream_t st) {
     // 6.9 TB/s each on the 355M decoder; without side-by-side vectors 6.2 on 2
     // ranks, with four blocks of 8 ranks' loads 6.7 on 8
-    if (world <= 2) return sync_tables<E, 2, 2, 4>(tables, partials, finish, st);
-    if (world <= 4) return sync_tables<E, 4, 1, 4>(tables, partials, finish, st);
-    return sync_tables<E, 4, 1, 5>(tables, partials, finish, st);
+    if (world <= 2) return sync_tables<E, 2, 2, 4>(tables, n, partials, finish, st);
+    if (world <= 4) return sync_tables<E, 4, 1, 4>(tables, n, partials, finish, st);
+    return sync_tables<E, 4, 1, 5>(tables, n, partials, finish, st);
 }
 
 template <class E>
-static cudaError_t sync_size(const SyncPlan& p, double* partials, const NormFinish& f, cudaStream_t st) {
-    if (!p.small.empty()) return sync_world<E>(p.world, p.small, partials, f, st);
-    if (!p.medium.empty()) return sync_world<E>(p.world, p.medium, partials, f, st);
-    return sync_world<E>(p.world, p.large, partials, f, st);
+static cudaError_t sync_size(const SyncPlan& p, NormSpace ws, const NormFinish& f, cudaStream_t st) {
+    auto run = [&](const auto& t) { return sync_world<E>(p.world, t.data(), t.size(), ws.partials, f, st); };
+    if (!p.small.empty()) return run(p.small);
+    if (!p.medium.empty()) return run(p.medium);
+    if (p.device.image.empty()) return run(p.large);
+    SyncDev d = p.dev;
+    d.tile_end = reinterpret_cast<const int32_t*>(ws.table);
+    d.member = reinterpret_cast<const Member*>(ws.table + p.device.entries_at);
+    d.ptr = reinterpret_cast<char* const*>(ws.table + p.device.more_at);
+    return sync_world<E>(p.world, &d, 1, ws.partials, f, st);
 }
 
 // Tiles up to which a launch adds its partials itself: a block that arrives
@@ -295,13 +336,13 @@ constexpr int32_t kSyncFinishTiles = 608;
 
 cudaError_t launch_sync_norm(const SyncPlan& p, NormSpace ws, float* norms, cudaStream_t st) {
     const int32_t first[2] = {0, p.tiles};
-    const size_t launches = p.small.size() + p.medium.size() + p.large.size();
+    const size_t launches = p.small.size() + p.medium.size() + p.large.size() + (p.device.image.empty() ? 0 : 1);
     const NormFinish f = norm_finish(ws, first, 1, p.world, norms, launches == 1 && p.tiles <= kSyncFinishTiles);
     cudaError_t e;
-    if (p.dtype == DDP_F32) e = sync_size<EF32>(p, ws.partials, f, st);
-    else if (p.dtype == kDtypeHook) e = sync_size<EHOOK>(p, ws.partials, f, st);
-    else if (p.dtype == kDtypeHook16) e = sync_size<EHOOK16>(p, ws.partials, f, st);
-    else e = sync_size<EBF16>(p, ws.partials, f, st);
+    if (p.dtype == DDP_F32) e = sync_size<EF32>(p, ws, f, st);
+    else if (p.dtype == kDtypeHook) e = sync_size<EHOOK>(p, ws, f, st);
+    else if (p.dtype == kDtypeHook16) e = sync_size<EHOOK16>(p, ws, f, st);
+    else e = sync_size<EBF16>(p, ws, f, st);
     if (e != cudaSuccess || f.counter) return e;
     return launch_norm_final(ws.partials, first, 1, p.world, norms, st);
 }

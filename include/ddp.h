@@ -652,11 +652,10 @@ int32_t ddp_bucket_allreduce_view_fp16(int32_t world, int32_t n_in_bucket, void*
  *   numel[n_params]       elements of each tensor (>= 0; their sum at most
  *                         DDP_MAX_NUMEL)
  *   dtype                 a ddp_dtype
- *   workspace             device memory, 8-byte aligned, of at least
+ *   workspace             device memory, 16-byte aligned, of at least
  *                         ddp_grad_set_workspace_bytes (DDP_ERR_CAPACITY if
- *                         smaller), for the set alone (its first norm clears
- *                         what has to start at zero); the set keeps it, the caller
- *                         owns it.  Calls on one set share it: order them (one
+ *                         smaller), for the set alone (its first call sets it
+ *                         up); the set keeps it, the caller owns it.  Calls on one set share it: order them (one
  *                         stream, or events)
  *   norms[world]          device float32, outside the tensors and the workspace
  *   max_norm              > 0 (may be infinite)
@@ -688,10 +687,9 @@ int32_t ddp_grad_set_destroy(ddp_grad_set* set);
  *
  * The handle checks its arguments and lays out its tables once; a run then
  * costs its launches.
- *   workspace     device memory, 8-byte aligned, of at least
+ *   workspace     device memory, 16-byte aligned, of at least
  *                 ddp_sync_norm_workspace_bytes (DDP_ERR_CAPACITY if smaller),
- *                 for the handle alone (its first run clears what has to start
- *                 at zero).  Runs of one handle share it: order them
+ *                 for the handle alone (its first run sets it up).  Runs of one handle share it: order them
  *   norms[world]  device float32, outside the gradients and the workspace
  * Other arguments as for ddp_sync_buckets (any algo it takes).  The handle keeps
  * the pointers until it is destroyed, the caller keeps the memory.
@@ -735,20 +733,21 @@ int32_t ddp_sync_norm_destroy(ddp_sync_norm* sync);
  *   no_decay[n_params]   non-zero: this tensor gets no weight decay (biases,
  *                        norms' weights); NULL: all decay
  *   steps[world]         device int32: steps taken so far, 0 at the start
- *   workspace            DDP_ADAMW_WORKSPACE_BYTES of device memory, 8-byte
- *                        aligned, for the handle alone (its first step clears
- *                        it).  Steps of one handle must not overlap on the GPU
+ *   workspace            device memory, 16-byte aligned, of at least
+ *                        ddp_adamw_workspace_bytes (DDP_ERR_CAPACITY if smaller),
+ *                        for the handle alone (its first step sets it up).  Steps
+ *                        of one handle must not overlap on the GPU
  *   lr >= 0, 0 <= beta < 1, eps > 0, weight_decay >= 0, max_norm > 0 with norms
  * Nothing that a step writes may overlap anything else of the handle;
  * gradients may overlap each other (ranks may share one).  The handle keeps the
  * pointers until it is destroyed, the caller keeps the memory.
  */
-#define DDP_ADAMW_WORKSPACE_BYTES 16
 typedef struct ddp_adamw ddp_adamw;
+int32_t ddp_adamw_workspace_bytes(int32_t world, int32_t n_params, int64_t* bytes);
 int32_t ddp_adamw_create(int32_t world, int32_t n_params, void* const* params, const void* const* grads,
                          int32_t grad_dtype, void* const* exp_avg, void* const* exp_avg_sq, void* const* copies,
                          const int64_t* numel, const uint8_t* no_decay, int32_t* steps, void* workspace,
-                         ddp_adamw** out);
+                         int64_t workspace_bytes, ddp_adamw** out);
 int32_t ddp_adamw_step(ddp_adamw* adamw, double lr, double beta1, double beta2, double eps, double weight_decay,
                        const float* norms, double max_norm, void* stream);
 int32_t ddp_adamw_destroy(ddp_adamw* adamw);

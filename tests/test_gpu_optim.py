@@ -210,8 +210,9 @@ def test_set_on_another_stream_and_in_a_graph(sizes, limit):
         assert abs(_norm64(views[r]) - min(limit, float(want[r]))) < 1e-5
 
 
-def test_first_norm_inside_a_capture_then_eager_ones():
-    views, _ = _place(_values(2, [100_000, 333], 2), "apart", torch.float32)
+@pytest.mark.parametrize("sizes", [[100_000, 333], [1 + (37 * i) % 211 for i in range(900)]], ids=["few", "many"])
+def test_first_norm_inside_a_capture_then_eager_ones(sizes):
+    views, _ = _place(_values(2, sizes, 2), "apart", torch.float32)
     want = ddp.GradSet(views).norm().clone()
     s = ddp.GradSet(views)
     out = torch.zeros(2, device="cuda")
@@ -423,6 +424,45 @@ def test_adamw_bias_corrections(t0, beta):
     want = _adamw64(*old, 1.0, t0 + 1, 1e-3, beta[0], beta[1], 1e-8, 0.01)
     for x, (y, tol) in zip((p, m, v), want):
         assert bool(((x.double() - y).abs() <= tol).all())
+
+
+def test_many_tensors_through_changing_calls_and_a_graph():
+    """Tables that one launch's parameters do not take: captured before and after the other kernel's runs."""
+    world, sizes = 3, [1 + (37 * i) % 911 for i in range(500)]
+    plan = ddp.ddp_plan_buckets(sizes, ddp.F32, 64 << 10, 256 << 10)
+    views, held = _place([[t * 1e-2 for t in row] for row in _values(world, sizes, 4, 1.0)], "apart", torch.float32)
+    first = [[t.clone() for t in row] for row in views]
+
+    def reset():
+        for row, old in zip(views, first):
+            for t, o in zip(row, old):
+                t.copy_(o)
+    other, _ = _place([[t * 1e-2 for t in row] for row in _values(world, sizes, 4, 1.0)], "apart", torch.float32)
+    ddp.ddp_sync_buckets(other, plan, None, algo=ddp.DDP_ALGO_VIEW)
+    want = _norm64(other[0])
+    call = ddp.SyncNormCall(views, plan)
+
+    def check(norms):
+        torch.cuda.synchronize()
+        _check_held(held, "many tensors")
+        assert all(torch.equal(a, b) for x, y in zip(views, other) for a, b in zip(x, y))
+        assert bool(((norms.double() - want).abs() <= 16 * U * want).all())
+    check(call())
+    reset()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for cap in (7, 0):                                   # below four CTAs an SM: the sync's own kernels, then a norm pass
+        reset()
+        prev = ddp.ddp_set_max_ctas(cap)
+        try:
+            check(call())
+        finally:
+            ddp.ddp_set_max_ctas(prev)
+        reset()
+        graph.replay()
+        check(call.norms)
 
 
 def test_adamw_skips_ranks_whose_norm_is_not_finite():

@@ -13,6 +13,7 @@ import gradient_sync_plan_gb300 as ddp
 H = 0x7f0000000000                     # made-up device addresses, never dereferenced
 WS = H + (1 << 40)
 NORMS = H + (1 << 41)
+FREE = H + (1 << 42)
 INF, NAN = float("inf"), float("nan")
 
 
@@ -37,7 +38,7 @@ def _create(world, ptrs, sizes, dtype=0, ws=WS, ws_bytes=None, out=True):
     (-1, dict(world=0)), (-5, dict(world=513)), (-1, dict(dtype=7)), (-1, dict(sizes=[8, -1])),
     (-5, dict(sizes=[8, ddp.MAX_NUMEL + 1], ws_bytes=1 << 60)), (-1, dict(ptrs=[H, None])),
     (-2, dict(ptrs=[H + 2, H + 4096])), (-2, dict(ptrs=[H + 1, H + 4096], dtype=1)), (-1, dict(ptrs=[H, H + 28])),
-    (-1, dict(ws=None)), (-2, dict(ws=WS + 4)), (-5, dict(ws_bytes=7)), (-1, dict(ws=H + 16)), (-1, dict(out=False)),
+    (-1, dict(ws=None)), (-2, dict(ws=WS + 8)), (-5, dict(ws_bytes=7)), (-1, dict(ws=H + 16)), (-1, dict(out=False)),
 ])
 def test_grad_set_refusals(want, kw):
     args = dict(world=1, ptrs=[H, H + 4096], sizes=[8, 8])
@@ -96,7 +97,7 @@ def _sync(world=2, grads=(H, H + 4096), dtype=0, divisor=2, algo=ddp.DDP_ALGO_VI
 
 @pytest.mark.parametrize("want,kw", [
     (-1, dict(world=0)), (-5, dict(world=513)), (-1, dict(dtype=5)), (-1, dict(divisor=-1)), (-1, dict(out=False)),
-    (-1, dict(ws=None)), (-2, dict(ws=WS + 4)), (-5, dict(ws_bytes=8)), (-1, dict(ws=H + 4096)), (-1, dict(table=False)),
+    (-1, dict(ws=None)), (-2, dict(ws=WS + 8)), (-5, dict(ws_bytes=8)), (-1, dict(ws=H + 4096)), (-1, dict(table=False)),
     (-1, dict(algo=ddp.DDP_ALGO_DRYRUN)), (-1, dict(algo=99)), (-1, dict(algo=ddp.DDP_ALGO_FUSED)),
     (-1, dict(algo=ddp.DDP_ALGO_BF16_HOOK_VIEW, dtype=1)), (-1, dict(numel=(9,))), (-1, dict(numel=(-1,))),
     (-1, dict(offset=(1,))), (-1, dict(offset=(-1,))), (-1, dict(bucket=(1,))), (-1, dict(bucket=(-1,))),
@@ -122,19 +123,19 @@ def test_sync_norm_run_refusals():
 
 
 def _adamw(world=1, n=1, p=(H,), g=(H + (1 << 20),), m=(H + (2 << 20),), v=(H + (3 << 20),), c=None, sizes=(8,),
-           dtype=0, steps=NORMS, ws=WS, out=True):
+           dtype=0, steps=NORMS, ws=WS, ws_bytes=1 << 20, out=True):
     h = ctypes.c_void_p(1)
     tab = [None if t is None else _vp(*t) for t in (p, g, m, v, c)]
     st = ddp.lib().ddp_adamw_create(world, n, tab[0], tab[1], dtype, tab[2], tab[3], tab[4], _i64(*sizes), None, steps,
-                                    ws, ctypes.byref(h) if out else None)
+                                    ws, ws_bytes, ctypes.byref(h) if out else None)
     assert not out or st == 0 or h.value is None
     return st, h
 
 
 @pytest.mark.parametrize("want,kw", [
-    (-1, dict(world=0)), (-5, dict(world=513)), (-1, dict(n=-1)), (-1, dict(sizes=(-1,))), (-1, dict(dtype=2)),
+    (-5, dict(ws_bytes=256)), (-1, dict(world=0)), (-5, dict(world=513)), (-1, dict(n=-1)), (-1, dict(sizes=(-1,))), (-1, dict(dtype=2)),
     (-5, dict(sizes=(ddp.MAX_NUMEL + 1,))), (-1, dict(out=False)), (-1, dict(steps=None)), (-2, dict(steps=NORMS + 2)),
-    (-1, dict(ws=None)), (-2, dict(ws=WS + 4)), (-1, dict(ws=NORMS)),
+    (-1, dict(ws=None)), (-2, dict(ws=WS + 8)), (-1, dict(ws=NORMS)),
     (-1, dict(p=None)), (-1, dict(g=None)), (-1, dict(m=None)), (-1, dict(v=None)),
     (-1, dict(p=(None,))), (-1, dict(g=(None,))), (-1, dict(m=(None,))), (-1, dict(v=(None,))), (-1, dict(c=(None,))),
     (-2, dict(p=(H + 2,))), (-2, dict(g=(H + 2,))), (-2, dict(m=(H + 1,))), (-2, dict(v=(H + 2,))), (-2, dict(c=(H + (4 << 20) + 1,))),
@@ -152,11 +153,11 @@ def test_adamw_step_refusals():
     good = dict(lr=1e-3, b1=0.9, b2=0.999, eps=1e-8, wd=0.1, norms=None, max_norm=0.0)
     for kw in (dict(lr=-1.0), dict(lr=NAN), dict(lr=INF), dict(b1=1.0), dict(b2=1.0), dict(b1=-0.1), dict(b1=NAN),
                dict(eps=0.0), dict(eps=-1.0), dict(eps=1e-60), dict(eps=NAN), dict(wd=-0.1), dict(wd=INF),
-               dict(norms=WS + 4096), dict(norms=WS + 4096, max_norm=-1.0), dict(norms=WS + 4096, max_norm=NAN),
+               dict(norms=FREE), dict(norms=FREE, max_norm=-1.0), dict(norms=FREE, max_norm=NAN),
                dict(norms=H, max_norm=1.0), dict(norms=NORMS, max_norm=1.0)):
         a = {**good, **kw}
         assert L.ddp_adamw_step(h, a["lr"], a["b1"], a["b2"], a["eps"], a["wd"], a["norms"], a["max_norm"], None) == -1, kw
-    assert L.ddp_adamw_step(h, 1e-3, 0.9, 0.999, 1e-8, 0.0, WS + 4098, 1.0, None) == -2
+    assert L.ddp_adamw_step(h, 1e-3, 0.9, 0.999, 1e-8, 0.0, FREE + 2, 1.0, None) == -2
     L.ddp_adamw_destroy(h)
 
 
