@@ -130,11 +130,12 @@ int64_t adamw_tiles(const AdamWItem& it);
 // The kernel's tables, filled once.
 struct AdamWPlan;
 std::shared_ptr<const AdamWPlan> make_adamw_plan(const AdamWItem* items, int64_t n, int grad_dtype, bool copies);
-// norms may be null (no clipping).  steps[world] is read, and advanced for the
-// ranks that were updated; arrivals is one word, zero between calls.
 const DeviceTable* adamw_plan_table(const AdamWPlan& plan);
 constexpr int64_t kAdamWEntry = 56;
-cudaError_t launch_adamw(const AdamWPlan& plan, const char* table, int world, int grad_dtype, bool copies, const AdamWScalars& s,
-                         const float* norms, int32_t* steps, int32_t* arrivals, cudaStream_t stream);
+// norms may be null (no clipping).  steps[world] is read, and advanced for the
+// ranks that were updated; arrivals is one word, zero between calls; table is
+// where the plan's device table is, if it has one.
+cudaError_t launch_adamw(const AdamWPlan& plan, const char* table, int world, int grad_dtype, bool copies,
+                         const AdamWScalars& s, const float* norms, int32_t* steps, int32_t* arrivals, cudaStream_t stream);
 
 }  // namespace ddpk
