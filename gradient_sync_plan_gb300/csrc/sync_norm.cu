@@ -204,11 +204,11 @@ __global__ void __launch_bounds__(kThreads, MINB) k_sync_norm(const __grid_const
 // Vectors a thread takes of a tile: more of them share a block's fixed costs
 // (its start, the search, the sum), fewer spread a small call over the SMs,
 // and over many ranks one keeps each rank's stream in address order: 355M fp32
-// on 8 ranks 3.28 ms with one, 3.34 with four; on 2 ranks 1.33 and 0.82 ms.
+// on 8 ranks 3.23 ms with one, 3.32 with four; on 5 ranks 2.25 and 2.07 ms.
 constexpr int kSms = 152;
 int sync_norm_vecs(int world, int64_t numel, int dtype) {
     const int64_t vectors = numel / (16 / elem_bytes(dtype));
-    int v = world <= 4 ? 4 : 1;
+    int v = world <= 7 ? 4 : 1;
     while (v > 1 && vectors < (int64_t)v * kThreads * kSms * 8) v /= 2;
     return v;
 }
@@ -310,10 +310,10 @@ static cudaError_t sync_tables(const TAB* tables, size_t n, double* partials, co
 template <class E, class TAB>
 static cudaError_t sync_world(int world, const TAB* tables, size_t n, double* partials, const NormFinish& finish,
                               cudaStream_t st) {
-    // 6.9 TB/s each on the 355M decoder; without side-by-side vectors 6.2 on 2
-    // ranks, with four blocks of 8 ranks' loads 6.7 on 8
+    // 355M fp32: 6.9 TB/s on 2 and 5 ranks, 6.8 on 3, 7.0 on 4 and 8; without
+    // side-by-side vectors 6.2 on 2, with four blocks an SM 6.2 on 3, with four
+    // blocks of 8 ranks' loads 6.7 on 8
     if (world <= 2) return sync_tables<E, 2, 2, 4>(tables, n, partials, finish, st);
-    if (world <= 4) return sync_tables<E, 4, 1, 4>(tables, n, partials, finish, st);
     return sync_tables<E, 4, 1, 5>(tables, n, partials, finish, st);
 }
 
