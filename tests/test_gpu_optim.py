@@ -267,7 +267,7 @@ def _sync_views(world, sizes, dtype, seed, layout):
     (1, [1000, 3], "apart"), (2, [300_001, 7, 0, 40_000], "packed"), (3, [700_001, 1, 5, 900_000], "apart"),
     (5, [1, 2, 3], "odd"), (8, [400_003, 100_000, 999], "odd"), (8, [400_003, 100_000, 999], "apart"),
     (16, [260_000, 9], "apart"), (2, [6_000_001, 100], "apart"), (33, [50_001], "apart"), (4, [800_001, 5], "packed"),
-    (150, [3001, 40], "apart"), (2, [1 + (37 * i) % 911 for i in range(700)], "packed"),
+    (2, [0, 0], "apart"), (150, [3001, 40], "apart"), (2, [1 + (37 * i) % 911 for i in range(700)], "packed"),
 ])
 def test_sync_norm_keeps_the_syncs_bits(world, sizes, layout, dtype, algo):
     hook = algo in (ddp.DDP_ALGO_BF16_HOOK, ddp.DDP_ALGO_BF16_HOOK_VIEW, ddp.DDP_ALGO_FP16_HOOK_VIEW)
@@ -463,6 +463,49 @@ def test_many_tensors_through_changing_calls_and_a_graph():
         reset()
         graph.replay()
         check(call.norms)
+
+
+def _rows(world, count, size, seed, dtype=torch.float32, std=1.0):
+    """[world, count, size rounded up] with zeros past size, and its tensors as views."""
+    width = -(-size // 64) * 64
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.zeros(world, count, width, dtype=dtype, device="cuda")
+    x[:, :, :size].normal_(0.0, std, generator=g)
+    return x, [[x[r, i, :size] for i in range(count)] for r in range(world)]
+
+
+def test_lists_that_take_several_launches_of_their_own():
+    """More tensors than one launch's table takes, and too much data for a table in device memory."""
+    x, views = _rows(1, 1200, 120_001, 3)                # 2 launches of ranges, 576 MB
+    want = float(x.double().square().sum().sqrt())
+    s = ddp.GradSet(views)
+    got = float(s.norm()[0])
+    assert abs(got - want) <= 16 * U * want
+    y = x.double() * min(1.0, 0.25 * want / (got + 1e-6))
+    s.clip(0.25 * want)
+    assert bool(((x.double() - y).abs() <= 4 * U * y.abs() + TINY).all())
+    del s, x, y, views
+    x, views = _rows(2, 310, 110_001, 4)                 # 2 launches of members, 546 MB moved
+    other = x.clone()
+    theirs = [[other[r, i, :110_001] for i in range(310)] for r in range(2)]
+    plan = ddp.ddp_plan_buckets([110_001] * 310, ddp.F32)
+    ddp.ddp_sync_buckets(theirs, plan, None, algo=ddp.DDP_ALGO_VIEW)
+    norms = ddp.SyncNormCall(views, plan)()
+    assert torch.equal(x, other)
+    want = float(other[0].double().square().sum().sqrt())
+    assert bool(((norms.double() - want).abs() <= 16 * U * want).all())
+    del x, other, views, theirs
+    p, pv = _rows(1, 600, 40_001, 5, std=0.02)           # 2 launches of items, 672 MB
+    g, gv = _rows(1, 600, 40_001, 6, std=1e-2)
+    m, mv = _rows(1, 600, 40_001, 7, std=1e-3)
+    v, vv = _rows(1, 600, 40_001, 8, std=1e-3)
+    v.square_()
+    old = [t.clone() for t in (p, m, v, g)]
+    opt = ddp.AdamW(pv, gv, mv, vv, steps=torch.full((1,), 9, dtype=torch.int32, device="cuda"))
+    opt.step(1e-3, weight_decay=0.1)
+    assert opt.steps.tolist() == [10]
+    for t, (want, tol) in zip((p, m, v), _adamw64(*old, 1.0, 10, 1e-3, 0.9, 0.999, 1e-8, 0.1)):
+        assert bool(((t.double() - want).abs() <= tol).all())
 
 
 def test_adamw_skips_ranks_whose_norm_is_not_finite():
