@@ -108,8 +108,10 @@ __device__ __forceinline__ uint32_t magnitude_bits(float4 y) {
 __device__ __forceinline__ uint32_t magnitude_bits(uint4 y) { return (y.x | y.y | y.z | y.w) & 0x7FFF7FFFu; }
 
 // E: element type; G: ranks whose loads are in flight together; B: vectors a
-// thread folds side by side; MINB: blocks an SM has room for.
-template <class E, int G, int B, int MINB, class TAB>
+// thread folds side by side; MINB: blocks an SM has room for; FEW: there are few
+// tiles, and latency counts: a short one goes an element a thread, where a
+// vector's cut ends would go one after the other.
+template <class E, int G, int B, int MINB, bool FEW, class TAB>
 __global__ void __launch_bounds__(kThreads, MINB) k_sync_norm(const __grid_constant__ TAB b, double* partials,
                                                               const __grid_constant__ NormFinish finish) {
     using V = typename E::V;
@@ -125,14 +127,15 @@ __global__ void __launch_bounds__(kThreads, MINB) k_sync_norm(const __grid_const
     const int world = b.world;
     for (int tile = blockIdx.x; tile < b.tiles; tile += gridDim.x) {
         const int i = block_first_past(b.tile_end, b.n, tile, &slot);
-        // pieces: vectors at 16-byte boundaries, or elements where the ranks'
-        // pointers do not line up; positions count from e0, [head, tail) are the member's
+        // positions count from e0, which is at a 16-byte boundary if the ranks'
+        // pointers line up; [head, tail) are the member's
         const int tile_len = kRow * b.vecs;
-        const int step = b.member[i].lead != kRanksDiffer ? L : 1;
         const int lead = b.member[i].lead != kRanksDiffer ? (int)b.member[i].lead : 0;
         const int64_t e0 = (int64_t)(tile - (int)b.member[i].first) * tile_len - lead;
         const int head = e0 < 0 ? (int)-e0 : 0;
         const int tail = (int)min((int64_t)tile_len, b.member[i].numel - e0);
+        // pieces: vectors, or elements where the ranks' pointers do not line up
+        const int step = b.member[i].lead != kRanksDiffer && !(FEW && tail - head <= kThreads) ? L : 1;
         const int64_t q0 = b.member[i].offset + e0;
         const int j0 = chunk_of(q0 + head, b.member[i].clen, b.member[i].inv_clen);
         const int near = (int)min((int64_t)tile_len, (int64_t)(j0 + 1) * b.member[i].clen - q0);     // where chunk j0 ends
@@ -296,10 +299,15 @@ std::shared_ptr<const SyncPlan> make_sync_plan(int world, const SyncMember* memb
     return plan;
 }
 
-template <class E, int G, int B, int MINB, class TAB>
+// Tiles up to which a launch adds its partials itself: a block that arrives
+// waits for its stores first, which costs more than a second launch where there
+// are waves of blocks (3M elements on 3 ranks, 3100 tiles: 29 against 26 us).
+constexpr int32_t kSyncFinishTiles = 608;
+
+template <class E, int G, int B, int MINB, bool FEW, class TAB>
 static cudaError_t sync_tables(const TAB* tables, size_t n, double* partials, const NormFinish& finish, cudaStream_t st) {
     for (size_t k = 0; k < n; ++k) {
-        const cudaError_t e = launch_table(k_sync_norm<E, G, B, MINB, TAB>, dim3(cap_ctas(tables[k].tiles)),
+        const cudaError_t e = launch_table(k_sync_norm<E, G, B, MINB, FEW, TAB>, dim3(cap_ctas(tables[k].tiles)),
                                            dim3(kThreads), st, tables[k], partials, finish);
         if (e != cudaSuccess) return e;
         partials += tables[k].tiles;
@@ -308,18 +316,22 @@ static cudaError_t sync_tables(const TAB* tables, size_t n, double* partials, co
 }
 
 template <class E, class TAB>
-static cudaError_t sync_world(int world, const TAB* tables, size_t n, double* partials, const NormFinish& finish,
-                              cudaStream_t st) {
+static cudaError_t sync_world(int world, bool few, const TAB* tables, size_t n, double* partials,
+                              const NormFinish& finish, cudaStream_t st) {
     // 355M fp32: 6.9 TB/s on 2 and 5 ranks, 6.8 on 3, 7.0 on 4 and 8; without
     // side-by-side vectors 6.2 on 2, with four blocks an SM 6.2 on 3, with four
     // blocks of 8 ranks' loads 6.7 on 8
-    if (world <= 2) return sync_tables<E, 2, 2, 4>(tables, n, partials, finish, st);
-    return sync_tables<E, 4, 1, 5>(tables, n, partials, finish, st);
+    if (world <= 2) return sync_tables<E, 2, 2, 4, false>(tables, n, partials, finish, st);
+    // eight ranks' loads at a time: 181 tensors of 2336 elements on 13 ranks 10.0
+    // against 15.9 us (no gain on up to 4 ranks)
+    if (few && world > 4) return sync_tables<E, 8, 1, 3, true>(tables, n, partials, finish, st);
+    return sync_tables<E, 4, 1, 5, false>(tables, n, partials, finish, st);
 }
 
 template <class E>
 static cudaError_t sync_size(const SyncPlan& p, NormSpace ws, const NormFinish& f, cudaStream_t st) {
-    auto run = [&](const auto& t) { return sync_world<E>(p.world, t.data(), t.size(), ws.partials, f, st); };
+    const bool few = p.tiles <= kSyncFinishTiles;
+    auto run = [&](const auto& t) { return sync_world<E>(p.world, few, t.data(), t.size(), ws.partials, f, st); };
     if (!p.small.empty()) return run(p.small);
     if (!p.medium.empty()) return run(p.medium);
     if (p.device.image.empty()) return run(p.large);
@@ -327,13 +339,8 @@ static cudaError_t sync_size(const SyncPlan& p, NormSpace ws, const NormFinish& 
     d.tile_end = reinterpret_cast<const int32_t*>(ws.table);
     d.member = reinterpret_cast<const Member*>(ws.table + p.device.entries_at);
     d.ptr = reinterpret_cast<char* const*>(ws.table + p.device.more_at);
-    return sync_world<E>(p.world, &d, 1, ws.partials, f, st);
+    return sync_world<E>(p.world, few, &d, 1, ws.partials, f, st);
 }
-
-// Tiles up to which a launch adds its partials itself: a block that arrives
-// waits for its stores first, which costs more than a second launch where there
-// are waves of blocks (3M elements on 3 ranks, 3100 tiles: 29 against 26 us).
-constexpr int32_t kSyncFinishTiles = 608;
 
 cudaError_t launch_sync_norm(const SyncPlan& p, NormSpace ws, float* norms, cudaStream_t st) {
     const int32_t first[2] = {0, p.tiles};
