@@ -212,6 +212,13 @@ def _rank_tensors(bufs) -> list:
     return list(bufs)
 
 
+def _tensors(*tables) -> tuple:
+    """The tensors of tables [r][i] (None: no table).  A handle that holds their
+    addresses keeps these, not the lists it was given: a program may put other
+    tensors into its lists while the handle lives."""
+    return tuple(t for rows in tables if rows is not None for r in range(len(rows)) for t in rows[r])
+
+
 def _check_memory(t, memory: str, what: str) -> None:
     """Device entry points take device memory and host ones host memory: a
     host tensor handed to a kernel by mistake is a bad pointer on a GPU that
@@ -521,7 +528,9 @@ def ddp_sync_buckets(grads: Sequence[Sequence], plan, buckets: Optional[Sequence
 
 class SyncCall:
     """Pre-marshalled ddp_sync_buckets call: builds the pointer tables once so
-    that repeated steps over the same tensors cost one ctypes call each."""
+    that repeated steps over the same tensors cost one ctypes call each.  It
+    works on the tensors that it was given and keeps them: write new gradients
+    into them."""
 
     def __init__(self, grads, plan, buckets=None, divisor=None, algo=DDP_ALGO_FUSED):
         b_of, off, bn = plan
@@ -559,7 +568,7 @@ class SyncCall:
             self._buckets = None
         self.divisor = self.world if divisor is None else int(divisor)
         self.algo = int(algo)
-        self._keep = (grads, buckets)     # the tensors must outlive the call object
+        self._keep = _tensors(grads, buckets)
 
     def __call__(self, stream=None) -> None:
         _check("ddp_sync_buckets",
@@ -609,7 +618,8 @@ class Reducer:
         self.world = world
         self.n_params = len(b_of)
         self.n_buckets = len(bn)
-        self._keep = (grads, buckets, gtab, btab)
+        self._keep = _tensors(grads, buckets)
+        self._tables = (gtab, btab)
         h = ctypes.c_void_p()
         comm = 0 if algo == DDP_ALGO_DRYRUN else _stream(comm_stream)
         _check("ddp_reducer_create",
@@ -690,8 +700,8 @@ def _rank_words(t, world: int, dtype, what: str):
 
 class GradSet:
     """The gradients of one model at every rank (grads[r][i]), for their global
-    norm and clipping (ddp_grad_set_*).  The tensors are checked once; each call
-    is then one ctypes call.  `norms` holds the last norms, one a rank.  The
+    norm and clipping (ddp_grad_set_*).  The tensors are checked once, and kept;
+    each call is then one ctypes call.  `norms` holds the last norms, one a rank.  The
     workspace is allocated on the current stream: a call on another stream comes
     after it (wait_stream), and so do AdamW's and SyncNormCall's."""
 
@@ -707,7 +717,7 @@ class GradSet:
         device = grads[0][0].device if n else "cuda"
         self._workspace = torch.empty(need.value // 8, dtype=torch.float64, device=device)
         self.norms = torch.empty(self.world, dtype=torch.float32, device=device)
-        self._keep = grads
+        self._keep = _tensors(grads)
         h = ctypes.c_void_p()
         _check("ddp_grad_set_create",
                lib().ddp_grad_set_create(self.world, n, _vp_array(ptrs), sizes, code, self._workspace.data_ptr(),
@@ -793,7 +803,8 @@ class AdamW:
     order); gradients float32 or bfloat16, the others float32.  copies: bf16
     tensors that receive the new weights.  no_decay: one truth value a tensor,
     true where weight decay does not apply.  steps: int32 [world], the steps
-    taken so far (zeros if None)."""
+    taken so far (zeros if None).  The handle keeps these tensors: write new
+    gradients into them."""
 
     def __init__(self, params, grads, exp_avg, exp_avg_sq, copies=None, no_decay=None, steps=None):
         torch = _torch()
@@ -821,7 +832,7 @@ class AdamW:
         _check("ddp_adamw_workspace_bytes",
                lib().ddp_adamw_workspace_bytes(self.world, len(sizes), ctypes.byref(need)))
         self._workspace = torch.empty(need.value // 8, dtype=torch.float64, device=device)
-        self._keep = (params, grads, exp_avg, exp_avg_sq, copies)
+        self._keep = _tensors(params, grads, exp_avg, exp_avg_sq, copies) + (self.steps,)
         h = ctypes.c_void_p()
         _check("ddp_adamw_create",
                lib().ddp_adamw_create(self.world, len(sizes), _vp_array(pp), _vp_array(gp),
