@@ -698,12 +698,42 @@ def _rank_words(t, world: int, dtype, what: str):
     return t.data_ptr()
 
 
-class GradSet:
+class _OwnMemory:
+    """Device memory that a handle allocates for itself.  The allocator may give
+    it out again, in the order of the stream it was allocated on, as soon as the
+    handle is gone, while a call on another stream still works on it; so each
+    such stream is recorded with it, once, before its first call."""
+
+    def _owns(self, *tensors):
+        self._own_memory = tensors
+        self._streams = {_stream(None)}      # handles of the streams that the allocator knows of
+
+    def _on(self, stream) -> int:
+        """The handle of the stream a call runs on, which this memory now belongs to as well."""
+        handle = _stream(stream)
+        if handle not in self._streams:
+            cuda = _torch().cuda
+            if handle in (0, 1):             # the legacy default stream's two names
+                stream = cuda.default_stream()
+            elif stream is None:
+                stream = cuda.current_stream()
+            elif isinstance(stream, int):
+                stream = cuda.ExternalStream(handle)
+            for t in self._own_memory:
+                t.record_stream(stream)
+            self._streams.add(handle)
+        return handle
+
+
+class GradSet(_OwnMemory):
     """The gradients of one model at every rank (grads[r][i]), for their global
     norm and clipping (ddp_grad_set_*).  The tensors are checked once, and kept;
     each call is then one ctypes call.  `norms` holds the last norms, one a rank.  The
     workspace is allocated on the current stream: a call on another stream comes
-    after it (wait_stream), and so do AdamW's and SyncNormCall's."""
+    after it (wait_stream), and so do AdamW's and SyncNormCall's.  A handle may go
+    while its calls are still running; a captured graph needs it until the last
+    replay is over, and a stream given as a plain handle has to outlive it.  The
+    gradients' own memory is the caller's to keep until the calls are over."""
 
     def __init__(self, grads):
         torch = _torch()
@@ -717,6 +747,7 @@ class GradSet:
         device = grads[0][0].device if n else "cuda"
         self._workspace = torch.empty(need.value // 8, dtype=torch.float64, device=device)
         self.norms = torch.empty(self.world, dtype=torch.float32, device=device)
+        self._owns(self._workspace, self.norms)
         self._keep = _tensors(grads)
         h = ctypes.c_void_p()
         _check("ddp_grad_set_create",
@@ -731,16 +762,16 @@ class GradSet:
 
     def norm(self, out=None, stream=None):
         """norms[r] of every rank, into `out` or self.norms; returns that tensor."""
-        _check("ddp_grad_norm", self._lib.ddp_grad_norm(self._h, self._norms(out), _stream(stream)))
+        _check("ddp_grad_norm", self._lib.ddp_grad_norm(self._h, self._norms(out), self._on(stream)))
         return self.norms if out is None else out
 
     def clip(self, max_norm: float, norms=None, stream=None) -> None:
         """Scale each rank's gradients by min(1, max_norm / (norms[r] + 1e-6)), in place."""
-        _check("ddp_grad_clip", self._lib.ddp_grad_clip(self._h, self._norms(norms), max_norm, _stream(stream)))
+        _check("ddp_grad_clip", self._lib.ddp_grad_clip(self._h, self._norms(norms), max_norm, self._on(stream)))
 
     def norm_clip(self, max_norm: float, out=None, stream=None):
         """norm() and clip() by it; returns the norms before clipping."""
-        _check("ddp_grad_norm_clip", self._lib.ddp_grad_norm_clip(self._h, self._norms(out), max_norm, _stream(stream)))
+        _check("ddp_grad_norm_clip", self._lib.ddp_grad_norm_clip(self._h, self._norms(out), max_norm, self._on(stream)))
         return self.norms if out is None else out
 
     def close(self):
@@ -755,7 +786,7 @@ class GradSet:
             pass
 
 
-class SyncNormCall(SyncCall):
+class SyncNormCall(_OwnMemory, SyncCall):
     """SyncCall that also returns the norm of the averaged gradients
     (ddp_sync_norm_*): a [world] tensor, the same value for every rank.  The
     arguments are checked and laid out once; each call is one ctypes call."""
@@ -771,6 +802,7 @@ class SyncNormCall(SyncCall):
         device = grads[0][0].device if self.n_params else "cuda"
         self._workspace = torch.empty(need.value // 8, dtype=torch.float64, device=device)
         self.norms = torch.empty(self.world, dtype=torch.float32, device=device)
+        self._owns(self._workspace, self.norms)
         h = ctypes.c_void_p()
         _check("ddp_sync_norm_create",
                lib().ddp_sync_norm_create(self.world, self.n_params, self._grads, self._numel, self._b_of, self._off,
@@ -781,7 +813,7 @@ class SyncNormCall(SyncCall):
         self._own = self.norms.data_ptr()
 
     def __call__(self, stream=None):
-        _check("ddp_sync_norm_run", self._lib.ddp_sync_norm_run(self._h, self._own, _stream(stream)))
+        _check("ddp_sync_norm_run", self._lib.ddp_sync_norm_run(self._h, self._own, self._on(stream)))
         return self.norms
 
     def close(self):
@@ -796,7 +828,7 @@ class SyncNormCall(SyncCall):
             pass
 
 
-class AdamW:
+class AdamW(_OwnMemory):
     """AdamW over every tensor of every rank, clipping included (ddp_adamw_*).
 
     params, grads, exp_avg, exp_avg_sq: [r][i] device tensors (registration
@@ -832,6 +864,7 @@ class AdamW:
         _check("ddp_adamw_workspace_bytes",
                lib().ddp_adamw_workspace_bytes(self.world, len(sizes), ctypes.byref(need)))
         self._workspace = torch.empty(need.value // 8, dtype=torch.float64, device=device)
+        self._owns(self._workspace, *([self.steps] if steps is None else []))
         self._keep = _tensors(params, grads, exp_avg, exp_avg_sq, copies) + (self.steps,)
         h = ctypes.c_void_p()
         _check("ddp_adamw_create",
@@ -849,7 +882,7 @@ class AdamW:
         clip to max_norm, and skip a rank whose norm is not finite."""
         n = None if norms is None else _rank_words(norms, self.world, self._f32, "norms")
         _check("ddp_adamw_step",
-               self._lib.ddp_adamw_step(self._h, lr, betas[0], betas[1], eps, weight_decay, n, max_norm, _stream(stream)))
+               self._lib.ddp_adamw_step(self._h, lr, betas[0], betas[1], eps, weight_decay, n, max_norm, self._on(stream)))
 
     def close(self):
         if getattr(self, "_h", None):
