@@ -40,7 +40,8 @@ struct ddp_sync_norm {
     bool sync_ready = false;                                   // the workspace is set up for `sync`
     // rank 0's gradients, for a norm pass after a sync without one
     std::shared_ptr<const RangePlan> plan;
-    std::vector<std::pair<uintptr_t, uintptr_t>> spans;        // the gradients, buckets and the workspace, sorted
+    std::vector<std::pair<uintptr_t, uintptr_t>> spans;        // the gradients and the workspace, sorted
+    std::vector<std::pair<uintptr_t, uintptr_t>> bucket_spans; // the memory of the buckets, sorted and disjoint
     NormSpace space{nullptr, nullptr, nullptr};
     bool ready = false;                                        // the workspace is set up
 };
@@ -71,6 +72,17 @@ bool any_overlap(std::vector<Span>* v) {
     for (size_t i = 1; i < v->size(); ++i)
         if ((*v)[i].first < (*v)[i - 1].second) return true;
     return false;
+}
+
+// Sorts the spans and joins those that share a byte or touch.
+void unite(std::vector<Span>* v) {
+    std::sort(v->begin(), v->end());
+    size_t n = 0;
+    for (const Span& s : *v) {
+        if (n > 0 && s.first <= (*v)[n - 1].second) (*v)[n - 1].second = std::max((*v)[n - 1].second, s.second);
+        else (*v)[n++] = s;
+    }
+    v->resize(n);
 }
 
 // True if s shares a byte with one of the sorted, disjoint spans.
@@ -336,7 +348,9 @@ int32_t ddp_sync_norm_create(int32_t world, int32_t n_params, void* const* grads
             if (n == 0) continue;
             if ((st = check_ptr(buckets[k], bs))) return st;
             if (hits_any(s->spans, span_of(buckets[k], n * bs))) return DDP_ERR_INVALID;
+            s->bucket_spans.push_back(span_of(buckets[k], n * bs));
         }
+        unite(&s->bucket_spans);
     }
     // a member that continues the one before it, in its bucket and at every rank, joins it
     std::vector<SyncMember> members;
@@ -378,7 +392,8 @@ int32_t ddp_sync_norm_run(ddp_sync_norm* s, float* norms, void* stream) try {
     if (!s) return DDP_ERR_INVALID;
     int32_t st = check_ptr(norms, 4);
     if (st) return st;
-    if (hits_any(s->spans, span_of(norms, 4 * (int64_t)s->world))) return DDP_ERR_INVALID;
+    const Span out = span_of(norms, 4 * (int64_t)s->world);
+    if (hits_any(s->spans, out) || hits_any(s->bucket_spans, out)) return DDP_ERR_INVALID;
     cudaStream_t q = (cudaStream_t)stream;
     // the kernel with the norm is a register kernel: where the TMA-staged view
     // kernel is asked for, or the CTA budget is one that it needs, the sync

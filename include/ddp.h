@@ -690,7 +690,8 @@ int32_t ddp_grad_set_destroy(ddp_grad_set* set);
  *   workspace     device memory, 16-byte aligned, of at least
  *                 ddp_sync_norm_workspace_bytes (DDP_ERR_CAPACITY if smaller),
  *                 for the handle alone (its first run sets it up).  Runs of one handle share it: order them
- *   norms[world]  device float32, outside the gradients and the workspace
+ *   norms[world]  device float32, outside the gradients, the workspace and the
+ *                 bucket buffers of an algorithm that uses them
  * Other arguments as for ddp_sync_buckets (any algo it takes).  The handle keeps
  * the pointers until it is destroyed, the caller keeps the memory.
  */
