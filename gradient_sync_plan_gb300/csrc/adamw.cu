@@ -141,11 +141,17 @@ __global__ void __launch_bounds__(kThreads) k_adamw_advance(const float* norms, 
     advance_steps(norms, steps, world, threadIdx.x, kThreads);
 }
 
+// fp32 gradients with copies never take two groups a thread (make_adamw_plan):
+// no such kernel is built.
+template <class G, bool COPY>
+constexpr bool kOneGroup = COPY && sizeof(G) == 4;
+
 // V: groups of 4 elements a thread takes.
 template <class G, bool COPY, int V, class TAB>
-__global__ void __launch_bounds__(kThreads, V == 2 ? 3 : COPY && sizeof(G) == 4 ? 5 : 4) k_adamw(const __grid_constant__ TAB b,
+__global__ void __launch_bounds__(kThreads, V == 2 ? 3 : kOneGroup<G, COPY> ? 5 : 4) k_adamw(const __grid_constant__ TAB b,
                                                     const __grid_constant__ AdamWScalars s, const float* norms,
                                                     int32_t* steps, int32_t* arrivals, int world) {
+    static_assert(V == 1 || !kOneGroup<G, COPY>, "no call reaches this kernel");
     constexpr int64_t kTile = adamw_tile(V);
     __shared__ RankStep shared_step;
     __shared__ int slot;
@@ -329,8 +335,9 @@ static cudaError_t adamw_size(const AdamWPlan& p, const char* table, int world, 
 template <class G, bool COPY>
 static cudaError_t adamw(const AdamWPlan& p, const char* table, int world, const AdamWScalars& s, const float* norms,
                          int32_t* steps, int32_t* arrivals, cudaStream_t st) {
-    return p.vecs == 1 ? adamw_size<G, COPY, 1>(p, table, world, s, norms, steps, arrivals, st)
-                       : adamw_size<G, COPY, 2>(p, table, world, s, norms, steps, arrivals, st);
+    if constexpr (!kOneGroup<G, COPY>)
+        if (p.vecs == 2) return adamw_size<G, COPY, 2>(p, table, world, s, norms, steps, arrivals, st);
+    return adamw_size<G, COPY, 1>(p, table, world, s, norms, steps, arrivals, st);
 }
 
 cudaError_t launch_adamw(const AdamWPlan& p, const char* table, int world, int grad_dtype, bool copies,
