@@ -710,7 +710,7 @@ class _OwnMemory:
 
     def _on(self, stream) -> int:
         """The handle of the stream a call runs on, which this memory now belongs to as well."""
-        handle = _stream(stream)
+        handle = _raw_stream() if stream is None and _raw_stream is not None else _stream(stream)
         if handle not in self._streams:
             cuda = _torch().cuda
             if handle in (0, 1):             # the legacy default stream's two names
