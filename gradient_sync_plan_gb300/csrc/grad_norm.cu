@@ -7,8 +7,8 @@
 // cut into tiles at 128-byte boundaries of memory: every 16-byte access is
 // aligned wherever a tensor starts, and only a range's first and last vector
 // are taken element by element.  The tables are filled once and travel in the
-// kernels' parameters.  A norm block takes a run of up to four tiles and leaves
-// one partial sum; runs depend on the tensors alone and partials are added in a
+// kernels' parameters.  A norm block takes a run of up to sixteen tiles and
+// leaves one partial sum; runs depend on the tensors alone and partials are added in a
 // fixed order, so a norm does not depend on the grid that computed it.
 #include <cooperative_groups.h>
 
@@ -269,7 +269,8 @@ __device__ __forceinline__ double tile_squares(const typename E::V (&x)[kNormVec
 
 // HBM bounds it: one read of every gradient, 7.58 TB/s on 8 ranks x 355M fp32
 // (1.50 ms).  A thread adds a tile's squares in binary32 and the tiles in
-// binary64; the block joins its threads once a run.  32 registers, so that eight
+// binary64; the block joins its threads' totals, rounded to binary32, once a
+// run.  32 registers, so that eight
 // blocks an SM keep 128 KB of loads in flight: bf16 took 57 with the squares'
 // second pass inlined, and 112 instead of 102 us for 355M.
 template <class E, class TAB>

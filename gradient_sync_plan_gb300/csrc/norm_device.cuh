@@ -1,9 +1,15 @@
 // norm_device.cuh -- sums of squares, shared by the kernels that take a norm.
 //
-// A block adds the squares of its tile in binary32: at most some ten thousand
-// terms, all positive and added as a tree over short chains, so the sum's
-// relative error stays within chain length + 8 units of 2^-24, and far below
-// that on average.  Everything beyond a tile is added in binary64.  A square
+// A thread adds the squares of its part of a tile in binary32 and, where its
+// block takes several tiles for one partial sum, the tiles in binary64.  Its
+// total is rounded to binary32 and the block joins its threads in binary32;
+// partial sums are added in binary64.  That join is a tree of ten additions,
+// less than a long chain's own error, and half the words of one in binary64.
+// All terms are positive, so a partial sum's relative error stays within chain
+// length + 14 units of 2^-24 (3 additions of the chains, the rounding, the
+// join), and far below that on average.  The longest chain has 32 terms: a bf16
+// sync with four vectors a thread that go element by element (the ranks'
+// pointers lie differently against 16 bytes); elsewhere it has up to 16.  A square
 // leaves binary32's range long before its value does (2^-75 squares to nothing,
 // 2^64 to infinity), so a tile with a warp whose sum falls outside
 // [2^-90, 2^112] squares again with scaled values, from registers or memory that

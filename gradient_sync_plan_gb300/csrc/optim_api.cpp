@@ -397,7 +397,13 @@ int32_t ddp_sync_norm_run(ddp_sync_norm* s, float* norms, void* stream) try {
     cudaStream_t q = (cudaStream_t)stream;
     // the kernel with the norm is a register kernel: where the TMA-staged view
     // kernel is asked for, or the CTA budget is one that it needs, the sync
-    // runs as ddp_sync_buckets runs it and the norm takes a pass over rank 0
+    // runs as ddp_sync_buckets runs it and the norm takes a pass over rank 0.
+    // From 16 ranks, below 128 MiB moved, ddp_sync_buckets takes the TMA-staged
+    // kernel by itself; this call stays on its own there, which wins and loses
+    // (this call, then sync and norm pass, in us): 16 ranks of 1.26M elements in
+    // 184 tensors 36.2 and 43.1, of 500K in 40 19.0 and 17.6; 32 ranks of 30K in
+    // 40 15.3 and 30.3, of 250K in 40 21.9 and 18.8; 64 ranks of 16K in 40 28.6
+    // and 48.3, of 250K in 60 59.3 and 45.5
     const bool fused = s->sync && fused_kernel_override() != DDP_FUSED_TMA && !cta_cap_is_tight();
     if (fused) {
         NormSpace ws = s->space;

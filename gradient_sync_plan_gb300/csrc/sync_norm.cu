@@ -320,7 +320,11 @@ static cudaError_t sync_world(int world, bool few, const TAB* tables, size_t n, 
                               const NormFinish& finish, cudaStream_t st) {
     // 355M fp32: 6.9 TB/s on 2 and 5 ranks, 6.8 on 3, 7.0 on 4 and 8; without
     // side-by-side vectors 6.2 on 2, with four blocks an SM 6.2 on 3, with four
-    // blocks of 8 ranks' loads 6.7 on 8
+    // blocks of 8 ranks' loads 6.7 on 8.  The same shapes run the other types:
+    // bf16 6.4 TB/s on 2 ranks, 6.9 on 4 and 8; the bf16 hook 6.7, 6.9 and 6.9,
+    // the fp16 hook 6.5, 6.9 and 6.9.  Two vectors of 16-bit or hook arithmetic
+    // side by side spill 56 to 100 bytes, tables in device memory 52 to 288 but
+    // in the shape of eight ranks' loads
     if (world <= 2) return sync_tables<E, 2, 2, 4, false>(tables, n, partials, finish, st);
     // eight ranks' loads at a time: 181 tensors of 2336 elements on 13 ranks 10.0
     // against 15.9 us (no gain on up to 4 ranks)

@@ -630,11 +630,13 @@ int32_t ddp_bucket_allreduce_view_fp16(int32_t world, int32_t n_in_bucket, void*
  * its launches, however many tensors there are.
  *
  *   ddp_grad_norm       norms[r] = sqrt(sum of g^2 over every element of rank
- *                       r's tensors).  Squares are added in binary32 within a
- *                       tile of a few thousand and in binary64 beyond it; values
- *                       whose squares would leave binary32's range are scaled
- *                       first, so that a norm is right whenever it is itself a
- *                       binary32 number.  An infinity or NaN among the
+ *                       r's tensors).  Squares are added in binary32 by a
+ *                       thread within a tile of a few thousand elements, up to
+ *                       sixteen tiles in binary64; a block joins its threads'
+ *                       totals in binary32, and all beyond it is binary64.
+ *                       Values whose squares would leave binary32's range are
+ *                       scaled first, so that a norm is right whenever it is
+ *                       itself a binary32 number.  An infinity or NaN among the
  *                       gradients makes the norm one.  No elements: 0.
  *                       The additions' order depends on the tensors' sizes and
  *                       addresses only: neither ddp_set_max_ctas nor a repeat
@@ -642,8 +644,9 @@ int32_t ddp_bucket_allreduce_view_fp16(int32_t world, int32_t n_in_bucket, void*
  *   ddp_grad_clip       g <- c g with c = min(1, max_norm / (norms[r] + 1e-6)),
  *                       rounded once to the gradients' type; c = 1 leaves rank
  *                       r's gradients untouched.  An infinite norm gives c = 0
- *                       (and NaN where the gradient is infinite), a NaN norm
- *                       NaN: test the norms if that may happen.
+ *                       (and NaN where the gradient is infinite; an infinite
+ *                       max_norm with it NaN everywhere), a NaN norm NaN: test
+ *                       the norms if that may happen.
  *   ddp_grad_norm_clip  the two in order.
  *
  *   grads[world*n_params] host table of device pointers, rank-major; no two
@@ -655,8 +658,9 @@ int32_t ddp_bucket_allreduce_view_fp16(int32_t world, int32_t n_in_bucket, void*
  *   workspace             device memory, 16-byte aligned, of at least
  *                         ddp_grad_set_workspace_bytes (DDP_ERR_CAPACITY if
  *                         smaller), for the set alone (its first call sets it
- *                         up); the set keeps it, the caller owns it.  Calls on one set share it: order them (one
- *                         stream, or events)
+ *                         up); the set keeps it, the caller owns it.  Calls on
+ *                         one set share it: order them (one stream, or events).
+ *                         A captured call keeps working on it
  *   norms[world]          device float32, outside the tensors and the workspace
  *   max_norm              > 0 (may be infinite)
  * The set keeps these pointers until it is destroyed, the caller keeps the
@@ -689,7 +693,9 @@ int32_t ddp_grad_set_destroy(ddp_grad_set* set);
  * costs its launches.
  *   workspace     device memory, 16-byte aligned, of at least
  *                 ddp_sync_norm_workspace_bytes (DDP_ERR_CAPACITY if smaller),
- *                 for the handle alone (its first run sets it up).  Runs of one handle share it: order them
+ *                 for the handle alone (its first run sets it up).  Runs of
+ *                 one handle share it: order them.  A captured run keeps
+ *                 working on it
  *   norms[world]  device float32, outside the gradients, the workspace and the
  *                 bucket buffers of an algorithm that uses them
  * Other arguments as for ddp_sync_buckets (any algo it takes).  The handle keeps
@@ -737,7 +743,8 @@ int32_t ddp_sync_norm_destroy(ddp_sync_norm* sync);
  *   workspace            device memory, 16-byte aligned, of at least
  *                        ddp_adamw_workspace_bytes (DDP_ERR_CAPACITY if smaller),
  *                        for the handle alone (its first step sets it up).  Steps
- *                        of one handle must not overlap on the GPU
+ *                        of one handle must not overlap on the GPU.  A captured
+ *                        step keeps working on it
  *   lr >= 0, 0 <= beta < 1, eps > 0, weight_decay >= 0, max_norm > 0 with norms
  * Nothing that a step writes may overlap anything else of the handle;
  * gradients may overlap each other (ranks may share one).  The handle keeps the
