@@ -216,7 +216,11 @@ def _tensors(*tables) -> tuple:
     """The tensors of tables [r][i] (None: no table).  A handle that holds their
     addresses keeps these, not the lists it was given: a program may put other
     tensors into its lists while the handle lives."""
-    return tuple(t for rows in tables if rows is not None for r in range(len(rows)) for t in rows[r])
+    kept = []
+    for rows in tables:
+        for r in range(len(rows) if rows is not None else 0):
+            kept.extend(rows[r])
+    return tuple(kept)
 
 
 def _check_memory(t, memory: str, what: str) -> None:
