@@ -30,7 +30,9 @@ DDP_ALGO_BF16_HOOK = 4
 DDP_ALGO_BF16_HOOK_VIEW = 5
 DDP_ALGO_FP16_HOOK_VIEW = 6
 DDP_FUSED_AUTO, DDP_FUSED_VECTOR, DDP_FUSED_GROUP, DDP_FUSED_TMA = 0, 1, 2, 3
+DDP_LOSS_SUM, DDP_LOSS_MEAN, DDP_LOSS_WORLD_MEAN = 0, 1, 2
 DDP_MAX_WORLD = 512
+DDP_MAX_VOCAB, DDP_MAX_DIM, DDP_MAX_TEACHER = 1 << 24, 1 << 16, 256      # of a loss head
 MAX_NUMEL = 1 << 40                  # DDP_MAX_NUMEL: elements of one rank's buffer
 FIRST_BUCKET_BYTES = 1 << 20          # 1 MiB
 BUCKET_CAP_BYTES = 25 << 20           # 25 MiB
@@ -52,7 +54,9 @@ EXPORTS = ["ddp_status_string", "ddp_abi_version", "ddp_last_cuda_error", "ddp_d
            "ddp_reducer_launch_order", "ddp_reducer_bucket_times", "ddp_reducer_destroy",
            "ddp_grad_set_workspace_bytes", "ddp_grad_set_create", "ddp_grad_norm", "ddp_grad_clip", "ddp_grad_norm_clip",
            "ddp_grad_set_destroy", "ddp_sync_norm_workspace_bytes", "ddp_sync_norm_create", "ddp_sync_norm_run",
-           "ddp_sync_norm_destroy", "ddp_adamw_workspace_bytes", "ddp_adamw_create", "ddp_adamw_step", "ddp_adamw_destroy"]
+           "ddp_sync_norm_destroy", "ddp_adamw_workspace_bytes", "ddp_adamw_create", "ddp_adamw_step", "ddp_adamw_destroy",
+           "ddp_loss_head_workspace_bytes", "ddp_loss_head_create", "ddp_cross_entropy", "ddp_cross_entropy_grad",
+           "ddp_distill", "ddp_distill_grad", "ddp_loss_head_destroy"]
 
 
 class DDPError(RuntimeError):
@@ -138,6 +142,15 @@ def lib() -> ctypes.CDLL:
                                            P(vp)]
             L.ddp_adamw_step.argtypes = [vp, f64, f64, f64, f64, f64, vp, f64, vp]
             L.ddp_adamw_destroy.argtypes = [vp]
+            L.ddp_loss_head_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32, i32, P(i64)]
+            L.ddp_loss_head_create.argtypes = [i32, P(vp), P(vp), i32, i32, i32, i32, i32, vp, i64, P(vp)]
+            tokens, labels, losses = [vp, P(i32), P(vp), i64], [P(vp), i64, i32], [P(vp), vp]
+            teacher = [i32, P(vp), i32, P(vp), f64, f64]
+            L.ddp_cross_entropy.argtypes = tokens + labels + losses + [vp]
+            L.ddp_cross_entropy_grad.argtypes = tokens + labels + [f64, i32] + losses + [P(vp), vp]
+            L.ddp_distill.argtypes = tokens + teacher + labels + losses + [vp]
+            L.ddp_distill_grad.argtypes = tokens + teacher + labels + [f64, i32] + losses + [P(vp), vp]
+            L.ddp_loss_head_destroy.argtypes = [vp]
             for name in EXPORTS[4:]:   # every entry point from ddp_set_max_ctas on returns a status
                 getattr(L, name).restype = i32
             _lib = L
@@ -891,6 +904,142 @@ class AdamW(_OwnMemory):
     def close(self):
         if getattr(self, "_h", None):
             lib().ddp_adamw_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class LossHead(_OwnMemory):
+    """The losses over a vocabulary that a step's gradients begin with, and those
+    gradients (ddp_loss_head_*): cross entropy, and distillation from a teacher's top
+    logits, from the hidden states and the head's weights, without keeping logits.
+
+    weights[r]: rank r's [vocab, dim] tensor, float32 or bfloat16; grads[r]: the
+    tensors that its gradients go to (None: losses alone).  Calls take up to max_tokens
+    tokens a rank, and max_teacher entries of a teacher a token.  The handle keeps
+    these tensors; `loss` holds the last losses, one a rank.  hidden, targets and so
+    on are lists with a tensor a rank: hidden [tokens, dim] (rows may be apart, equally
+    at every rank), targets int64 [tokens].  The workspace is
+    allocated on the current stream: a call on another stream comes after it
+    (wait_stream).  A handle may go while its calls are still running; a captured
+    graph needs it until the last replay is over."""
+
+    def __init__(self, weights, grads=None, max_tokens: int = 1, max_teacher: int = 0):
+        torch = _torch()
+        self.world = len(weights)
+        types = (torch.float32, torch.bfloat16)
+        wp, _, self.dtype = _tensor_table([[w] for w in weights], "weights", types)
+        shape = tuple(weights[0].shape) if weights else (0, 0)
+        if len(shape) != 2 or any(tuple(w.shape) != shape for w in weights):
+            raise ValueError("weights: [vocab, dim] tensors, one a rank")
+        self.vocab, self.dim = shape
+        gp = None
+        if grads is not None:
+            if len(grads) != self.world or any(tuple(g.shape) != shape for g in grads):
+                raise ValueError("grads: tensors of the weights' shape, one a rank")
+            gp = _vp_array(_tensor_table([[g] for g in grads], "grads", (self.dtype,))[0])
+        code = BF16 if self.dtype == torch.bfloat16 else F32
+        need = ctypes.c_int64(0)
+        _check("ddp_loss_head_workspace_bytes",
+               lib().ddp_loss_head_workspace_bytes(self.world, self.vocab, self.dim, code, int(max_tokens), int(max_teacher),
+                                                   0 if grads is None else 1, ctypes.byref(need)))
+        self.device = weights[0].device
+        self._same_device("weights", weights, grads or [])
+        self._workspace = torch.empty(need.value, dtype=torch.uint8, device=self.device)
+        self.loss = torch.empty(self.world, dtype=torch.float32, device=self.device)
+        self._owns(self._workspace, self.loss)
+        self._keep = tuple(weights) + tuple(grads or [])
+        h = ctypes.c_void_p()
+        _check("ddp_loss_head_create",
+               lib().ddp_loss_head_create(self.world, _vp_array(wp), gp, self.vocab, self.dim, code, int(max_tokens),
+                                          int(max_teacher), self._workspace.data_ptr(), need.value, ctypes.byref(h)))
+        self._h = h
+        self._lib = lib()
+
+    def _same_device(self, what, *lists):
+        device = _torch().cuda.current_device()
+        for ts in lists:
+            for t in ts:
+                if t is not None and (not t.is_cuda or t.device.index != device):
+                    raise ValueError(f"{what} must be in device memory of the current device")
+
+    def _table(self, ts, what: str, dtypes, shapes):
+        """Pointers of contiguous tensors, one a rank, of these shapes."""
+        if len(ts) != self.world:
+            raise ValueError(f"{what}: one tensor a rank")
+        for t, shape in zip(ts, shapes):
+            if t.dtype not in dtypes or t.dtype != ts[0].dtype or tuple(t.shape) != shape or not t.is_contiguous():
+                raise ValueError(f"{what}: contiguous tensors of {' or '.join(map(str, dtypes))}, {shape} here")
+        self._same_device(what, ts)
+        return _vp_array([t.data_ptr() for t in ts])
+
+    def _call(self, fn, hidden, targets, teacher, gradients, ignore_index, reduction, token_losses, out, stream):
+        torch = _torch()
+        if len(hidden) != self.world:
+            raise ValueError("hidden: one tensor a rank")
+        stride = None
+        for h in hidden:
+            if h.dim() != 2 or h.shape[1] != self.dim or h.dtype != self.dtype or (self.dim > 1 and h.stride(1) != 1):
+                raise ValueError(f"hidden: [tokens, {self.dim}] tensors of {self.dtype}, elements of a row together")
+            if h.shape[0] > 1:
+                stride = h.stride(0) if stride is None else stride
+                if h.stride(0) != stride:
+                    raise ValueError("hidden: rows equally far apart at every rank")
+        self._same_device("hidden", hidden)
+        tokens = [h.shape[0] for h in hidden]
+        flat = [(n,) for n in tokens]
+        args = [self._h, _i32_array(tokens), _vp_array([h.data_ptr() for h in hidden]), self.dim if stride is None else stride]
+        if teacher is not None:
+            logits, indices, temperature, alpha = teacher
+            k = logits[0].shape[1] if len(logits) and logits[0].dim() == 2 else 0
+            rows = [(n, k) for n in tokens]
+            lp = self._table(logits, "teacher", (torch.float32, torch.bfloat16), rows)
+            args += [k, lp, dtype_code(logits[0]), self._table(indices, "indices", (torch.int64,), rows), temperature, alpha]
+        args += [None if targets is None else self._table(targets, "targets", (torch.int64,), flat), ignore_index, reduction]
+        if gradients is not None:
+            args += [gradients[1], 1 if gradients[2] else 0]
+        args.append(None if token_losses is None else self._table(token_losses, "token_losses", (torch.float32,), flat))
+        args.append(_rank_words(self.loss if out is None else out, self.world, torch.float32, "out"))
+        if gradients is not None:
+            args.append(self._table(gradients[0], "grad_hidden", (self.dtype,), [(n, self.dim) for n in tokens]))
+        _check(fn, getattr(self._lib, fn)(*args, self._on(stream)))
+        return self.loss if out is None else out
+
+    def cross_entropy(self, hidden, targets, ignore_index: int = -100, reduction: int = DDP_LOSS_MEAN, token_losses=None,
+                      out=None, stream=None):
+        """loss[r] of every rank, into `out` or self.loss; returns that tensor.
+        token_losses[r]: float32 [tokens] tensors for each token's loss."""
+        return self._call("ddp_cross_entropy", hidden, targets, None, None, ignore_index, reduction, token_losses, out, stream)
+
+    def cross_entropy_grad(self, hidden, targets, grad_hidden, ignore_index: int = -100, reduction: int = DDP_LOSS_MEAN,
+                           scale: float = 1.0, accumulate: bool = False, token_losses=None, out=None, stream=None):
+        """cross_entropy(), and the gradients of scale * loss[r]: into grad_hidden[r]
+        (as hidden[r], contiguous) and the handle's grads (added to them if accumulate)."""
+        return self._call("ddp_cross_entropy_grad", hidden, targets, None, (grad_hidden, scale, accumulate), ignore_index,
+                          reduction, token_losses, out, stream)
+
+    def distill(self, hidden, teacher, indices, temperature: float = 1.0, alpha: float = 1.0, targets=None,
+                ignore_index: int = -100, reduction: int = DDP_LOSS_MEAN, token_losses=None, out=None, stream=None):
+        """The distillation loss from teacher[r] ([tokens, entries] logits, float32 or
+        bfloat16) at the columns indices[r] (int64; negative: no entry), with a share of
+        1 - alpha of the targets' cross entropy."""
+        return self._call("ddp_distill", hidden, targets, (teacher, indices, temperature, alpha), None, ignore_index,
+                          reduction, token_losses, out, stream)
+
+    def distill_grad(self, hidden, teacher, indices, grad_hidden, temperature: float = 1.0, alpha: float = 1.0, targets=None,
+                     ignore_index: int = -100, reduction: int = DDP_LOSS_MEAN, scale: float = 1.0, accumulate: bool = False,
+                     token_losses=None, out=None, stream=None):
+        """distill(), and the gradients as cross_entropy_grad's."""
+        return self._call("ddp_distill_grad", hidden, targets, (teacher, indices, temperature, alpha),
+                          (grad_hidden, scale, accumulate), ignore_index, reduction, token_losses, out, stream)
+
+    def close(self):
+        if getattr(self, "_h", None):
+            lib().ddp_loss_head_destroy(self._h)
             self._h = None
 
     def __del__(self):

@@ -1,0 +1,514 @@
+// loss_api.cpp -- the C ABI of the loss head: argument checks, the workspace's
+// layout, tensor maps, and the order of a call's launches.
+//
+// A call runs: the teachers' lists (distillation) and the scan, for all ranks; then
+// for groups of kLossRanks ranks the gather, the logits' statistics and their
+// combination into losses; with gradients also, for each piece of the vocabulary,
+// its logits' gradients and the two products with them, and the join.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <climits>
+#include <cmath>
+#include <memory>
+#include <vector>
+
+#include "ddp_abi_guard.h"
+#include "ddp.h"
+#include "ddp_spans.h"
+#include "ddp_trace.h"
+#include "loss_internal.h"
+
+using namespace ddpk;
+
+namespace {
+
+// Bytes of a piece's logits' gradients that the workspace has room for.  A piece is written once and read a few
+// times, so that it need not fit the L2; fewer pieces mean fewer passes over the hidden states' sums.
+constexpr int64_t kPieceBytes = (int64_t)512 << 20;
+constexpr int64_t kSms = 152;
+constexpr int64_t kPieceAlign = 256;              // columns of a piece: a multiple of the tiles'
+
+int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
+
+// How many parts the depth of the hidden states' gradients is cut into, for at least two tiles an SM and four k
+// blocks a part.
+int64_t splits_for(int64_t rows, int64_t dim, int64_t width) {
+    const int64_t tiles = std::max<int64_t>(1, rows / kTileM * ((dim + kTileN - 1) / kTileN));
+    const int64_t blocks = (width + kTileK - 1) / kTileK;
+    const int64_t want = std::min((2 * kSms + tiles - 1) / tiles, (blocks + 3) / 4);
+    const int64_t part = (blocks + want - 1) / want;
+    return (blocks + part - 1) / part;
+}
+
+// The widest piece of `bytes` for the rows of a group, balanced over the pieces that the vocabulary then takes.
+int64_t piece_width(int64_t bytes, int64_t rows, int64_t vocab, int64_t planes) {
+    const int64_t all = round_up(vocab, kPieceAlign);
+    int64_t w = std::max(bytes / (2 * planes * std::max<int64_t>(rows, 1)) / kPieceAlign * kPieceAlign, kPieceAlign);
+    w = std::min(w, all);
+    const int64_t pieces = (all + w - 1) / w;
+    return round_up((vocab + pieces - 1) / pieces, kPieceAlign);
+}
+
+struct Sizes {
+    int64_t counts, done, row_token, token_row, row_column, valid, columns, starts, share, entropy, z, value, partial, coef,
+        block_loss, gathered, acc, piece, weights;   // offsets, and the last two also bytes below
+    int64_t acc_bytes, piece_bytes, weights_bytes, total;
+};
+
+}  // namespace
+
+struct ddp_loss_head {
+    int32_t world = 0, vocab = 0, dim = 0, dtype = 0, max_tokens = 0, max_teacher = 0;
+    std::vector<const void*> weights;
+    std::vector<void*> grads;
+    char* workspace = nullptr;
+    Sizes at{};
+    std::vector<std::pair<uintptr_t, uintptr_t>> read, written;    // the weights; the workspace and the gradients
+    std::vector<CUtensorMap> maps;                                 // of the weights, or their planes
+    int64_t copied = 0;                                            // bytes of a rank's planes in the workspace, 0: none
+    int32_t* status = nullptr;
+    int device = -1;                                               // that maps and status belong to
+};
+
+namespace {
+
+int planes_of(int32_t dtype) { return dtype == DDP_F32 ? 3 : 1; }
+
+Sizes layout(int64_t world, int64_t vocab, int64_t dim, int32_t dtype, int64_t max_tokens, int64_t max_teacher, bool grads) {
+    Sizes s{};
+    const int64_t rows = world * round_up(max_tokens, kLossRowAlign), planes = planes_of(dtype), dimp = round_up(dim, kTileK);
+    const int64_t list = max_teacher + 1, units = (vocab + kLossUnit - 1) / kLossUnit;
+    const int64_t group = std::min<int64_t>(world, kLossRanks) * round_up(max_tokens, kLossRowAlign);
+    int64_t at = 0;
+    const auto put = [&](int64_t* offset, int64_t bytes) {
+        *offset = at;
+        at += round_up(bytes, 256);
+    };
+    put(&s.counts, 4 * world);
+    put(&s.done, 4);
+    put(&s.row_token, 4 * rows);
+    put(&s.token_row, 4 * rows);
+    put(&s.row_column, 4 * rows);
+    put(&s.block_loss, 8 * (rows / kLossBlockRows));
+    put(&s.z, 4 * rows * list);
+    put(&s.partial, (max_teacher ? 16 : 8) * units * rows);
+    if (max_teacher) {
+        put(&s.valid, rows);
+        put(&s.columns, 4 * rows * list);
+        put(&s.starts, 2 * rows * (units + 1));
+        put(&s.share, 4 * rows * list);
+        put(&s.entropy, 4 * rows);
+    }
+    put(&s.gathered, 2 * planes * rows * dimp);
+    s.weights_bytes = 2 * planes * vocab * dimp;
+    // planes of the weights: always for float32; for bf16 where rows do not start on 16-byte boundaries
+    put(&s.weights, dtype == DDP_F32 || dim % 8 ? world * s.weights_bytes : 0);
+    if (grads) {
+        put(&s.value, 4 * rows * list);
+        put(&s.coef, 16 * rows);
+        // at most 2 kSms / tiles + 1 splits (splits_for), for any number of rows up to these
+        s.acc_bytes = 4 * (2 * kSms * kTileM * kTileN + rows * dimp);
+        put(&s.acc, s.acc_bytes);
+        s.piece_bytes = 2 * planes * group * piece_width(kPieceBytes, group, vocab, planes);
+        put(&s.piece, s.piece_bytes);
+    }
+    s.total = at;
+    return s;
+}
+
+int32_t check_head(int32_t world, int32_t vocab, int32_t dim, int32_t dtype, int32_t max_tokens, int32_t max_teacher) {
+    const int32_t st = common_checks(world, 0, dtype);
+    if (st) return st;
+    if (vocab < 1 || dim < 1 || max_tokens < 1 || max_teacher < 0) return DDP_ERR_INVALID;
+    if (vocab > DDP_MAX_VOCAB || dim > DDP_MAX_DIM || max_teacher > DDP_MAX_TEACHER ||
+        world * round_up(max_tokens, kLossRowAlign) > ((int64_t)1 << 28))
+        return DDP_ERR_CAPACITY;
+    return DDP_OK;
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+cudaError_t encoder(EncodeFn* fn) {
+    static std::atomic<EncodeFn> found{nullptr};
+    *fn = found.load();
+    if (*fn) return cudaSuccess;
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q);
+    if (e != cudaSuccess) return e;
+    if (q != cudaDriverEntryPointSuccess || !p) return cudaErrorNotSupported;
+    *fn = reinterpret_cast<EncodeFn>(p);
+    found.store(*fn);
+    return cudaSuccess;
+}
+
+// [planes][rows][columns] bf16, plane_bytes apart, in boxes of 64 x 64.
+int32_t map_bf16(CUtensorMap* m, const void* base, int64_t columns, int64_t rows, int64_t row_bytes, int64_t planes,
+                 int64_t plane_bytes) {
+    EncodeFn fn;
+    const int32_t st = cuda_status(encoder(&fn));
+    if (st) return st;
+    const cuuint64_t dims[3] = {(cuuint64_t)columns, (cuuint64_t)rows, (cuuint64_t)planes};
+    const cuuint64_t strides[2] = {(cuuint64_t)row_bytes, (cuuint64_t)round_up(plane_bytes, 16)};
+    const cuuint32_t box[3] = {64, 64, 1}, steps[3] = {1, 1, 1};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, steps,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? DDP_OK : cuda_status(cudaErrorInvalidValue);
+}
+// [rows][columns] float32 in boxes of 128 rows of 32.
+int32_t map_f32(CUtensorMap* m, const void* base, int64_t columns, int64_t rows) {
+    EncodeFn fn;
+    const int32_t st = cuda_status(encoder(&fn));
+    if (st) return st;
+    const cuuint64_t dims[2] = {(cuuint64_t)columns, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)columns * 4};
+    const cuuint32_t box[2] = {32, kTileM}, steps[2] = {1, 1};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(base), dims, strides, box, steps,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? DDP_OK : cuda_status(cudaErrorInvalidValue);
+}
+
+// What belongs to the device that a head's memory is on, at its first call.
+int32_t bind_device(ddp_loss_head* h) {
+    int device = 0;
+    int32_t st = cuda_status(cudaGetDevice(&device));
+    if (st) return st;
+    if (h->device >= 0) return device == h->device ? DDP_OK : DDP_ERR_INVALID;
+    if ((st = cuda_status(device_status_address(&h->status)))) return st;
+    const int64_t dimp = round_up(h->dim, kTileK), planes = planes_of(h->dtype);
+    h->maps.resize(h->world);
+    for (int32_t r = 0; r < h->world; ++r) {
+        if (h->copied)
+            st = map_bf16(&h->maps[r], h->workspace + h->at.weights + r * h->copied, dimp, h->vocab, 2 * dimp, planes,
+                          2 * h->vocab * dimp);
+        else
+            st = map_bf16(&h->maps[r], h->weights[r], h->dim, h->vocab, 2 * (int64_t)h->dim, 1, 2 * (int64_t)h->vocab * h->dim);
+        if (st) return st;
+    }
+    h->device = device;
+    return DDP_OK;
+}
+
+// The arguments that the four losses share.
+struct Args {
+    const int32_t* tokens;
+    const void* const* hidden;
+    int64_t hidden_stride;
+    const int64_t* const* targets;
+    int64_t ignore_index;
+    int32_t reduction;
+    float* const* token_losses;
+    float* loss;
+    // distillation
+    int32_t n_teacher = 0;
+    const void* const* teacher = nullptr;
+    int32_t teacher_dtype = DDP_F32;
+    const int64_t* const* indices = nullptr;
+    double temperature = 1.0, alpha = 0.0;
+    // gradients
+    bool grad = false;
+    double scale = 1.0;
+    int32_t accumulate = 0;
+    void* const* grad_hidden = nullptr;
+};
+
+int32_t check_args(const ddp_loss_head& h, const Args& a) {
+    if (!a.tokens || a.reduction < DDP_LOSS_SUM || a.reduction > DDP_LOSS_WORLD_MEAN) return DDP_ERR_INVALID;
+    const bool distill = a.alpha != 0.0;
+    if (!a.hidden || (!distill && !a.targets) || a.hidden_stride < h.dim) return DDP_ERR_INVALID;
+    if (a.hidden_stride > DDP_MAX_NUMEL / std::max(h.max_tokens, 1)) return DDP_ERR_CAPACITY;
+    if (distill) {
+        if (!a.teacher || !a.indices || a.n_teacher < 1) return DDP_ERR_INVALID;
+        if (a.n_teacher > h.max_teacher) return DDP_ERR_CAPACITY;
+        if (a.teacher_dtype != DDP_F32 && a.teacher_dtype != DDP_BF16) return DDP_ERR_INVALID;
+        if (!((float)a.temperature > 0.f) || !std::isfinite((float)a.temperature) ||
+            !std::isfinite((float)(1.0 / a.temperature)) || !(a.alpha > 0.0 && a.alpha <= 1.0) || !((float)a.alpha > 0.f))
+            return DDP_ERR_INVALID;
+        if (!a.targets && a.alpha != 1.0) return DDP_ERR_INVALID;
+    }
+    if (a.grad && (h.grads.empty() || !a.grad_hidden || !std::isfinite((float)a.scale))) return DDP_ERR_INVALID;
+    int32_t st = check_ptr(a.loss, 4);
+    if (st) return st;
+    const int64_t es = elem_bytes(h.dtype), ts = elem_bytes(a.teacher_dtype);
+    std::vector<Span> written(h.written), read(h.read);
+    written.push_back(span_of(a.loss, 4 * (int64_t)h.world));
+    for (int32_t r = 0; r < h.world; ++r) {
+        const int64_t n = a.tokens[r];
+        if (n < 0) return DDP_ERR_INVALID;
+        if (n > h.max_tokens) return DDP_ERR_CAPACITY;
+        if (n == 0) continue;
+        if ((st = check_ptr(a.hidden[r], es))) return st;
+        read.push_back(span_of(a.hidden[r], ((n - 1) * a.hidden_stride + h.dim) * es));
+        if (a.targets) {
+            if ((st = check_ptr(a.targets[r], 8))) return st;
+            read.push_back(span_of(a.targets[r], 8 * n));
+        }
+        if (distill) {
+            if ((st = check_ptr(a.teacher[r], ts)) || (st = check_ptr(a.indices[r], 8))) return st;
+            read.push_back(span_of(a.teacher[r], ts * n * a.n_teacher));
+            read.push_back(span_of(a.indices[r], 8 * n * a.n_teacher));
+        }
+        if (a.token_losses && a.token_losses[r]) {
+            if ((st = check_ptr(a.token_losses[r], 4))) return st;
+            written.push_back(span_of(a.token_losses[r], 4 * n));
+        }
+        if (a.grad) {
+            if ((st = check_ptr(a.grad_hidden[r], es))) return st;
+            written.push_back(span_of(a.grad_hidden[r], n * h.dim * es));
+        }
+    }
+    if (any_overlap(&written)) return DDP_ERR_INVALID;
+    for (const Span& s : read)
+        if (hits_any(written, s)) return DDP_ERR_INVALID;
+    return DDP_OK;
+}
+
+int32_t run(ddp_loss_head* h, const Args& a, cudaStream_t stream) {
+    int32_t st = check_args(*h, a);
+    if (st) return st;
+    if ((st = bind_device(h))) return st;
+    const bool distill = a.alpha != 0.0;
+    LossCall c{};
+    c.vocab = h->vocab;
+    c.dim = h->dim;
+    c.dimp = (int32_t)round_up(h->dim, kTileK);
+    c.dtype = h->dtype;
+    c.planes = planes_of(h->dtype);
+    c.teacher_dtype = a.teacher_dtype;
+    c.n_teacher = a.n_teacher;
+    c.list = distill ? a.n_teacher + (a.targets ? 1 : 0) : 1;
+    c.units = (h->vocab + kLossUnit - 1) / kLossUnit;
+    c.reduction = a.reduction;
+    c.alpha = (float)a.alpha;
+    c.temperature = (float)a.temperature;
+    c.inv_temperature = (float)(1.0 / a.temperature);
+    c.two = distill && c.alpha < 1.f && c.temperature != 1.f;
+    c.hidden_stride = a.hidden_stride;
+    c.ignore_index = a.ignore_index;
+    c.scale = (float)a.scale;
+    char* w = h->workspace;
+    const Sizes& at = h->at;
+    c.counts = reinterpret_cast<int32_t*>(w + at.counts);
+    c.done = reinterpret_cast<int32_t*>(w + at.done);
+    c.row_token = reinterpret_cast<int32_t*>(w + at.row_token);
+    c.token_row = reinterpret_cast<int32_t*>(w + at.token_row);
+    c.row_column = reinterpret_cast<int32_t*>(w + at.row_column);
+    c.valid = reinterpret_cast<uint8_t*>(w + at.valid);
+    c.columns = reinterpret_cast<int32_t*>(w + at.columns);
+    c.starts = reinterpret_cast<uint16_t*>(w + at.starts);
+    c.share = reinterpret_cast<float*>(w + at.share);
+    c.entropy = reinterpret_cast<float*>(w + at.entropy);
+    c.z = reinterpret_cast<float*>(w + at.z);
+    c.value = a.grad ? reinterpret_cast<float*>(w + at.value) : nullptr;
+    c.partial = reinterpret_cast<float*>(w + at.partial);
+    c.coef = reinterpret_cast<float4*>(w + at.coef);
+    c.block_loss = reinterpret_cast<double*>(w + at.block_loss);
+    c.gathered = w + at.gathered;
+    c.acc = reinterpret_cast<float*>(w + at.acc);
+    c.status = h->status;
+
+    // the groups of ranks, and where their rows are
+    std::vector<LossGroup> groups((h->world + kLossRanks - 1) / kLossRanks);
+    int64_t rows = 0;
+    for (int32_t r = 0; r < h->world; ++r) {
+        LossGroup& g = groups[r / kLossRanks];
+        const int i = r % kLossRanks;
+        if (i == 0) {
+            g = LossGroup{};
+            g.world = h->world;
+            g.first = r;
+            g.row0[0] = (int32_t)rows;
+        }
+        g.n = i + 1;
+        const int32_t n = a.tokens[r];
+        g.tokens[i] = n;
+        g.hidden[i] = a.hidden[r];
+        g.targets[i] = a.targets ? a.targets[r] : nullptr;
+        g.teacher[i] = distill ? a.teacher[r] : nullptr;
+        g.indices[i] = distill ? a.indices[r] : nullptr;
+        g.token_losses[i] = a.token_losses ? a.token_losses[r] : nullptr;
+        g.grad_hidden[i] = a.grad ? a.grad_hidden[r] : nullptr;
+        rows += round_up(n, kLossRowAlign);
+        g.row0[i + 1] = (int32_t)rows;
+    }
+    c.rows = std::max<int64_t>(rows, kLossRowAlign);
+    // the pieces: one width for all groups
+    int64_t most = kLossRowAlign;
+    for (const LossGroup& g : groups) most = std::max<int64_t>(most, g.row0[g.n] - g.row0[0]);
+    const int64_t width = a.grad ? piece_width(at.piece_bytes, most, h->vocab, c.planes) : h->vocab;
+
+    for (const LossGroup& g : groups) {
+        if (distill && (st = cuda_status(launch_loss_teacher(g, c, stream)))) return st;
+        if ((st = cuda_status(launch_loss_scan(g, c, stream)))) return st;
+    }
+    if (h->copied)
+        for (int32_t r = 0; r < h->world; ++r)
+            if ((st = cuda_status(launch_loss_planes(h->weights[r], w + at.weights + r * h->copied, h->vocab, c, stream)))) return st;
+
+    LossGemm m{};
+    m.c = c;
+    m.limit_ns = std::max(wait_limit_ns(), 2000000000ull);
+    m.accumulate = a.accumulate;
+    if ((st = map_bf16(&m.hidden, c.gathered, c.dimp, c.rows, 2 * c.dimp, c.planes, 2 * c.rows * c.dimp))) return st;
+    if (a.grad) {
+        m.splits = (int32_t)splits_for(c.rows, c.dim, width);
+        const int64_t blocks = (std::min<int64_t>(width, h->vocab) + kTileK - 1) / kTileK;
+        m.split_blocks = (int32_t)((blocks + m.splits - 1) / m.splits);
+        if ((st = map_f32(&m.acc, c.acc, c.dimp, m.splits * c.rows))) return st;
+        m.vec = 1;
+        for (void* p : h->grads)
+            if (reinterpret_cast<uintptr_t>(p) % (h->dtype == DDP_F32 ? 16 : 8) || h->dim % 4) m.vec = 0;
+    }
+    for (const LossGroup& g : groups) {
+        const int64_t span = g.row0[g.n] - g.row0[0], row_tiles = span / kTileM;
+        m.n = g.n;
+        m.first = g.first;
+        std::copy(g.row0, g.row0 + kLossRanks + 1, m.row0);
+        for (int i = 0; i < g.n; ++i) {
+            m.weights[i] = h->maps[g.first + i];
+            m.grads[i] = a.grad ? h->grads[g.first + i] : nullptr;
+        }
+        if (span > 0) {
+            m.piece0 = 0;
+            m.width = h->vocab;
+            if ((st = cuda_status(launch_loss_gather(g, c, stream))) ||
+                (st = cuda_status(launch_loss_gemm(LossPhase::kStats, m, row_tiles * ((h->vocab + kTileN - 1) / kTileN), stream))))
+                return st;
+        }
+        if ((st = cuda_status(launch_loss_combine(g, c, a.loss, stream)))) return st;
+        if (!a.grad) continue;
+        if (span > 0 &&
+            (st = map_bf16(&m.piece, w + at.piece, width, span, 2 * width, c.planes, 2 * span * width)))
+            return st;
+        const int64_t dim_tiles = (h->dim + kTileN - 1) / kTileN;
+        for (int64_t v = 0; v < h->vocab; v += width) {
+            m.piece0 = (int32_t)v;
+            m.width = (int32_t)std::min<int64_t>(width, h->vocab - v);
+            m.add = v > 0;
+            if ((st = cuda_status(launch_loss_gemm(LossPhase::kGrad, m, row_tiles * ((m.width + kTileN - 1) / kTileN), stream))) ||
+                (st = cuda_status(launch_loss_gemm(LossPhase::kProducts, m,
+                                                   row_tiles * dim_tiles * m.splits +
+                                                       g.n * ((m.width + kTileM - 1) / kTileM) * dim_tiles,
+                                                   stream))))
+                return st;
+        }
+        if (span > 0 && (st = cuda_status(launch_loss_join(g, c, m.splits, stream)))) return st;
+    }
+    return DDP_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int32_t ddp_loss_head_workspace_bytes(int32_t world, int32_t vocab, int32_t dim, int32_t dtype, int32_t max_tokens,
+                                      int32_t max_teacher, int32_t with_grads, int64_t* bytes) try {
+    DDP_TRACE_CALL();
+    const int32_t st = check_head(world, vocab, dim, dtype, max_tokens, max_teacher);
+    if (st) return st;
+    if (!bytes) return DDP_ERR_INVALID;
+    *bytes = layout(world, vocab, dim, dtype, max_tokens, max_teacher, with_grads != 0).total;
+    return DDP_OK;
+} DDP_ABI_CATCH
+
+int32_t ddp_loss_head_create(int32_t world, const void* const* weights, void* const* grads, int32_t vocab, int32_t dim,
+                             int32_t dtype, int32_t max_tokens, int32_t max_teacher, void* workspace,
+                             int64_t workspace_bytes, ddp_loss_head** out) try {
+    DDP_TRACE_CALL();
+    if (!out) return DDP_ERR_INVALID;
+    *out = nullptr;
+    int32_t st = check_head(world, vocab, dim, dtype, max_tokens, max_teacher);
+    if (st) return st;
+    if (!weights) return DDP_ERR_INVALID;
+    if ((st = check_ptr(workspace, 256))) return st;
+    std::unique_ptr<ddp_loss_head> h(new ddp_loss_head());
+    h->world = world;
+    h->vocab = vocab;
+    h->dim = dim;
+    h->dtype = dtype;
+    h->max_tokens = max_tokens;
+    h->max_teacher = max_teacher;
+    h->workspace = static_cast<char*>(workspace);
+    h->at = layout(world, vocab, dim, dtype, max_tokens, max_teacher, grads != nullptr);
+    if (workspace_bytes < h->at.total) return DDP_ERR_CAPACITY;
+    const int64_t es = elem_bytes(dtype), bytes = (int64_t)vocab * dim * es;
+    h->written.push_back(span_of(workspace, h->at.total));
+    for (int32_t r = 0; r < world; ++r) {
+        if ((st = check_ptr(weights[r], dtype == DDP_F32 || dim % 8 ? es : 16))) return st;
+        h->weights.push_back(weights[r]);
+        h->read.push_back(span_of(weights[r], bytes));
+        if (!grads) continue;
+        if ((st = check_ptr(grads[r], es))) return st;
+        h->grads.push_back(grads[r]);
+        h->written.push_back(span_of(grads[r], bytes));
+    }
+    if (dtype == DDP_F32 || dim % 8) h->copied = h->at.weights_bytes;
+    if (any_overlap(&h->written)) return DDP_ERR_INVALID;
+    for (const Span& s : h->read)
+        if (hits_any(h->written, s)) return DDP_ERR_INVALID;
+    *out = h.release();
+    return DDP_OK;
+} DDP_ABI_CATCH
+
+int32_t ddp_cross_entropy(ddp_loss_head* head, const int32_t* tokens, const void* const* hidden, int64_t hidden_stride,
+                          const int64_t* const* targets, int64_t ignore_index, int32_t reduction,
+                          float* const* token_losses, float* loss, void* stream) try {
+    DDP_TRACE_CALL();
+    if (!head) return DDP_ERR_INVALID;
+    return run(head, Args{tokens, hidden, hidden_stride, targets, ignore_index, reduction, token_losses, loss},
+               (cudaStream_t)stream);
+} DDP_ABI_CATCH
+
+int32_t ddp_cross_entropy_grad(ddp_loss_head* head, const int32_t* tokens, const void* const* hidden,
+                               int64_t hidden_stride, const int64_t* const* targets, int64_t ignore_index,
+                               int32_t reduction, double scale, int32_t accumulate, float* const* token_losses,
+                               float* loss, void* const* grad_hidden, void* stream) try {
+    DDP_TRACE_CALL();
+    if (!head) return DDP_ERR_INVALID;
+    Args a{tokens, hidden, hidden_stride, targets, ignore_index, reduction, token_losses, loss};
+    a.grad = true;
+    a.scale = scale;
+    a.accumulate = accumulate;
+    a.grad_hidden = grad_hidden;
+    return run(head, a, (cudaStream_t)stream);
+} DDP_ABI_CATCH
+
+int32_t ddp_distill(ddp_loss_head* head, const int32_t* tokens, const void* const* hidden, int64_t hidden_stride,
+                    int32_t n_teacher, const void* const* teacher, int32_t teacher_dtype, const int64_t* const* indices,
+                    double temperature, double alpha, const int64_t* const* targets, int64_t ignore_index,
+                    int32_t reduction, float* const* token_losses, float* loss, void* stream) try {
+    DDP_TRACE_CALL();
+    if (!head || !((float)alpha > 0.f)) return DDP_ERR_INVALID;
+    return run(head,
+               Args{tokens, hidden, hidden_stride, targets, ignore_index, reduction, token_losses, loss, n_teacher, teacher,
+                    teacher_dtype, indices, temperature, alpha},
+               (cudaStream_t)stream);
+} DDP_ABI_CATCH
+
+int32_t ddp_distill_grad(ddp_loss_head* head, const int32_t* tokens, const void* const* hidden, int64_t hidden_stride,
+                         int32_t n_teacher, const void* const* teacher, int32_t teacher_dtype,
+                         const int64_t* const* indices, double temperature, double alpha,
+                         const int64_t* const* targets, int64_t ignore_index, int32_t reduction, double scale,
+                         int32_t accumulate, float* const* token_losses, float* loss, void* const* grad_hidden,
+                         void* stream) try {
+    DDP_TRACE_CALL();
+    if (!head || !((float)alpha > 0.f)) return DDP_ERR_INVALID;
+    return run(head,
+               Args{tokens, hidden, hidden_stride, targets, ignore_index, reduction, token_losses, loss, n_teacher, teacher,
+                    teacher_dtype, indices, temperature, alpha, true, scale, accumulate, grad_hidden},
+               (cudaStream_t)stream);
+} DDP_ABI_CATCH
+
+int32_t ddp_loss_head_destroy(ddp_loss_head* head) try {
+    DDP_TRACE_CALL();
+    delete head;
+    return DDP_OK;
+} DDP_ABI_CATCH
+
+}  // extern "C"

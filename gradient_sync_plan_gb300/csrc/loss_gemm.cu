@@ -1,0 +1,719 @@
+// loss_gemm.cu -- the loss head's matrix products on the fifth-generation tensor
+// cores, with the softmax in their epilogues.
+//
+// With h the rows of learned tokens [T, d], w the weights [V, d] and dz the
+// logits' gradients of one piece of the vocabulary [T, Vp]:
+//   kStats     z = h w^T, never stored: every tile of 128 x 256 logits leaves a
+//              maximum and a sum of exponentials for each row and 128 columns,
+//              and the logits at the columns that a row lists;
+//   kGrad      z again, piece by piece: dz = f (softmax(z) - target), bf16;
+//   kProducts  dh += dz w (over the piece's columns) and dw = dz^T h (over T).
+// Both operands of kProducts are read as they lie in memory: the tensor cores
+// take matrices whose rows run along the depth or across it.
+//
+// One block an SM walks over tiles.  A thread issues the tiles' loads (TMA, boxes
+// of 64 x 64 elements, a ring of stages in shared memory), another the products
+// (tcgen05.mma, accumulators in tensor memory, two tiles' worth), eight warps
+// take finished tiles out of tensor memory while the next one is computed.
+//
+// float32 operands are three bf16 planes, x = x0 + x1 + x2 (8 bits of the
+// significand each); of the nine products of planes the six larger are summed,
+// smallest first: what is left out is below 2^-24 of the terms.
+//
+// All waits are bounded: one that runs out sets DDP_ERR_TIMEOUT in the device
+// status word, the block's roles stop, loads in flight and products are waited
+// for, and tensor memory is freed.
+#include <algorithm>
+
+#include "ddp_device.cuh"
+#include "loss_internal.h"
+
+namespace ddpk {
+namespace {
+
+constexpr int kStages = 4;
+constexpr int kBytesA = kTileM * kTileK * 2, kBytesB = kTileN * kTileK * 2;
+constexpr int kBytesStage = kBytesA + kBytesB;
+constexpr int kBytesBox = 64 * 64 * 2;
+constexpr int kBytesStaging = 128 * 128;               // 128 rows of 128 bytes
+constexpr int kFirstEpilogueWarp = 4, kEpilogueWarps = 8;
+constexpr int kGemmThreads = 32 * (kFirstEpilogueWarp + kEpilogueWarps);
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct Control {
+    uint64_t full[kStages], empty[kStages];
+    uint64_t ready[2], taken[2];                       // accumulators
+    uint64_t drain;
+    uint32_t tmem;
+    int32_t stop;
+    int32_t go[2][2];                                  // by group and accumulators: the tile is there
+    int32_t counts[kLossRanks];
+};
+constexpr int kSmem = 1024 + kStages * kBytesStage + 2 * kBytesStaging + (int)sizeof(Control);
+static_assert(kSmem <= 227 * 1024, "shared memory of a block");
+
+__device__ __forceinline__ uint32_t smem_of(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ void bar_init(uint64_t* b, uint32_t n) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_of(b)), "r"(n) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint64_t* b, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_of(b)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint64_t* b) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_of(b)) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_of(b)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ unsigned long long now_ns() {
+    unsigned long long t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+// At most limit_ns, or until another role of the block has given up; false then.
+__device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, Control* s, const LossGemm& g) {
+    if (bar_try(b, parity)) return true;
+    const unsigned long long t0 = now_ns();
+    while (!bar_try(b, parity)) {
+        if (*(volatile int32_t*)&s->stop) return false;
+        if (now_ns() - t0 > g.limit_ns) {
+            *(volatile int32_t*)&s->stop = 1;
+            atomicExch(g.c.status, DDP_ERR_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+// The same after a role has given up: for what is still in flight.
+__device__ __forceinline__ void bar_wait_rest(uint64_t* b, uint32_t parity, const LossGemm& g) {
+    const unsigned long long t0 = now_ns();
+    while (!bar_try(b, parity))
+        if (now_ns() - t0 > g.limit_ns) return;
+}
+
+__device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(smem_of(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_of(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, const void* src, int x, int y, int z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map),
+                 "r"(smem_of(src)), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map),
+                 "r"(smem_of(src)), "r"(x), "r"(y)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_add_2d(const CUtensorMap* map, const void* src, int x, int y) {
+    asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map),
+                 "r"(smem_of(src)), "r"(x), "r"(y)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void tma_read_done() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void tma_all_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void to_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ void group_sync(int group) { asm volatile("bar.sync %0, 128;" ::"r"(group + 1) : "memory"); }
+
+// Shared-memory matrix descriptor: 128-byte swizzle, groups of 8 rows of 128 bytes
+// 1024 bytes apart; lbo: bytes between runs of 64 elements across the depth.
+__device__ __forceinline__ uint64_t matrix_desc(uint32_t addr, uint32_t lbo) {
+    return (uint64_t)((addr & 0x3FFFF) >> 4) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// Instruction descriptor: bf16 x bf16 into float32, kTileM x kTileN; `across`: rows run across the depth.
+__device__ __forceinline__ uint32_t product_desc(bool a_across, bool b_across) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((a_across ? 1u : 0u) << 15) | ((b_across ? 1u : 0u) << 16) |
+           ((uint32_t)(kTileN >> 3) << 17) | ((uint32_t)(kTileM >> 4) << 24);
+}
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(desc), "r"((uint32_t)add)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_of(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+__device__ __forceinline__ void tmem_load(float* v, uint32_t addr) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// 2^x by the special-function unit: off by 2^-22 of the value at most, 0 below 2^-126.
+__device__ __forceinline__ float exp2_of(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// A tile: rank, first row (of all ranks' rows; a column of the piece for dw), first column, k blocks.
+struct Tile {
+    int rank, m, n, k0, k1, split;
+    bool weights;                          // of dw
+};
+
+__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// Tiles of rank i in the phase: of its rows first, of its weights' gradients behind those of all ranks.
+template <LossPhase PHASE>
+__device__ __forceinline__ int row_tiles(const LossGemm& g, const int32_t* counts, int i) {
+    const int m = ceil_div(counts[i], kTileM);
+    if (PHASE == LossPhase::kStats) return m * ceil_div(g.c.vocab, kTileN);
+    if (PHASE == LossPhase::kGrad) return m * ceil_div(g.width, kTileN);
+    return m * ceil_div(g.c.dim, kTileN) * g.splits;
+}
+__device__ __forceinline__ int weight_tiles(const LossGemm& g, const int32_t* counts, int i) {
+    if (counts[i] == 0 && g.accumulate) return 0;
+    return ceil_div(g.width, kTileM) * ceil_div(g.c.dim, kTileN);
+}
+template <LossPhase PHASE>
+__device__ __forceinline__ bool find_tile(const LossGemm& g, const int32_t* counts, int t, Tile* w) {
+    for (int i = 0; i < g.n; ++i) {
+        const int n = row_tiles<PHASE>(g, counts, i);
+        if (t >= n) {
+            t -= n;
+            continue;
+        }
+        w->rank = i;
+        w->weights = false;
+        w->split = 0;
+        const int m = ceil_div(counts[i], kTileM);
+        if (PHASE != LossPhase::kProducts) {           // rows' tiles of one column block together: they share the weights
+            w->m = g.row0[i] + t % m * kTileM;
+            w->n = t / m * kTileN;
+            w->k0 = 0;
+            w->k1 = g.c.dimp / kTileK;
+        } else {
+            const int nt = ceil_div(g.c.dim, kTileN);
+            w->n = t % nt * kTileN;
+            t /= nt;
+            w->m = g.row0[i] + t % m * kTileM;
+            w->split = t / m;
+            w->k0 = w->split * g.split_blocks;
+            w->k1 = min(w->k0 + g.split_blocks, ceil_div(g.width, kTileK));
+        }
+        return true;
+    }
+    if constexpr (PHASE == LossPhase::kProducts) {
+        for (int i = 0; i < g.n; ++i) {
+            const int n = weight_tiles(g, counts, i);
+            if (t >= n) {
+                t -= n;
+                continue;
+            }
+            const int nt = ceil_div(g.c.dim, kTileN);
+            w->rank = i;
+            w->weights = true;
+            w->split = 0;
+            w->n = t % nt * kTileN;
+            w->m = t / nt * kTileM;
+            w->k0 = 0;
+            w->k1 = ceil_div(counts[i], kTileK);
+            return true;
+        }
+    }
+    return false;
+}
+
+__device__ constexpr int8_t kPlaneA[6] = {2, 1, 0, 1, 0, 0};
+__device__ constexpr int8_t kPlaneB[6] = {0, 1, 2, 0, 1, 0};
+
+// ---- producer -----------------------------------------------------------------
+template <LossPhase PHASE, bool F32>
+__device__ void produce(const LossGemm& g, Control* s, char* stages) {
+    int stage = 0, issued = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    Tile w;
+    for (int t = blockIdx.x; ok && find_tile<PHASE>(g, s->counts, t, &w); t += gridDim.x) {
+        const CUtensorMap* wmap = &g.weights[w.rank];
+        for (int q = 0; ok && q < (F32 ? 6 : 1); ++q) {
+            const int pa = F32 ? kPlaneA[q] : 0, pb = F32 ? kPlaneB[q] : 0;
+            for (int kb = w.k0; kb < w.k1; ++kb) {
+                if (!bar_wait(&s->empty[stage], phase ^ 1, s, g)) {
+                    ok = false;
+                    break;
+                }
+                char* a = stages + stage * kBytesStage;
+                char* b = a + kBytesA;
+                uint64_t* bar = &s->full[stage];
+                bar_expect(bar, kBytesStage);
+                const int k = kb * kTileK;
+                if (PHASE != LossPhase::kProducts) {
+                    for (int j = 0; j < kTileM / 64; ++j) tma_load(a + j * kBytesBox, &g.hidden, k, w.m + 64 * j, pa, bar);
+                    for (int j = 0; j < kTileN / 64; ++j)
+                        tma_load(b + j * kBytesBox, wmap, k, g.piece0 + w.n + 64 * j, pb, bar);
+                } else if (!w.weights) {
+                    for (int j = 0; j < kTileM / 64; ++j)
+                        tma_load(a + j * kBytesBox, &g.piece, k, w.m - g.row0[0] + 64 * j, pa, bar);
+                    for (int j = 0; j < kTileN / 64; ++j) tma_load(b + j * kBytesBox, wmap, w.n + 64 * j, g.piece0 + k, pb, bar);
+                } else {
+                    const int row = g.row0[w.rank] + k;
+                    for (int j = 0; j < kTileM / 64; ++j)
+                        tma_load(a + j * kBytesBox, &g.piece, w.m + 64 * j, row - g.row0[0], pa, bar);
+                    for (int j = 0; j < kTileN / 64; ++j) tma_load(b + j * kBytesBox, &g.hidden, w.n + 64 * j, row, pb, bar);
+                }
+                ++issued;
+                if (++stage == kStages) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+    }
+    if (!ok)                               // loads in flight, before the block's shared memory goes
+        for (int i = max(0, issued - kStages); i < issued; ++i) bar_wait_rest(&s->full[i % kStages], (i / kStages) & 1, g);
+}
+
+// ---- products -----------------------------------------------------------------
+template <LossPhase PHASE, bool F32>
+__device__ void multiply(const LossGemm& g, Control* s, char* stages, uint32_t tmem) {
+    int stage = 0, buf = 0;
+    uint32_t phase = 0, taken = 1;
+    bool ok = true;
+    Tile w;
+    for (int t = blockIdx.x; ok && find_tile<PHASE>(g, s->counts, t, &w); t += gridDim.x) {
+        const bool a_across = PHASE == LossPhase::kProducts && w.weights, b_across = PHASE == LossPhase::kProducts;
+        const uint32_t desc = product_desc(a_across, b_across);
+        // 16 elements of depth: 32 bytes along a row, or 16 rows of 128 bytes
+        const uint32_t step_a = a_across ? 16 * 128 / 16 : 2, step_b = b_across ? 16 * 128 / 16 : 2;
+        if (!bar_wait(&s->taken[buf], taken, s, g)) {
+            ok = false;
+            break;
+        }
+        fence_after();
+        const int blocks = (w.k1 - w.k0) * (F32 ? 6 : 1);
+        for (int i = 0; i < blocks; ++i) {
+            if (!bar_wait(&s->full[stage], phase, s, g)) {
+                ok = false;
+                break;
+            }
+            fence_after();
+            const uint32_t a = smem_of(stages + stage * kBytesStage);
+            const uint64_t da = matrix_desc(a, kBytesBox), db = matrix_desc(a + kBytesA, kBytesBox);
+#pragma unroll
+            for (int k = 0; k < kTileK / 16; ++k)
+                mma(tmem + buf * kTileN, da + k * step_a, db + k * step_b, desc, i > 0 || k > 0);
+            mma_commit(&s->empty[stage]);
+            if (++stage == kStages) {
+                stage = 0;
+                phase ^= 1;
+            }
+        }
+        if (!ok) break;
+        mma_commit(&s->ready[buf]);
+        if (buf == 1) taken ^= 1;
+        buf ^= 1;
+    }
+    if (!ok) {                             // products in flight, before tensor memory goes
+        mma_commit(&s->drain);
+        bar_wait_rest(&s->drain, 0, g);
+    }
+}
+
+// ---- epilogues -----------------------------------------------------------------
+// A thread has one row of the tile and 128 of its columns; `mine` is its row of
+// the group's staging buffer (128 bytes), whose 16-byte pieces are permuted by `turn`.
+struct Lane {
+    int group, quarter, lane, row;         // row of the tile
+    uint32_t tmem;                         // the row's columns of this group
+    char* staging;                         // the group's
+    char* mine;
+    int turn;
+    bool leader;                           // of the group's 128 threads
+};
+
+__device__ __forceinline__ void stage_floats(const Lane& l, const float* v) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        *reinterpret_cast<float4*>(l.mine + ((i ^ l.turn) << 4)) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+}
+__device__ __forceinline__ float staged_float(const Lane& l, int i) {
+    return *reinterpret_cast<const float*>(l.mine + (((i >> 2) ^ l.turn) << 4) + (i & 3) * 4);
+}
+
+// The columns that a row lists within its group's columns, in order.
+template <bool LIST>
+struct Listed {
+    int64_t at;                            // of the entry in the arrays [][list]
+    int64_t end;
+    int column;                            // of the entry; past every column where there is none
+    const int32_t* columns;
+    __device__ __forceinline__ void start(const LossCall& c, int row, int token, int first, bool valid) {
+        columns = c.columns;
+        if (LIST) {
+            const uint16_t* s = c.starts + (int64_t)token * (c.units + 1) + first / kLossUnit;
+            at = (int64_t)token * c.list;
+            end = at + (valid ? s[1] : 0);
+            at += valid ? s[0] : 0;
+            column = at < end ? columns[at] : INT32_MAX;
+        } else {
+            at = row;
+            column = valid ? c.row_column[row] : INT32_MAX;
+            if (column < first || column >= first + kLossUnit) column = INT32_MAX;
+        }
+    }
+    __device__ __forceinline__ void next() {
+        ++at;
+        column = LIST && at < end ? columns[at] : INT32_MAX;
+    }
+};
+
+template <bool TWO, bool LIST>
+__device__ __forceinline__ void stats_tile(const LossGemm& g, const Tile& w, const Lane& l, Control* s, uint64_t* taken) {
+    const LossCall& c = g.c;
+    const int row = w.m + l.row, first = w.n + l.group * kLossUnit;
+    const bool valid = row - g.row0[w.rank] < s->counts[w.rank];
+    Listed<LIST> hit;
+    hit.start(c, row, LIST && valid ? g.row0[w.rank] + c.row_token[row] : 0, first, valid && first < c.vocab);
+    const float k1 = TWO ? kLog2e : c.inv_temperature * kLog2e, k2 = c.inv_temperature * kLog2e;
+    float top = -INFINITY, sum = 0.f, sum2 = 0.f;
+#pragma unroll 1
+    for (int j = 0; j < kLossUnit / 32; ++j) {
+        float v[32];
+        tmem_load(v, l.tmem + j * 32);
+        tmem_wait();
+        if (j == kLossUnit / 32 - 1) {
+            fence_before();
+            bar_arrive(taken);
+        }
+        const int col = first + j * 32;
+        if (__any_sync(0xffffffffu, hit.column < col + 32)) {
+            stage_floats(l, v);
+            while (hit.column < col + 32) {
+                c.z[hit.at] = staged_float(l, hit.column - col);
+                hit.next();
+            }
+        }
+        if (col + 32 > c.vocab) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (col + i >= c.vocab) v[i] = -INFINITY;
+        }
+        float m = top;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) m = fmaxf(m, v[i]);
+        const float ref = m == -INFINITY ? 0.f : m;    // a row of -infinity so far: no terms
+        sum *= exp2_of((top - ref) * k1);
+        if (TWO) sum2 *= exp2_of((top - ref) * k2);
+        top = m;
+        float part[4] = {0.f, 0.f, 0.f, 0.f}, part2[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const float d = v[i] - ref;
+            part[i & 3] += exp2_of(d * k1);
+            if (TWO) part2[i & 3] += exp2_of(d * k2);
+        }
+        sum += (part[0] + part[1]) + (part[2] + part[3]);
+        if (TWO) sum2 += (part2[0] + part2[1]) + (part2[2] + part2[3]);
+    }
+    if (valid && first < c.vocab) {
+        const int64_t at = (int64_t)(first / kLossUnit) * c.rows + row;
+        if (TWO) reinterpret_cast<float4*>(c.partial)[at] = make_float4(top, sum, sum2, 0.f);
+        else reinterpret_cast<float2*>(c.partial)[at] = make_float2(top, sum);
+    }
+}
+
+template <bool F32, bool TWO, bool LIST>
+__device__ __forceinline__ void grad_tile(const LossGemm& g, const Tile& w, const Lane& l, Control* s, uint64_t* taken) {
+    const LossCall& c = g.c;
+    const int row = w.m + l.row, first = g.piece0 + w.n + l.group * kLossUnit;
+    const bool valid = row - g.row0[w.rank] < s->counts[w.rank];
+    Listed<LIST> hit;
+    hit.start(c, row, LIST && valid ? g.row0[w.rank] + c.row_token[row] : 0, first, valid && first < c.vocab);
+    const float4 coef = valid ? c.coef[row] : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float k1 = TWO ? kLog2e : c.inv_temperature * kLog2e, k2 = c.inv_temperature * kLog2e;
+#pragma unroll 1
+    for (int j = 0; j < kLossUnit / 64; ++j) {
+        float v[64];
+        tmem_load(v, l.tmem + j * 64);
+        tmem_load(v + 32, l.tmem + j * 64 + 32);
+        tmem_wait();
+        if (j == kLossUnit / 64 - 1) {
+            fence_before();
+            bar_arrive(taken);
+        }
+        const int col = first + j * 64;
+#pragma unroll
+        for (int i = 0; i < 64; ++i) {
+            float p = coef.y * exp2_of(fmaf(v[i], k1, -coef.x));
+            if (TWO) p = fmaf(coef.w, exp2_of(fmaf(v[i], k2, -coef.z)), p);
+            v[i] = valid && col + i < c.vocab ? p : 0.f;
+        }
+        const Listed<LIST> before = hit;
+#pragma unroll
+        for (int q = 0; q < (F32 ? 3 : 1); ++q) {
+            if (l.leader) tma_read_done();
+            group_sync(l.group);           // the staging buffer is free
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                uint32_t x[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float& lo = v[8 * i + 2 * e];
+                    float& hi = v[8 * i + 2 * e + 1];
+                    x[e] = bf16x2_rn(lo, hi);
+                    if (F32) {
+                        lo -= bf16_lo(x[e]);
+                        hi -= bf16_hi(x[e]);
+                    }
+                }
+                *reinterpret_cast<uint4*>(l.mine + ((i ^ l.turn) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+            hit = before;
+            while (hit.column < col + 64) {            // the exact gradient where a target or a teacher has its say
+                float value = c.value[hit.at];
+                for (int k = 0; k < q; ++k) value -= bf16_to_f32(f32_to_bf16_rn(value));
+                const int i = hit.column - col;
+                *reinterpret_cast<uint16_t*>(l.mine + (((i >> 3) ^ l.turn) << 4) + (i & 7) * 2) = f32_to_bf16_rn(value);
+                hit.next();
+            }
+            to_async_proxy();
+            group_sync(l.group);
+            if (l.leader) {
+                const int x = w.n + l.group * kLossUnit + j * 64, y = w.m - g.row0[0];
+                tma_store(&g.piece, l.staging, x, y, q);
+                tma_store(&g.piece, l.staging + 64 * 128, x, y + 64, q);
+                tma_commit();
+            }
+        }
+    }
+}
+
+// dh: the tile goes to its split's part of acc, added there by the copy engine from the second piece on (one
+// writer an element and launch, so the order is fixed).
+__device__ __forceinline__ void hidden_tile(const LossGemm& g, const Tile& w, const Lane& l, uint64_t* taken) {
+#pragma unroll 1
+    for (int j = 0; j < kTileN / 2 / 32; ++j) {
+        const int col = w.n + l.group * (kTileN / 2) + j * 32;
+        float v[32];
+        tmem_load(v, l.tmem + j * 32);
+        tmem_wait();
+        if (j == kTileN / 2 / 32 - 1) {
+            fence_before();
+            bar_arrive(taken);
+        }
+        // the same for the whole group: no column of acc, or no depth in a shorter last piece
+        if (col >= g.c.dimp || w.k1 <= w.k0) continue;
+        if (l.leader) tma_read_done();
+        group_sync(l.group);
+        stage_floats(l, v);
+        to_async_proxy();
+        group_sync(l.group);
+        if (l.leader) {
+            const int y = (int)(w.split * g.c.rows) + w.m;
+            if (g.add) tma_add_2d(&g.acc, l.staging, col, y);
+            else tma_store_2d(&g.acc, l.staging, col, y);
+            tma_commit();
+        }
+    }
+}
+
+// dw: rows of the weights' gradients, rounded once, written row by row.
+template <bool F32>
+__device__ __forceinline__ void weights_tile(const LossGemm& g, const Tile& w, const Lane& l, uint64_t* taken) {
+    const LossCall& c = g.c;
+    const bool none = w.k1 <= w.k0;                    // a rank without learned tokens
+    const int v0 = g.piece0 + w.m + l.quarter * 32;
+    const int rows = min(32, min(g.piece0 + g.width, c.vocab) - v0);
+    if (l.leader) tma_read_done();
+    group_sync(l.group);
+#pragma unroll 1
+    for (int j = 0; j < kTileN / 2 / 32; ++j) {
+        float v[32];
+        tmem_load(v, l.tmem + j * 32);
+        tmem_wait();
+        if (j == kTileN / 2 / 32 - 1) {
+            fence_before();
+            bar_arrive(taken);
+        }
+        const int col = w.n + l.group * (kTileN / 2) + j * 32;
+        if (col >= c.dim) continue;
+        if (none) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0.f;
+        }
+        __syncwarp();
+        stage_floats(l, v);
+        __syncwarp();
+        const int x = col + (l.lane & 7) * 4;          // four columns of a row
+        for (int i = l.lane >> 3; i < rows; i += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(l.staging + (l.quarter * 32 + i) * 128 +
+                                                              (((l.lane & 7) ^ (i & 7)) << 4));
+            const int64_t at = (int64_t)(v0 + i) * c.dim + x;
+            if (F32) {
+                float* out = static_cast<float*>(g.grads[w.rank]) + at;
+                if (g.vec) {
+                    if (x < c.dim) {
+                        float4 r = f;
+                        if (g.accumulate) {
+                            const float4 o = *reinterpret_cast<const float4*>(out);
+                            r = make_float4(o.x + f.x, o.y + f.y, o.z + f.z, o.w + f.w);
+                        }
+                        *reinterpret_cast<float4*>(out) = r;
+                    }
+                } else {
+                    const float e[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (x + k < c.dim) out[k] = g.accumulate ? out[k] + e[k] : e[k];
+                }
+            } else {
+                uint16_t* out = static_cast<uint16_t*>(g.grads[w.rank]) + at;
+                if (g.vec) {
+                    if (x < c.dim) {
+                        float4 r = f;
+                        if (g.accumulate) {
+                            const uint2 o = *reinterpret_cast<const uint2*>(out);
+                            r = make_float4(bf16_lo(o.x) + f.x, bf16_hi(o.x) + f.y, bf16_lo(o.y) + f.z, bf16_hi(o.y) + f.w);
+                        }
+                        *reinterpret_cast<uint2*>(out) = make_uint2(bf16x2_rn(r.x, r.y), bf16x2_rn(r.z, r.w));
+                    }
+                } else {
+                    const float e[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (x + k < c.dim) out[k] = f32_to_bf16_rn(g.accumulate ? bf16_to_f32(out[k]) + e[k] : e[k]);
+                }
+            }
+        }
+    }
+}
+
+template <LossPhase PHASE, bool F32, bool TWO, bool LIST>
+__global__ void __launch_bounds__(kGemmThreads, 1) k_loss_gemm(const __grid_constant__ LossGemm g) {
+    extern __shared__ char raw[];
+    char* smem = raw + (1024 - (smem_of(raw) & 1023)) % 1024;
+    char* staging = smem + kStages * kBytesStage;
+    Control* s = reinterpret_cast<Control*>(staging + 2 * kBytesStaging);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    pdl_release();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            bar_init(&s->full[i], 1);
+            bar_init(&s->empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            bar_init(&s->ready[i], 1);
+            bar_init(&s->taken[i], 32 * kEpilogueWarps);
+        }
+        bar_init(&s->drain, 1);
+        s->stop = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == 2) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_of(&s->tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    pdl_acquire();
+    if (threadIdx.x < g.n) s->counts[threadIdx.x] = g.c.counts[g.first + threadIdx.x];
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = *(volatile uint32_t*)&s->tmem;
+    if (warp == 0) {
+        if (lane == 0) produce<PHASE, F32>(g, s, smem);
+    } else if (warp == 1) {
+        if (lane == 0) multiply<PHASE, F32>(g, s, smem, tmem);
+    } else if (warp >= kFirstEpilogueWarp) {
+        Lane l;
+        l.group = (warp - kFirstEpilogueWarp) / 4;
+        l.quarter = warp % 4;
+        l.lane = lane;
+        l.row = l.quarter * 32 + lane;
+        l.staging = staging + l.group * kBytesStaging;
+        l.mine = l.staging + l.row * 128;
+        l.turn = l.row & 7;
+        l.leader = l.row == 0;
+        int buf = 0;
+        uint32_t phase = 0;
+        Tile w;
+        for (int t = blockIdx.x; find_tile<PHASE>(g, s->counts, t, &w); t += gridDim.x) {
+            // one thread decides for its group, whose threads meet at barriers within a tile
+            volatile int32_t* go = &s->go[l.group][buf];
+            if (l.leader) *go = bar_wait(&s->ready[buf], phase, s, g);
+            group_sync(l.group);
+            if (!*go) break;
+            fence_after();
+            l.tmem = tmem + ((uint32_t)(l.quarter * 32) << 16) + buf * kTileN + l.group * (kTileN / 2);
+            uint64_t* taken = &s->taken[buf];
+            if (PHASE == LossPhase::kStats) stats_tile<TWO, LIST>(g, w, l, s, taken);
+            else if (PHASE == LossPhase::kGrad) grad_tile<F32, TWO, LIST>(g, w, l, s, taken);
+            else if (!w.weights) hidden_tile(g, w, l, taken);
+            else weights_tile<F32>(g, w, l, taken);
+            if (buf == 1) phase ^= 1;
+            buf ^= 1;
+        }
+        if (l.leader) tma_all_done();
+    }
+    __syncwarp();
+    fence_before();
+    __syncthreads();
+    if (warp == 2) {
+        fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
+template <LossPhase PHASE, bool F32, bool TWO, bool LIST>
+cudaError_t launch(const LossGemm& g, int64_t most_tiles, cudaStream_t stream) {
+    const auto kernel = k_loss_gemm<PHASE, F32, TWO, LIST>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    const int grid = cap_ctas(std::min<int64_t>(most_tiles, sm_count()));
+    return launch_dependent(kernel, dim3(grid), dim3(kGemmThreads), kSmem, stream, g);
+}
+
+template <LossPhase PHASE, bool F32>
+cudaError_t launch_kind(const LossGemm& g, int64_t most_tiles, cudaStream_t stream) {
+    if (PHASE == LossPhase::kProducts) return launch<PHASE, F32, false, false>(g, most_tiles, stream);
+    if (g.c.alpha == 0.f) return launch<PHASE, F32, false, false>(g, most_tiles, stream);
+    if (g.c.two) return launch<PHASE, F32, true, true>(g, most_tiles, stream);
+    return launch<PHASE, F32, false, true>(g, most_tiles, stream);
+}
+
+template <LossPhase PHASE>
+cudaError_t launch_type(const LossGemm& g, int64_t most_tiles, cudaStream_t stream) {
+    if (g.c.dtype == DDP_F32) return launch_kind<PHASE, true>(g, most_tiles, stream);
+    return launch_kind<PHASE, false>(g, most_tiles, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_loss_gemm(LossPhase phase, const LossGemm& g, int64_t most_tiles, cudaStream_t stream) {
+    if (most_tiles <= 0) return cudaSuccess;
+    if (phase == LossPhase::kStats) return launch_type<LossPhase::kStats>(g, most_tiles, stream);
+    if (phase == LossPhase::kGrad) return launch_type<LossPhase::kGrad>(g, most_tiles, stream);
+    return launch_type<LossPhase::kProducts>(g, most_tiles, stream);
+}
+
+}  // namespace ddpk

@@ -1,0 +1,115 @@
+// loss_internal.h -- what the loss head's sources share on the host side and in
+// their kernels' parameters.  Not part of the C ABI (see include/ddp.h).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "ddp_internal.h"
+
+namespace ddpk {
+
+// Ranks of one launch; more take further launches.
+constexpr int kLossRanks = 16;
+// A rank's learned tokens are gathered into rows of its own, from a multiple of kLossRowAlign on.
+constexpr int kLossRowAlign = 128;
+// Columns of a partial softmax statistic and of a bin of listed columns.
+constexpr int kLossUnit = 128;
+// Tile of the products: rows, columns, depth of a shared-memory stage.
+constexpr int kTileM = 128, kTileN = 256, kTileK = 64;
+
+// One group of ranks as the row kernels see it.  Rows are numbered through all
+// ranks: rank i of the group has rows row0[i] .. row0[i + 1], its first counts[i]
+// hold its learned tokens.
+struct LossGroup {
+    int32_t n;                            // ranks
+    int32_t world, first;                 // of all, and the group's first
+    int32_t row0[kLossRanks + 1];
+    int32_t tokens[kLossRanks];
+    const void* hidden[kLossRanks];
+    const int64_t* targets[kLossRanks];   // null: none
+    const void* teacher[kLossRanks];
+    const int64_t* indices[kLossRanks];
+    float* token_losses[kLossRanks];      // null: not wanted
+    void* grad_hidden[kLossRanks];
+};
+
+// The call's constants, and the workspace's arrays (by row or token of all ranks).
+struct LossCall {
+    int32_t vocab, dim, dimp;             // dimp: dim rounded up to kTileK, a gathered row's length
+    int32_t dtype, planes;                // bf16 planes of an operand: 1, or 3 for float32
+    int32_t teacher_dtype, n_teacher, list;   // list: columns a token lists (1: its target)
+    int32_t units;                        // statistics units of the vocabulary
+    int32_t reduction, two;               // two: softmaxes of two temperatures
+    int64_t hidden_stride, ignore_index;
+    float inv_temperature, temperature;   // of the distillation
+    float alpha;                          // its share; 0: cross entropy alone
+    float scale;                          // of the gradients
+    int64_t rows;                         // rows of all ranks
+
+    int32_t* counts;                      // [world]
+    int32_t* done;                        // blocks of a combine launch that are through
+    int32_t* row_token;                   // [rows] the token (of its rank) that a row holds
+    int32_t* token_row;                   // [rows] the row (of its rank) of a token, -1: not learned
+    int32_t* row_column;                  // [rows] target's column
+    uint8_t* valid;                       // [rows] by token: learned (distillation)
+    int32_t* columns;                     // [rows][list] by token, ascending
+    uint16_t* starts;                     // [rows][units + 1] by token: entries before a unit
+    float* share;                         // [rows][list] by token: teacher's probability of the entry
+    float* entropy;                       // [rows] by token: sum of q log q
+    float* z;                             // [rows][list] logits at the listed columns
+    float* value;                         // [rows][list] gradients there
+    float* partial;                       // [units][rows] float2, or float4 for two temperatures
+    float4* coef;                         // [rows] {lse, factor, lse at the temperature, its factor}, lse in bits (log2)
+    double* block_loss;                   // [rows / kLossBlockRows]
+    void* gathered;                       // [planes][rows][dimp] bf16
+    float* acc;                           // [splits][rows][dimp]
+    int32_t* status;                      // the device status word
+};
+constexpr int kLossBlockRows = 32;        // rows of a combine block
+
+// Products.  kStats: logits' statistics and listed logits.  kGrad: logits' gradients of a
+// piece of the vocabulary, to `piece`.  kProducts: the piece's share of the hidden states' gradients
+// (added to acc) and its rows of the weights' gradients.
+enum class LossPhase { kStats = 0, kGrad = 1, kProducts = 2 };
+
+struct LossGemm {
+    CUtensorMap hidden;                   // gathered rows
+    CUtensorMap piece;                    // [planes][rows of the group][piece columns] bf16
+    CUtensorMap acc;                      // [splits * rows][dimp] float32
+    CUtensorMap weights[kLossRanks];
+    void* grads[kLossRanks];
+    int32_t row0[kLossRanks + 1];
+    int32_t n, first;
+    int32_t piece0, width;                // the piece's first column and its columns
+    int32_t splits, split_blocks;         // of the hidden states' gradients: parts of the piece's depth, their k blocks
+    int32_t add;                          // add to acc (else write)
+    int32_t accumulate;                   // add to the weights' gradients
+    int32_t vec;                          // their rows take 16-byte (float32) or 8-byte (bf16) accesses
+    unsigned long long limit_ns;
+    LossCall c;
+};
+static_assert(sizeof(LossGemm) < 8192, "travels in the kernel's parameters");
+
+cudaError_t launch_loss_gemm(LossPhase phase, const LossGemm& g, int64_t most_tiles, cudaStream_t stream);
+
+// ---- rows (loss_rows.cu) ---------------------------------------------------
+// Teachers' entries: sorted lists, probabilities, which tokens are learned.
+cudaError_t launch_loss_teacher(const LossGroup& g, const LossCall& c, cudaStream_t stream);
+// Which tokens are learned, and their rows.
+cudaError_t launch_loss_scan(const LossGroup& g, const LossCall& c, cudaStream_t stream);
+// Their hidden states, into the rows; rows up to the next tile's end are zeroed.
+cudaError_t launch_loss_gather(const LossGroup& g, const LossCall& c, cudaStream_t stream);
+// A matrix [rows][dim] as [planes][rows][dimp] bf16, zeros behind dim.
+cudaError_t launch_loss_planes(const void* src, void* dst, int64_t rows, const LossCall& c, cudaStream_t stream);
+// Partial statistics to losses and to the gradients' coefficients.
+cudaError_t launch_loss_combine(const LossGroup& g, const LossCall& c, float* loss, cudaStream_t stream);
+// acc's splits to the hidden states' gradients, zeros for tokens that are not learned.
+cudaError_t launch_loss_join(const LossGroup& g, const LossCall& c, int splits, cudaStream_t stream);
+
+// The address of the device status word, and the TMA kernels' wait limit (ring_tma.cu).
+cudaError_t device_status_address(int32_t** word);
+unsigned long long wait_limit_ns();
+
+}  // namespace ddpk

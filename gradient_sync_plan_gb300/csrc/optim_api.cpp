@@ -17,6 +17,7 @@
 #include "ddp_abi_guard.h"
 #include "ddp.h"
 #include "ddp_trace.h"
+#include "ddp_spans.h"
 #include "optim_internal.h"
 
 using namespace ddpk;
@@ -59,38 +60,6 @@ struct ddp_adamw {
 
 namespace {
 
-using Span = std::pair<uintptr_t, uintptr_t>;      // [first, second) in bytes
-
-Span span_of(const void* p, int64_t bytes) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    return Span{a, a + (uintptr_t)bytes};
-}
-
-// Sorts the spans; true if two of them share a byte.
-bool any_overlap(std::vector<Span>* v) {
-    std::sort(v->begin(), v->end());
-    for (size_t i = 1; i < v->size(); ++i)
-        if ((*v)[i].first < (*v)[i - 1].second) return true;
-    return false;
-}
-
-// Sorts the spans and joins those that share a byte or touch.
-void unite(std::vector<Span>* v) {
-    std::sort(v->begin(), v->end());
-    size_t n = 0;
-    for (const Span& s : *v) {
-        if (n > 0 && s.first <= (*v)[n - 1].second) (*v)[n - 1].second = std::max((*v)[n - 1].second, s.second);
-        else (*v)[n++] = s;
-    }
-    v->resize(n);
-}
-
-// True if s shares a byte with one of the sorted, disjoint spans.
-bool hits_any(const std::vector<Span>& sorted, Span s) {
-    auto it = std::lower_bound(sorted.begin(), sorted.end(), Span{s.second, 0});
-    return it != sorted.begin() && std::prev(it)->second > s.first;
-}
-
 // World, tensor count and sizes shared by the creating calls.  A rank's
 // elements are capped as one buffer's are, so that sums of bytes and tiles fit.
 int32_t check_sizes(int32_t world, int32_t n_params, const int64_t* numel, int32_t dtype) {
@@ -105,11 +74,6 @@ int32_t check_sizes(int32_t world, int32_t n_params, const int64_t* numel, int32
         if (total > DDP_MAX_NUMEL) return DDP_ERR_CAPACITY;
     }
     return DDP_OK;
-}
-
-int32_t check_ptr(const void* p, int64_t align) {
-    if (!p) return DDP_ERR_INVALID;
-    return reinterpret_cast<uintptr_t>(p) % (uintptr_t)align ? DDP_ERR_ALIGN : DDP_OK;
 }
 
 // Appends tensor (p, bytes) of rank r, joined to the range before it where it continues it.

@@ -668,6 +668,15 @@ void set_wait_limit_ns(unsigned long long ns, unsigned long long* previous) {
 
 void plant_stall(long long tile) { g_stall_tile.store(tile < 0 ? -1 : tile); }
 
+unsigned long long wait_limit_ns() { return g_wait_limit_ns.load(); }
+
+cudaError_t device_status_address(int32_t** word) {
+    void* p = nullptr;
+    const cudaError_t e = cudaGetSymbolAddress(&p, g_device_status);
+    *word = static_cast<int32_t*>(p);
+    return e;
+}
+
 cudaError_t read_device_status(int32_t* out, bool clear) {
     int32_t v = 0;
     cudaError_t e = cudaMemcpyFromSymbol(&v, g_device_status, sizeof(v));

@@ -25,8 +25,8 @@
  *   - Ownership: the caller owns every host and device buffer.  The library
  *     allocates no device memory at run time (the no-alloc entry point's
  *     64 MiB array is a static device array) and keeps no pointer after a
- *     call returns (except a ddp_reducer, a ddp_grad_set, a ddp_sync_norm and a
- *     ddp_adamw, which keep the tables they were created with).  State kept between calls: cached device attributes,
+ *     call returns (except a ddp_reducer, a ddp_grad_set, a ddp_sync_norm, a ddp_adamw
+ *     and a ddp_loss_head, which keep the tables they were created with).  State kept between calls: cached device attributes,
  *     the two process-wide settings (ddp_set_max_ctas, ddp_set_fused_kernel)
  *     and the device status word (ddp_device_status).
  *   - Streams: `stream` is a cudaStream_t passed as void* (NULL = the legacy
@@ -153,7 +153,8 @@ int32_t ddp_set_fused_kernel(int32_t kind, int32_t* previous);
  * ddp_device_status -- the library's sticky device-side status word on the
  * current device: DDP_OK, or DDP_ERR_TIMEOUT if a kernel's bounded wait on an
  * asynchronous copy gave up (the kernel then stopped early, so the buffers
- * of that call hold partial results).  Synchronous: call it after the
+ * of that call hold partial results), or DDP_ERR_INVALID if a loss met a target
+ * or a teacher's index that is no column of the vocabulary.  Synchronous: call it after the
  * stream of interest has been synchronised.  clear != 0 resets the word.
  * Returns DDP_OK, DDP_ERR_INVALID (status NULL) or DDP_ERR_CUDA.
  */
@@ -162,7 +163,7 @@ int32_t ddp_device_status(int32_t* status, int32_t clear);
 /*
  * ddp_set_wait_limit_ms -- limit of every bounded device-side wait in the
  * TMA-staged kernels (the fused ring's, the fused tree's and the fused
- * view's), in
+ * view's; the loss head's products wait 2000 ms at least), in
  * milliseconds, for launches from now on in this process; 0 restores the
  * default of 2000 ms.  A kernel whose wait runs out sets the device status
  * word to DDP_ERR_TIMEOUT (ddp_device_status) and stops early instead of
@@ -759,6 +760,108 @@ int32_t ddp_adamw_create(int32_t world, int32_t n_params, void* const* params, c
 int32_t ddp_adamw_step(ddp_adamw* adamw, double lr, double beta1, double beta2, double eps, double weight_decay,
                        const float* norms, double max_norm, void* stream);
 int32_t ddp_adamw_destroy(ddp_adamw* adamw);
+
+/*
+ * ddp_loss_head -- where a step's gradients begin: the loss of every rank's tokens
+ * over a vocabulary, and its gradients, from the hidden states before the head
+ * projection and the head's weights.  The logits are never kept: they are computed
+ * in tiles on the tensor cores, and of a tile only its rows' softmax statistics
+ * leave the SM; the gradients go through the vocabulary in pieces that fit the
+ * workspace.
+ *
+ * Rank r has tokens[r] tokens, h_t its hidden states and w_j its weights' rows:
+ *     z_tj = h_t . w_j      p = softmax(z_t)      u = z_t / temperature
+ *   ddp_cross_entropy        L_t = -log p[targets_t]; a token whose target is
+ *                            ignore_index is not learned
+ *   ddp_distill              with q the softmax of the token's teacher logits /
+ *                            temperature over its entries (index_k, logit_k):
+ *                            L_t = alpha temperature^2 sum_k q_k (log q_k -
+ *                            log softmax(u)[index_k]) + (1 - alpha) (-log p[targets_t])
+ *                            An entry with a negative index or a logit of -infinity is
+ *                            none.  Two entries of one column add up.  Not learned:
+ *                            a token without entries, or, with targets, one whose
+ *                            target is ignore_index
+ *   loss[r] = f_r sum_t L_t over the learned tokens, 0 if there are none, with
+ *     DDP_LOSS_SUM         f_r = 1
+ *     DDP_LOSS_MEAN        f_r = 1 / (learned tokens of rank r)
+ *     DDP_LOSS_WORLD_MEAN  f_r = world / (learned tokens of all ranks): averaging the
+ *                          ranks' gradients then gives the gradient of the mean over
+ *                          all tokens, however unevenly they lie
+ *   ..._grad                 the same, and the gradients of scale x loss[r]: with
+ *                            respect to the hidden states (zeros for tokens that are not
+ *                            learned), and to the weights, written to the head's
+ *                            gradient tensors or, with accumulate != 0, added to them
+ *                            (one rounding of the sum)
+ * What a token that is not learned holds is never read: its hidden states and
+ * teacher may be NaN.  A target, or an index of a token that is otherwise learned,
+ * that is >= vocab (a target also < 0 and not ignore_index) makes the device status
+ * DDP_ERR_INVALID; such a token, or entry, is left out.
+ *
+ * Types.  DDP_BF16: products of bf16 values, summed in binary32; the logits'
+ * gradients are rounded to bf16 for the two products with them, everything else is
+ * binary32 and rounded once at the end.  DDP_F32: operands are split into three bf16
+ * parts and the six larger products of parts summed, which loses less than
+ * binary32's own rounding.  Sums have a fixed order: the same call gives the same
+ * bits, under any ddp_set_max_ctas.
+ *
+ *   weights[world]       host table of device pointers, [vocab][dim] of dtype; bf16
+ *                        weights with dim a multiple of 8 start on 16-byte boundaries
+ *                        (DDP_ERR_ALIGN).  float32 weights, and bf16 ones of other
+ *                        dims, are copied into the workspace by every call
+ *   grads[world]         host table, gradients of the same shape and type; NULL: the
+ *                        ..._grad calls are refused.  No two may overlap
+ *   vocab, dim           1 .. DDP_MAX_VOCAB, 1 .. DDP_MAX_DIM
+ *   max_tokens           most tokens of a rank that a call may have (1 or more; with
+ *                        world up to 2^28 together)
+ *   max_teacher          most entries a token's teacher may have, 0 (no distillation)
+ *                        .. DDP_MAX_TEACHER
+ *   workspace            device memory, 256-byte aligned, of at least
+ *                        ddp_loss_head_workspace_bytes (DDP_ERR_CAPACITY if smaller),
+ *                        for the head alone.  Calls on one head share it: order them.
+ *                        A captured call keeps working on it
+ *   tokens[world]        0 .. max_tokens (DDP_ERR_CAPACITY above)
+ *   hidden[world]        device pointers of dtype, rows of dim values hidden_stride
+ *                        elements apart (>= dim)
+ *   targets[world]       device int64; for ddp_distill NULL: none (alpha is 1 then)
+ *   teacher[world]       device [tokens][n_teacher] logits of teacher_dtype
+ *   indices[world]       device int64 [tokens][n_teacher]
+ *   temperature > 0, 0 < alpha <= 1, 1 <= n_teacher <= max_teacher
+ *   token_losses[world]  device float32 L_t (0: not learned); NULL, or NULL entries:
+ *                        not wanted
+ *   loss[world]          device float32
+ *   grad_hidden[world]   device [tokens][dim] of dtype, rows dim apart
+ * Pointers of a rank without tokens may be NULL.  Nothing that a call writes may
+ * overlap anything else of it or of the head.  The head keeps the pointers it was
+ * created with, the caller keeps the memory.
+ */
+#define DDP_MAX_VOCAB (1 << 24)
+#define DDP_MAX_DIM (1 << 16)
+#define DDP_MAX_TEACHER 256
+typedef enum { DDP_LOSS_SUM = 0, DDP_LOSS_MEAN = 1, DDP_LOSS_WORLD_MEAN = 2 } ddp_loss_reduction;
+typedef struct ddp_loss_head ddp_loss_head;
+int32_t ddp_loss_head_workspace_bytes(int32_t world, int32_t vocab, int32_t dim, int32_t dtype, int32_t max_tokens,
+                                      int32_t max_teacher, int32_t with_grads, int64_t* bytes);
+int32_t ddp_loss_head_create(int32_t world, const void* const* weights, void* const* grads, int32_t vocab, int32_t dim,
+                             int32_t dtype, int32_t max_tokens, int32_t max_teacher, void* workspace,
+                             int64_t workspace_bytes, ddp_loss_head** out);
+int32_t ddp_cross_entropy(ddp_loss_head* head, const int32_t* tokens, const void* const* hidden, int64_t hidden_stride,
+                          const int64_t* const* targets, int64_t ignore_index, int32_t reduction,
+                          float* const* token_losses, float* loss, void* stream);
+int32_t ddp_cross_entropy_grad(ddp_loss_head* head, const int32_t* tokens, const void* const* hidden,
+                               int64_t hidden_stride, const int64_t* const* targets, int64_t ignore_index,
+                               int32_t reduction, double scale, int32_t accumulate, float* const* token_losses,
+                               float* loss, void* const* grad_hidden, void* stream);
+int32_t ddp_distill(ddp_loss_head* head, const int32_t* tokens, const void* const* hidden, int64_t hidden_stride,
+                    int32_t n_teacher, const void* const* teacher, int32_t teacher_dtype, const int64_t* const* indices,
+                    double temperature, double alpha, const int64_t* const* targets, int64_t ignore_index,
+                    int32_t reduction, float* const* token_losses, float* loss, void* stream);
+int32_t ddp_distill_grad(ddp_loss_head* head, const int32_t* tokens, const void* const* hidden, int64_t hidden_stride,
+                         int32_t n_teacher, const void* const* teacher, int32_t teacher_dtype,
+                         const int64_t* const* indices, double temperature, double alpha,
+                         const int64_t* const* targets, int64_t ignore_index, int32_t reduction, double scale,
+                         int32_t accumulate, float* const* token_losses, float* loss, void* const* grad_hidden,
+                         void* stream);
+int32_t ddp_loss_head_destroy(ddp_loss_head* head);
 
 #ifdef __cplusplus
 }
