@@ -25,9 +25,13 @@ using namespace ddpk;
 
 namespace {
 
-// Bytes of a piece's logits' gradients that the workspace has room for.  A piece is written once and read a few
-// times, so that it need not fit the L2; fewer pieces mean fewer passes over the hidden states' sums.
-constexpr int64_t kPieceBytes = (int64_t)512 << 20;
+// Bytes of logits' gradients that the workspace has room for at most.  bf16: where a rank's tokens by the whole
+// vocabulary fit, the exponentials are kept from the loss to the gradients and the logits are computed once, group of
+// ranks by group of ranks; else, and for float32 (whose gradients are three planes), the vocabulary goes in pieces.  A
+// piece is written once and read a few times, so that it need not fit the L2.
+constexpr int64_t kKeepBytes = (int64_t)2 << 30, kPieceBytes = (int64_t)512 << 20;
+// Temperatures whose two softmaxes' exponentials come from one another by a power up to this.
+constexpr float kKeepPower = 4.f;
 constexpr int64_t kSms = 152;
 constexpr int64_t kPieceAlign = 256;              // columns of a piece: a multiple of the tiles'
 
@@ -81,7 +85,7 @@ Sizes layout(int64_t world, int64_t vocab, int64_t dim, int32_t dtype, int64_t m
     Sizes s{};
     const int64_t rows = world * round_up(max_tokens, kLossRowAlign), planes = planes_of(dtype), dimp = round_up(dim, kTileK);
     const int64_t list = max_teacher + 1, units = (vocab + kLossUnit - 1) / kLossUnit;
-    const int64_t group = std::min<int64_t>(world, kLossRanks) * round_up(max_tokens, kLossRowAlign);
+    const int64_t rank = round_up(max_tokens, kLossRowAlign), group = std::min<int64_t>(world, kLossRanks) * rank;
     int64_t at = 0;
     const auto put = [&](int64_t* offset, int64_t bytes) {
         *offset = at;
@@ -112,7 +116,10 @@ Sizes layout(int64_t world, int64_t vocab, int64_t dim, int32_t dtype, int64_t m
         // at most 2 kSms / tiles + 1 splits (splits_for), for any number of rows up to these
         s.acc_bytes = 4 * (2 * kSms * kTileM * kTileN + rows * dimp);
         put(&s.acc, s.acc_bytes);
+        const int64_t row = 2 * round_up(vocab, kPieceAlign);      // of kept exponentials
         s.piece_bytes = 2 * planes * group * piece_width(kPieceBytes, group, vocab, planes);
+        if (dtype == DDP_BF16 && rank * row <= kKeepBytes)
+            s.piece_bytes = std::max(s.piece_bytes, std::min(group, kKeepBytes / row / kLossRowAlign * kLossRowAlign) * row);
         put(&s.piece, s.piece_bytes);
     }
     s.total = at;
@@ -314,19 +321,23 @@ int32_t run(ddp_loss_head* h, const Args& a, cudaStream_t stream) {
     c.status = h->status;
 
     // the groups of ranks, and where their rows are
-    std::vector<LossGroup> groups((h->world + kLossRanks - 1) / kLossRanks);
+    const int64_t vocab_width = round_up(h->vocab, kPieceAlign);
+    const bool may_keep = a.grad && h->dtype == DDP_BF16 && (!c.two || std::max(c.temperature, c.inv_temperature) <= kKeepPower);
+    const int64_t keep_rows = may_keep ? at.piece_bytes / (2 * vocab_width) : 0;
+    std::vector<LossGroup> groups;
     int64_t rows = 0;
     for (int32_t r = 0; r < h->world; ++r) {
-        LossGroup& g = groups[r / kLossRanks];
-        const int i = r % kLossRanks;
-        if (i == 0) {
-            g = LossGroup{};
-            g.world = h->world;
-            g.first = r;
-            g.row0[0] = (int32_t)rows;
-        }
-        g.n = i + 1;
         const int32_t n = a.tokens[r];
+        const int64_t mine = round_up(n, kLossRowAlign);
+        if (groups.empty() || groups.back().n == kLossRanks ||
+            (keep_rows > 0 && rows > groups.back().row0[0] && rows + mine - groups.back().row0[0] > keep_rows)) {
+            groups.push_back(LossGroup{});
+            groups.back().world = h->world;
+            groups.back().first = r;
+            groups.back().row0[0] = (int32_t)rows;
+        }
+        LossGroup& g = groups.back();
+        const int i = g.n++;
         g.tokens[i] = n;
         g.hidden[i] = a.hidden[r];
         g.targets[i] = a.targets ? a.targets[r] : nullptr;
@@ -334,14 +345,10 @@ int32_t run(ddp_loss_head* h, const Args& a, cudaStream_t stream) {
         g.indices[i] = distill ? a.indices[r] : nullptr;
         g.token_losses[i] = a.token_losses ? a.token_losses[r] : nullptr;
         g.grad_hidden[i] = a.grad ? a.grad_hidden[r] : nullptr;
-        rows += round_up(n, kLossRowAlign);
+        rows += mine;
         g.row0[i + 1] = (int32_t)rows;
     }
     c.rows = std::max<int64_t>(rows, kLossRowAlign);
-    // the pieces: one width for all groups
-    int64_t most = kLossRowAlign;
-    for (const LossGroup& g : groups) most = std::max<int64_t>(most, g.row0[g.n] - g.row0[0]);
-    const int64_t width = a.grad ? piece_width(at.piece_bytes, most, h->vocab, c.planes) : h->vocab;
 
     for (const LossGroup& g : groups) {
         if (distill && (st = cuda_status(launch_loss_teacher(g, c, stream)))) return st;
@@ -357,10 +364,6 @@ int32_t run(ddp_loss_head* h, const Args& a, cudaStream_t stream) {
     m.accumulate = a.accumulate;
     if ((st = map_bf16(&m.hidden, c.gathered, c.dimp, c.rows, 2 * c.dimp, c.planes, 2 * c.rows * c.dimp))) return st;
     if (a.grad) {
-        m.splits = (int32_t)splits_for(c.rows, c.dim, width);
-        const int64_t blocks = (std::min<int64_t>(width, h->vocab) + kTileK - 1) / kTileK;
-        m.split_blocks = (int32_t)((blocks + m.splits - 1) / m.splits);
-        if ((st = map_f32(&m.acc, c.acc, c.dimp, m.splits * c.rows))) return st;
         m.vec = 1;
         for (void* p : h->grads)
             if (reinterpret_cast<uintptr_t>(p) % (h->dtype == DDP_F32 ? 16 : 8) || h->dim % 4) m.vec = 0;
@@ -374,28 +377,36 @@ int32_t run(ddp_loss_head* h, const Args& a, cudaStream_t stream) {
             m.weights[i] = h->maps[g.first + i];
             m.grads[i] = a.grad ? h->grads[g.first + i] : nullptr;
         }
+        const bool keep = span > 0 && span <= keep_rows;
+        const int64_t width = !a.grad || keep ? vocab_width : piece_width(at.piece_bytes, span, h->vocab, c.planes);
+        if (a.grad) {
+            m.splits = (int32_t)splits_for(c.rows, c.dim, std::min<int64_t>(width, h->vocab));
+            const int64_t blocks = (std::min<int64_t>(width, h->vocab) + kTileK - 1) / kTileK;
+            m.split_blocks = (int32_t)((blocks + m.splits - 1) / m.splits);
+            if ((st = map_f32(&m.acc, c.acc, c.dimp, m.splits * c.rows))) return st;
+            if (span > 0 && (st = map_bf16(&m.piece, w + at.piece, width, span, 2 * width, c.planes, 2 * span * width))) return st;
+        }
         if (span > 0) {
             m.piece0 = 0;
             m.width = h->vocab;
             if ((st = cuda_status(launch_loss_gather(g, c, stream))) ||
-                (st = cuda_status(launch_loss_gemm(LossPhase::kStats, m, row_tiles * ((h->vocab + kTileN - 1) / kTileN), stream))))
+                (st = cuda_status(launch_loss_gemm(keep ? LossPhase::kKeep : LossPhase::kStats, m,
+                                                   row_tiles * ((h->vocab + kTileN - 1) / kTileN), stream))))
                 return st;
         }
         if ((st = cuda_status(launch_loss_combine(g, c, a.loss, stream)))) return st;
         if (!a.grad) continue;
-        if (span > 0 &&
-            (st = map_bf16(&m.piece, w + at.piece, width, span, 2 * width, c.planes, 2 * span * width)))
-            return st;
         const int64_t dim_tiles = (h->dim + kTileN - 1) / kTileN;
         for (int64_t v = 0; v < h->vocab; v += width) {
             m.piece0 = (int32_t)v;
             m.width = (int32_t)std::min<int64_t>(width, h->vocab - v);
             m.add = v > 0;
-            if ((st = cuda_status(launch_loss_gemm(LossPhase::kGrad, m, row_tiles * ((m.width + kTileN - 1) / kTileN), stream))) ||
-                (st = cuda_status(launch_loss_gemm(LossPhase::kProducts, m,
-                                                   row_tiles * dim_tiles * m.splits +
-                                                       g.n * ((m.width + kTileM - 1) / kTileM) * dim_tiles,
-                                                   stream))))
+            if (keep) st = cuda_status(launch_loss_convert(g, c, w + at.piece, width, stream));
+            else st = cuda_status(launch_loss_gemm(LossPhase::kGrad, m, row_tiles * ((m.width + kTileN - 1) / kTileN), stream));
+            if (st || (st = cuda_status(launch_loss_gemm(LossPhase::kProducts, m,
+                                                         row_tiles * dim_tiles * m.splits +
+                                                             g.n * ((m.width + kTileM - 1) / kTileM) * dim_tiles,
+                                                         stream))))
                 return st;
         }
         if (span > 0 && (st = cuda_status(launch_loss_join(g, c, m.splits, stream)))) return st;

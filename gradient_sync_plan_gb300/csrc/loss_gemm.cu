@@ -6,7 +6,10 @@
 //   kStats     z = h w^T, never stored: every tile of 128 x 256 logits leaves a
 //              maximum and a sum of exponentials for each row and 128 columns,
 //              and the logits at the columns that a row lists;
-//   kGrad      z again, piece by piece: dz = f (softmax(z) - target), bf16;
+//   kKeep      the same, and the exponentials themselves in 16 bits, where those of
+//              all columns have room; a pass of its own makes dz of them;
+//   kGrad      where they have not: z again, piece by piece, and
+//              dz = f (softmax(z) - target), bf16;
 //   kProducts  dh += dz w (over the piece's columns) and dw = dz^T h (over T).
 // Both operands of kProducts are read as they lie in memory: the tensor cores
 // take matrices whose rows run along the depth or across it.
@@ -39,6 +42,7 @@ constexpr int kBytesStaging = 128 * 128;               // 128 rows of 128 bytes
 constexpr int kFirstEpilogueWarp = 4, kEpilogueWarps = 8;
 constexpr int kGemmThreads = 32 * (kFirstEpilogueWarp + kEpilogueWarps);
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kKeepScale = (float)(1 << kKeepBits);
 
 struct Control {
     uint64_t full[kStages], empty[kStages];
@@ -186,7 +190,7 @@ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; 
 template <LossPhase PHASE>
 __device__ __forceinline__ int row_tiles(const LossGemm& g, const int32_t* counts, int i) {
     const int m = ceil_div(counts[i], kTileM);
-    if (PHASE == LossPhase::kStats) return m * ceil_div(g.c.vocab, kTileN);
+    if (PHASE == LossPhase::kStats || PHASE == LossPhase::kKeep) return m * ceil_div(g.c.vocab, kTileN);
     if (PHASE == LossPhase::kGrad) return m * ceil_div(g.width, kTileN);
     return m * ceil_div(g.c.dim, kTileN) * g.splits;
 }
@@ -387,7 +391,9 @@ struct Listed {
     }
 };
 
-template <bool TWO, bool LIST>
+// Twice over the row's 128 logits: their maximum, and their exponentials relative to it.  KEEP: the exponentials go to
+// the piece's buffer as binary16, 2^kKeepBits for the row's largest, so that those down to 2^-29 of it keep 11 bits.
+template <bool TWO, bool LIST, bool KEEP>
 __device__ __forceinline__ void stats_tile(const LossGemm& g, const Tile& w, const Lane& l, Control* s, uint64_t* taken) {
     const LossCall& c = g.c;
     const int row = w.m + l.row, first = w.n + l.group * kLossUnit;
@@ -395,16 +401,16 @@ __device__ __forceinline__ void stats_tile(const LossGemm& g, const Tile& w, con
     Listed<LIST> hit;
     hit.start(c, row, LIST && valid ? g.row0[w.rank] + c.row_token[row] : 0, first, valid && first < c.vocab);
     const float k1 = TWO ? kLog2e : c.inv_temperature * kLog2e, k2 = c.inv_temperature * kLog2e;
-    float top = -INFINITY, sum = 0.f, sum2 = 0.f;
+    if (KEEP) {
+        if (l.leader) tma_read_done();
+        group_sync(l.group);               // the staging buffer is free
+    }
+    float top = -INFINITY;
 #pragma unroll 1
     for (int j = 0; j < kLossUnit / 32; ++j) {
         float v[32];
         tmem_load(v, l.tmem + j * 32);
         tmem_wait();
-        if (j == kLossUnit / 32 - 1) {
-            fence_before();
-            bar_arrive(taken);
-        }
         const int col = first + j * 32;
         if (__any_sync(0xffffffffu, hit.column < col + 32)) {
             stage_floats(l, v);
@@ -418,27 +424,78 @@ __device__ __forceinline__ void stats_tile(const LossGemm& g, const Tile& w, con
             for (int i = 0; i < 32; ++i)
                 if (col + i >= c.vocab) v[i] = -INFINITY;
         }
-        float m = top;
+        float m[4] = {top, v[1], v[2], v[3]};
+        m[0] = fmaxf(top, v[0]);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) m = fmaxf(m, v[i]);
-        const float ref = m == -INFINITY ? 0.f : m;    // a row of -infinity so far: no terms
-        sum *= exp2_of((top - ref) * k1);
-        if (TWO) sum2 *= exp2_of((top - ref) * k2);
-        top = m;
-        float part[4] = {0.f, 0.f, 0.f, 0.f}, part2[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int i = 4; i < 32; ++i) m[i & 3] = fmaxf(m[i & 3], v[i]);
+        top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+    }
+    const float ref = top == -INFINITY ? 0.f : top;    // nothing but -infinity: no terms
+    const float a1 = -ref * k1, a2 = -ref * k2;
+    const bool flat = TWO && k2 < k1;                  // the flatter softmax's exponentials are kept
+    float sum[4] = {0.f, 0.f, 0.f, 0.f}, sum2[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    for (int j = 0; j < kLossUnit / 64; ++j) {
+        const int col = first + j * 64;
+        uint32_t kept[32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const float d = v[i] - ref;
-            part[i & 3] += exp2_of(d * k1);
-            if (TWO) part2[i & 3] += exp2_of(d * k2);
+        for (int h = 0; h < 2; ++h) {
+            float v[32];
+            tmem_load(v, l.tmem + j * 64 + h * 32);
+            tmem_wait();
+            if (h == 1 && j == kLossUnit / 64 - 1) {
+                fence_before();
+                bar_arrive(taken);
+            }
+            if (col + h * 32 + 32 > c.vocab) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (col + h * 32 + i >= c.vocab) v[i] = -INFINITY;
+            }
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+                float e[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float x = exp2_of(fmaf(v[i + k], k1, a1));
+                    sum[(i + k) & 3] += x;
+                    e[k] = x;
+                    if (TWO) {
+                        const float y = exp2_of(fmaf(v[i + k], k2, a2));
+                        sum2[(i + k) & 3] += y;
+                        e[k] = flat ? y : x;
+                    }
+                }
+                if (KEEP) {
+                    const __half2 p = __floats2half2_rn(e[0] * kKeepScale, e[1] * kKeepScale);
+                    kept[h * 16 + i / 2] = *reinterpret_cast<const uint32_t*>(&p);
+                }
+            }
         }
-        sum += (part[0] + part[1]) + (part[2] + part[3]);
-        if (TWO) sum2 += (part2[0] + part2[1]) + (part2[2] + part2[3]);
+        if (KEEP) {
+            if (j > 0) {
+                if (l.leader) tma_read_done();
+                group_sync(l.group);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<uint4*>(l.mine + ((i ^ l.turn) << 4)) =
+                    make_uint4(kept[4 * i], kept[4 * i + 1], kept[4 * i + 2], kept[4 * i + 3]);
+            to_async_proxy();
+            group_sync(l.group);
+            if (l.leader) {
+                const int x = w.n + l.group * kLossUnit + j * 64, y = w.m - g.row0[0];
+                tma_store(&g.piece, l.staging, x, y, 0);
+                tma_store(&g.piece, l.staging + 64 * 128, x, y + 64, 0);
+                tma_commit();
+            }
+        }
     }
     if (valid && first < c.vocab) {
         const int64_t at = (int64_t)(first / kLossUnit) * c.rows + row;
-        if (TWO) reinterpret_cast<float4*>(c.partial)[at] = make_float4(top, sum, sum2, 0.f);
-        else reinterpret_cast<float2*>(c.partial)[at] = make_float2(top, sum);
+        const float t = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        if (TWO) reinterpret_cast<float4*>(c.partial)[at] = make_float4(top, t, (sum2[0] + sum2[1]) + (sum2[2] + sum2[3]), 0.f);
+        else reinterpret_cast<float2*>(c.partial)[at] = make_float2(top, t);
     }
 }
 
@@ -666,7 +723,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_loss_gemm(const __grid_cons
             fence_after();
             l.tmem = tmem + ((uint32_t)(l.quarter * 32) << 16) + buf * kTileN + l.group * (kTileN / 2);
             uint64_t* taken = &s->taken[buf];
-            if (PHASE == LossPhase::kStats) stats_tile<TWO, LIST>(g, w, l, s, taken);
+            if (PHASE == LossPhase::kStats || PHASE == LossPhase::kKeep) stats_tile<TWO, LIST, PHASE == LossPhase::kKeep>(g, w, l, s, taken);
             else if (PHASE == LossPhase::kGrad) grad_tile<F32, TWO, LIST>(g, w, l, s, taken);
             else if (!w.weights) hidden_tile(g, w, l, taken);
             else weights_tile<F32>(g, w, l, taken);
@@ -712,6 +769,7 @@ cudaError_t launch_type(const LossGemm& g, int64_t most_tiles, cudaStream_t stre
 cudaError_t launch_loss_gemm(LossPhase phase, const LossGemm& g, int64_t most_tiles, cudaStream_t stream) {
     if (most_tiles <= 0) return cudaSuccess;
     if (phase == LossPhase::kStats) return launch_type<LossPhase::kStats>(g, most_tiles, stream);
+    if (phase == LossPhase::kKeep) return launch_kind<LossPhase::kKeep, false>(g, most_tiles, stream);
     if (phase == LossPhase::kGrad) return launch_type<LossPhase::kGrad>(g, most_tiles, stream);
     return launch_type<LossPhase::kProducts>(g, most_tiles, stream);
 }

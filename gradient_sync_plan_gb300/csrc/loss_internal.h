@@ -69,10 +69,12 @@ struct LossCall {
 };
 constexpr int kLossBlockRows = 32;        // rows of a combine block
 
-// Products.  kStats: logits' statistics and listed logits.  kGrad: logits' gradients of a
+// Products.  kStats: logits' statistics and listed logits.  kKeep: those, and the logits' exponentials relative to
+// their unit's largest, binary16 scaled by 2^kKeepBits, to `piece` (bf16 operands).  kGrad: logits' gradients of a
 // piece of the vocabulary, to `piece`.  kProducts: the piece's share of the hidden states' gradients
 // (added to acc) and its rows of the weights' gradients.
-enum class LossPhase { kStats = 0, kGrad = 1, kProducts = 2 };
+enum class LossPhase { kStats = 0, kGrad = 1, kProducts = 2, kKeep = 3 };
+constexpr int kKeepBits = 15;             // largest of a unit: 2^15, below binary16's 65504
 
 struct LossGemm {
     CUtensorMap hidden;                   // gathered rows
@@ -105,6 +107,8 @@ cudaError_t launch_loss_gather(const LossGroup& g, const LossCall& c, cudaStream
 cudaError_t launch_loss_planes(const void* src, void* dst, int64_t rows, const LossCall& c, cudaStream_t stream);
 // Partial statistics to losses and to the gradients' coefficients.
 cudaError_t launch_loss_combine(const LossGroup& g, const LossCall& c, float* loss, cudaStream_t stream);
+// Kept exponentials [rows of the group][width] to the logits' gradients, in place.
+cudaError_t launch_loss_convert(const LossGroup& g, const LossCall& c, void* piece, int64_t width, cudaStream_t stream);
 // acc's splits to the hidden states' gradients, zeros for tokens that are not learned.
 cudaError_t launch_loss_join(const LossGroup& g, const LossCall& c, int splits, cudaStream_t stream);
 

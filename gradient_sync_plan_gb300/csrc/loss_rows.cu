@@ -249,8 +249,9 @@ __global__ void __launch_bounds__(kThreads) k_planes(const char* src, uint16_t* 
 }
 
 // ---- losses and coefficients -------------------------------------------------------
-// A block takes 32 rows of a rank, a row a lane: each warp joins every eighth unit's statistics, the first joins the
+// A block takes 32 rows of a rank, a row a lane: each warp joins every 32nd unit's statistics, the first joins the
 // warps'.  Distillation then takes the rows' lists, a warp a row.  The last block adds the blocks' losses.
+constexpr int kCombineWarps = 32;
 __device__ __forceinline__ void join_stats(float& m, float& s, float& s2, float om, float os, float os2, float k1, float k2) {
     const float top = fmaxf(m, om);
     const float ref = top == -INFINITY ? 0.f : top;
@@ -261,9 +262,9 @@ __device__ __forceinline__ void join_stats(float& m, float& s, float& s2, float 
 }
 
 template <bool TWO>
-__global__ void __launch_bounds__(kThreads) k_combine(const __grid_constant__ LossGroup g, const __grid_constant__ LossCall c,
+__global__ void __launch_bounds__(32 * kCombineWarps) k_combine(const __grid_constant__ LossGroup g, const __grid_constant__ LossCall c,
                                                       float* loss) {
-    __shared__ float tops[kWarps][32], sums[kWarps][32], sums2[kWarps][32];
+    __shared__ float tops[kCombineWarps][32], sums[kCombineWarps][32], sums2[kCombineWarps][32];
     __shared__ float lse1[32], lse2[32], losses[32];
     __shared__ int64_t total;
     __shared__ bool final;
@@ -288,18 +289,26 @@ __global__ void __launch_bounds__(kThreads) k_combine(const __grid_constant__ Lo
             if (threadIdx.x == 0) c.block_loss[block] = 0.0;
             continue;
         }
+        // a warp's maximum first, so that the loads of each pass do not wait for one another
         float m = -INFINITY, s = 0.f, s2 = 0.f;
-        if (valid)
-            for (int u = warp; u < c.units; u += kWarps) {
+        const int step = TWO ? 4 : 2;
+        if (valid) {
+#pragma unroll 8
+            for (int u = warp; u < c.units; u += kCombineWarps) m = fmaxf(m, c.partial[((int64_t)u * c.rows + row) * step]);
+            const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll 8
+            for (int u = warp; u < c.units; u += kCombineWarps) {
                 const int64_t at = (int64_t)u * c.rows + row;
                 if (TWO) {
                     const float4 p = reinterpret_cast<const float4*>(c.partial)[at];
-                    join_stats(m, s, s2, p.x, p.y, p.z, k1, k2);
+                    s += p.y * exp2f((p.x - ref) * k1);
+                    s2 += p.z * exp2f((p.x - ref) * k2);
                 } else {
                     const float2 p = reinterpret_cast<const float2*>(c.partial)[at];
-                    join_stats(m, s, s2, p.x, p.y, 0.f, k1, k2);
+                    s += p.y * exp2f((p.x - ref) * k1);
                 }
             }
+        }
         tops[warp][lane] = m;
         sums[warp][lane] = s;
         sums2[warp][lane] = s2;
@@ -307,7 +316,7 @@ __global__ void __launch_bounds__(kThreads) k_combine(const __grid_constant__ Lo
         const double f = c.reduction == DDP_LOSS_SUM ? 1.0 : c.reduction == DDP_LOSS_MEAN ? 1.0 / count : (double)g.world / total;
         const float factor = (float)(f * c.scale);
         if (warp == 0 && valid) {
-            for (int k = 1; k < kWarps; ++k) join_stats(m, s, s2, tops[k][lane], sums[k][lane], sums2[k][lane], k1, k2);
+            for (int k = 1; k < kCombineWarps; ++k) join_stats(m, s, s2, tops[k][lane], sums[k][lane], sums2[k][lane], k1, k2);
             const float single = TWO ? 1.f : c.inv_temperature;
             lse1[lane] = m * single + logf(s);
             lse2[lane] = TWO ? m * c.inv_temperature + logf(s2) : lse1[lane];
@@ -330,7 +339,7 @@ __global__ void __launch_bounds__(kThreads) k_combine(const __grid_constant__ Lo
         }
         if (c.alpha != 0.f) {
             __syncthreads();
-            for (int k = warp; k < kLossBlockRows; k += kWarps) {
+            for (int k = warp; k < kLossBlockRows; k += kCombineWarps) {
                 const int rr = block * kLossBlockRows + k;
                 if (rr - g.row0[i] >= count) break;
                 const int64_t token = g.row0[i] + c.row_token[rr], at = token * c.list;
@@ -380,7 +389,7 @@ __global__ void __launch_bounds__(kThreads) k_combine(const __grid_constant__ Lo
     __syncthreads();
     if (!final) return;
     __threadfence();
-    for (int i = warp; i < g.n; i += kWarps) {
+    for (int i = warp; i < g.n; i += kCombineWarps) {
         const int count = c.counts[g.first + i];
         double sum = 0.0;
         for (int b = g.row0[i] / kLossBlockRows + lane; b < g.row0[i + 1] / kLossBlockRows; b += 32)
@@ -392,6 +401,90 @@ __global__ void __launch_bounds__(kThreads) k_combine(const __grid_constant__ Lo
         }
     }
     if (threadIdx.x == 0) *c.done = 0;     // for the next group's launch
+}
+
+// ---- kept exponentials to the logits' gradients ---------------------------------------
+// dz = f e 2^(reference - lse): what the products' own epilogue computes where exponentials are not kept, rounded to
+// bf16 once more from 11 bits.  Of two softmaxes the flatter one's exponentials x are kept; the other's are x^r with
+// r <= kKeepPower, which multiplies their rounding by r.  A warp takes kConvertColumns columns of a row; memory bound.
+constexpr int kConvertColumns = 1024;
+
+template <bool TWO, bool LIST>
+__global__ void __launch_bounds__(kThreads) k_convert(const __grid_constant__ LossGroup g, const __grid_constant__ LossCall c,
+                                                      uint16_t* piece, int64_t width) {
+    pdl_release();
+    pdl_acquire();
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const float k1 = TWO ? kLog2e : c.inv_temperature * kLog2e, k2 = c.inv_temperature * kLog2e, kept = TWO ? fminf(k1, k2) : k1;
+    const float r1 = k1 / kept, r2 = k2 / kept;
+    const int64_t parts = (width + kConvertColumns - 1) / kConvertColumns;
+    const int64_t items = (g.row0[g.n] - g.row0[0]) * parts;
+    for (int64_t item = (int64_t)blockIdx.x * kWarps + warp; item < items; item += (int64_t)gridDim.x * kWarps) {
+        const int row = g.row0[0] + (int)(item / parts);
+        const int i = rank_of(g, row), r = row - g.row0[i], count = c.counts[g.first + i];
+        if (r >= padded(count)) continue;
+        const int64_t first = item % parts * kConvertColumns;
+        uint16_t* at = piece + (int64_t)(row - g.row0[0]) * width + first + lane * 8;
+        if (r >= count) {
+#pragma unroll
+            for (int j = 0; j < kConvertColumns / 256; ++j)
+                if (first + j * 256 < width) *reinterpret_cast<uint4*>(at + j * 256) = make_uint4(0u, 0u, 0u, 0u);
+            continue;
+        }
+        uint4 x[kConvertColumns / 256];
+        float top[kConvertColumns / 256];
+#pragma unroll
+        for (int j = 0; j < kConvertColumns / 256; ++j)
+            if (first + j * 256 < width) {
+                x[j] = *reinterpret_cast<const uint4*>(at + j * 256);
+                const int64_t u = (first + j * 256 + lane * 8) / kLossUnit;
+                top[j] = u < c.units ? c.partial[(u * c.rows + row) * (TWO ? 4 : 2)] : -INFINITY;
+            }
+        const float4 coef = c.coef[row];
+        const int64_t token = LIST ? g.row0[i] + c.row_token[row] : 0;
+        const int32_t column = LIST ? 0 : c.row_column[row];
+#pragma unroll
+        for (int j = 0; j < kConvertColumns / 256; ++j) {
+            if (first + j * 256 >= width) break;
+            const int col = (int)first + j * 256 + lane * 8;
+            const float ref = top[j] == -INFINITY ? 0.f : top[j];
+            const float s1 = exp2f(fmaf(ref, k1, -coef.x) - kKeepBits) * coef.y;
+            const float b1 = fmaf(ref, k1, -coef.x) - kKeepBits * r1, b2 = fmaf(ref, k2, -coef.z) - kKeepBits * r2;
+            uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
+                if (TWO) {
+                    const float lo = __log2f(f.x), hi = __log2f(f.y);      // 0: -infinity, and 0 again
+                    w[e] = bf16x2_rn(coef.y * exp2f(fmaf(lo, r1, b1)) + coef.w * exp2f(fmaf(lo, r2, b2)),
+                                     coef.y * exp2f(fmaf(hi, r1, b1)) + coef.w * exp2f(fmaf(hi, r2, b2)));
+                } else {
+                    w[e] = bf16x2_rn(f.x * s1, f.y * s1);
+                }
+            }
+            // the exact gradient where a target or a teacher has its say
+            const auto put = [&](int32_t k, float value) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (k == col + e) {
+                        const uint32_t h = f32_to_bf16_rn(value);
+                        w[e / 2] = e % 2 ? (w[e / 2] & 0xFFFFu) | h << 16 : (w[e / 2] & 0xFFFF0000u) | h;
+                    }
+            };
+            if (LIST) {
+                if (col < c.vocab) {
+                    const uint16_t* starts = c.starts + token * (c.units + 1) + col / kLossUnit;
+                    for (int k = starts[0]; k < starts[1]; ++k) {
+                        const int32_t there = c.columns[token * c.list + k];
+                        if (there >= col && there < col + 8) put(there, c.value[token * c.list + k]);
+                    }
+                }
+            } else if (column >= col && column < col + 8) {
+                put(column, c.value[row]);
+            }
+            *reinterpret_cast<uint4*>(at + j * 256) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
 }
 
 // ---- hidden states' gradients --------------------------------------------------------
@@ -459,8 +552,14 @@ cudaError_t launch_loss_planes(const void* src, void* dst, int64_t rows, const L
 
 cudaError_t launch_loss_combine(const LossGroup& g, const LossCall& c, float* loss, cudaStream_t stream) {
     const int64_t blocks = (g.row0[g.n] - g.row0[0]) / kLossBlockRows;
-    return launch_dependent(c.two ? k_combine<true> : k_combine<false>, dim3(cap_ctas(std::min<int64_t>(blocks, 8 * sm_count()))),
-                            dim3(kThreads), 0, stream, g, c, loss);
+    return launch_dependent(c.two ? k_combine<true> : k_combine<false>, dim3(cap_ctas(std::min<int64_t>(blocks, 2 * sm_count()))),
+                            dim3(32 * kCombineWarps), 0, stream, g, c, loss);
+}
+
+cudaError_t launch_loss_convert(const LossGroup& g, const LossCall& c, void* piece, int64_t width, cudaStream_t stream) {
+    const auto kernel = c.two ? k_convert<true, true> : c.alpha != 0.f ? k_convert<false, true> : k_convert<false, false>;
+    const int64_t items = (g.row0[g.n] - g.row0[0]) * ((width + kConvertColumns - 1) / kConvertColumns);
+    return launch_dependent(kernel, dim3(warp_grid(items)), dim3(kThreads), 0, stream, g, c, static_cast<uint16_t*>(piece), width);
 }
 
 cudaError_t launch_loss_join(const LossGroup& g, const LossCall& c, int splits, cudaStream_t stream) {
