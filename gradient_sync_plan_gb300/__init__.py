@@ -947,11 +947,15 @@ class LossHead(_OwnMemory):
         _check("ddp_loss_head_workspace_bytes",
                lib().ddp_loss_head_workspace_bytes(self.world, self.vocab, self.dim, code, int(max_tokens), int(max_teacher),
                                                    0 if grads is None else 1, ctypes.byref(need)))
-        self.device = weights[0].device
         self._same_device("weights", weights, grads or [])
-        self._workspace = torch.empty(need.value, dtype=torch.uint8, device=self.device)
-        self.loss = torch.empty(self.world, dtype=torch.float32, device=self.device)
+        self._index = weights[0].get_device()
+        self._current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+        self._workspace = torch.empty(need.value, dtype=torch.uint8, device=weights[0].device)
+        self.loss = torch.empty(self.world, dtype=torch.float32, device=weights[0].device)
+        self._own = self.loss.data_ptr()
         self._owns(self._workspace, self.loss)
+        self._Pointers, self._Counts = ctypes.c_void_p * self.world, ctypes.c_int32 * self.world
+        self._floats, self._ints = (torch.float32, torch.bfloat16), (torch.int64,)
         self._keep = tuple(weights) + tuple(grads or [])
         h = ctypes.c_void_p()
         _check("ddp_loss_head_create",
@@ -964,50 +968,78 @@ class LossHead(_OwnMemory):
         device = _torch().cuda.current_device()
         for ts in lists:
             for t in ts:
-                if t is not None and (not t.is_cuda or t.device.index != device):
+                if t.get_device() != device:
                     raise ValueError(f"{what} must be in device memory of the current device")
 
     def _table(self, ts, what: str, dtypes, shapes):
-        """Pointers of contiguous tensors, one a rank, of these shapes."""
-        if len(ts) != self.world:
+        """Pointers of contiguous tensors, one a rank, of these shapes and one of these types."""
+        world, device = self.world, self._index
+        if len(ts) != world:
             raise ValueError(f"{what}: one tensor a rank")
-        for t, shape in zip(ts, shapes):
-            if t.dtype not in dtypes or t.dtype != ts[0].dtype or tuple(t.shape) != shape or not t.is_contiguous():
-                raise ValueError(f"{what}: contiguous tensors of {' or '.join(map(str, dtypes))}, {shape} here")
-        self._same_device(what, ts)
-        return _vp_array([t.data_ptr() for t in ts])
+        ptrs, dtype = self._Pointers(), ts[0].dtype
+        for r in range(world):
+            t = ts[r]
+            if t.shape != shapes[r] or t.dtype is not dtype or not t.is_contiguous():
+                raise ValueError(f"{what}: contiguous tensors of {' or '.join(map(str, dtypes))}, {shapes[r]} here")
+            if t.get_device() != device:
+                raise ValueError(f"{what} must be in device memory of the handle's device")
+            ptrs[r] = t.data_ptr()
+        if dtype not in dtypes:
+            raise ValueError(f"{what}: tensors of {' or '.join(map(str, dtypes))}")
+        return ptrs
 
     def _call(self, fn, hidden, targets, teacher, gradients, ignore_index, reduction, token_losses, out, stream):
-        torch = _torch()
-        if len(hidden) != self.world:
+        world, dim, dtype, device = self.world, self.dim, self.dtype, self._index
+        if len(hidden) != world:
             raise ValueError("hidden: one tensor a rank")
-        stride = None
-        for h in hidden:
-            if h.dim() != 2 or h.shape[1] != self.dim or h.dtype != self.dtype or (self.dim > 1 and h.stride(1) != 1):
-                raise ValueError(f"hidden: [tokens, {self.dim}] tensors of {self.dtype}, elements of a row together")
-            if h.shape[0] > 1:
-                stride = h.stride(0) if stride is None else stride
-                if h.stride(0) != stride:
+        if device != self._current():
+            raise ValueError("the handle's device must be the current one")
+        # every call's tensors are new ones: this loop and _table are most of a small call's time on the host
+        stride, rows, flat, tokens, ptrs = dim, [], [], self._Counts(), self._Pointers()
+        several = False
+        for r in range(world):
+            h = hidden[r]
+            shape = h.shape
+            if len(shape) != 2 or shape[1] != dim or h.dtype is not dtype:
+                raise ValueError(f"hidden: [tokens, {dim}] tensors of {dtype}")
+            if h.get_device() != device:
+                raise ValueError("hidden must be in device memory of the handle's device")
+            n = shape[0]
+            apart, step = h.stride()
+            if step != 1 and dim > 1:
+                raise ValueError("hidden: the elements of a row together")
+            if n > 1:
+                if several and apart != stride:
                     raise ValueError("hidden: rows equally far apart at every rank")
-        self._same_device("hidden", hidden)
-        tokens = [h.shape[0] for h in hidden]
-        flat = [(n,) for n in tokens]
-        args = [self._h, _i32_array(tokens), _vp_array([h.data_ptr() for h in hidden]), self.dim if stride is None else stride]
+                stride, several = apart, True
+            tokens[r] = n
+            ptrs[r] = h.data_ptr()
+            rows.append(shape)
+            flat.append((n,))
+        args = [self._h, tokens, ptrs, stride]
         if teacher is not None:
             logits, indices, temperature, alpha = teacher
             k = logits[0].shape[1] if len(logits) and logits[0].dim() == 2 else 0
-            rows = [(n, k) for n in tokens]
-            lp = self._table(logits, "teacher", (torch.float32, torch.bfloat16), rows)
-            args += [k, lp, dtype_code(logits[0]), self._table(indices, "indices", (torch.int64,), rows), temperature, alpha]
-        args += [None if targets is None else self._table(targets, "targets", (torch.int64,), flat), ignore_index, reduction]
+            entries = [(n, k) for n in tokens]
+            args += (k, self._table(logits, "teacher", self._floats, entries), dtype_code(logits[0]),
+                     self._table(indices, "indices", self._ints, entries), temperature, alpha)
+        args += (None if targets is None else self._table(targets, "targets", self._ints, flat), ignore_index, reduction)
         if gradients is not None:
-            args += [gradients[1], 1 if gradients[2] else 0]
-        args.append(None if token_losses is None else self._table(token_losses, "token_losses", (torch.float32,), flat))
-        args.append(_rank_words(self.loss if out is None else out, self.world, torch.float32, "out"))
+            args += (gradients[1], 1 if gradients[2] else 0)
+        args.append(None if token_losses is None else self._table(token_losses, "token_losses", self._floats[:1], flat))
+        if out is None:
+            out = self.loss
+            args.append(self._own)
+        else:
+            args.append(_rank_words(out, world, self._floats[0], "out"))
+            if out.get_device() != device:
+                raise ValueError("out must be in device memory of the handle's device")
         if gradients is not None:
-            args.append(self._table(gradients[0], "grad_hidden", (self.dtype,), [(n, self.dim) for n in tokens]))
-        _check(fn, getattr(self._lib, fn)(*args, self._on(stream)))
-        return self.loss if out is None else out
+            args.append(self._table(gradients[0], "grad_hidden", (dtype,), rows))
+        status = getattr(self._lib, fn)(*args, self._on(stream))
+        if status:
+            _check(fn, status)
+        return out
 
     def cross_entropy(self, hidden, targets, ignore_index: int = -100, reduction: int = DDP_LOSS_MEAN, token_losses=None,
                       out=None, stream=None):

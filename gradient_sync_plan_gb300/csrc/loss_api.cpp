@@ -350,6 +350,16 @@ int32_t run(ddp_loss_head* h, const Args& a, cudaStream_t stream) {
     }
     c.rows = std::max<int64_t>(rows, kLossRowAlign);
 
+    if (groups.size() == 1 && loss_is_small(groups[0], c)) {
+        LossSmall m{};
+        for (int32_t r = 0; r < h->world; ++r) {
+            m.weights[r] = h->weights[r];
+            m.grads[r] = a.grad ? h->grads[r] : nullptr;
+        }
+        m.grad = a.grad;
+        m.accumulate = a.accumulate;
+        return cuda_status(launch_loss_small(groups[0], c, m, a.loss, stream));
+    }
     for (const LossGroup& g : groups) {
         if (distill && (st = cuda_status(launch_loss_teacher(g, c, stream)))) return st;
         if ((st = cuda_status(launch_loss_scan(g, c, stream)))) return st;

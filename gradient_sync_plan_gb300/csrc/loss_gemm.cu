@@ -27,6 +27,9 @@
 // status word, the block's roles stop, loads in flight and products are waited
 // for, and tensor memory is freed.
 #include <algorithm>
+#include <mutex>
+#include <set>
+#include <utility>
 
 #include "ddp_device.cuh"
 #include "loss_internal.h"
@@ -744,7 +747,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_loss_gemm(const __grid_cons
 template <LossPhase PHASE, bool F32, bool TWO, bool LIST>
 cudaError_t launch(const LossGemm& g, int64_t most_tiles, cudaStream_t stream) {
     const auto kernel = k_loss_gemm<PHASE, F32, TWO, LIST>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    const cudaError_t e = allow_shared_memory((const void*)kernel, kSmem);
     if (e != cudaSuccess) return e;
     const int grid = cap_ctas(std::min<int64_t>(most_tiles, sm_count()));
     return launch_dependent(kernel, dim3(grid), dim3(kGemmThreads), kSmem, stream, g);
@@ -765,6 +768,19 @@ cudaError_t launch_type(const LossGemm& g, int64_t most_tiles, cudaStream_t stre
 }
 
 }  // namespace
+
+cudaError_t allow_shared_memory(const void* kernel, int bytes) {
+    static std::mutex lock;
+    static std::set<std::pair<int, const void*>> done;
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    const std::lock_guard<std::mutex> hold(lock);
+    if (done.count({device, kernel})) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.insert({device, kernel});
+    return e;
+}
 
 cudaError_t launch_loss_gemm(LossPhase phase, const LossGemm& g, int64_t most_tiles, cudaStream_t stream) {
     if (most_tiles <= 0) return cudaSuccess;

@@ -112,6 +112,22 @@ cudaError_t launch_loss_convert(const LossGroup& g, const LossCall& c, void* pie
 // acc's splits to the hidden states' gradients, zeros for tokens that are not learned.
 cudaError_t launch_loss_join(const LossGroup& g, const LossCall& c, int splits, cudaStream_t stream);
 
+// ---- little data (loss_small.cu) --------------------------------------------
+struct LossSmall {
+    const void* weights[kLossRanks];
+    void* grads[kLossRanks];
+    int32_t grad, accumulate;
+    int32_t most_tokens;                  // of a rank
+};
+// Elements of the weights, products of a matrix product of a rank, and teachers' entries of all ranks up to which one launch does
+// everything.
+constexpr int64_t kSmallWeights = 16384, kSmallWork = 1 << 19, kSmallEntries = 16384;
+bool loss_is_small(const LossGroup& g, const LossCall& c);
+cudaError_t launch_loss_small(const LossGroup& g, const LossCall& c, LossSmall m, float* loss, cudaStream_t stream);
+
+// Lets a kernel take this much dynamic shared memory, once a process and device.
+cudaError_t allow_shared_memory(const void* kernel, int bytes);
+
 // The address of the device status word, and the TMA kernels' wait limit (ring_tma.cu).
 cudaError_t device_status_address(int32_t** word);
 unsigned long long wait_limit_ns();
