@@ -71,13 +71,18 @@ struct ddp_loss_head {
     char* workspace = nullptr;
     Sizes at{};
     std::vector<std::pair<uintptr_t, uintptr_t>> read, written;    // the weights; the workspace and the gradients
-    std::vector<CUtensorMap> maps;                                 // of the weights, or their planes
+    std::vector<CUtensorMap> maps;                                 // of a rank's weights or planes: along and across, for single blocks and pairs
+    std::vector<CUtensorMap> outs;                                 // of the gradients
+    bool stores = false;                                           // whose rows all start on 16-byte boundaries
     int64_t copied = 0;                                            // bytes of a rank's planes in the workspace, 0: none
     int32_t* status = nullptr;
     int device = -1;                                               // that maps and status belong to
 };
 
 namespace {
+
+// Whether the products read the weights from the workspace: float32's planes, and bf16 rows that are not whole boxes.
+bool is_copied(int32_t dtype, int64_t dim) { return dtype == DDP_F32 || dim % kTileK != 0; }
 
 int planes_of(int32_t dtype) { return dtype == DDP_F32 ? 3 : 1; }
 
@@ -108,8 +113,7 @@ Sizes layout(int64_t world, int64_t vocab, int64_t dim, int32_t dtype, int64_t m
     }
     put(&s.gathered, 2 * planes * rows * dimp);
     s.weights_bytes = 2 * planes * vocab * dimp;
-    // planes of the weights: always for float32; for bf16 where rows do not start on 16-byte boundaries
-    put(&s.weights, dtype == DDP_F32 || dim % 8 ? world * s.weights_bytes : 0);
+    put(&s.weights, is_copied(dtype, dim) ? world * s.weights_bytes : 0);
     if (grads) {
         put(&s.value, 4 * rows * list);
         put(&s.coef, 16 * rows);
@@ -153,31 +157,38 @@ cudaError_t encoder(EncodeFn* fn) {
     return cudaSuccess;
 }
 
-// [planes][rows][columns] bf16, plane_bytes apart, in boxes of 64 x 64.
-int32_t map_bf16(CUtensorMap* m, const void* base, int64_t columns, int64_t rows, int64_t row_bytes, int64_t planes,
-                 int64_t plane_bytes) {
+// A matrix of bf16 planes [planes][rows][columns], columns a multiple of 64, as [planes][columns / 64][rows][64] in boxes
+// of `box_rows` rows and `box_blocks` blocks of columns.
+int32_t map_load(CUtensorMap* m, const void* base, int64_t columns, int64_t rows, int64_t planes, int box_rows, int box_blocks) {
     EncodeFn fn;
     const int32_t st = cuda_status(encoder(&fn));
     if (st) return st;
-    const cuuint64_t dims[3] = {(cuuint64_t)columns, (cuuint64_t)rows, (cuuint64_t)planes};
-    const cuuint64_t strides[2] = {(cuuint64_t)row_bytes, (cuuint64_t)round_up(plane_bytes, 16)};
-    const cuuint32_t box[3] = {64, 64, 1}, steps[3] = {1, 1, 1};
-    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, steps,
+    const cuuint64_t dims[4] = {64, (cuuint64_t)rows, (cuuint64_t)(columns / 64), (cuuint64_t)planes};
+    const cuuint64_t strides[3] = {(cuuint64_t)(2 * columns), 128, (cuuint64_t)(2 * columns * rows)};
+    const cuuint32_t box[4] = {64, (cuuint32_t)box_rows, (cuuint32_t)box_blocks, 1}, steps[4] = {1, 1, 1, 1};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, steps,
                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? DDP_OK : cuda_status(cudaErrorInvalidValue);
 }
-// [rows][columns] float32 in boxes of 128 rows of 32.
-int32_t map_f32(CUtensorMap* m, const void* base, int64_t columns, int64_t rows) {
+// Boxes of an operand's stage: rows along the depth, or kTileK rows of the depth and their columns across it.
+int32_t map_along(CUtensorMap* m, const void* base, int64_t columns, int64_t rows, int64_t planes, int box_rows) {
+    return map_load(m, base, columns, rows, planes, box_rows, 1);
+}
+int32_t map_across(CUtensorMap* m, const void* base, int64_t columns, int64_t rows, int64_t planes, int box_columns) {
+    return map_load(m, base, columns, rows, planes, kTileK, box_columns / 64);
+}
+// [rows][columns] in boxes of 128 rows of 128 bytes, for stores.
+int32_t map_out(CUtensorMap* m, const void* base, int32_t dtype, int64_t columns, int64_t rows) {
     EncodeFn fn;
     const int32_t st = cuda_status(encoder(&fn));
     if (st) return st;
     const cuuint64_t dims[2] = {(cuuint64_t)columns, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)columns * 4};
-    const cuuint32_t box[2] = {32, kTileM}, steps[2] = {1, 1};
-    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(base), dims, strides, box, steps,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const cuuint64_t strides[1] = {(cuuint64_t)(columns * elem_bytes(dtype))};
+    const cuuint32_t box[2] = {(cuuint32_t)(128 / elem_bytes(dtype)), kTileM}, steps[2] = {1, 1};
+    const CUresult r = fn(m, dtype == DDP_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                          const_cast<void*>(base), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? DDP_OK : cuda_status(cudaErrorInvalidValue);
 }
 
@@ -189,14 +200,15 @@ int32_t bind_device(ddp_loss_head* h) {
     if (h->device >= 0) return device == h->device ? DDP_OK : DDP_ERR_INVALID;
     if ((st = cuda_status(device_status_address(&h->status)))) return st;
     const int64_t dimp = round_up(h->dim, kTileK), planes = planes_of(h->dtype);
-    h->maps.resize(h->world);
+    h->maps.resize(4 * h->world);
+    h->outs.resize(h->stores ? h->world : 0);
     for (int32_t r = 0; r < h->world; ++r) {
-        if (h->copied)
-            st = map_bf16(&h->maps[r], h->workspace + h->at.weights + r * h->copied, dimp, h->vocab, 2 * dimp, planes,
-                          2 * h->vocab * dimp);
-        else
-            st = map_bf16(&h->maps[r], h->weights[r], h->dim, h->vocab, 2 * (int64_t)h->dim, 1, 2 * (int64_t)h->vocab * h->dim);
-        if (st) return st;
+        const void* base = h->copied ? h->workspace + h->at.weights + r * h->copied : static_cast<const void*>(h->weights[r]);
+        for (int cg = 1; cg <= 2; ++cg)
+            if ((st = map_along(&h->maps[4 * r + 2 * (cg - 1)], base, dimp, h->vocab, planes, kTileN / cg)) ||
+                (st = map_across(&h->maps[4 * r + 2 * (cg - 1) + 1], base, dimp, h->vocab, planes, kTileN / cg)))
+                return st;
+        if (h->stores && (st = map_out(&h->outs[r], h->grads[r], h->dtype, h->dim, h->vocab))) return st;
     }
     h->device = device;
     return DDP_OK;
@@ -372,20 +384,27 @@ int32_t run(ddp_loss_head* h, const Args& a, cudaStream_t stream) {
     m.c = c;
     m.limit_ns = std::max(wait_limit_ns(), 2000000000ull);
     m.accumulate = a.accumulate;
-    if ((st = map_bf16(&m.hidden, c.gathered, c.dimp, c.rows, 2 * c.dimp, c.planes, 2 * c.rows * c.dimp))) return st;
-    if (a.grad) {
-        m.vec = 1;
-        for (void* p : h->grads)
-            if (reinterpret_cast<uintptr_t>(p) % (h->dtype == DDP_F32 ? 16 : 8) || h->dim % 4) m.vec = 0;
+    // a pair's tiles are 256 rows: 3/4 of them and more hold tokens there
+    int64_t tokens = 0, pair_rows = 0;
+    for (int32_t r = 0; r < h->world; ++r) {
+        tokens += a.tokens[r];
+        pair_rows += round_up(a.tokens[r], 2 * kTileM);
     }
+    m.pairs = 4 * tokens >= 3 * pair_rows && cap_ctas(2) == 2;
+    const int cg = m.pairs ? 2 : 1;
+    CUtensorMap hidden[2];                 // along, across
+    if ((st = map_along(&hidden[0], c.gathered, c.dimp, c.rows, c.planes, kTileM)) ||
+        (st = map_across(&hidden[1], c.gathered, c.dimp, c.rows, c.planes, kTileN / cg)))
+        return st;
+    if (a.grad) m.store = h->stores && !a.accumulate;
     for (const LossGroup& g : groups) {
-        const int64_t span = g.row0[g.n] - g.row0[0], row_tiles = span / kTileM;
+        const int64_t span = g.row0[g.n] - g.row0[0];
         m.n = g.n;
         m.first = g.first;
         std::copy(g.row0, g.row0 + kLossRanks + 1, m.row0);
         for (int i = 0; i < g.n; ++i) {
-            m.weights[i] = h->maps[g.first + i];
             m.grads[i] = a.grad ? h->grads[g.first + i] : nullptr;
+            if (a.grad && h->stores) m.out[i] = h->outs[g.first + i];
         }
         const bool keep = span > 0 && span <= keep_rows;
         const int64_t width = !a.grad || keep ? vocab_width : piece_width(at.piece_bytes, span, h->vocab, c.planes);
@@ -393,31 +412,35 @@ int32_t run(ddp_loss_head* h, const Args& a, cudaStream_t stream) {
             m.splits = (int32_t)splits_for(c.rows, c.dim, std::min<int64_t>(width, h->vocab));
             const int64_t blocks = (std::min<int64_t>(width, h->vocab) + kTileK - 1) / kTileK;
             m.split_blocks = (int32_t)((blocks + m.splits - 1) / m.splits);
-            if ((st = map_f32(&m.acc, c.acc, c.dimp, m.splits * c.rows))) return st;
-            if (span > 0 && (st = map_bf16(&m.piece, w + at.piece, width, span, 2 * width, c.planes, 2 * span * width))) return st;
+            if ((st = map_out(&m.acc, c.acc, DDP_F32, c.dimp, m.splits * c.rows))) return st;
+            if (span > 0 && ((st = map_along(&m.piece, w + at.piece, width, span, c.planes, kTileM)) ||
+                             (st = map_across(&m.piece_across, w + at.piece, width, span, c.planes, kTileM)) ||
+                             (st = map_out(&m.piece_out, w + at.piece, DDP_BF16, width, span * c.planes))))
+                return st;
         }
+        const auto operands = [&](bool across) {
+            m.hidden = hidden[across];
+            for (int i = 0; i < g.n; ++i) m.weights[i] = h->maps[4 * (g.first + i) + 2 * (cg - 1) + across];
+        };
+        operands(false);
         if (span > 0) {
             m.piece0 = 0;
             m.width = h->vocab;
             if ((st = cuda_status(launch_loss_gather(g, c, stream))) ||
-                (st = cuda_status(launch_loss_gemm(keep ? LossPhase::kKeep : LossPhase::kStats, m,
-                                                   row_tiles * ((h->vocab + kTileN - 1) / kTileN), stream))))
+                (st = cuda_status(launch_loss_gemm(keep ? LossPhase::kKeep : LossPhase::kStats, m, stream))))
                 return st;
         }
         if ((st = cuda_status(launch_loss_combine(g, c, a.loss, stream)))) return st;
         if (!a.grad) continue;
-        const int64_t dim_tiles = (h->dim + kTileN - 1) / kTileN;
         for (int64_t v = 0; v < h->vocab; v += width) {
             m.piece0 = (int32_t)v;
             m.width = (int32_t)std::min<int64_t>(width, h->vocab - v);
             m.add = v > 0;
+            operands(false);
             if (keep) st = cuda_status(launch_loss_convert(g, c, w + at.piece, width, stream));
-            else st = cuda_status(launch_loss_gemm(LossPhase::kGrad, m, row_tiles * ((m.width + kTileN - 1) / kTileN), stream));
-            if (st || (st = cuda_status(launch_loss_gemm(LossPhase::kProducts, m,
-                                                         row_tiles * dim_tiles * m.splits +
-                                                             g.n * ((m.width + kTileM - 1) / kTileM) * dim_tiles,
-                                                         stream))))
-                return st;
+            else st = cuda_status(launch_loss_gemm(LossPhase::kGrad, m, stream));
+            operands(true);
+            if (st || (st = cuda_status(launch_loss_gemm(LossPhase::kProducts, m, stream)))) return st;
         }
         if (span > 0 && (st = cuda_status(launch_loss_join(g, c, m.splits, stream)))) return st;
     }
@@ -461,7 +484,7 @@ int32_t ddp_loss_head_create(int32_t world, const void* const* weights, void* co
     const int64_t es = elem_bytes(dtype), bytes = (int64_t)vocab * dim * es;
     h->written.push_back(span_of(workspace, h->at.total));
     for (int32_t r = 0; r < world; ++r) {
-        if ((st = check_ptr(weights[r], dtype == DDP_F32 || dim % 8 ? es : 16))) return st;
+        if ((st = check_ptr(weights[r], is_copied(dtype, dim) ? es : 16))) return st;
         h->weights.push_back(weights[r]);
         h->read.push_back(span_of(weights[r], bytes));
         if (!grads) continue;
@@ -469,7 +492,9 @@ int32_t ddp_loss_head_create(int32_t world, const void* const* weights, void* co
         h->grads.push_back(grads[r]);
         h->written.push_back(span_of(grads[r], bytes));
     }
-    if (dtype == DDP_F32 || dim % 8) h->copied = h->at.weights_bytes;
+    if (is_copied(dtype, dim)) h->copied = h->at.weights_bytes;
+    h->stores = grads != nullptr && dim * es % 16 == 0;
+    for (void* p : h->grads) h->stores &= reinterpret_cast<uintptr_t>(p) % 16 == 0;
     if (any_overlap(&h->written)) return DDP_ERR_INVALID;
     for (const Span& s : h->read)
         if (hits_any(h->written, s)) return DDP_ERR_INVALID;

@@ -14,8 +14,8 @@
 // Both operands of kProducts are read as they lie in memory: the tensor cores
 // take matrices whose rows run along the depth or across it.
 //
-// One block an SM walks over tiles.  A thread issues the tiles' loads (TMA, boxes
-// of 64 x 64 elements, a ring of stages in shared memory), another the products
+// One block an SM walks over tiles.  A thread issues the tiles' loads (TMA, one an
+// operand and stage of a ring in shared memory), another the products
 // (tcgen05.mma, accumulators in tensor memory, two tiles' worth), eight warps
 // take finished tiles out of tensor memory while the next one is computed.
 //
@@ -37,9 +37,14 @@
 namespace ddpk {
 namespace {
 
-constexpr int kStages = 4;
-constexpr int kBytesA = kTileM * kTileK * 2, kBytesB = kTileN * kTileK * 2;
-constexpr int kBytesStage = kBytesA + kBytesB;
+// CG blocks of a cluster work on one tile of CG * 128 rows: each has its rows of A and 1 / CG of B's columns.
+template <int CG>
+struct Shape {
+    static constexpr int kStages = CG == 2 ? 6 : 4;
+    static constexpr int kBytesA = kTileM * kTileK * 2, kBytesB = kTileN / CG * kTileK * 2;
+    static constexpr int kBytesStage = kBytesA + kBytesB;
+};
+constexpr int kMostStages = 6;
 constexpr int kBytesBox = 64 * 64 * 2;
 constexpr int kBytesStaging = 128 * 128;               // 128 rows of 128 bytes
 constexpr int kFirstEpilogueWarp = 4, kEpilogueWarps = 8;
@@ -48,7 +53,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kKeepScale = (float)(1 << kKeepBits);
 
 struct Control {
-    uint64_t full[kStages], empty[kStages];
+    uint64_t full[kMostStages], empty[kMostStages];
     uint64_t ready[2], taken[2];                       // accumulators
     uint64_t drain;
     uint32_t tmem;
@@ -56,7 +61,10 @@ struct Control {
     int32_t go[2][2];                                  // by group and accumulators: the tile is there
     int32_t counts[kLossRanks];
 };
-constexpr int kSmem = 1024 + kStages * kBytesStage + 2 * kBytesStaging + (int)sizeof(Control);
+constexpr int kStageBytes = 192 * 1024;
+static_assert(Shape<1>::kStages * Shape<1>::kBytesStage == kStageBytes && Shape<2>::kStages * Shape<2>::kBytesStage == kStageBytes,
+              "stages of either shape");
+constexpr int kSmem = 1024 + kStageBytes + 2 * kBytesStaging + (int)sizeof(Control);
 static_assert(kSmem <= 227 * 1024, "shared memory of a block");
 
 __device__ __forceinline__ uint32_t smem_of(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -69,6 +77,28 @@ __device__ __forceinline__ void bar_expect(uint64_t* b, uint32_t bytes) {
 }
 __device__ __forceinline__ void bar_arrive(uint64_t* b) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_of(b)) : "memory");
+}
+// The address, in the cluster, of this block's `p` in the cluster's first block.
+__device__ __forceinline__ uint32_t in_first_block(const void* p) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_of(p)));
+    return a;
+}
+// A warp's arrival at the first block's barrier.
+template <int CG>
+__device__ __forceinline__ void warp_arrive(uint64_t* b, int lane) {
+    __syncwarp();
+    if (lane != 0) return;
+    if constexpr (CG == 1) bar_arrive(b);
+    else asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(in_first_block(b)) : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ int cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return (int)r;
 }
 __device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t parity) {
     uint32_t ok;
@@ -107,16 +137,20 @@ __device__ __forceinline__ void bar_wait_rest(uint64_t* b, uint32_t parity, cons
         if (now_ns() - t0 > g.limit_ns) return;
 }
 
-__device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
-        ::"r"(smem_of(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_of(bar))
-        : "memory");
-}
-__device__ __forceinline__ void tma_store(const CUtensorMap* map, const void* src, int x, int y, int z) {
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map),
-                 "r"(smem_of(src)), "r"(x), "r"(y), "r"(z)
-                 : "memory");
+// A box of a matrix seen as [planes][columns / 64][rows][64], from column x (a multiple of 64) and row y.
+// bar: an address in the cluster (this block's own or, of a pair, the first's).
+template <int CG>
+__device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int x, int y, int plane, uint32_t bar) {
+    if constexpr (CG == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+            ::"r"(smem_of(dst)), "l"(map), "r"(0), "r"(y), "r"(x / 64), "r"(plane), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+            "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_of(dst)), "l"(map), "r"(0), "r"(y), "r"(x / 64), "r"(plane), "r"(bar)
+            : "memory");
 }
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int x, int y) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map),
@@ -141,21 +175,36 @@ __device__ __forceinline__ uint64_t matrix_desc(uint32_t addr, uint32_t lbo) {
     return (uint64_t)((addr & 0x3FFFF) >> 4) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
            ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
-// Instruction descriptor: bf16 x bf16 into float32, kTileM x kTileN; `across`: rows run across the depth.
-__device__ __forceinline__ uint32_t product_desc(bool a_across, bool b_across) {
+// Instruction descriptor: bf16 x bf16 into float32, m x n; `across`: rows run across the depth.
+__device__ __forceinline__ uint32_t product_desc(bool a_across, bool b_across, int m, int n) {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((a_across ? 1u : 0u) << 15) | ((b_across ? 1u : 0u) << 16) |
-           ((uint32_t)(kTileN >> 3) << 17) | ((uint32_t)(kTileM >> 4) << 24);
+           ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
+template <int CG>
 __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(desc), "r"((uint32_t)add)
-        : "memory");
+    if constexpr (CG == 1)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(desc), "r"((uint32_t)add)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(desc), "r"((uint32_t)add)
+            : "memory");
 }
+// The products issued so far arrive at the barrier, of a pair at both blocks'.
+template <int CG>
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_of(bar))
-                 : "memory");
+    if constexpr (CG == 1)
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_of(bar)) : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                         smem_of(bar)),
+                     "h"((uint16_t)3)
+                     : "memory");
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -181,9 +230,10 @@ __device__ __forceinline__ float exp2_of(float x) {
     return y;
 }
 
-// A tile: rank, first row (of all ranks' rows; a column of the piece for dw), first column, k blocks.
+// A tile: rank, first row (of all ranks' rows; a column of the piece for dw), first column, columns (of the products: a
+// multiple of 64 for each block), k blocks.
 struct Tile {
-    int rank, m, n, k0, k1, split;
+    int rank, m, n, columns, k0, k1, split;
     bool weights;                          // of dw
 };
 
@@ -191,20 +241,15 @@ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; 
 
 // Tiles of rank i in the phase: of its rows first, of its weights' gradients behind those of all ranks.
 template <LossPhase PHASE>
-__device__ __forceinline__ int row_tiles(const LossGemm& g, const int32_t* counts, int i) {
-    const int m = ceil_div(counts[i], kTileM);
-    if (PHASE == LossPhase::kStats || PHASE == LossPhase::kKeep) return m * ceil_div(g.c.vocab, kTileN);
-    if (PHASE == LossPhase::kGrad) return m * ceil_div(g.width, kTileN);
-    return m * ceil_div(g.c.dim, kTileN) * g.splits;
+__device__ __forceinline__ int phase_columns(const LossGemm& g) {
+    return PHASE == LossPhase::kProducts ? g.c.dim : PHASE == LossPhase::kGrad ? g.width : g.c.vocab;
 }
-__device__ __forceinline__ int weight_tiles(const LossGemm& g, const int32_t* counts, int i) {
-    if (counts[i] == 0 && g.accumulate) return 0;
-    return ceil_div(g.width, kTileM) * ceil_div(g.c.dim, kTileN);
-}
-template <LossPhase PHASE>
+template <LossPhase PHASE, int CG>
 __device__ __forceinline__ bool find_tile(const LossGemm& g, const int32_t* counts, int t, Tile* w) {
+    constexpr int M = CG * kTileM;
+    const int all = phase_columns<PHASE>(g), nt = ceil_div(all, kTileN);
     for (int i = 0; i < g.n; ++i) {
-        const int n = row_tiles<PHASE>(g, counts, i);
+        const int m = ceil_div(counts[i], M), n = m * nt * (PHASE == LossPhase::kProducts ? g.splits : 1);
         if (t >= n) {
             t -= n;
             continue;
@@ -212,38 +257,37 @@ __device__ __forceinline__ bool find_tile(const LossGemm& g, const int32_t* coun
         w->rank = i;
         w->weights = false;
         w->split = 0;
-        const int m = ceil_div(counts[i], kTileM);
         if (PHASE != LossPhase::kProducts) {           // rows' tiles of one column block together: they share the weights
-            w->m = g.row0[i] + t % m * kTileM;
+            w->m = g.row0[i] + t % m * M;
             w->n = t / m * kTileN;
             w->k0 = 0;
             w->k1 = g.c.dimp / kTileK;
         } else {
-            const int nt = ceil_div(g.c.dim, kTileN);
             w->n = t % nt * kTileN;
             t /= nt;
-            w->m = g.row0[i] + t % m * kTileM;
+            w->m = g.row0[i] + t % m * M;
             w->split = t / m;
             w->k0 = w->split * g.split_blocks;
             w->k1 = min(w->k0 + g.split_blocks, ceil_div(g.width, kTileK));
         }
+        w->columns = ceil_div(min(all - w->n, kTileN), 64 * CG) * 64 * CG;
         return true;
     }
     if constexpr (PHASE == LossPhase::kProducts) {
         for (int i = 0; i < g.n; ++i) {
-            const int n = weight_tiles(g, counts, i);
+            const int n = counts[i] == 0 && g.accumulate ? 0 : ceil_div(g.width, M) * nt;
             if (t >= n) {
                 t -= n;
                 continue;
             }
-            const int nt = ceil_div(g.c.dim, kTileN);
             w->rank = i;
             w->weights = true;
             w->split = 0;
             w->n = t % nt * kTileN;
-            w->m = t / nt * kTileM;
+            w->m = t / nt * M;
             w->k0 = 0;
             w->k1 = ceil_div(counts[i], kTileK);
+            w->columns = ceil_div(min(all - w->n, kTileN), 64 * CG) * 64 * CG;
             return true;
         }
     }
@@ -254,14 +298,17 @@ __device__ constexpr int8_t kPlaneA[6] = {2, 1, 0, 1, 0, 0};
 __device__ constexpr int8_t kPlaneB[6] = {0, 1, 2, 0, 1, 0};
 
 // ---- producer -----------------------------------------------------------------
-template <LossPhase PHASE, bool F32>
-__device__ void produce(const LossGemm& g, Control* s, char* stages) {
+// Of a pair, each block loads its own operands; all arrive at the first block's barrier.
+template <LossPhase PHASE, bool F32, int CG>
+__device__ void produce(const LossGemm& g, Control* s, char* stages, int block, int t0, int step) {
+    using S = Shape<CG>;
     int stage = 0, issued = 0;
     uint32_t phase = 0;
     bool ok = true;
     Tile w;
-    for (int t = blockIdx.x; ok && find_tile<PHASE>(g, s->counts, t, &w); t += gridDim.x) {
+    for (int t = t0; ok && find_tile<PHASE, CG>(g, s->counts, t, &w); t += step) {
         const CUtensorMap* wmap = &g.weights[w.rank];
+        const int bm = w.m + block * kTileM, bn = w.n + block * (w.columns / CG);
         for (int q = 0; ok && q < (F32 ? 6 : 1); ++q) {
             const int pa = F32 ? kPlaneA[q] : 0, pb = F32 ? kPlaneB[q] : 0;
             for (int kb = w.k0; kb < w.k1; ++kb) {
@@ -269,47 +316,60 @@ __device__ void produce(const LossGemm& g, Control* s, char* stages) {
                     ok = false;
                     break;
                 }
-                char* a = stages + stage * kBytesStage;
-                char* b = a + kBytesA;
-                uint64_t* bar = &s->full[stage];
-                bar_expect(bar, kBytesStage);
+                char* a = stages + stage * S::kBytesStage;
+                char* b = a + S::kBytesA;
+                if (block == 0) bar_expect(&s->full[stage], CG * S::kBytesStage);
+                const uint32_t bar = CG == 1 ? smem_of(&s->full[stage]) : in_first_block(&s->full[stage]);
                 const int k = kb * kTileK;
                 if (PHASE != LossPhase::kProducts) {
-                    for (int j = 0; j < kTileM / 64; ++j) tma_load(a + j * kBytesBox, &g.hidden, k, w.m + 64 * j, pa, bar);
-                    for (int j = 0; j < kTileN / 64; ++j)
-                        tma_load(b + j * kBytesBox, wmap, k, g.piece0 + w.n + 64 * j, pb, bar);
+                    tma_load<CG>(a, &g.hidden, k, bm, pa, bar);
+                    tma_load<CG>(b, wmap, k, g.piece0 + bn, pb, bar);
                 } else if (!w.weights) {
-                    for (int j = 0; j < kTileM / 64; ++j)
-                        tma_load(a + j * kBytesBox, &g.piece, k, w.m - g.row0[0] + 64 * j, pa, bar);
-                    for (int j = 0; j < kTileN / 64; ++j) tma_load(b + j * kBytesBox, wmap, w.n + 64 * j, g.piece0 + k, pb, bar);
+                    tma_load<CG>(a, &g.piece, k, bm - g.row0[0], pa, bar);
+                    tma_load<CG>(b, wmap, bn, g.piece0 + k, pb, bar);
                 } else {
                     const int row = g.row0[w.rank] + k;
-                    for (int j = 0; j < kTileM / 64; ++j)
-                        tma_load(a + j * kBytesBox, &g.piece, w.m + 64 * j, row - g.row0[0], pa, bar);
-                    for (int j = 0; j < kTileN / 64; ++j) tma_load(b + j * kBytesBox, &g.hidden, w.n + 64 * j, row, pb, bar);
+                    tma_load<CG>(a, &g.piece_across, bm, row - g.row0[0], pa, bar);
+                    tma_load<CG>(b, &g.hidden, bn, row, pb, bar);
                 }
                 ++issued;
-                if (++stage == kStages) {
+                if (++stage == S::kStages) {
                     stage = 0;
                     phase ^= 1;
                 }
             }
         }
     }
-    if (!ok)                               // loads in flight, before the block's shared memory goes
-        for (int i = max(0, issued - kStages); i < issued; ++i) bar_wait_rest(&s->full[i % kStages], (i / kStages) & 1, g);
+    // what the products still have to report arrives here before the block ends
+    for (int i = 0; ok && i < S::kStages; ++i) {
+        ok = bar_wait(&s->empty[stage], phase ^ 1, s, g);
+        if (++stage == S::kStages) {
+            stage = 0;
+            phase ^= 1;
+        }
+    }
+    if (!ok) {                             // loads in flight, before the block's shared memory goes
+        if (block == 0) {
+            for (int i = max(0, issued - S::kStages); i < issued; ++i)
+                bar_wait_rest(&s->full[i % S::kStages], (i / S::kStages) & 1, g);
+        } else {                           // they report to the other block: far longer than a load takes
+            const unsigned long long t1 = now_ns();
+            while (now_ns() - t1 < 10000000ull) {}
+        }
+    }
 }
 
 // ---- products -----------------------------------------------------------------
-template <LossPhase PHASE, bool F32>
-__device__ void multiply(const LossGemm& g, Control* s, char* stages, uint32_t tmem) {
+template <LossPhase PHASE, bool F32, int CG>
+__device__ void multiply(const LossGemm& g, Control* s, char* stages, uint32_t tmem, int t0, int step) {
+    using S = Shape<CG>;
     int stage = 0, buf = 0;
     uint32_t phase = 0, taken = 1;
     bool ok = true;
     Tile w;
-    for (int t = blockIdx.x; ok && find_tile<PHASE>(g, s->counts, t, &w); t += gridDim.x) {
+    for (int t = t0; ok && find_tile<PHASE, CG>(g, s->counts, t, &w); t += step) {
         const bool a_across = PHASE == LossPhase::kProducts && w.weights, b_across = PHASE == LossPhase::kProducts;
-        const uint32_t desc = product_desc(a_across, b_across);
+        const uint32_t desc = product_desc(a_across, b_across, CG * kTileM, w.columns);
         // 16 elements of depth: 32 bytes along a row, or 16 rows of 128 bytes
         const uint32_t step_a = a_across ? 16 * 128 / 16 : 2, step_b = b_across ? 16 * 128 / 16 : 2;
         if (!bar_wait(&s->taken[buf], taken, s, g)) {
@@ -324,24 +384,24 @@ __device__ void multiply(const LossGemm& g, Control* s, char* stages, uint32_t t
                 break;
             }
             fence_after();
-            const uint32_t a = smem_of(stages + stage * kBytesStage);
-            const uint64_t da = matrix_desc(a, kBytesBox), db = matrix_desc(a + kBytesA, kBytesBox);
+            const uint32_t a = smem_of(stages + stage * S::kBytesStage);
+            const uint64_t da = matrix_desc(a, kBytesBox), db = matrix_desc(a + S::kBytesA, kBytesBox);
 #pragma unroll
             for (int k = 0; k < kTileK / 16; ++k)
-                mma(tmem + buf * kTileN, da + k * step_a, db + k * step_b, desc, i > 0 || k > 0);
-            mma_commit(&s->empty[stage]);
-            if (++stage == kStages) {
+                mma<CG>(tmem + buf * kTileN, da + k * step_a, db + k * step_b, desc, i > 0 || k > 0);
+            mma_commit<CG>(&s->empty[stage]);
+            if (++stage == S::kStages) {
                 stage = 0;
                 phase ^= 1;
             }
         }
         if (!ok) break;
-        mma_commit(&s->ready[buf]);
+        mma_commit<CG>(&s->ready[buf]);
         if (buf == 1) taken ^= 1;
         buf ^= 1;
     }
     if (!ok) {                             // products in flight, before tensor memory goes
-        mma_commit(&s->drain);
+        mma_commit<CG>(&s->drain);
         bar_wait_rest(&s->drain, 0, g);
     }
 }
@@ -396,7 +456,7 @@ struct Listed {
 
 // Twice over the row's 128 logits: their maximum, and their exponentials relative to it.  KEEP: the exponentials go to
 // the piece's buffer as binary16, 2^kKeepBits for the row's largest, so that those down to 2^-29 of it keep 11 bits.
-template <bool TWO, bool LIST, bool KEEP>
+template <bool TWO, bool LIST, bool KEEP, int CG>
 __device__ __forceinline__ void stats_tile(const LossGemm& g, const Tile& w, const Lane& l, Control* s, uint64_t* taken) {
     const LossCall& c = g.c;
     const int row = w.m + l.row, first = w.n + l.group * kLossUnit;
@@ -448,7 +508,7 @@ __device__ __forceinline__ void stats_tile(const LossGemm& g, const Tile& w, con
             tmem_wait();
             if (h == 1 && j == kLossUnit / 64 - 1) {
                 fence_before();
-                bar_arrive(taken);
+                warp_arrive<CG>(taken, l.lane);
             }
             if (col + h * 32 + 32 > c.vocab) {
 #pragma unroll
@@ -488,8 +548,7 @@ __device__ __forceinline__ void stats_tile(const LossGemm& g, const Tile& w, con
             group_sync(l.group);
             if (l.leader) {
                 const int x = w.n + l.group * kLossUnit + j * 64, y = w.m - g.row0[0];
-                tma_store(&g.piece, l.staging, x, y, 0);
-                tma_store(&g.piece, l.staging + 64 * 128, x, y + 64, 0);
+                tma_store_2d(&g.piece_out, l.staging, x, y);
                 tma_commit();
             }
         }
@@ -502,7 +561,7 @@ __device__ __forceinline__ void stats_tile(const LossGemm& g, const Tile& w, con
     }
 }
 
-template <bool F32, bool TWO, bool LIST>
+template <bool F32, bool TWO, bool LIST, int CG>
 __device__ __forceinline__ void grad_tile(const LossGemm& g, const Tile& w, const Lane& l, Control* s, uint64_t* taken) {
     const LossCall& c = g.c;
     const int row = w.m + l.row, first = g.piece0 + w.n + l.group * kLossUnit;
@@ -519,7 +578,7 @@ __device__ __forceinline__ void grad_tile(const LossGemm& g, const Tile& w, cons
         tmem_wait();
         if (j == kLossUnit / 64 - 1) {
             fence_before();
-            bar_arrive(taken);
+            warp_arrive<CG>(taken, l.lane);
         }
         const int col = first + j * 64;
 #pragma unroll
@@ -560,8 +619,7 @@ __device__ __forceinline__ void grad_tile(const LossGemm& g, const Tile& w, cons
             group_sync(l.group);
             if (l.leader) {
                 const int x = w.n + l.group * kLossUnit + j * 64, y = w.m - g.row0[0];
-                tma_store(&g.piece, l.staging, x, y, q);
-                tma_store(&g.piece, l.staging + 64 * 128, x, y + 64, q);
+                tma_store_2d(&g.piece_out, l.staging, x, q * (g.row0[g.n] - g.row0[0]) + y);
                 tma_commit();
             }
         }
@@ -570,6 +628,7 @@ __device__ __forceinline__ void grad_tile(const LossGemm& g, const Tile& w, cons
 
 // dh: the tile goes to its split's part of acc, added there by the copy engine from the second piece on (one
 // writer an element and launch, so the order is fixed).
+template <int CG>
 __device__ __forceinline__ void hidden_tile(const LossGemm& g, const Tile& w, const Lane& l, uint64_t* taken) {
 #pragma unroll 1
     for (int j = 0; j < kTileN / 2 / 32; ++j) {
@@ -579,7 +638,7 @@ __device__ __forceinline__ void hidden_tile(const LossGemm& g, const Tile& w, co
         tmem_wait();
         if (j == kTileN / 2 / 32 - 1) {
             fence_before();
-            bar_arrive(taken);
+            warp_arrive<CG>(taken, l.lane);
         }
         // the same for the whole group: no column of acc, or no depth in a shorter last piece
         if (col >= g.c.dimp || w.k1 <= w.k0) continue;
@@ -597,11 +656,50 @@ __device__ __forceinline__ void hidden_tile(const LossGemm& g, const Tile& w, co
     }
 }
 
-// dw: rows of the weights' gradients, rounded once, written row by row.
-template <bool F32>
+// dw: rows of the weights' gradients, rounded once.  Where rows start on 16-byte boundaries the copy engine writes
+// them; else, and to add to what is there, a warp goes row by row, a lane a column.
+template <bool F32, int CG>
 __device__ __forceinline__ void weights_tile(const LossGemm& g, const Tile& w, const Lane& l, uint64_t* taken) {
     const LossCall& c = g.c;
     const bool none = w.k1 <= w.k0;                    // a rank without learned tokens
+    constexpr int kColumns = F32 ? 32 : 64;            // of 128 bytes
+    if (g.store) {
+#pragma unroll 1
+        for (int j = 0; j < kTileN / 2 / kColumns; ++j) {
+            float v[kColumns];
+#pragma unroll
+            for (int h = 0; h < kColumns / 32; ++h) tmem_load(v + h * 32, l.tmem + j * kColumns + h * 32);
+            tmem_wait();
+            if (j == kTileN / 2 / kColumns - 1) {
+                fence_before();
+                warp_arrive<CG>(taken, l.lane);
+            }
+            const int col = w.n + l.group * (kTileN / 2) + j * kColumns;
+            if (col >= c.dim) continue;                // the same for the whole group
+            if (none) {
+#pragma unroll
+                for (int i = 0; i < kColumns; ++i) v[i] = 0.f;
+            }
+            if (l.leader) tma_read_done();
+            group_sync(l.group);
+            if constexpr (F32) {
+                stage_floats(l, v);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    *reinterpret_cast<uint4*>(l.mine + ((i ^ l.turn) << 4)) =
+                        make_uint4(bf16x2_rn(v[8 * i], v[8 * i + 1]), bf16x2_rn(v[8 * i + 2], v[8 * i + 3]),
+                                   bf16x2_rn(v[8 * i + 4], v[8 * i + 5]), bf16x2_rn(v[8 * i + 6], v[8 * i + 7]));
+            }
+            to_async_proxy();
+            group_sync(l.group);
+            if (l.leader && g.piece0 + w.m < c.vocab) {    // a pair's second block may be past the last row
+                tma_store_2d(&g.out[w.rank], l.staging, col, g.piece0 + w.m);
+                tma_commit();
+            }
+        }
+        return;
+    }
     const int v0 = g.piece0 + w.m + l.quarter * 32;
     const int rows = min(32, min(g.piece0 + g.width, c.vocab) - v0);
     if (l.leader) tma_read_done();
@@ -613,7 +711,7 @@ __device__ __forceinline__ void weights_tile(const LossGemm& g, const Tile& w, c
         tmem_wait();
         if (j == kTileN / 2 / 32 - 1) {
             fence_before();
-            bar_arrive(taken);
+            warp_arrive<CG>(taken, l.lane);
         }
         const int col = w.n + l.group * (kTileN / 2) + j * 32;
         if (col >= c.dim) continue;
@@ -624,66 +722,42 @@ __device__ __forceinline__ void weights_tile(const LossGemm& g, const Tile& w, c
         __syncwarp();
         stage_floats(l, v);
         __syncwarp();
-        const int x = col + (l.lane & 7) * 4;          // four columns of a row
-        for (int i = l.lane >> 3; i < rows; i += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(l.staging + (l.quarter * 32 + i) * 128 +
-                                                              (((l.lane & 7) ^ (i & 7)) << 4));
+        const int x = col + l.lane;
+        if (x >= c.dim) continue;
+        for (int i = 0; i < rows; ++i) {
+            float f = *reinterpret_cast<const float*>(l.staging + (l.quarter * 32 + i) * 128 + (((l.lane >> 2) ^ (i & 7)) << 4) +
+                                                      (l.lane & 3) * 4);
             const int64_t at = (int64_t)(v0 + i) * c.dim + x;
             if (F32) {
                 float* out = static_cast<float*>(g.grads[w.rank]) + at;
-                if (g.vec) {
-                    if (x < c.dim) {
-                        float4 r = f;
-                        if (g.accumulate) {
-                            const float4 o = *reinterpret_cast<const float4*>(out);
-                            r = make_float4(o.x + f.x, o.y + f.y, o.z + f.z, o.w + f.w);
-                        }
-                        *reinterpret_cast<float4*>(out) = r;
-                    }
-                } else {
-                    const float e[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (x + k < c.dim) out[k] = g.accumulate ? out[k] + e[k] : e[k];
-                }
+                *out = g.accumulate ? *out + f : f;
             } else {
                 uint16_t* out = static_cast<uint16_t*>(g.grads[w.rank]) + at;
-                if (g.vec) {
-                    if (x < c.dim) {
-                        float4 r = f;
-                        if (g.accumulate) {
-                            const uint2 o = *reinterpret_cast<const uint2*>(out);
-                            r = make_float4(bf16_lo(o.x) + f.x, bf16_hi(o.x) + f.y, bf16_lo(o.y) + f.z, bf16_hi(o.y) + f.w);
-                        }
-                        *reinterpret_cast<uint2*>(out) = make_uint2(bf16x2_rn(r.x, r.y), bf16x2_rn(r.z, r.w));
-                    }
-                } else {
-                    const float e[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (x + k < c.dim) out[k] = f32_to_bf16_rn(g.accumulate ? bf16_to_f32(out[k]) + e[k] : e[k]);
-                }
+                if (g.accumulate) f += bf16_to_f32(*out);
+                *out = f32_to_bf16_rn(f);
             }
         }
     }
 }
 
-template <LossPhase PHASE, bool F32, bool TWO, bool LIST>
+template <LossPhase PHASE, bool F32, bool TWO, bool LIST, int CG>
 __global__ void __launch_bounds__(kGemmThreads, 1) k_loss_gemm(const __grid_constant__ LossGemm g) {
+    using S = Shape<CG>;
     extern __shared__ char raw[];
     char* smem = raw + (1024 - (smem_of(raw) & 1023)) % 1024;
-    char* staging = smem + kStages * kBytesStage;
+    char* staging = smem + kStageBytes;
     Control* s = reinterpret_cast<Control*>(staging + 2 * kBytesStaging);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int block = CG == 1 ? 0 : cluster_rank(), t0 = blockIdx.x / CG, step = gridDim.x / CG;
     pdl_release();
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < S::kStages; ++i) {
             bar_init(&s->full[i], 1);
             bar_init(&s->empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(&s->ready[i], 1);
-            bar_init(&s->taken[i], 32 * kEpilogueWarps);
+            bar_init(&s->taken[i], CG * kEpilogueWarps);
         }
         bar_init(&s->drain, 1);
         s->stop = 0;
@@ -691,19 +765,25 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_loss_gemm(const __grid_cons
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     if (warp == 2) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_of(&s->tmem)) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        if constexpr (CG == 1) {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_of(&s->tmem)) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_of(&s->tmem)) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        }
     }
     pdl_acquire();
     if (threadIdx.x < g.n) s->counts[threadIdx.x] = g.c.counts[g.first + threadIdx.x];
     fence_before();
     __syncthreads();
+    if constexpr (CG == 2) cluster_sync();             // the other block's barriers are there
     fence_after();
     const uint32_t tmem = *(volatile uint32_t*)&s->tmem;
     if (warp == 0) {
-        if (lane == 0) produce<PHASE, F32>(g, s, smem);
+        if (lane == 0) produce<PHASE, F32, CG>(g, s, smem, block, t0, step);
     } else if (warp == 1) {
-        if (lane == 0) multiply<PHASE, F32>(g, s, smem, tmem);
+        if (lane == 0 && block == 0) multiply<PHASE, F32, CG>(g, s, smem, tmem, t0, step);
     } else if (warp >= kFirstEpilogueWarp) {
         Lane l;
         l.group = (warp - kFirstEpilogueWarp) / 4;
@@ -717,19 +797,21 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_loss_gemm(const __grid_cons
         int buf = 0;
         uint32_t phase = 0;
         Tile w;
-        for (int t = blockIdx.x; find_tile<PHASE>(g, s->counts, t, &w); t += gridDim.x) {
+        for (int t = t0; find_tile<PHASE, CG>(g, s->counts, t, &w); t += step) {
             // one thread decides for its group, whose threads meet at barriers within a tile
             volatile int32_t* go = &s->go[l.group][buf];
             if (l.leader) *go = bar_wait(&s->ready[buf], phase, s, g);
             group_sync(l.group);
             if (!*go) break;
             fence_after();
+            w.m += block * kTileM;
             l.tmem = tmem + ((uint32_t)(l.quarter * 32) << 16) + buf * kTileN + l.group * (kTileN / 2);
             uint64_t* taken = &s->taken[buf];
-            if (PHASE == LossPhase::kStats || PHASE == LossPhase::kKeep) stats_tile<TWO, LIST, PHASE == LossPhase::kKeep>(g, w, l, s, taken);
-            else if (PHASE == LossPhase::kGrad) grad_tile<F32, TWO, LIST>(g, w, l, s, taken);
-            else if (!w.weights) hidden_tile(g, w, l, taken);
-            else weights_tile<F32>(g, w, l, taken);
+            if (PHASE == LossPhase::kStats || PHASE == LossPhase::kKeep)
+                stats_tile<TWO, LIST, PHASE == LossPhase::kKeep, CG>(g, w, l, s, taken);
+            else if (PHASE == LossPhase::kGrad) grad_tile<F32, TWO, LIST, CG>(g, w, l, s, taken);
+            else if (!w.weights) hidden_tile<CG>(g, w, l, taken);
+            else weights_tile<F32, CG>(g, w, l, taken);
             if (buf == 1) phase ^= 1;
             buf ^= 1;
         }
@@ -738,33 +820,68 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_loss_gemm(const __grid_cons
     __syncwarp();
     fence_before();
     __syncthreads();
+    if constexpr (CG == 2) cluster_sync();             // nothing of the other block's is under way to this one
     if (warp == 2) {
         fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+        if constexpr (CG == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+        else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
 }
 
-template <LossPhase PHASE, bool F32, bool TWO, bool LIST>
+template <LossPhase PHASE, bool F32, bool TWO, bool LIST, int CG>
 cudaError_t launch(const LossGemm& g, int64_t most_tiles, cudaStream_t stream) {
-    const auto kernel = k_loss_gemm<PHASE, F32, TWO, LIST>;
-    const cudaError_t e = allow_shared_memory((const void*)kernel, kSmem);
+    const auto kernel = k_loss_gemm<PHASE, F32, TWO, LIST, CG>;
+    cudaError_t e = allow_shared_memory((const void*)kernel, kSmem);
     if (e != cudaSuccess) return e;
-    const int grid = cap_ctas(std::min<int64_t>(most_tiles, sm_count()));
-    return launch_dependent(kernel, dim3(grid), dim3(kGemmThreads), kSmem, stream, g);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(cap_ctas(std::min<int64_t>(most_tiles * CG, sm_count())) / CG * CG);
+    cfg.blockDim = dim3(kGemmThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CG == 1 ? 1 : 2;
+    e = cudaLaunchKernelEx(&cfg, kernel, g);
+    const cudaError_t last = cudaGetLastError();
+    return e != cudaSuccess ? e : last;
+}
+
+// Tiles of `rows` rows and `columns` columns, both in tiles of the shape.
+int64_t tile_count(LossPhase phase, const LossGemm& g, int cg) {
+    int64_t rows = 0, weights = 0;
+    for (int i = 0; i < g.n; ++i) rows += (g.row0[i + 1] - g.row0[i] + cg * kTileM - 1) / (cg * kTileM);
+    const int64_t columns = phase == LossPhase::kProducts ? g.c.dim : phase == LossPhase::kGrad ? g.width : g.c.vocab;
+    const int64_t nt = (columns + kTileN - 1) / kTileN;
+    if (phase == LossPhase::kProducts) {
+        rows *= g.splits;
+        weights = (int64_t)g.n * ((g.width + cg * kTileM - 1) / (cg * kTileM));
+    }
+    return (rows + weights) * nt;
+}
+
+template <LossPhase PHASE, bool F32, bool TWO, bool LIST>
+cudaError_t launch_shape(const LossGemm& g, cudaStream_t stream) {
+    if (g.pairs) return launch<PHASE, F32, TWO, LIST, 2>(g, tile_count(PHASE, g, 2), stream);
+    return launch<PHASE, F32, TWO, LIST, 1>(g, tile_count(PHASE, g, 1), stream);
 }
 
 template <LossPhase PHASE, bool F32>
-cudaError_t launch_kind(const LossGemm& g, int64_t most_tiles, cudaStream_t stream) {
-    if (PHASE == LossPhase::kProducts) return launch<PHASE, F32, false, false>(g, most_tiles, stream);
-    if (g.c.alpha == 0.f) return launch<PHASE, F32, false, false>(g, most_tiles, stream);
-    if (g.c.two) return launch<PHASE, F32, true, true>(g, most_tiles, stream);
-    return launch<PHASE, F32, false, true>(g, most_tiles, stream);
+cudaError_t launch_kind(const LossGemm& g, cudaStream_t stream) {
+    if (PHASE == LossPhase::kProducts) return launch_shape<PHASE, F32, false, false>(g, stream);
+    if (g.c.alpha == 0.f) return launch_shape<PHASE, F32, false, false>(g, stream);
+    if (g.c.two) return launch_shape<PHASE, F32, true, true>(g, stream);
+    return launch_shape<PHASE, F32, false, true>(g, stream);
 }
 
 template <LossPhase PHASE>
-cudaError_t launch_type(const LossGemm& g, int64_t most_tiles, cudaStream_t stream) {
-    if (g.c.dtype == DDP_F32) return launch_kind<PHASE, true>(g, most_tiles, stream);
-    return launch_kind<PHASE, false>(g, most_tiles, stream);
+cudaError_t launch_type(const LossGemm& g, cudaStream_t stream) {
+    if (g.c.dtype == DDP_F32) return launch_kind<PHASE, true>(g, stream);
+    return launch_kind<PHASE, false>(g, stream);
 }
 
 }  // namespace
@@ -782,12 +899,12 @@ cudaError_t allow_shared_memory(const void* kernel, int bytes) {
     return e;
 }
 
-cudaError_t launch_loss_gemm(LossPhase phase, const LossGemm& g, int64_t most_tiles, cudaStream_t stream) {
-    if (most_tiles <= 0) return cudaSuccess;
-    if (phase == LossPhase::kStats) return launch_type<LossPhase::kStats>(g, most_tiles, stream);
-    if (phase == LossPhase::kKeep) return launch_kind<LossPhase::kKeep, false>(g, most_tiles, stream);
-    if (phase == LossPhase::kGrad) return launch_type<LossPhase::kGrad>(g, most_tiles, stream);
-    return launch_type<LossPhase::kProducts>(g, most_tiles, stream);
+cudaError_t launch_loss_gemm(LossPhase phase, const LossGemm& g, cudaStream_t stream) {
+    if (tile_count(phase, g, 1) == 0) return cudaSuccess;
+    if (phase == LossPhase::kStats) return launch_type<LossPhase::kStats>(g, stream);
+    if (phase == LossPhase::kKeep) return launch_kind<LossPhase::kKeep, false>(g, stream);
+    if (phase == LossPhase::kGrad) return launch_type<LossPhase::kGrad>(g, stream);
+    return launch_type<LossPhase::kProducts>(g, stream);
 }
 
 }  // namespace ddpk

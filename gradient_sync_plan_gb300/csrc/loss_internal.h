@@ -13,7 +13,7 @@ namespace ddpk {
 // Ranks of one launch; more take further launches.
 constexpr int kLossRanks = 16;
 // A rank's learned tokens are gathered into rows of its own, from a multiple of kLossRowAlign on.
-constexpr int kLossRowAlign = 128;
+constexpr int kLossRowAlign = 256;
 // Columns of a partial softmax statistic and of a bin of listed columns.
 constexpr int kLossUnit = 128;
 // Tile of the products: rows, columns, depth of a shared-memory stage.
@@ -77,10 +77,14 @@ enum class LossPhase { kStats = 0, kGrad = 1, kProducts = 2, kKeep = 3 };
 constexpr int kKeepBits = 15;             // largest of a unit: 2^15, below binary16's 65504
 
 struct LossGemm {
-    CUtensorMap hidden;                   // gathered rows
-    CUtensorMap piece;                    // [planes][rows of the group][piece columns] bf16
-    CUtensorMap acc;                      // [splits * rows][dimp] float32
-    CUtensorMap weights[kLossRanks];
+    // loads, in boxes of what a block's stage takes along the depth (rows of an operand) or, where the phase's product
+    // is over their rows, across it
+    CUtensorMap hidden;                   // gathered rows; across for kProducts
+    CUtensorMap piece, piece_across;      // [planes][rows of the group][piece columns] bf16
+    CUtensorMap weights[kLossRanks];      // across for kProducts
+    // stores, in boxes of 128 rows of 128 bytes
+    CUtensorMap piece_out, acc;           // acc: [splits * rows][dimp] float32
+    CUtensorMap out[kLossRanks];          // the weights' gradients, where `store`
     void* grads[kLossRanks];
     int32_t row0[kLossRanks + 1];
     int32_t n, first;
@@ -88,13 +92,14 @@ struct LossGemm {
     int32_t splits, split_blocks;         // of the hidden states' gradients: parts of the piece's depth, their k blocks
     int32_t add;                          // add to acc (else write)
     int32_t accumulate;                   // add to the weights' gradients
-    int32_t vec;                          // their rows take 16-byte (float32) or 8-byte (bf16) accesses
+    int32_t store;                        // the copy engine writes them: 16-byte aligned rows, not accumulated
+    int32_t pairs;                        // blocks work in pairs
     unsigned long long limit_ns;
     LossCall c;
 };
 static_assert(sizeof(LossGemm) < 8192, "travels in the kernel's parameters");
 
-cudaError_t launch_loss_gemm(LossPhase phase, const LossGemm& g, int64_t most_tiles, cudaStream_t stream);
+cudaError_t launch_loss_gemm(LossPhase phase, const LossGemm& g, cudaStream_t stream);
 
 // ---- rows (loss_rows.cu) ---------------------------------------------------
 // Teachers' entries: sorted lists, probabilities, which tokens are learned.

@@ -39,7 +39,8 @@ __device__ __forceinline__ int rank_of(const LossGroup& g, int row) {
     while (i + 1 < g.n && row >= g.row0[i + 1]) ++i;
     return i;
 }
-__device__ __forceinline__ int padded(int count) { return (count + kLossRowAlign - 1) / kLossRowAlign * kLossRowAlign; }
+// Rows that a product over a rank's rows reads.
+__device__ __forceinline__ int padded(int count) { return (count + kTileK - 1) / kTileK * kTileK; }
 
 // Whether a target is a column; one that is neither that nor the ignored value is reported.
 __device__ __forceinline__ bool learned(int64_t y, const LossCall& c) {

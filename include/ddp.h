@@ -805,7 +805,7 @@ int32_t ddp_adamw_destroy(ddp_adamw* adamw);
  * bits, under any ddp_set_max_ctas.
  *
  *   weights[world]       host table of device pointers, [vocab][dim] of dtype; bf16
- *                        weights with dim a multiple of 8 start on 16-byte boundaries
+ *                        weights with dim a multiple of 64 start on 16-byte boundaries
  *                        (DDP_ERR_ALIGN).  float32 weights, and bf16 ones of other
  *                        dims, are copied into the workspace by every call
  *   grads[world]         host table, gradients of the same shape and type; NULL: the

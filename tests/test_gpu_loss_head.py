@@ -66,7 +66,7 @@ class Run:
 
 SIZES = [([1], 100, 32), ([1], 1, 8), ([3], 2, 1), ([16, 7], 100, 32), ([128], 256, 64), ([129], 257, 65), ([130, 1, 64], 513, 96),
          ([300], 1000, 256), ([257, 300], 391, 515), ([40], 5003, 7), ([33], 127, 1000), ([1], 20000, 3), ([2, 1], 1030, 64),
-         ([3], 1, 20000), ([0, 5], 700, 40)]
+         ([3], 1, 20000), ([0, 5], 700, 40), ([256], 256, 256), ([512, 1024], 129, 72), ([250], 3000, 520)]
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
@@ -86,7 +86,7 @@ def test_cross_entropy_gradients(tokens, vocab, dim, dtype):
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("temperature,alpha,targets", [(1.0, 1.0, False), (2.0, 1.0, False), (1.0, 0.3, True), (2.5, 0.7, True),
                                                        (0.5, 1.0, True), (0.4, 0.5, True), (9.0, 0.5, True)])
-@pytest.mark.parametrize("tokens,vocab,dim,k", [([5], 40, 32, 1), ([16, 7], 100, 32, 8), ([130, 200], 777, 128, 64),
+@pytest.mark.parametrize("tokens,vocab,dim,k", [([5], 40, 32, 1), ([16, 7], 100, 32, 8), ([130, 200], 777, 128, 64), ([500, 256], 515, 72, 20),
                                                 ([64], 300, 66, 256), ([3, 1], 1100, 64, 5)])
 def test_distillation(tokens, vocab, dim, k, temperature, alpha, targets, dtype):
     x = _inputs(tokens, vocab, dim, dtype, ignored=0.2 if targets else 0.0, seed=k + dim, teacher=k)
@@ -97,8 +97,9 @@ def test_distillation(tokens, vocab, dim, k, temperature, alpha, targets, dtype)
     alone.check(alone.distill(grad=False, reduction="world_mean", **how), grad=False, distill=True, reduction="world_mean", **how)
 
 
-SMALL, TILES = ([16, 7], 100, 32), ([130, 40], 777, 128)      # one launch, and the tensor cores' kernels
-BOTH = pytest.mark.parametrize("tokens,vocab,dim", [SMALL, TILES])
+SMALL, TILES = ([16, 7], 100, 32), ([130, 40], 777, 128)      # one launch; the tensor cores' kernels
+PAIRS = ([256, 500], 777, 200)                                # whose blocks work in pairs
+BOTH = pytest.mark.parametrize("tokens,vocab,dim", [SMALL, TILES, PAIRS])
 TYPES = pytest.mark.parametrize("dtype", [BF16, F32])
 
 
@@ -240,7 +241,7 @@ def test_hidden_states_in_wider_rows(tokens, vocab, dim, dtype):
 
 
 @TYPES
-@pytest.mark.parametrize("dim", [32, 33, 130])
+@pytest.mark.parametrize("dim", [32, 33, 130, 128])
 def test_tensors_at_odd_addresses(dtype, dim):
     tokens, vocab = [70], 601
     x = _inputs(tokens, vocab, dim, dtype, seed=12)
@@ -254,7 +255,7 @@ def test_tensors_at_odd_addresses(dtype, dim):
     run = Run(x)
     run.gw = [moved(run.gw[0], 1)]
     weights = x["weights"]
-    if dtype == F32 or dim % 8:                           # other bf16 weights start on 16-byte boundaries
+    if dtype == F32 or dim % 64:                          # other bf16 weights start on 16-byte boundaries
         weights = [moved(weights[0], 1).copy_(weights[0])]
     run.head = ddp.LossHead(weights, run.gw, max_tokens=70)
     x["hidden"] = [moved(x["hidden"][0], 3).copy_(x["hidden"][0])]
@@ -268,9 +269,9 @@ def test_tensors_at_odd_addresses(dtype, dim):
 @BOTH
 def test_repeats_caps_and_larger_handles_change_nothing(tokens, vocab, dim):
     x = _inputs(tokens, vocab, dim, seed=13, teacher=6, ignored=0.2)
-    runs = [Run(x), Run(x, max_teacher=40), Run(x)]
-    for k, run in enumerate(runs):
-        previous = ddp.ddp_set_max_ctas(3 if k == 2 else 0)
+    runs = [Run(x), Run(x, max_teacher=40), Run(x), Run(x)]
+    for run, cap in zip(runs, (0, 0, 3, 1)):
+        previous = ddp.ddp_set_max_ctas(cap)
         try:
             for _ in range(2):
                 run.distill(alpha=0.5, temperature=2.0, reduction="world_mean")
