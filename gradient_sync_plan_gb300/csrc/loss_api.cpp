@@ -97,7 +97,7 @@ Sizes layout(int64_t world, int64_t vocab, int64_t dim, int32_t dtype, int64_t m
         at += round_up(bytes, 256);
     };
     put(&s.counts, 4 * world);
-    put(&s.done, 4);
+    put(&s.done, 12);
     put(&s.row_token, 4 * rows);
     put(&s.token_row, 4 * rows);
     put(&s.row_column, 4 * rows);
@@ -315,6 +315,7 @@ int32_t run(ddp_loss_head* h, const Args& a, cudaStream_t stream) {
     const Sizes& at = h->at;
     c.counts = reinterpret_cast<int32_t*>(w + at.counts);
     c.done = reinterpret_cast<int32_t*>(w + at.done);
+    c.next = c.done + 1;
     c.row_token = reinterpret_cast<int32_t*>(w + at.row_token);
     c.token_row = reinterpret_cast<int32_t*>(w + at.token_row);
     c.row_column = reinterpret_cast<int32_t*>(w + at.row_column);

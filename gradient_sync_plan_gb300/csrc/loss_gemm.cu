@@ -52,9 +52,20 @@ constexpr int kGemmThreads = 32 * (kFirstEpilogueWarp + kEpilogueWarps);
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kKeepScale = (float)(1 << kKeepBits);
 
+// A tile: rank (-1: no more tiles), first row (of all ranks' rows; a column of the piece for dw), first column, columns (of
+// the products: a multiple of 64 for each block), k blocks.
+struct alignas(16) Tile {
+    int32_t rank, m, n, columns, k0, k1, split;
+    int32_t weights;                       // of dw
+};
+constexpr int kTileWords = sizeof(Tile) / 4;
+constexpr int kQueue = 4;
+
 struct Control {
+    Tile queue[kQueue], mail[kQueue];
     uint64_t full[kMostStages], empty[kMostStages];
     uint64_t ready[2], taken[2];                       // accumulators
+    uint64_t tile_full[kQueue], tile_empty[kQueue], mail_full[kQueue];
     uint64_t drain;
     uint32_t tmem;
     int32_t stop;
@@ -78,19 +89,20 @@ __device__ __forceinline__ void bar_expect(uint64_t* b, uint32_t bytes) {
 __device__ __forceinline__ void bar_arrive(uint64_t* b) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_of(b)) : "memory");
 }
-// The address, in the cluster, of this block's `p` in the cluster's first block.
-__device__ __forceinline__ uint32_t in_first_block(const void* p) {
+// The address, in the cluster, of this block's `p` in the cluster's block `to`.
+__device__ __forceinline__ uint32_t in_block(const void* p, int to) {
     uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_of(p)));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_of(p)), "r"(to));
     return a;
 }
-// A warp's arrival at the first block's barrier.
-template <int CG>
+// An arrival at another block's barrier.  Its release at cluster scope takes about a thousand cycles: only threads that
+// nothing waits for in the meantime come here.
+__device__ __forceinline__ void arrive_at(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
 __device__ __forceinline__ void warp_arrive(uint64_t* b, int lane) {
     __syncwarp();
-    if (lane != 0) return;
-    if constexpr (CG == 1) bar_arrive(b);
-    else asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(in_first_block(b)) : "memory");
+    if (lane == 0) bar_arrive(b);
 }
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -111,16 +123,42 @@ __device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
+// For what another block of the cluster has written: about two thousand cycles.
+__device__ __forceinline__ bool bar_try_cluster(uint64_t* b, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_of(b)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// Whether the phase is complete, at once.
+__device__ __forceinline__ bool bar_test(uint64_t* b, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_of(b)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 __device__ __forceinline__ unsigned long long now_ns() {
     unsigned long long t;
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
     return t;
 }
 // At most limit_ns, or until another role of the block has given up; false then.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, Control* s, const LossGemm& g) {
-    if (bar_try(b, parity)) return true;
+    const auto complete = [&] { return CLUSTER ? bar_try_cluster(b, parity) : bar_try(b, parity); };
+    if (complete()) return true;
     const unsigned long long t0 = now_ns();
-    while (!bar_try(b, parity)) {
+    while (!complete()) {
         if (*(volatile int32_t*)&s->stop) return false;
         if (now_ns() - t0 > g.limit_ns) {
             *(volatile int32_t*)&s->stop = 1;
@@ -230,13 +268,6 @@ __device__ __forceinline__ float exp2_of(float x) {
     return y;
 }
 
-// A tile: rank, first row (of all ranks' rows; a column of the piece for dw), first column, columns (of the products: a
-// multiple of 64 for each block), k blocks.
-struct Tile {
-    int rank, m, n, columns, k0, k1, split;
-    bool weights;                          // of dw
-};
-
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 // Tiles of rank i in the phase: of its rows first, of its weights' gradients behind those of all ranks.
@@ -294,19 +325,140 @@ __device__ __forceinline__ bool find_tile(const LossGemm& g, const int32_t* coun
     return false;
 }
 
+__device__ __forceinline__ void put_tile(Tile* at, const Tile& w) {
+    static_assert(sizeof(Tile) == 32, "two vectors");
+    const int32_t* from = reinterpret_cast<const int32_t*>(&w);
+#pragma unroll
+    for (int i = 0; i < 8; i += 4)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(smem_of(at) + 4 * i), "r"(from[i]), "r"(from[i + 1]),
+                     "r"(from[i + 2]), "r"(from[i + 3])
+                     : "memory");
+}
+__device__ __forceinline__ void get_tile(Tile* w, const Tile* at) {
+    int32_t* to = reinterpret_cast<int32_t*>(w);
+#pragma unroll
+    for (int i = 0; i < 8; i += 4)
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(to[i]), "=r"(to[i + 1]), "=r"(to[i + 2]), "=r"(to[i + 3])
+                     : "r"(smem_of(at) + 4 * i)
+                     : "memory");
+}
+
+// ---- the tiles' queue -----------------------------------------------------------
+// Tiles differ in depth, so blocks take them as they come: the first each by its number, the others from a counter in
+// device memory.  A thread of the cluster's first block decodes them ahead of the other roles and puts them into its
+// queue and the second block's mail, which a thread there copies to its own queue: waiting for another block's writes,
+// like reporting to one, takes some two thousand cycles, which no role that works on tiles should spend.  Who computes a
+// tile changes no value.  The last cluster to finish leaves the counters at zero.
+template <LossPhase PHASE, int CG>
+__device__ void schedule(const LossGemm& g, Control* s) {
+    const int clusters = gridDim.x / CG;
+    uint32_t phase = 1;
+    int t = blockIdx.x / CG;
+    for (int n = 0;; ++n) {
+        const int slot = n % kQueue;
+        Tile w;
+        const bool more = find_tile<PHASE, CG>(g, s->counts, t, &w);
+        if (!more) w.rank = -1;
+        if (more) t = clusters + atomicAdd(g.c.next, 1);
+        if (!bar_wait(&s->tile_empty[slot], phase, s, g)) break;
+        put_tile(&s->queue[slot], w);
+        bar_arrive(&s->tile_full[slot]);
+        if constexpr (CG == 2) {
+            const int32_t* words = reinterpret_cast<const int32_t*>(&w);
+            const uint32_t at = in_block(&s->mail[slot], 1);
+#pragma unroll
+            for (int i = 0; i < kTileWords; ++i)
+                asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(at + 4 * i), "r"(words[i]) : "memory");
+            arrive_at(in_block(&s->mail_full[slot], 1));
+        }
+        if (slot == kQueue - 1) phase ^= 1;
+        if (!more) break;
+    }
+    __threadfence();
+    if (atomicAdd(g.c.next + 1, 1) == clusters - 1) {
+        g.c.next[0] = 0;
+        g.c.next[1] = 0;
+    }
+}
+
+// The place of a role in its block's queue.
+struct Queue {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ bool wait(Control* s, const LossGemm& g) {
+        return bar_wait(&s->tile_full[slot], phase, s, g);
+    }
+    __device__ __forceinline__ void read(Control* s, Tile* w) const { get_tile(w, &s->queue[slot]); }
+    __device__ __forceinline__ void done(Control* s) {
+        bar_arrive(&s->tile_empty[slot]);
+        step();
+    }
+    __device__ __forceinline__ void step() {
+        if (++slot == kQueue) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+    // For a role of one thread: the next tile; false at the end, or where the wait gave up (rank then is -2).
+    __device__ __forceinline__ bool next(Control* s, const LossGemm& g, Tile* w) {
+        if (!wait(s, g)) {
+            w->rank = -2;
+            return false;
+        }
+        read(s, w);
+        done(s);
+        return w->rank >= 0;
+    }
+};
+
+// Who reads a block's queue: the loads and the epilogue's warps; in the first block also the products, and of a pair the
+// other block's word that all there have.
+__device__ constexpr int queue_readers(int cg, int block) { return 1 + kEpilogueWarps + (block == 0 ? cg : 0); }
+
+// The second block of a pair: a thread copies its mail to its queue (a place whose mail has come is free there: its readers'
+// arrivals were passed on before).
+__device__ void copy_mail(const LossGemm& g, Control* s) {
+    Queue queue;
+    Tile w;
+    do {
+        if (!bar_wait<true>(&s->mail_full[queue.slot], queue.phase, s, g)) return;
+        get_tile(&w, &s->mail[queue.slot]);
+        put_tile(&s->queue[queue.slot], w);
+        bar_arrive(&s->tile_full[queue.slot]);
+        queue.step();
+    } while (w.rank >= 0);
+}
+// Another passes on to the first block's queue and products what its warps are through with.
+__device__ void pass_on(const LossGemm& g, Control* s) {
+    Queue queue;
+    Tile w;
+    for (int n = 0;; ++n) {
+        if (!queue.wait(s, g)) return;
+        queue.read(s, &w);                 // not one of the readers: the place is free only after its own arrival there
+        if (!bar_wait(&s->tile_empty[queue.slot], queue.phase, s, g)) return;
+        arrive_at(in_block(&s->tile_empty[queue.slot], 0));
+        if (w.rank < 0) return;
+        queue.step();
+        if (!bar_wait(&s->taken[n & 1], (n >> 1) & 1, s, g)) return;
+        arrive_at(in_block(&s->taken[n & 1], 0));
+    }
+}
+
 __device__ constexpr int8_t kPlaneA[6] = {2, 1, 0, 1, 0, 0};
 __device__ constexpr int8_t kPlaneB[6] = {0, 1, 2, 0, 1, 0};
 
 // ---- producer -----------------------------------------------------------------
 // Of a pair, each block loads its own operands; all arrive at the first block's barrier.
 template <LossPhase PHASE, bool F32, int CG>
-__device__ void produce(const LossGemm& g, Control* s, char* stages, int block, int t0, int step) {
+__device__ void produce(const LossGemm& g, Control* s, char* stages, int block) {
     using S = Shape<CG>;
     int stage = 0, issued = 0;
     uint32_t phase = 0;
     bool ok = true;
+    Queue queue;
     Tile w;
-    for (int t = t0; ok && find_tile<PHASE, CG>(g, s->counts, t, &w); t += step) {
+    while (ok && queue.next(s, g, &w)) {
         const CUtensorMap* wmap = &g.weights[w.rank];
         const int bm = w.m + block * kTileM, bn = w.n + block * (w.columns / CG);
         for (int q = 0; ok && q < (F32 ? 6 : 1); ++q) {
@@ -319,7 +471,7 @@ __device__ void produce(const LossGemm& g, Control* s, char* stages, int block, 
                 char* a = stages + stage * S::kBytesStage;
                 char* b = a + S::kBytesA;
                 if (block == 0) bar_expect(&s->full[stage], CG * S::kBytesStage);
-                const uint32_t bar = CG == 1 ? smem_of(&s->full[stage]) : in_first_block(&s->full[stage]);
+                const uint32_t bar = CG == 1 ? smem_of(&s->full[stage]) : in_block(&s->full[stage], 0);
                 const int k = kb * kTileK;
                 if (PHASE != LossPhase::kProducts) {
                     tma_load<CG>(a, &g.hidden, k, bm, pa, bar);
@@ -340,6 +492,7 @@ __device__ void produce(const LossGemm& g, Control* s, char* stages, int block, 
             }
         }
     }
+    ok = ok && w.rank == -1;
     // what the products still have to report arrives here before the block ends
     for (int i = 0; ok && i < S::kStages; ++i) {
         ok = bar_wait(&s->empty[stage], phase ^ 1, s, g);
@@ -360,47 +513,51 @@ __device__ void produce(const LossGemm& g, Control* s, char* stages, int block, 
 }
 
 // ---- products -----------------------------------------------------------------
+// The tensor cores' own queue is short: the next stage is looked up before a stage's last product is issued, and the next
+// tile while the present one's are.
 template <LossPhase PHASE, bool F32, int CG>
-__device__ void multiply(const LossGemm& g, Control* s, char* stages, uint32_t tmem, int t0, int step) {
+__device__ void multiply(const LossGemm& g, Control* s, char* stages, uint32_t tmem) {
     using S = Shape<CG>;
     int stage = 0, buf = 0;
     uint32_t phase = 0, taken = 1;
-    bool ok = true;
-    Tile w;
-    for (int t = t0; ok && find_tile<PHASE, CG>(g, s->counts, t, &w); t += step) {
+    bool ok = true, there = false;
+    Queue queue;
+    Tile w, after;
+    bool more = queue.next(s, g, &w);
+    while (more) {
         const bool a_across = PHASE == LossPhase::kProducts && w.weights, b_across = PHASE == LossPhase::kProducts;
         const uint32_t desc = product_desc(a_across, b_across, CG * kTileM, w.columns);
         // 16 elements of depth: 32 bytes along a row, or 16 rows of 128 bytes
         const uint32_t step_a = a_across ? 16 * 128 / 16 : 2, step_b = b_across ? 16 * 128 / 16 : 2;
-        if (!bar_wait(&s->taken[buf], taken, s, g)) {
-            ok = false;
-            break;
-        }
+        if (!(ok = bar_wait(&s->taken[buf], taken, s, g))) break;
         fence_after();
-        const int blocks = (w.k1 - w.k0) * (F32 ? 6 : 1);
+        const int blocks = max(w.k1 - w.k0, 0) * (F32 ? 6 : 1);
         for (int i = 0; i < blocks; ++i) {
-            if (!bar_wait(&s->full[stage], phase, s, g)) {
-                ok = false;
-                break;
-            }
+            if (!there && !(ok = bar_wait(&s->full[stage], phase, s, g))) break;
             fence_after();
             const uint32_t a = smem_of(stages + stage * S::kBytesStage);
             const uint64_t da = matrix_desc(a, kBytesBox), db = matrix_desc(a + S::kBytesA, kBytesBox);
-#pragma unroll
-            for (int k = 0; k < kTileK / 16; ++k)
-                mma<CG>(tmem + buf * kTileN, da + k * step_a, db + k * step_b, desc, i > 0 || k > 0);
-            mma_commit<CG>(&s->empty[stage]);
+            uint64_t* const empty = &s->empty[stage];
             if (++stage == S::kStages) {
                 stage = 0;
                 phase ^= 1;
             }
+#pragma unroll
+            for (int k = 0; k < kTileK / 16; ++k) {
+                if (k == kTileK / 16 - 1) there = bar_test(&s->full[stage], phase);
+                mma<CG>(tmem + buf * kTileN, da + k * step_a, db + k * step_b, desc, i > 0 || k > 0);
+            }
+            mma_commit<CG>(empty);
+            if (i == 0) more = queue.next(s, g, &after);
         }
         if (!ok) break;
         mma_commit<CG>(&s->ready[buf]);
+        if (blocks == 0) more = queue.next(s, g, &after);
         if (buf == 1) taken ^= 1;
         buf ^= 1;
+        w = after;
     }
-    if (!ok) {                             // products in flight, before tensor memory goes
+    if (!ok || w.rank == -2) {             // products in flight, before tensor memory goes
         mma_commit<CG>(&s->drain);
         bar_wait_rest(&s->drain, 0, g);
     }
@@ -508,7 +665,7 @@ __device__ __forceinline__ void stats_tile(const LossGemm& g, const Tile& w, con
             tmem_wait();
             if (h == 1 && j == kLossUnit / 64 - 1) {
                 fence_before();
-                warp_arrive<CG>(taken, l.lane);
+                warp_arrive(taken, l.lane);
             }
             if (col + h * 32 + 32 > c.vocab) {
 #pragma unroll
@@ -578,7 +735,7 @@ __device__ __forceinline__ void grad_tile(const LossGemm& g, const Tile& w, cons
         tmem_wait();
         if (j == kLossUnit / 64 - 1) {
             fence_before();
-            warp_arrive<CG>(taken, l.lane);
+            warp_arrive(taken, l.lane);
         }
         const int col = first + j * 64;
 #pragma unroll
@@ -638,7 +795,7 @@ __device__ __forceinline__ void hidden_tile(const LossGemm& g, const Tile& w, co
         tmem_wait();
         if (j == kTileN / 2 / 32 - 1) {
             fence_before();
-            warp_arrive<CG>(taken, l.lane);
+            warp_arrive(taken, l.lane);
         }
         // the same for the whole group: no column of acc, or no depth in a shorter last piece
         if (col >= g.c.dimp || w.k1 <= w.k0) continue;
@@ -672,7 +829,7 @@ __device__ __forceinline__ void weights_tile(const LossGemm& g, const Tile& w, c
             tmem_wait();
             if (j == kTileN / 2 / kColumns - 1) {
                 fence_before();
-                warp_arrive<CG>(taken, l.lane);
+                warp_arrive(taken, l.lane);
             }
             const int col = w.n + l.group * (kTileN / 2) + j * kColumns;
             if (col >= c.dim) continue;                // the same for the whole group
@@ -711,7 +868,7 @@ __device__ __forceinline__ void weights_tile(const LossGemm& g, const Tile& w, c
         tmem_wait();
         if (j == kTileN / 2 / 32 - 1) {
             fence_before();
-            warp_arrive<CG>(taken, l.lane);
+            warp_arrive(taken, l.lane);
         }
         const int col = w.n + l.group * (kTileN / 2) + j * 32;
         if (col >= c.dim) continue;
@@ -748,7 +905,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_loss_gemm(const __grid_cons
     char* staging = smem + kStageBytes;
     Control* s = reinterpret_cast<Control*>(staging + 2 * kBytesStaging);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int block = CG == 1 ? 0 : cluster_rank(), t0 = blockIdx.x / CG, step = gridDim.x / CG;
+    const int block = CG == 1 ? 0 : cluster_rank();
     pdl_release();
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kStages; ++i) {
@@ -757,7 +914,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_loss_gemm(const __grid_cons
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(&s->ready[i], 1);
-            bar_init(&s->taken[i], CG * kEpilogueWarps);
+            bar_init(&s->taken[i], kEpilogueWarps + (CG == 2 && block == 0));
+        }
+        for (int i = 0; i < kQueue; ++i) {
+            bar_init(&s->tile_full[i], 1);
+            bar_init(&s->mail_full[i], 1);
+            bar_init(&s->tile_empty[i], queue_readers(CG, block));
         }
         bar_init(&s->drain, 1);
         s->stop = 0;
@@ -781,9 +943,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_loss_gemm(const __grid_cons
     fence_after();
     const uint32_t tmem = *(volatile uint32_t*)&s->tmem;
     if (warp == 0) {
-        if (lane == 0) produce<PHASE, F32, CG>(g, s, smem, block, t0, step);
+        if (lane == 0) produce<PHASE, F32, CG>(g, s, smem, block);
     } else if (warp == 1) {
-        if (lane == 0 && block == 0) multiply<PHASE, F32, CG>(g, s, smem, tmem, t0, step);
+        if (lane == 0 && block == 0) multiply<PHASE, F32, CG>(g, s, smem, tmem);
+    } else if (warp == 3) {
+        if (lane == 0 && block == 0) schedule<PHASE, CG>(g, s);
+        if (lane == 0 && block == 1) copy_mail(g, s);
+    } else if (warp == 2) {
+        if (lane == 0 && block == 1) pass_on(g, s);
     } else if (warp >= kFirstEpilogueWarp) {
         Lane l;
         l.group = (warp - kFirstEpilogueWarp) / 4;
@@ -796,13 +963,23 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_loss_gemm(const __grid_cons
         l.leader = l.row == 0;
         int buf = 0;
         uint32_t phase = 0;
+        Queue queue;
         Tile w;
-        for (int t = t0; find_tile<PHASE, CG>(g, s->counts, t, &w); t += step) {
+        while (true) {
             // one thread decides for its group, whose threads meet at barriers within a tile
             volatile int32_t* go = &s->go[l.group][buf];
-            if (l.leader) *go = bar_wait(&s->ready[buf], phase, s, g);
+            if (l.leader) {
+                int state = queue.wait(s, g);
+                if (state && *(volatile int32_t*)&s->queue[queue.slot].rank >= 0) state = bar_wait(&s->ready[buf], phase, s, g);
+                *go = state;
+            }
             group_sync(l.group);
             if (!*go) break;
+            queue.read(s, &w);
+            __syncwarp();
+            if (lane == 0) bar_arrive(&s->tile_empty[queue.slot]);
+            queue.step();
+            if (w.rank < 0) break;
             fence_after();
             w.m += block * kTileM;
             l.tmem = tmem + ((uint32_t)(l.quarter * 32) << 16) + buf * kTileN + l.group * (kTileN / 2);

@@ -50,6 +50,7 @@ struct LossCall {
 
     int32_t* counts;                      // [world]
     int32_t* done;                        // blocks of a combine launch that are through
+    int32_t* next;                        // [2] tiles taken of a products' launch, and clusters that are through
     int32_t* row_token;                   // [rows] the token (of its rank) that a row holds
     int32_t* token_row;                   // [rows] the row (of its rank) of a token, -1: not learned
     int32_t* row_column;                  // [rows] target's column

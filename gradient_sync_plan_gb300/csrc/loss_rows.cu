@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(kScanThreads) k_scan(const __grid_constant__ L
     pdl_release();
     pdl_acquire();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    if (blockIdx.x == 0 && threadIdx.x == 0) *c.done = 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *c.done = c.next[0] = c.next[1] = 0;
     for (int i = blockIdx.x; i < g.n; i += gridDim.x) {
         const int row0 = g.row0[i], n = g.tokens[i];
         int count = 0;
