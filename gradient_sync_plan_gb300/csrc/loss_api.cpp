@@ -25,10 +25,10 @@ using namespace ddpk;
 
 namespace {
 
-// Bytes of logits' gradients that the workspace has room for at most.  bf16: where a rank's tokens by the whole
-// vocabulary fit, the exponentials are kept from the loss to the gradients and the logits are computed once, group of
-// ranks by group of ranks; else, and for float32 (whose gradients are three planes), the vocabulary goes in pieces.  A
-// piece is written once and read a few times, so that it need not fit the L2.
+// Bytes of logits' exponentials and gradients that the workspace has room for at most.  Where a rank's tokens by the
+// whole vocabulary fit, the exponentials are kept from the loss to the gradients and the logits are computed once, group
+// of ranks by group of ranks; else the vocabulary goes in pieces of kPieceBytes.  A piece is written once and read a few
+// times, so that it need not fit the L2.
 constexpr int64_t kKeepBytes = (int64_t)2 << 30, kPieceBytes = (int64_t)512 << 20;
 // Temperatures whose two softmaxes' exponentials come from one another by a power up to this.
 constexpr float kKeepPower = 4.f;
@@ -58,7 +58,8 @@ int64_t piece_width(int64_t bytes, int64_t rows, int64_t vocab, int64_t planes) 
 
 struct Sizes {
     int64_t counts, done, row_token, token_row, row_column, valid, columns, starts, share, entropy, z, value, partial, coef,
-        block_loss, gathered, acc, piece, weights;   // offsets, and the last two also bytes below
+        block_loss, gathered, acc, kept, piece, weights;    // offsets
+    int64_t keep_rows;                            // rows of a group whose exponentials are kept
     int64_t acc_bytes, piece_bytes, weights_bytes, total;
 };
 
@@ -83,6 +84,9 @@ namespace {
 
 // Whether the products read the weights from the workspace: float32's planes, and bf16 rows that are not whole boxes.
 bool is_copied(int32_t dtype, int64_t dim) { return dtype == DDP_F32 || dim % kTileK != 0; }
+
+// Bytes of a logit where exponentials are kept: binary16 that becomes bf16 in place, or a float32 beside three planes.
+int64_t kept_bytes(int32_t dtype) { return dtype == DDP_F32 ? 10 : 2; }
 
 int planes_of(int32_t dtype) { return dtype == DDP_F32 ? 3 : 1; }
 
@@ -120,10 +124,13 @@ Sizes layout(int64_t world, int64_t vocab, int64_t dim, int32_t dtype, int64_t m
         // at most 2 kSms / tiles + 1 splits (splits_for), for any number of rows up to these
         s.acc_bytes = 4 * (2 * kSms * kTileM * kTileN + rows * dimp);
         put(&s.acc, s.acc_bytes);
-        const int64_t row = 2 * round_up(vocab, kPieceAlign);      // of kept exponentials
         s.piece_bytes = 2 * planes * group * piece_width(kPieceBytes, group, vocab, planes);
-        if (dtype == DDP_BF16 && rank * row <= kKeepBytes)
-            s.piece_bytes = std::max(s.piece_bytes, std::min(group, kKeepBytes / row / kLossRowAlign * kLossRowAlign) * row);
+        const int64_t width = round_up(vocab, kPieceAlign), row = kept_bytes(dtype) * width;
+        if (rank * row <= kKeepBytes) {
+            s.keep_rows = std::min(group, kKeepBytes / row / kLossRowAlign * kLossRowAlign);
+            s.piece_bytes = std::max(s.piece_bytes, 2 * planes * s.keep_rows * width);
+        }
+        put(&s.kept, dtype == DDP_F32 ? 4 * s.keep_rows * width : 0);
         put(&s.piece, s.piece_bytes);
     }
     s.total = at;
@@ -335,8 +342,8 @@ int32_t run(ddp_loss_head* h, const Args& a, cudaStream_t stream) {
 
     // the groups of ranks, and where their rows are
     const int64_t vocab_width = round_up(h->vocab, kPieceAlign);
-    const bool may_keep = a.grad && h->dtype == DDP_BF16 && (!c.two || std::max(c.temperature, c.inv_temperature) <= kKeepPower);
-    const int64_t keep_rows = may_keep ? at.piece_bytes / (2 * vocab_width) : 0;
+    const bool may_keep = a.grad && (!c.two || std::max(c.temperature, c.inv_temperature) <= kKeepPower);
+    const int64_t keep_rows = may_keep ? at.keep_rows : 0;
     std::vector<LossGroup> groups;
     int64_t rows = 0;
     for (int32_t r = 0; r < h->world; ++r) {
@@ -378,8 +385,12 @@ int32_t run(ddp_loss_head* h, const Args& a, cudaStream_t stream) {
         if ((st = cuda_status(launch_loss_scan(g, c, stream)))) return st;
     }
     if (h->copied)
-        for (int32_t r = 0; r < h->world; ++r)
-            if ((st = cuda_status(launch_loss_planes(h->weights[r], w + at.weights + r * h->copied, h->vocab, c, stream)))) return st;
+        for (const LossGroup& g : groups) {
+            LossWeights p{};
+            p.n = g.n;
+            std::copy(h->weights.begin() + g.first, h->weights.begin() + g.first + g.n, p.weights);
+            if ((st = cuda_status(launch_loss_planes(p, w + at.weights + g.first * h->copied, h->copied, c, stream)))) return st;
+        }
 
     LossGemm m{};
     m.c = c;
@@ -416,7 +427,8 @@ int32_t run(ddp_loss_head* h, const Args& a, cudaStream_t stream) {
             if ((st = map_out(&m.acc, c.acc, DDP_F32, c.dimp, m.splits * c.rows))) return st;
             if (span > 0 && ((st = map_along(&m.piece, w + at.piece, width, span, c.planes, kTileM)) ||
                              (st = map_across(&m.piece_across, w + at.piece, width, span, c.planes, kTileM)) ||
-                             (st = map_out(&m.piece_out, w + at.piece, DDP_BF16, width, span * c.planes))))
+                             (st = map_out(&m.piece_out, w + at.piece, DDP_BF16, width, span * c.planes)) ||
+                             (st = map_out(&m.keep_out, h->dtype == DDP_F32 ? w + at.kept : w + at.piece, h->dtype, width, span))))
                 return st;
         }
         const auto operands = [&](bool across) {
@@ -438,7 +450,7 @@ int32_t run(ddp_loss_head* h, const Args& a, cudaStream_t stream) {
             m.width = (int32_t)std::min<int64_t>(width, h->vocab - v);
             m.add = v > 0;
             operands(false);
-            if (keep) st = cuda_status(launch_loss_convert(g, c, w + at.piece, width, stream));
+            if (keep) st = cuda_status(launch_loss_convert(g, c, h->dtype == DDP_F32 ? w + at.kept : w + at.piece, w + at.piece, width, stream));
             else st = cuda_status(launch_loss_gemm(LossPhase::kGrad, m, stream));
             operands(true);
             if (st || (st = cuda_status(launch_loss_gemm(LossPhase::kProducts, m, stream)))) return st;

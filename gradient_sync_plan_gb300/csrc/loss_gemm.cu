@@ -611,9 +611,10 @@ struct Listed {
     }
 };
 
-// Twice over the row's 128 logits: their maximum, and their exponentials relative to it.  KEEP: the exponentials go to
-// the piece's buffer as binary16, 2^kKeepBits for the row's largest, so that those down to 2^-29 of it keep 11 bits.
-template <bool TWO, bool LIST, bool KEEP, int CG>
+// Twice over the row's 128 logits: their maximum, and their exponentials relative to it.  KEEP: the exponentials are
+// stored, for bf16 operands as binary16, 2^kKeepBits for the row's largest, so that those down to 2^-29 of it keep 11
+// bits, for float32 as they are.
+template <bool F32, bool TWO, bool LIST, bool KEEP, int CG>
 __device__ __forceinline__ void stats_tile(const LossGemm& g, const Tile& w, const Lane& l, Control* s, uint64_t* taken) {
     const LossCall& c = g.c;
     const int row = w.m + l.row, first = w.n + l.group * kLossUnit;
@@ -654,16 +655,17 @@ __device__ __forceinline__ void stats_tile(const LossGemm& g, const Tile& w, con
     const float a1 = -ref * k1, a2 = -ref * k2;
     const bool flat = TWO && k2 < k1;                  // the flatter softmax's exponentials are kept
     float sum[4] = {0.f, 0.f, 0.f, 0.f}, sum2[4] = {0.f, 0.f, 0.f, 0.f};
+    constexpr int kColumns = KEEP && !F32 ? 64 : 32;   // kept in 128 bytes
 #pragma unroll 1
-    for (int j = 0; j < kLossUnit / 64; ++j) {
-        const int col = first + j * 64;
+    for (int j = 0; j < kLossUnit / kColumns; ++j) {
+        const int col = first + j * kColumns;
         uint32_t kept[32];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < kColumns / 32; ++h) {
             float v[32];
-            tmem_load(v, l.tmem + j * 64 + h * 32);
+            tmem_load(v, l.tmem + j * kColumns + h * 32);
             tmem_wait();
-            if (h == 1 && j == kLossUnit / 64 - 1) {
+            if (h == kColumns / 32 - 1 && j == kLossUnit / kColumns - 1) {
                 fence_before();
                 warp_arrive(taken, l.lane);
             }
@@ -686,7 +688,10 @@ __device__ __forceinline__ void stats_tile(const LossGemm& g, const Tile& w, con
                         e[k] = flat ? y : x;
                     }
                 }
-                if (KEEP) {
+                if (KEEP && F32) {
+                    kept[i] = __float_as_uint(e[0]);
+                    kept[i + 1] = __float_as_uint(e[1]);
+                } else if (KEEP) {
                     const __half2 p = __floats2half2_rn(e[0] * kKeepScale, e[1] * kKeepScale);
                     kept[h * 16 + i / 2] = *reinterpret_cast<const uint32_t*>(&p);
                 }
@@ -704,8 +709,7 @@ __device__ __forceinline__ void stats_tile(const LossGemm& g, const Tile& w, con
             to_async_proxy();
             group_sync(l.group);
             if (l.leader) {
-                const int x = w.n + l.group * kLossUnit + j * 64, y = w.m - g.row0[0];
-                tma_store_2d(&g.piece_out, l.staging, x, y);
+                tma_store_2d(&g.keep_out, l.staging, w.n + l.group * kLossUnit + j * kColumns, w.m - g.row0[0]);
                 tma_commit();
             }
         }
@@ -985,7 +989,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_loss_gemm(const __grid_cons
             l.tmem = tmem + ((uint32_t)(l.quarter * 32) << 16) + buf * kTileN + l.group * (kTileN / 2);
             uint64_t* taken = &s->taken[buf];
             if (PHASE == LossPhase::kStats || PHASE == LossPhase::kKeep)
-                stats_tile<TWO, LIST, PHASE == LossPhase::kKeep, CG>(g, w, l, s, taken);
+                stats_tile<F32, TWO, LIST, PHASE == LossPhase::kKeep, CG>(g, w, l, s, taken);
             else if (PHASE == LossPhase::kGrad) grad_tile<F32, TWO, LIST, CG>(g, w, l, s, taken);
             else if (!w.weights) hidden_tile<CG>(g, w, l, taken);
             else weights_tile<F32, CG>(g, w, l, taken);
@@ -1079,7 +1083,7 @@ cudaError_t allow_shared_memory(const void* kernel, int bytes) {
 cudaError_t launch_loss_gemm(LossPhase phase, const LossGemm& g, cudaStream_t stream) {
     if (tile_count(phase, g, 1) == 0) return cudaSuccess;
     if (phase == LossPhase::kStats) return launch_type<LossPhase::kStats>(g, stream);
-    if (phase == LossPhase::kKeep) return launch_kind<LossPhase::kKeep, false>(g, stream);
+    if (phase == LossPhase::kKeep) return launch_type<LossPhase::kKeep>(g, stream);
     if (phase == LossPhase::kGrad) return launch_type<LossPhase::kGrad>(g, stream);
     return launch_type<LossPhase::kProducts>(g, stream);
 }

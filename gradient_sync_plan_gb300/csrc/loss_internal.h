@@ -71,7 +71,7 @@ struct LossCall {
 constexpr int kLossBlockRows = 32;        // rows of a combine block
 
 // Products.  kStats: logits' statistics and listed logits.  kKeep: those, and the logits' exponentials relative to
-// their unit's largest, binary16 scaled by 2^kKeepBits, to `piece` (bf16 operands).  kGrad: logits' gradients of a
+// their unit's largest: of bf16 operands binary16 scaled by 2^kKeepBits, of float32 ones as they are.  kGrad: logits' gradients of a
 // piece of the vocabulary, to `piece`.  kProducts: the piece's share of the hidden states' gradients
 // (added to acc) and its rows of the weights' gradients.
 enum class LossPhase { kStats = 0, kGrad = 1, kProducts = 2, kKeep = 3 };
@@ -84,7 +84,7 @@ struct LossGemm {
     CUtensorMap piece, piece_across;      // [planes][rows of the group][piece columns] bf16
     CUtensorMap weights[kLossRanks];      // across for kProducts
     // stores, in boxes of 128 rows of 128 bytes
-    CUtensorMap piece_out, acc;           // acc: [splits * rows][dimp] float32
+    CUtensorMap piece_out, keep_out, acc; // acc: [splits * rows][dimp] float32
     CUtensorMap out[kLossRanks];          // the weights' gradients, where `store`
     void* grads[kLossRanks];
     int32_t row0[kLossRanks + 1];
@@ -109,12 +109,17 @@ cudaError_t launch_loss_teacher(const LossGroup& g, const LossCall& c, cudaStrea
 cudaError_t launch_loss_scan(const LossGroup& g, const LossCall& c, cudaStream_t stream);
 // Their hidden states, into the rows; rows up to the next tile's end are zeroed.
 cudaError_t launch_loss_gather(const LossGroup& g, const LossCall& c, cudaStream_t stream);
-// A matrix [rows][dim] as [planes][rows][dimp] bf16, zeros behind dim.
-cudaError_t launch_loss_planes(const void* src, void* dst, int64_t rows, const LossCall& c, cudaStream_t stream);
+// The weights of a group's ranks as [planes][vocab][dimp] bf16, zeros behind dim, `bytes` a rank.
+struct LossWeights {
+    int32_t n;
+    const void* weights[kLossRanks];
+};
+cudaError_t launch_loss_planes(const LossWeights& m, void* dst, int64_t bytes, const LossCall& c, cudaStream_t stream);
 // Partial statistics to losses and to the gradients' coefficients.
 cudaError_t launch_loss_combine(const LossGroup& g, const LossCall& c, float* loss, cudaStream_t stream);
-// Kept exponentials [rows of the group][width] to the logits' gradients, in place.
-cudaError_t launch_loss_convert(const LossGroup& g, const LossCall& c, void* piece, int64_t width, cudaStream_t stream);
+// Kept exponentials [rows of the group][width] to the logits' gradients' planes in `piece`; bf16: in place, `kept` is `piece`.
+cudaError_t launch_loss_convert(const LossGroup& g, const LossCall& c, const void* kept, void* piece, int64_t width,
+                                cudaStream_t stream);
 // acc's splits to the hidden states' gradients, zeros for tokens that are not learned.
 cudaError_t launch_loss_join(const LossGroup& g, const LossCall& c, int splits, cudaStream_t stream);
 

@@ -192,8 +192,14 @@ __device__ __forceinline__ void row_to_planes(const void* src, uint16_t* dst, in
     for (int x = lane * 8; x < dimp; x += 256) {
         if (F32) {
             float v[8];
+            if (src && vec && x + 8 <= dim) {
+                const float4 a = ld_stream<float4>(static_cast<const float*>(src) + x);
+                const float4 b = ld_stream<float4>(static_cast<const float*>(src) + x + 4);
+                v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+            } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = src && x + e < dim ? static_cast<const float*>(src)[x + e] : 0.f;
+                for (int e = 0; e < 8; ++e) v[e] = src && x + e < dim ? static_cast<const float*>(src)[x + e] : 0.f;
+            }
 #pragma unroll
             for (int q = 0; q < 3; ++q) {
                 uint32_t w[4];
@@ -238,35 +244,35 @@ __global__ void __launch_bounds__(kThreads) k_gather(const __grid_constant__ Los
     }
 }
 
+// Matrices [rows][dim] of the group's ranks, each to planes of its own, planes of a rank `bytes` apart.
 template <bool F32>
-__global__ void __launch_bounds__(kThreads) k_planes(const char* src, uint16_t* dst, int64_t rows, int dim, int dimp) {
+__global__ void __launch_bounds__(kThreads) k_planes(const __grid_constant__ LossWeights m, char* dst, int64_t bytes, int rows,
+                                                     int dim, int dimp) {
     pdl_release();
     pdl_acquire();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int64_t stride = (int64_t)dim * (F32 ? 4 : 2);
-    const bool vec = ((uintptr_t)src | (uintptr_t)stride) % 16 == 0;
-    for (int64_t row = (int64_t)blockIdx.x * kWarps + warp; row < rows; row += (int64_t)gridDim.x * kWarps)
-        row_to_planes<F32>(src + row * stride, dst + row * dimp, rows * dimp, dim, dimp, vec, lane);
+    for (int64_t at = (int64_t)blockIdx.x * kWarps + warp; at < (int64_t)m.n * rows; at += (int64_t)gridDim.x * kWarps) {
+        const int i = (int)(at / rows);
+        const int64_t row = at - (int64_t)i * rows;
+        const char* src = static_cast<const char*>(m.weights[i]);
+        const bool vec = ((uintptr_t)src | (uintptr_t)stride) % 16 == 0;
+        row_to_planes<F32>(src + row * stride, reinterpret_cast<uint16_t*>(dst + i * bytes) + row * dimp, (int64_t)rows * dimp, dim,
+                           dimp, vec, lane);
+    }
 }
 
 // ---- losses and coefficients -------------------------------------------------------
-// A block takes 32 rows of a rank, a row a lane: each warp joins every 32nd unit's statistics, the first joins the
-// warps'.  Distillation then takes the rows' lists, a warp a row.  The last block adds the blocks' losses.
+// A block takes 32 rows of a rank, a row a lane: each warp joins every 32nd unit's statistics; then a warp a
+// row joins the warps' and takes the row's target or list.  The last block adds the blocks' losses.
 constexpr int kCombineWarps = 32;
-__device__ __forceinline__ void join_stats(float& m, float& s, float& s2, float om, float os, float os2, float k1, float k2) {
-    const float top = fmaxf(m, om);
-    const float ref = top == -INFINITY ? 0.f : top;
-    const float a = m - ref, b = om - ref;
-    s = s * exp2f(a * k1) + os * exp2f(b * k1);
-    s2 = s2 * exp2f(a * k2) + os2 * exp2f(b * k2);
-    m = top;
-}
+static_assert(kCombineWarps == kLossBlockRows, "a warp a row joins the warps' parts");
 
 template <bool TWO>
 __global__ void __launch_bounds__(32 * kCombineWarps) k_combine(const __grid_constant__ LossGroup g, const __grid_constant__ LossCall c,
                                                       float* loss) {
-    __shared__ float tops[kCombineWarps][32], sums[kCombineWarps][32], sums2[kCombineWarps][32];
-    __shared__ float lse1[32], lse2[32], losses[32];
+    __shared__ float tops[kCombineWarps][33], sums[kCombineWarps][33], sums2[kCombineWarps][33];
+    __shared__ float losses[32];
     __shared__ int64_t total;
     __shared__ bool final;
     pdl_release();
@@ -290,25 +296,37 @@ __global__ void __launch_bounds__(32 * kCombineWarps) k_combine(const __grid_con
             if (threadIdx.x == 0) c.block_loss[block] = 0.0;
             continue;
         }
-        // a warp's maximum first, so that the loads of each pass do not wait for one another
+        // eight units' loads at a time, none of which waits for another
         float m = -INFINITY, s = 0.f, s2 = 0.f;
-        const int step = TWO ? 4 : 2;
-        if (valid) {
-#pragma unroll 8
-            for (int u = warp; u < c.units; u += kCombineWarps) m = fmaxf(m, c.partial[((int64_t)u * c.rows + row) * step]);
-            const float ref = m == -INFINITY ? 0.f : m;
-#pragma unroll 8
-            for (int u = warp; u < c.units; u += kCombineWarps) {
-                const int64_t at = (int64_t)u * c.rows + row;
-                if (TWO) {
-                    const float4 p = reinterpret_cast<const float4*>(c.partial)[at];
-                    s += p.y * exp2f((p.x - ref) * k1);
-                    s2 += p.z * exp2f((p.x - ref) * k2);
-                } else {
-                    const float2 p = reinterpret_cast<const float2*>(c.partial)[at];
-                    s += p.y * exp2f((p.x - ref) * k1);
+        for (int u0 = warp; valid && u0 < c.units; u0 += 8 * kCombineWarps) {
+            float4 p[8];
+            float top = m;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int u = u0 + e * kCombineWarps;
+                p[e] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+                if (u < c.units) {
+                    const int64_t at = (int64_t)u * c.rows + row;
+                    if (TWO) {
+                        p[e] = reinterpret_cast<const float4*>(c.partial)[at];
+                    } else {
+                        const float2 q = reinterpret_cast<const float2*>(c.partial)[at];
+                        p[e].x = q.x;
+                        p[e].y = q.y;
+                    }
                 }
             }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) top = fmaxf(top, p[e].x);
+            const float ref = top == -INFINITY ? 0.f : top;
+            s *= exp2f((m - ref) * k1);
+            s2 *= exp2f((m - ref) * k2);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                s += p[e].y * exp2f((p[e].x - ref) * k1);
+                if (TWO) s2 += p[e].z * exp2f((p[e].x - ref) * k2);
+            }
+            m = top;
         }
         tops[warp][lane] = m;
         sums[warp][lane] = s;
@@ -316,36 +334,33 @@ __global__ void __launch_bounds__(32 * kCombineWarps) k_combine(const __grid_con
         __syncthreads();
         const double f = c.reduction == DDP_LOSS_SUM ? 1.0 : c.reduction == DDP_LOSS_MEAN ? 1.0 / count : (double)g.world / total;
         const float factor = (float)(f * c.scale);
-        if (warp == 0 && valid) {
-            for (int k = 1; k < kCombineWarps; ++k) join_stats(m, s, s2, tops[k][lane], sums[k][lane], sums2[k][lane], k1, k2);
-            const float single = TWO ? 1.f : c.inv_temperature;
-            lse1[lane] = m * single + logf(s);
-            lse2[lane] = TWO ? m * c.inv_temperature + logf(s2) : lse1[lane];
-            if (c.value) {
-                float4 coef = make_float4(lse1[lane] * kLog2e, factor, 0.f, 0.f);
+        // a warp a row
+        const int rr = block * kLossBlockRows + warp;
+        if (rr - g.row0[i] < count) {
+            const float part = tops[lane][warp], top = warp_max(part), ref = top == -INFINITY ? 0.f : top;
+            const float sum = warp_sum(sums[lane][warp] * exp2f((part - ref) * k1));
+            const float sum2 = TWO ? warp_sum(sums2[lane][warp] * exp2f((part - ref) * k2)) : 0.f;
+            const float a = top * (TWO ? 1.f : c.inv_temperature) + logf(sum), b = TWO ? top * c.inv_temperature + logf(sum2) : a;
+            if (c.value && lane == 0) {
+                float4 coef = make_float4(a * kLog2e, factor, 0.f, 0.f);
                 if (TWO) {
                     coef.y = (1.f - c.alpha) * factor;
-                    coef.z = lse2[lane] * kLog2e;
+                    coef.z = b * kLog2e;
                     coef.w = c.alpha * c.temperature * factor;
                 } else if (c.alpha != 0.f) {           // alpha 1, or temperature 1
                     coef.y = (1.f - c.alpha + c.alpha * c.temperature) * factor;
                 }
-                c.coef[row] = coef;
+                c.coef[rr] = coef;
             }
             if (c.alpha == 0.f) {
-                const float d = c.z[row] - lse1[lane];
-                losses[lane] = -d;
-                if (c.value) c.value[row] = factor * expm1f(d);
-            }
-        }
-        if (c.alpha != 0.f) {
-            __syncthreads();
-            for (int k = warp; k < kLossBlockRows; k += kCombineWarps) {
-                const int rr = block * kLossBlockRows + k;
-                if (rr - g.row0[i] >= count) break;
+                if (lane == 0) {
+                    const float d = c.z[rr] - a;
+                    losses[warp] = -d;
+                    if (c.value) c.value[rr] = factor * expm1f(d);
+                }
+            } else {
                 const int64_t token = g.row0[i] + c.row_token[rr], at = token * c.list;
                 const int n = c.starts[token * (c.units + 1) + c.units];
-                const float a = lse1[k], b = lse2[k];
                 float cross = 0.f, hard = 0.f;
                 for (int e = lane; e < n; e += 32) {
                     const float q = c.share[at + e], z = c.z[at + e];
@@ -370,11 +385,11 @@ __global__ void __launch_bounds__(32 * kCombineWarps) k_combine(const __grid_con
                 hard = warp_sum(hard);
                 if (lane == 0) {
                     const float soft = c.alpha * c.temperature * c.temperature * (c.entropy[token] + cross);
-                    losses[k] = c.alpha < 1.f ? (1.f - c.alpha) * hard + soft : soft;
+                    losses[warp] = c.alpha < 1.f ? (1.f - c.alpha) * hard + soft : soft;
                 }
             }
-            __syncthreads();
         }
+        __syncthreads();
         if (warp == 0) {
             if (valid && g.token_losses[i]) g.token_losses[i][c.row_token[row]] = losses[lane];
             const double sum = warp_sum(valid ? (double)losses[lane] : 0.0);
@@ -405,39 +420,55 @@ __global__ void __launch_bounds__(32 * kCombineWarps) k_combine(const __grid_con
 }
 
 // ---- kept exponentials to the logits' gradients ---------------------------------------
-// dz = f e 2^(reference - lse): what the products' own epilogue computes where exponentials are not kept, rounded to
-// bf16 once more from 11 bits.  Of two softmaxes the flatter one's exponentials x are kept; the other's are x^r with
-// r <= kKeepPower, which multiplies their rounding by r.  A warp takes kConvertColumns columns of a row; memory bound.
+// dz = f e 2^(reference - lse): what the products' own epilogue computes where exponentials are not kept, from 11 bits
+// of them for bf16 operands and all for float32.  Of two softmaxes the flatter one's exponentials x are kept; the other's
+// are x^r with r <= kKeepPower, which multiplies their rounding by r.  A warp takes kConvertColumns columns of a row.
+// Memory bound: 8 x 1024 x 50257 bf16, 1.65 GB read and written, in 0.24 ms.
 constexpr int kConvertColumns = 1024;
 
-template <bool TWO, bool LIST>
+// 2^x and log2 x by the special-function unit where 11 bits were kept, else as exact as they come.
+template <bool F32>
+__device__ __forceinline__ float power_of_two(float x) {
+    if constexpr (F32) return exp2f(x);
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <bool F32, bool TWO, bool LIST>
 __global__ void __launch_bounds__(kThreads) k_convert(const __grid_constant__ LossGroup g, const __grid_constant__ LossCall c,
-                                                      uint16_t* piece, int64_t width) {
+                                                      const char* kept, uint16_t* piece, int64_t width) {
+    constexpr int kSteps = kConvertColumns / 256, kVecs = F32 ? 2 : 1;
+    constexpr float kBits = F32 ? 0.f : (float)kKeepBits;
     pdl_release();
     pdl_acquire();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const float k1 = TWO ? kLog2e : c.inv_temperature * kLog2e, k2 = c.inv_temperature * kLog2e, kept = TWO ? fminf(k1, k2) : k1;
-    const float r1 = k1 / kept, r2 = k2 / kept;
+    const float k1 = TWO ? kLog2e : c.inv_temperature * kLog2e, k2 = c.inv_temperature * kLog2e;
+    const bool flat = TWO && k2 < k1;                  // the second softmax's were kept
+    const float r = TWO ? (flat ? k1 / k2 : k2 / k1) : 1.f;
     const int64_t parts = (width + kConvertColumns - 1) / kConvertColumns;
-    const int64_t items = (g.row0[g.n] - g.row0[0]) * parts;
+    const int64_t rows = g.row0[g.n] - g.row0[0], items = rows * parts;
     for (int64_t item = (int64_t)blockIdx.x * kWarps + warp; item < items; item += (int64_t)gridDim.x * kWarps) {
         const int row = g.row0[0] + (int)(item / parts);
-        const int i = rank_of(g, row), r = row - g.row0[i], count = c.counts[g.first + i];
-        if (r >= padded(count)) continue;
-        const int64_t first = item % parts * kConvertColumns;
-        uint16_t* at = piece + (int64_t)(row - g.row0[0]) * width + first + lane * 8;
-        if (r >= count) {
+        const int i = rank_of(g, row), t = row - g.row0[i], count = c.counts[g.first + i];
+        if (t >= padded(count)) continue;
+        const int64_t first = item % parts * kConvertColumns, at = (int64_t)(row - g.row0[0]) * width + first + lane * 8;
+        if (t >= count) {
+            for (int q = 0; q < (F32 ? 3 : 1); ++q)
 #pragma unroll
-            for (int j = 0; j < kConvertColumns / 256; ++j)
-                if (first + j * 256 < width) *reinterpret_cast<uint4*>(at + j * 256) = make_uint4(0u, 0u, 0u, 0u);
+                for (int j = 0; j < kSteps; ++j)
+                    if (first + j * 256 < width)
+                        *reinterpret_cast<uint4*>(piece + q * rows * width + at + j * 256) = make_uint4(0u, 0u, 0u, 0u);
             continue;
         }
-        uint4 x[kConvertColumns / 256];
-        float top[kConvertColumns / 256];
+        uint4 x[kSteps][kVecs];
+        float top[kSteps];
 #pragma unroll
-        for (int j = 0; j < kConvertColumns / 256; ++j)
+        for (int j = 0; j < kSteps; ++j)
             if (first + j * 256 < width) {
-                x[j] = *reinterpret_cast<const uint4*>(at + j * 256);
+#pragma unroll
+                for (int h = 0; h < kVecs; ++h)
+                    x[j][h] = *reinterpret_cast<const uint4*>(kept + (at + j * 256) * (F32 ? 4 : 2) + 16 * h);
                 const int64_t u = (first + j * 256 + lane * 8) / kLossUnit;
                 top[j] = u < c.units ? c.partial[(u * c.rows + row) * (TWO ? 4 : 2)] : -INFINITY;
             }
@@ -445,32 +476,41 @@ __global__ void __launch_bounds__(kThreads) k_convert(const __grid_constant__ Lo
         const int64_t token = LIST ? g.row0[i] + c.row_token[row] : 0;
         const int32_t column = LIST ? 0 : c.row_column[row];
 #pragma unroll
-        for (int j = 0; j < kConvertColumns / 256; ++j) {
+        for (int j = 0; j < kSteps; ++j) {
             if (first + j * 256 >= width) break;
             const int col = (int)first + j * 256 + lane * 8;
             const float ref = top[j] == -INFINITY ? 0.f : top[j];
-            const float s1 = exp2f(fmaf(ref, k1, -coef.x) - kKeepBits) * coef.y;
-            const float b1 = fmaf(ref, k1, -coef.x) - kKeepBits * r1, b2 = fmaf(ref, k2, -coef.z) - kKeepBits * r2;
-            uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+            float v[8];
+            if constexpr (F32) {
+                const uint32_t w[8] = {x[j][0].x, x[j][0].y, x[j][0].z, x[j][0].w, x[j][1].x, x[j][1].y, x[j][1].z, x[j][1].w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
-                if (TWO) {
-                    const float lo = __log2f(f.x), hi = __log2f(f.y);      // 0: -infinity, and 0 again
-                    w[e] = bf16x2_rn(coef.y * exp2f(fmaf(lo, r1, b1)) + coef.w * exp2f(fmaf(lo, r2, b2)),
-                                     coef.y * exp2f(fmaf(hi, r1, b1)) + coef.w * exp2f(fmaf(hi, r2, b2)));
-                } else {
-                    w[e] = bf16x2_rn(f.x * s1, f.y * s1);
+                for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(w[e]);
+            } else {
+                const uint32_t w[4] = {x[j][0].x, x[j][0].y, x[j][0].z, x[j][0].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
+                    v[2 * e] = f.x;
+                    v[2 * e + 1] = f.y;
                 }
+            }
+            const float b1 = fmaf(ref, k1, -coef.x), b2 = fmaf(ref, k2, -coef.z);
+            if (TWO) {
+                const float own = flat ? exp2f(b2 - kBits) * coef.w : exp2f(b1 - kBits) * coef.y;
+                const float other = (flat ? b1 : b2) - kBits * r, factor = flat ? coef.y : coef.w;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)            // log2 of 0: -infinity, and 0 again
+                    v[e] = fmaf(factor, power_of_two<F32>(fmaf(F32 ? log2f(v[e]) : __log2f(v[e]), r, other)), v[e] * own);
+            } else {
+                const float own = exp2f(b1 - kBits) * coef.y;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] *= own;
             }
             // the exact gradient where a target or a teacher has its say
             const auto put = [&](int32_t k, float value) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    if (k == col + e) {
-                        const uint32_t h = f32_to_bf16_rn(value);
-                        w[e / 2] = e % 2 ? (w[e / 2] & 0xFFFFu) | h << 16 : (w[e / 2] & 0xFFFF0000u) | h;
-                    }
+                    if (k == col + e) v[e] = value;
             };
             if (LIST) {
                 if (col < c.vocab) {
@@ -483,7 +523,19 @@ __global__ void __launch_bounds__(kThreads) k_convert(const __grid_constant__ Lo
             } else if (column >= col && column < col + 8) {
                 put(column, c.value[row]);
             }
-            *reinterpret_cast<uint4*>(at + j * 256) = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+            for (int q = 0; q < (F32 ? 3 : 1); ++q) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    w[e] = bf16x2_rn(v[2 * e], v[2 * e + 1]);
+                    if (F32) {
+                        v[2 * e] -= bf16_lo(w[e]);
+                        v[2 * e + 1] -= bf16_hi(w[e]);
+                    }
+                }
+                *reinterpret_cast<uint4*>(piece + q * rows * width + at + j * 256) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
         }
     }
 }
@@ -501,28 +553,39 @@ __global__ void __launch_bounds__(kThreads) k_join(const __grid_constant__ LossG
         const int r = c.token_row[at];
         char* out = static_cast<char*>(g.grad_hidden[i]) + (int64_t)t * c.dim * (F32 ? 4 : 2);
         const bool vec = ((uintptr_t)g.grad_hidden[i] | (uintptr_t)(c.dim * (F32 ? 4 : 2))) % (F32 ? 16 : 8) == 0;
-        for (int x = lane * 4; x < c.dim; x += 128) {
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (r >= 0)
-                for (int s = 0; s < splits; ++s) {
-                    const float4 p = *reinterpret_cast<const float4*>(c.acc + (s * c.rows + g.row0[i] + r) * c.dimp + x);
-                    v = make_float4(v.x + p.x, v.y + p.y, v.z + p.z, v.w + p.w);
+        constexpr int kSteps = 4;                      // columns' loads at a time
+        for (int x0 = lane * 4; x0 < c.dim; x0 += 128 * kSteps) {
+            float4 v[kSteps] = {};
+            if (r >= 0) {
+                const float* p = c.acc + ((int64_t)g.row0[i] + r) * c.dimp + x0;
+                for (int s = 0; s < splits; ++s, p += c.rows * c.dimp)
+#pragma unroll
+                    for (int j = 0; j < kSteps; ++j)
+                        if (x0 + j * 128 < c.dim) {
+                            const float4 q = *reinterpret_cast<const float4*>(p + j * 128);
+                            v[j] = make_float4(v[j].x + q.x, v[j].y + q.y, v[j].z + q.z, v[j].w + q.w);
+                        }
+            }
+#pragma unroll
+            for (int j = 0; j < kSteps; ++j) {
+                const int x = x0 + j * 128;
+                if (x >= c.dim) break;
+                const float e[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+                if (F32) {
+                    float* o = reinterpret_cast<float*>(out) + x;
+                    if (vec) *reinterpret_cast<float4*>(o) = v[j];
+                    else
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (x + k < c.dim) o[k] = e[k];
+                } else {
+                    uint16_t* o = reinterpret_cast<uint16_t*>(out) + x;
+                    if (vec) *reinterpret_cast<uint2*>(o) = make_uint2(bf16x2_rn(e[0], e[1]), bf16x2_rn(e[2], e[3]));
+                    else
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (x + k < c.dim) o[k] = f32_to_bf16_rn(e[k]);
                 }
-            const float e[4] = {v.x, v.y, v.z, v.w};
-            if (F32) {
-                float* o = reinterpret_cast<float*>(out) + x;
-                if (vec) *reinterpret_cast<float4*>(o) = v;
-                else
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (x + k < c.dim) o[k] = e[k];
-            } else {
-                uint16_t* o = reinterpret_cast<uint16_t*>(out) + x;
-                if (vec) *reinterpret_cast<uint2*>(o) = make_uint2(bf16x2_rn(v.x, v.y), bf16x2_rn(v.z, v.w));
-                else
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (x + k < c.dim) o[k] = f32_to_bf16_rn(e[k]);
             }
         }
     }
@@ -546,9 +609,9 @@ cudaError_t launch_loss_gather(const LossGroup& g, const LossCall& c, cudaStream
                             dim3(kThreads), 0, stream, g, c);
 }
 
-cudaError_t launch_loss_planes(const void* src, void* dst, int64_t rows, const LossCall& c, cudaStream_t stream) {
-    return launch_dependent(c.dtype == DDP_F32 ? k_planes<true> : k_planes<false>, dim3(warp_grid(rows)), dim3(kThreads), 0, stream,
-                            static_cast<const char*>(src), static_cast<uint16_t*>(dst), rows, c.dim, c.dimp);
+cudaError_t launch_loss_planes(const LossWeights& m, void* dst, int64_t bytes, const LossCall& c, cudaStream_t stream) {
+    return launch_dependent(c.dtype == DDP_F32 ? k_planes<true> : k_planes<false>, dim3(warp_grid((int64_t)m.n * c.vocab)),
+                            dim3(kThreads), 0, stream, m, static_cast<char*>(dst), bytes, c.vocab, c.dim, c.dimp);
 }
 
 cudaError_t launch_loss_combine(const LossGroup& g, const LossCall& c, float* loss, cudaStream_t stream) {
@@ -557,10 +620,16 @@ cudaError_t launch_loss_combine(const LossGroup& g, const LossCall& c, float* lo
                             dim3(32 * kCombineWarps), 0, stream, g, c, loss);
 }
 
-cudaError_t launch_loss_convert(const LossGroup& g, const LossCall& c, void* piece, int64_t width, cudaStream_t stream) {
-    const auto kernel = c.two ? k_convert<true, true> : c.alpha != 0.f ? k_convert<false, true> : k_convert<false, false>;
+template <bool F32>
+static cudaError_t convert(const LossGroup& g, const LossCall& c, const void* kept, void* piece, int64_t width, cudaStream_t stream) {
+    const auto kernel = c.two ? k_convert<F32, true, true> : c.alpha != 0.f ? k_convert<F32, false, true> : k_convert<F32, false, false>;
     const int64_t items = (g.row0[g.n] - g.row0[0]) * ((width + kConvertColumns - 1) / kConvertColumns);
-    return launch_dependent(kernel, dim3(warp_grid(items)), dim3(kThreads), 0, stream, g, c, static_cast<uint16_t*>(piece), width);
+    return launch_dependent(kernel, dim3(warp_grid(items)), dim3(kThreads), 0, stream, g, c, static_cast<const char*>(kept),
+                            static_cast<uint16_t*>(piece), width);
+}
+cudaError_t launch_loss_convert(const LossGroup& g, const LossCall& c, const void* kept, void* piece, int64_t width,
+                                cudaStream_t stream) {
+    return c.dtype == DDP_F32 ? convert<true>(g, c, kept, piece, width, stream) : convert<false>(g, c, kept, piece, width, stream);
 }
 
 cudaError_t launch_loss_join(const LossGroup& g, const LossCall& c, int splits, cudaStream_t stream) {
