@@ -1,10 +1,11 @@
 // loss_api.cpp -- the C ABI of the loss head: argument checks, the workspace's
 // layout, tensor maps, and the order of a call's launches.
 //
-// A call runs: the teachers' lists (distillation) and the scan, for all ranks; then
-// for groups of kLossRanks ranks the gather, the logits' statistics and their
-// combination into losses; with gradients also, for each piece of the vocabulary,
-// its logits' gradients and the two products with them, and the join.
+// A call of little data is one launch.  Another runs, for all ranks, the teachers'
+// lists (distillation) and the gather of learned tokens; then for groups of ranks
+// the logits' statistics and their combination into losses; with gradients also,
+// for each piece of the vocabulary (or once, where exponentials are kept), its
+// logits' gradients and the two products with them, and the join.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -380,10 +381,9 @@ int32_t run(ddp_loss_head* h, const Args& a, cudaStream_t stream) {
         m.accumulate = a.accumulate;
         return cuda_status(launch_loss_small(groups[0], c, m, a.loss, stream));
     }
-    for (const LossGroup& g : groups) {
-        if (distill && (st = cuda_status(launch_loss_teacher(g, c, stream)))) return st;
-        if ((st = cuda_status(launch_loss_scan(g, c, stream)))) return st;
-    }
+    for (const LossGroup& g : groups)
+        if ((distill && (st = cuda_status(launch_loss_teacher(g, c, stream)))) || (st = cuda_status(launch_loss_gather(g, c, stream))))
+            return st;
     if (h->copied)
         for (const LossGroup& g : groups) {
             LossWeights p{};
@@ -439,9 +439,7 @@ int32_t run(ddp_loss_head* h, const Args& a, cudaStream_t stream) {
         if (span > 0) {
             m.piece0 = 0;
             m.width = h->vocab;
-            if ((st = cuda_status(launch_loss_gather(g, c, stream))) ||
-                (st = cuda_status(launch_loss_gemm(keep ? LossPhase::kKeep : LossPhase::kStats, m, stream))))
-                return st;
+            if ((st = cuda_status(launch_loss_gemm(keep ? LossPhase::kKeep : LossPhase::kStats, m, stream)))) return st;
         }
         if ((st = cuda_status(launch_loss_combine(g, c, a.loss, stream)))) return st;
         if (!a.grad) continue;

@@ -885,18 +885,27 @@ __device__ __forceinline__ void weights_tile(const LossGemm& g, const Tile& w, c
         __syncwarp();
         const int x = col + l.lane;
         if (x >= c.dim) continue;
-        for (int i = 0; i < rows; ++i) {
-            float f = *reinterpret_cast<const float*>(l.staging + (l.quarter * 32 + i) * 128 + (((l.lane >> 2) ^ (i & 7)) << 4) +
-                                                      (l.lane & 3) * 4);
-            const int64_t at = (int64_t)(v0 + i) * c.dim + x;
-            if (F32) {
-                float* out = static_cast<float*>(g.grads[w.rank]) + at;
-                *out = g.accumulate ? *out + f : f;
-            } else {
-                uint16_t* out = static_cast<uint16_t*>(g.grads[w.rank]) + at;
-                if (g.accumulate) f += bf16_to_f32(*out);
-                *out = f32_to_bf16_rn(f);
+        constexpr int kRows = 8;                       // rows' loads at a time
+        for (int i0 = 0; i0 < rows; i0 += kRows) {
+            float f[kRows];
+            const int64_t at = (int64_t)(v0 + i0) * c.dim + x;
+            float* out32 = static_cast<float*>(g.grads[w.rank]) + at;
+            uint16_t* out16 = static_cast<uint16_t*>(g.grads[w.rank]) + at;
+#pragma unroll
+            for (int i = 0; i < kRows; ++i)
+                f[i] = *reinterpret_cast<const float*>(l.staging + (l.quarter * 32 + i0 + i) * 128 +
+                                                       (((l.lane >> 2) ^ ((i0 + i) & 7)) << 4) + (l.lane & 3) * 4);
+            if (g.accumulate) {
+#pragma unroll
+                for (int i = 0; i < kRows; ++i)
+                    if (i0 + i < rows) f[i] += F32 ? out32[(int64_t)i * c.dim] : bf16_to_f32(out16[(int64_t)i * c.dim]);
             }
+#pragma unroll
+            for (int i = 0; i < kRows; ++i)
+                if (i0 + i < rows) {
+                    if (F32) out32[(int64_t)i * c.dim] = f[i];
+                    else out16[(int64_t)i * c.dim] = f32_to_bf16_rn(f[i]);
+                }
         }
     }
 }

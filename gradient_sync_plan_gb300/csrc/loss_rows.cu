@@ -17,7 +17,6 @@ namespace ddpk {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kScanThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMostList = DDP_MAX_TEACHER + 1;
 
@@ -131,60 +130,6 @@ __global__ void __launch_bounds__(kThreads) k_teacher(const __grid_constant__ Lo
 }
 
 // ---- rows of learned tokens -------------------------------------------------------
-// A block a rank; four tokens a thread and pass.
-__global__ void __launch_bounds__(kScanThreads) k_scan(const __grid_constant__ LossGroup g, const __grid_constant__ LossCall c) {
-    __shared__ int32_t before[kScanThreads / 32];
-    pdl_release();
-    pdl_acquire();
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    if (blockIdx.x == 0 && threadIdx.x == 0) *c.done = c.next[0] = c.next[1] = 0;
-    for (int i = blockIdx.x; i < g.n; i += gridDim.x) {
-        const int row0 = g.row0[i], n = g.tokens[i];
-        int count = 0;
-        for (int t0 = 0; t0 < n; t0 += 4 * kScanThreads) {
-            const int mine = t0 + 4 * threadIdx.x;
-            int64_t y[4];
-            bool ok[4];
-            int sum = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = mine + e < n && g.targets[i] ? g.targets[i][mine + e] : 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                ok[e] = mine + e < n && (c.alpha == 0.f ? learned(y[e], c) : c.valid[row0 + mine + e] != 0);
-                sum += ok[e];
-            }
-            int in_warp = sum;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int x = __shfl_up_sync(0xffffffffu, in_warp, d);
-                if (lane >= d) in_warp += x;
-            }
-            if (lane == 31) before[warp] = in_warp;
-            __syncthreads();
-            int row = count + in_warp - sum;
-            for (int k = 0; k < kScanThreads / 32; ++k) {
-                if (k < warp) row += before[k];
-                count += before[k];
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int t = mine + e;
-                if (t >= n) break;
-                c.token_row[row0 + t] = ok[e] ? row : -1;
-                if (ok[e]) {
-                    c.row_token[row0 + row] = t;
-                    c.row_column[row0 + row] = (int32_t)y[e];
-                    ++row;
-                } else if (g.token_losses[i]) {
-                    g.token_losses[i][t] = 0.f;
-                }
-            }
-            __syncthreads();
-        }
-        if (threadIdx.x == 0) c.counts[g.first + i] = count;
-    }
-}
-
 // One row to its bf16 planes, zeros from `dim` on; src null: a row of zeros.  A warp.
 template <bool F32>
 __device__ __forceinline__ void row_to_planes(const void* src, uint16_t* dst, int64_t plane, int dim, int dimp, bool vec,
@@ -226,21 +171,84 @@ __device__ __forceinline__ void row_to_planes(const void* src, uint16_t* dst, in
     }
 }
 
+// Learned tokens' hidden states into rows, in the tokens' order.  A block takes a chunk of a rank's tokens: it counts the
+// learned ones before the chunk by itself (8 bytes a token from the L2, for at most kMostChunks blocks a rank: a launch
+// of its own for the counts would take longer), places its own, and copies their rows, a warp a row.  A rank's last
+// block writes the count and zeroes the rows that pad it.
+constexpr int kChunk = 8, kMostChunks = 1024;
+__host__ __device__ __forceinline__ int chunk_of(int tokens) {
+    const int most = (tokens + kMostChunks - 1) / kMostChunks;
+    return most > kChunk ? most : kChunk;
+}
+__host__ __device__ __forceinline__ int chunks_of(int tokens) {      // one for a rank without tokens: its count
+    return tokens > 0 ? (tokens + chunk_of(tokens) - 1) / chunk_of(tokens) : 1;
+}
+
 template <bool F32>
-__global__ void __launch_bounds__(kThreads) k_gather(const __grid_constant__ LossGroup g, const __grid_constant__ LossCall c) {
+__global__ void __launch_bounds__(kThreads) k_gather(const __grid_constant__ LossGroup g, const __grid_constant__ LossCall c,
+                                                     int items) {
+    __shared__ int32_t sums[kWarps];
+    __shared__ int32_t token[kThreads];
     pdl_release();
     pdl_acquire();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int first = g.row0[0], last = g.row0[g.n];
-    for (int row = first + blockIdx.x * kWarps + warp; row < last; row += gridDim.x * kWarps) {
-        const int i = rank_of(g, row), r = row - g.row0[i], count = c.counts[g.first + i];
-        if (r >= padded(count)) continue;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *c.done = c.next[0] = c.next[1] = 0;
+    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        int i = 0, chunk = item;
+        while (chunk >= chunks_of(g.tokens[i])) chunk -= chunks_of(g.tokens[i++]);
+        const int n = g.tokens[i], row0 = g.row0[i], t0 = chunk * chunk_of(n), t1 = min(n, t0 + chunk_of(n));
+        const auto is_learned = [&](int t) {
+            if (c.alpha != 0.f) return c.valid[row0 + t] != 0;
+            const int64_t y = g.targets[i][t];
+            return y != c.ignore_index && y >= 0 && y < c.vocab;
+        };
+        int sum = 0;
+#pragma unroll 4
+        for (int t = threadIdx.x; t < t0; t += kThreads) sum += is_learned(t);
+        sum = warp_sum(sum);
+        __syncthreads();
+        if (lane == 0) sums[warp] = sum;
+        __syncthreads();
+        int count = 0;
+        for (int k = 0; k < kWarps; ++k) count += sums[k];
         const char* h = static_cast<const char*>(g.hidden[i]);
         const int es = F32 ? 4 : 2;
         const bool vec = ((uintptr_t)h | (uintptr_t)(c.hidden_stride * es)) % 16 == 0;
-        const void* src = r < count ? h + (int64_t)c.row_token[row] * c.hidden_stride * es : nullptr;
-        row_to_planes<F32>(src, static_cast<uint16_t*>(c.gathered) + (int64_t)row * c.dimp, c.rows * c.dimp, c.dim, c.dimp, vec,
-                           lane);
+        uint16_t* rows = static_cast<uint16_t*>(c.gathered) + (int64_t)row0 * c.dimp;
+        for (int b = t0; b < t1; b += kThreads) {
+            const int t = b + threadIdx.x;
+            bool ok = false;
+            if (t < t1) ok = c.alpha == 0.f ? learned(g.targets[i][t], c) : is_learned(t);
+            const uint32_t there = __ballot_sync(0xffffffffu, ok);
+            __syncthreads();
+            if (lane == 0) sums[warp] = __popc(there);
+            __syncthreads();
+            int before = 0, all = 0;
+            for (int k = 0; k < kWarps; ++k) {
+                if (k < warp) before += sums[k];
+                all += sums[k];
+            }
+            before += __popc(there & ((1u << lane) - 1));
+            if (ok) {
+                token[before] = t;
+                c.row_token[row0 + count + before] = t;
+                if (c.alpha == 0.f) c.row_column[row0 + count + before] = (int32_t)g.targets[i][t];
+            }
+            if (t < t1) {
+                c.token_row[row0 + t] = ok ? count + before : -1;
+                if (!ok && g.token_losses[i]) g.token_losses[i][t] = 0.f;
+            }
+            __syncthreads();
+            for (int k = warp; k < all; k += kWarps)
+                row_to_planes<F32>(h + (int64_t)token[k] * c.hidden_stride * es, rows + (int64_t)(count + k) * c.dimp,
+                                   c.rows * c.dimp, c.dim, c.dimp, vec, lane);
+            count += all;
+        }
+        if (t1 == n) {
+            if (threadIdx.x == 0) c.counts[g.first + i] = count;
+            for (int r = count + warp; r < padded(count); r += kWarps)
+                row_to_planes<F32>(nullptr, rows + (int64_t)r * c.dimp, c.rows * c.dimp, c.dim, c.dimp, false, lane);
+        }
     }
 }
 
@@ -600,13 +608,11 @@ cudaError_t launch_loss_teacher(const LossGroup& g, const LossCall& c, cudaStrea
     return launch_dependent(k_teacher, dim3(warp_grid(g.row0[g.n] - g.row0[0])), dim3(kThreads), 0, stream, g, c);
 }
 
-cudaError_t launch_loss_scan(const LossGroup& g, const LossCall& c, cudaStream_t stream) {
-    return launch_dependent(k_scan, dim3(cap_ctas(g.n)), dim3(kScanThreads), 0, stream, g, c);
-}
-
 cudaError_t launch_loss_gather(const LossGroup& g, const LossCall& c, cudaStream_t stream) {
-    return launch_dependent(c.dtype == DDP_F32 ? k_gather<true> : k_gather<false>, dim3(warp_grid(g.row0[g.n] - g.row0[0])),
-                            dim3(kThreads), 0, stream, g, c);
+    int64_t items = 0;
+    for (int i = 0; i < g.n; ++i) items += chunks_of(g.tokens[i]);
+    return launch_dependent(c.dtype == DDP_F32 ? k_gather<true> : k_gather<false>, dim3(cap_ctas(items)), dim3(kThreads), 0, stream, g,
+                            c, (int)items);
 }
 
 cudaError_t launch_loss_planes(const LossWeights& m, void* dst, int64_t bytes, const LossCall& c, cudaStream_t stream) {
