@@ -316,6 +316,7 @@ int32_t run(ddp_loss_head* h, const Args& a, cudaStream_t stream) {
     c.temperature = (float)a.temperature;
     c.inv_temperature = (float)(1.0 / a.temperature);
     c.two = distill && c.alpha < 1.f && c.temperature != 1.f;
+    c.unit = 1.f + kCutPerStep * (float)(c.dimp / 16);
     c.hidden_stride = a.hidden_stride;
     c.ignore_index = a.ignore_index;
     c.scale = (float)a.scale;

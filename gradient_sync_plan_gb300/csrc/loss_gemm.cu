@@ -56,8 +56,13 @@ constexpr float kKeepScale = (float)(1 << kKeepBits);
 // the products: a multiple of 64 for each block), k blocks.
 struct alignas(16) Tile {
     int32_t rank, m, n, columns, k0, k1, split;
-    int32_t weights;                       // of dw
+    int32_t flags;
+    __device__ __forceinline__ bool weights() const { return flags & 1; }      // of dw
+    __device__ __forceinline__ bool more() const { return flags & 2; }         // added to the depth before
 };
+// float32 sums are taken out of tensor memory and added up elsewhere every so many k blocks: the tensor cores cut what they
+// add to a long sum (kCutPerStep), by 2e-5 of the result over a depth of 50257.
+constexpr int kMostDepth = 16;
 constexpr int kTileWords = sizeof(Tile) / 4;
 constexpr int kQueue = 4;
 
@@ -286,7 +291,7 @@ __device__ __forceinline__ bool find_tile(const LossGemm& g, const int32_t* coun
             continue;
         }
         w->rank = i;
-        w->weights = false;
+        w->flags = 0;
         w->split = 0;
         if (PHASE != LossPhase::kProducts) {           // rows' tiles of one column block together: they share the weights
             w->m = g.row0[i] + t % m * M;
@@ -312,7 +317,7 @@ __device__ __forceinline__ bool find_tile(const LossGemm& g, const int32_t* coun
                 continue;
             }
             w->rank = i;
-            w->weights = true;
+            w->flags = 1;
             w->split = 0;
             w->n = t % nt * kTileN;
             w->m = t / nt * M;
@@ -350,30 +355,45 @@ __device__ __forceinline__ void get_tile(Tile* w, const Tile* at) {
 // queue and the second block's mail, which a thread there copies to its own queue: waiting for another block's writes,
 // like reporting to one, takes some two thousand cycles, which no role that works on tiles should spend.  Who computes a
 // tile changes no value.  The last cluster to finish leaves the counters at zero.
-template <LossPhase PHASE, int CG>
+template <int CG>
+__device__ __forceinline__ void enqueue(Control* s, int slot, const Tile& w) {
+    put_tile(&s->queue[slot], w);
+    bar_arrive(&s->tile_full[slot]);
+    if constexpr (CG == 2) {
+        const int32_t* words = reinterpret_cast<const int32_t*>(&w);
+        const uint32_t at = in_block(&s->mail[slot], 1);
+#pragma unroll
+        for (int i = 0; i < kTileWords; ++i)
+            asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(at + 4 * i), "r"(words[i]) : "memory");
+        arrive_at(in_block(&s->mail_full[slot], 1));
+    }
+}
+template <LossPhase PHASE, bool F32, int CG>
 __device__ void schedule(const LossGemm& g, Control* s) {
     const int clusters = gridDim.x / CG;
+    int slot = 0, t = blockIdx.x / CG;
     uint32_t phase = 1;
-    int t = blockIdx.x / CG;
-    for (int n = 0;; ++n) {
-        const int slot = n % kQueue;
+    bool more = true;
+    while (more) {
         Tile w;
-        const bool more = find_tile<PHASE, CG>(g, s->counts, t, &w);
-        if (!more) w.rank = -1;
+        more = find_tile<PHASE, CG>(g, s->counts, t, &w);
         if (more) t = clusters + atomicAdd(g.c.next, 1);
-        if (!bar_wait(&s->tile_empty[slot], phase, s, g)) break;
-        put_tile(&s->queue[slot], w);
-        bar_arrive(&s->tile_full[slot]);
-        if constexpr (CG == 2) {
-            const int32_t* words = reinterpret_cast<const int32_t*>(&w);
-            const uint32_t at = in_block(&s->mail[slot], 1);
-#pragma unroll
-            for (int i = 0; i < kTileWords; ++i)
-                asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(at + 4 * i), "r"(words[i]) : "memory");
-            arrive_at(in_block(&s->mail_full[slot], 1));
-        }
-        if (slot == kQueue - 1) phase ^= 1;
-        if (!more) break;
+        else w.rank = -1;
+        const int end = w.k1;
+        do {                               // a tile's depth, in parts that follow each other
+            if (F32 && PHASE == LossPhase::kProducts && more) w.k1 = min(end, w.k0 + kMostDepth);
+            if (!bar_wait(&s->tile_empty[slot], phase, s, g)) {
+                more = false;
+                break;
+            }
+            enqueue<CG>(s, slot, w);
+            if (++slot == kQueue) {
+                slot = 0;
+                phase ^= 1;
+            }
+            w.k0 = w.k1;
+            w.flags |= 2;
+        } while (more && w.k1 < end);
     }
     __threadfence();
     if (atomicAdd(g.c.next + 1, 1) == clusters - 1) {
@@ -476,7 +496,7 @@ __device__ void produce(const LossGemm& g, Control* s, char* stages, int block) 
                 if (PHASE != LossPhase::kProducts) {
                     tma_load<CG>(a, &g.hidden, k, bm, pa, bar);
                     tma_load<CG>(b, wmap, k, g.piece0 + bn, pb, bar);
-                } else if (!w.weights) {
+                } else if (!w.weights()) {
                     tma_load<CG>(a, &g.piece, k, bm - g.row0[0], pa, bar);
                     tma_load<CG>(b, wmap, bn, g.piece0 + k, pb, bar);
                 } else {
@@ -525,7 +545,7 @@ __device__ void multiply(const LossGemm& g, Control* s, char* stages, uint32_t t
     Tile w, after;
     bool more = queue.next(s, g, &w);
     while (more) {
-        const bool a_across = PHASE == LossPhase::kProducts && w.weights, b_across = PHASE == LossPhase::kProducts;
+        const bool a_across = PHASE == LossPhase::kProducts && w.weights(), b_across = PHASE == LossPhase::kProducts;
         const uint32_t desc = product_desc(a_across, b_across, CG * kTileM, w.columns);
         // 16 elements of depth: 32 bytes along a row, or 16 rows of 128 bytes
         const uint32_t step_a = a_across ? 16 * 128 / 16 : 2, step_b = b_across ? 16 * 128 / 16 : 2;
@@ -621,7 +641,7 @@ __device__ __forceinline__ void stats_tile(const LossGemm& g, const Tile& w, con
     const bool valid = row - g.row0[w.rank] < s->counts[w.rank];
     Listed<LIST> hit;
     hit.start(c, row, LIST && valid ? g.row0[w.rank] + c.row_token[row] : 0, first, valid && first < c.vocab);
-    const float k1 = TWO ? kLog2e : c.inv_temperature * kLog2e, k2 = c.inv_temperature * kLog2e;
+    const float k1 = c.unit * (TWO ? kLog2e : c.inv_temperature * kLog2e), k2 = c.unit * (c.inv_temperature * kLog2e);
     if (KEEP) {
         if (l.leader) tma_read_done();
         group_sync(l.group);               // the staging buffer is free
@@ -636,7 +656,7 @@ __device__ __forceinline__ void stats_tile(const LossGemm& g, const Tile& w, con
         if (__any_sync(0xffffffffu, hit.column < col + 32)) {
             stage_floats(l, v);
             while (hit.column < col + 32) {
-                c.z[hit.at] = staged_float(l, hit.column - col);
+                c.z[hit.at] = c.unit * staged_float(l, hit.column - col);
                 hit.next();
             }
         }
@@ -730,7 +750,7 @@ __device__ __forceinline__ void grad_tile(const LossGemm& g, const Tile& w, cons
     Listed<LIST> hit;
     hit.start(c, row, LIST && valid ? g.row0[w.rank] + c.row_token[row] : 0, first, valid && first < c.vocab);
     const float4 coef = valid ? c.coef[row] : make_float4(0.f, 0.f, 0.f, 0.f);
-    const float k1 = TWO ? kLog2e : c.inv_temperature * kLog2e, k2 = c.inv_temperature * kLog2e;
+    const float k1 = c.unit * (TWO ? kLog2e : c.inv_temperature * kLog2e), k2 = c.unit * (c.inv_temperature * kLog2e);
 #pragma unroll 1
     for (int j = 0; j < kLossUnit / 64; ++j) {
         float v[64];
@@ -787,9 +807,19 @@ __device__ __forceinline__ void grad_tile(const LossGemm& g, const Tile& w, cons
     }
 }
 
+// What a sum lost where the tensor cores cut it (kCutPerStep), for results in float32; of the six passes the last
+// adds what counts.
+template <bool F32, int N>
+__device__ __forceinline__ void uncut(float (&v)[N], const Tile& w) {
+    if constexpr (F32) {
+        const float f = 1.f + kCutPerStep * (float)((w.k1 - w.k0) * (kTileK / 16));
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] *= f;
+    }
+}
+
 // dh: the tile goes to its split's part of acc, added there by the copy engine from the second piece on (one
 // writer an element and launch, so the order is fixed).
-template <int CG>
 __device__ __forceinline__ void hidden_tile(const LossGemm& g, const Tile& w, const Lane& l, uint64_t* taken) {
 #pragma unroll 1
     for (int j = 0; j < kTileN / 2 / 32; ++j) {
@@ -803,14 +833,17 @@ __device__ __forceinline__ void hidden_tile(const LossGemm& g, const Tile& w, co
         }
         // the same for the whole group: no column of acc, or no depth in a shorter last piece
         if (col >= g.c.dimp || w.k1 <= w.k0) continue;
-        if (l.leader) tma_read_done();
+        if (l.leader) {
+            if (w.more()) tma_all_done();  // the part before has been added
+            else tma_read_done();
+        }
         group_sync(l.group);
         stage_floats(l, v);
         to_async_proxy();
         group_sync(l.group);
         if (l.leader) {
             const int y = (int)(w.split * g.c.rows) + w.m;
-            if (g.add) tma_add_2d(&g.acc, l.staging, col, y);
+            if (g.add || w.more()) tma_add_2d(&g.acc, l.staging, col, y);
             else tma_store_2d(&g.acc, l.staging, col, y);
             tma_commit();
         }
@@ -841,7 +874,11 @@ __device__ __forceinline__ void weights_tile(const LossGemm& g, const Tile& w, c
 #pragma unroll
                 for (int i = 0; i < kColumns; ++i) v[i] = 0.f;
             }
-            if (l.leader) tma_read_done();
+            uncut<F32>(v, w);
+            if (l.leader) {
+                if (F32 && w.more()) tma_all_done();
+                else tma_read_done();
+            }
             group_sync(l.group);
             if constexpr (F32) {
                 stage_floats(l, v);
@@ -855,7 +892,8 @@ __device__ __forceinline__ void weights_tile(const LossGemm& g, const Tile& w, c
             to_async_proxy();
             group_sync(l.group);
             if (l.leader && g.piece0 + w.m < c.vocab) {    // a pair's second block may be past the last row
-                tma_store_2d(&g.out[w.rank], l.staging, col, g.piece0 + w.m);
+                if (F32 && w.more()) tma_add_2d(&g.out[w.rank], l.staging, col, g.piece0 + w.m);
+                else tma_store_2d(&g.out[w.rank], l.staging, col, g.piece0 + w.m);
                 tma_commit();
             }
         }
@@ -880,6 +918,7 @@ __device__ __forceinline__ void weights_tile(const LossGemm& g, const Tile& w, c
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = 0.f;
         }
+        uncut<F32>(v, w);
         __syncwarp();
         stage_floats(l, v);
         __syncwarp();
@@ -895,7 +934,7 @@ __device__ __forceinline__ void weights_tile(const LossGemm& g, const Tile& w, c
             for (int i = 0; i < kRows; ++i)
                 f[i] = *reinterpret_cast<const float*>(l.staging + (l.quarter * 32 + i0 + i) * 128 +
                                                        (((l.lane >> 2) ^ ((i0 + i) & 7)) << 4) + (l.lane & 3) * 4);
-            if (g.accumulate) {
+            if (g.accumulate || (F32 && w.more())) {
 #pragma unroll
                 for (int i = 0; i < kRows; ++i)
                     if (i0 + i < rows) f[i] += F32 ? out32[(int64_t)i * c.dim] : bf16_to_f32(out16[(int64_t)i * c.dim]);
@@ -960,7 +999,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_loss_gemm(const __grid_cons
     } else if (warp == 1) {
         if (lane == 0 && block == 0) multiply<PHASE, F32, CG>(g, s, smem, tmem);
     } else if (warp == 3) {
-        if (lane == 0 && block == 0) schedule<PHASE, CG>(g, s);
+        if (lane == 0 && block == 0) schedule<PHASE, F32, CG>(g, s);
         if (lane == 0 && block == 1) copy_mail(g, s);
     } else if (warp == 2) {
         if (lane == 0 && block == 1) pass_on(g, s);
@@ -1000,7 +1039,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_loss_gemm(const __grid_cons
             if (PHASE == LossPhase::kStats || PHASE == LossPhase::kKeep)
                 stats_tile<F32, TWO, LIST, PHASE == LossPhase::kKeep, CG>(g, w, l, s, taken);
             else if (PHASE == LossPhase::kGrad) grad_tile<F32, TWO, LIST, CG>(g, w, l, s, taken);
-            else if (!w.weights) hidden_tile<CG>(g, w, l, taken);
+            else if (!w.weights()) hidden_tile(g, w, l, taken);
             else weights_tile<F32, CG>(g, w, l, taken);
             if (buf == 1) phase ^= 1;
             buf ^= 1;

@@ -8,7 +8,7 @@
 // tokens of d elements the gather and the join read and write T d elements each.
 // Nothing here uses atomics on values: every sum has one order.
 #include <algorithm>
-#include <cfloat>
+#include <type_traits>
 
 #include "ddp_device.cuh"
 #include "loss_internal.h"
@@ -279,6 +279,7 @@ static_assert(kCombineWarps == kLossBlockRows, "a warp a row joins the warps' pa
 template <bool TWO>
 __global__ void __launch_bounds__(32 * kCombineWarps) k_combine(const __grid_constant__ LossGroup g, const __grid_constant__ LossCall c,
                                                       float* loss) {
+    using Part = std::conditional_t<TWO, float4, float2>;
     __shared__ float tops[kCombineWarps][33], sums[kCombineWarps][33], sums2[kCombineWarps][33];
     __shared__ float losses[32];
     __shared__ int64_t total;
@@ -294,7 +295,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) k_combine(const __grid_con
         if (lane == 0) total = n;
     }
     __syncthreads();
-    const float k1 = TWO ? kLog2e : c.inv_temperature * kLog2e, k2 = c.inv_temperature * kLog2e;
+    const float k1 = c.unit * (TWO ? kLog2e : c.inv_temperature * kLog2e), k2 = c.unit * (c.inv_temperature * kLog2e);
     const int first = g.row0[0] / kLossBlockRows, last = g.row0[g.n] / kLossBlockRows;
     for (int block = first + blockIdx.x; block < last; block += gridDim.x) {
         const int row = block * kLossBlockRows + lane, i = rank_of(g, block * kLossBlockRows);
@@ -306,33 +307,26 @@ __global__ void __launch_bounds__(32 * kCombineWarps) k_combine(const __grid_con
         }
         // eight units' loads at a time, none of which waits for another
         float m = -INFINITY, s = 0.f, s2 = 0.f;
-        for (int u0 = warp; valid && u0 < c.units; u0 += 8 * kCombineWarps) {
-            float4 p[8];
+        const Part* mine = reinterpret_cast<const Part*>(c.partial) + min(row, (int)c.rows - 1);
+        for (int u0 = warp; u0 < c.units; u0 += 8 * kCombineWarps) {
+            Part p[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) p[e] = mine[min(u0 + e * kCombineWarps, c.units - 1) * c.rows];
             float top = m;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const int u = u0 + e * kCombineWarps;
-                p[e] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
-                if (u < c.units) {
-                    const int64_t at = (int64_t)u * c.rows + row;
-                    if (TWO) {
-                        p[e] = reinterpret_cast<const float4*>(c.partial)[at];
-                    } else {
-                        const float2 q = reinterpret_cast<const float2*>(c.partial)[at];
-                        p[e].x = q.x;
-                        p[e].y = q.y;
-                    }
-                }
+                if (u0 + e * kCombineWarps >= c.units) p[e].x = -INFINITY;
+                top = fmaxf(top, p[e].x);
             }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) top = fmaxf(top, p[e].x);
             const float ref = top == -INFINITY ? 0.f : top;
             s *= exp2f((m - ref) * k1);
-            s2 *= exp2f((m - ref) * k2);
+            if constexpr (TWO) s2 *= exp2f((m - ref) * k2);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                s += p[e].y * exp2f((p[e].x - ref) * k1);
-                if (TWO) s2 += p[e].z * exp2f((p[e].x - ref) * k2);
+                // a unit of nothing but -infinity, or none: no terms
+                const bool none = p[e].x == -INFINITY;
+                s += none ? 0.f : p[e].y * exp2f((p[e].x - ref) * k1);
+                if constexpr (TWO) s2 += none ? 0.f : p[e].z * exp2f((p[e].x - ref) * k2);
             }
             m = top;
         }
@@ -348,7 +342,8 @@ __global__ void __launch_bounds__(32 * kCombineWarps) k_combine(const __grid_con
             const float part = tops[lane][warp], top = warp_max(part), ref = top == -INFINITY ? 0.f : top;
             const float sum = warp_sum(sums[lane][warp] * exp2f((part - ref) * k1));
             const float sum2 = TWO ? warp_sum(sums2[lane][warp] * exp2f((part - ref) * k2)) : 0.f;
-            const float a = top * (TWO ? 1.f : c.inv_temperature) + logf(sum), b = TWO ? top * c.inv_temperature + logf(sum2) : a;
+            const float logit = c.unit * top;
+            const float a = logit * (TWO ? 1.f : c.inv_temperature) + logf(sum), b = TWO ? logit * c.inv_temperature + logf(sum2) : a;
             if (c.value && lane == 0) {
                 float4 coef = make_float4(a * kLog2e, factor, 0.f, 0.f);
                 if (TWO) {
@@ -451,7 +446,7 @@ __global__ void __launch_bounds__(kThreads) k_convert(const __grid_constant__ Lo
     pdl_release();
     pdl_acquire();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const float k1 = TWO ? kLog2e : c.inv_temperature * kLog2e, k2 = c.inv_temperature * kLog2e;
+    const float k1 = c.unit * (TWO ? kLog2e : c.inv_temperature * kLog2e), k2 = c.unit * (c.inv_temperature * kLog2e);
     const bool flat = TWO && k2 < k1;                  // the second softmax's were kept
     const float r = TWO ? (flat ? k1 / k2 : k2 / k1) : 1.f;
     const int64_t parts = (width + kConvertColumns - 1) / kConvertColumns;

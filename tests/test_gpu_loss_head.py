@@ -66,7 +66,8 @@ class Run:
 
 SIZES = [([1], 100, 32), ([1], 1, 8), ([3], 2, 1), ([16, 7], 100, 32), ([128], 256, 64), ([129], 257, 65), ([130, 1, 64], 513, 96),
          ([300], 1000, 256), ([257, 300], 391, 515), ([40], 5003, 7), ([33], 127, 1000), ([1], 20000, 3), ([2, 1], 1030, 64),
-         ([3], 1, 20000), ([0, 5], 700, 40), ([256], 256, 256), ([512, 1024], 129, 72), ([250], 3000, 520)]
+         ([3], 1, 20000), ([0, 5], 700, 40), ([256], 256, 256), ([512, 1024], 129, 72), ([250], 3000, 520), ([2500], 4500, 24),
+         ([4200], 300, 21)]
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
