@@ -143,7 +143,8 @@ int32_t check_head(int32_t world, int32_t vocab, int32_t dim, int32_t dtype, int
     if (st) return st;
     if (vocab < 1 || dim < 1 || max_tokens < 1 || max_teacher < 0) return DDP_ERR_INVALID;
     if (vocab > DDP_MAX_VOCAB || dim > DDP_MAX_DIM || max_teacher > DDP_MAX_TEACHER ||
-        world * round_up(max_tokens, kLossRowAlign) > ((int64_t)1 << 28))
+        world * round_up(max_tokens, kLossRowAlign) > ((int64_t)1 << 28) ||
+        world * round_up(max_tokens, kLossRowAlign) / kTileM * ((vocab + kTileN - 1) / kTileN) > ((int64_t)1 << 30))   // tiles
         return DDP_ERR_CAPACITY;
     return DDP_OK;
 }

@@ -811,8 +811,8 @@ int32_t ddp_adamw_destroy(ddp_adamw* adamw);
  *   grads[world]         host table, gradients of the same shape and type; NULL: the
  *                        ..._grad calls are refused.  No two may overlap
  *   vocab, dim           1 .. DDP_MAX_VOCAB, 1 .. DDP_MAX_DIM
- *   max_tokens           most tokens of a rank that a call may have (1 or more; with
- *                        world up to 2^28 together)
+ *   max_tokens           most tokens of a rank that a call may have (1 or more; all
+ *                        ranks' up to 2^28, and up to 2^45 logits)
  *   max_teacher          most entries a token's teacher may have, 0 (no distillation)
  *                        .. DDP_MAX_TEACHER
  *   workspace            device memory, 256-byte aligned, of at least
