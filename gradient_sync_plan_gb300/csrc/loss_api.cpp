@@ -398,13 +398,16 @@ int32_t run(ddp_loss_head* h, const Args& a, cudaStream_t stream) {
     m.c = c;
     m.limit_ns = std::max(wait_limit_ns(), 2000000000ull);
     m.accumulate = a.accumulate;
-    // a pair's tiles are 256 rows: 3/4 of them and more hold tokens there
+    // A pair's tiles are 256 rows, 3/4 of which at least should hold tokens; below some rows its fewer, larger tiles fill
+    // the SMs worse.  Single blocks and pairs, in us, decoder's head (50257 x 1024, bf16): with gradients 256 tokens 172
+    // and 209, 600 213 and 220, 1000 290 and 271, 2048 499 and 449; losses alone 256 43 and 37, 300 49 and 51, 600 61 and
+    // 63, 1000 81 and 76.
     int64_t tokens = 0, pair_rows = 0;
     for (int32_t r = 0; r < h->world; ++r) {
         tokens += a.tokens[r];
         pair_rows += round_up(a.tokens[r], 2 * kTileM);
     }
-    m.pairs = 4 * tokens >= 3 * pair_rows && cap_ctas(2) == 2;
+    m.pairs = 4 * tokens >= 3 * pair_rows && (tokens >= 768 || (!a.grad && pair_rows == 2 * kTileM)) && cap_ctas(2) == 2;
     const int cg = m.pairs ? 2 : 1;
     CUtensorMap hidden[2];                 // along, across
     if ((st = map_along(&hidden[0], c.gathered, c.dimp, c.rows, c.planes, kTileM)) ||

@@ -544,51 +544,62 @@ __global__ void __launch_bounds__(kThreads) k_convert(const __grid_constant__ Lo
 }
 
 // ---- hidden states' gradients --------------------------------------------------------
-template <bool F32>
-__global__ void __launch_bounds__(kThreads) k_join(const __grid_constant__ LossGroup g, const __grid_constant__ LossCall c, int splits) {
+// A warp takes 128 * kSteps columns of a token and adds their splits in order.  Few splits come with many tokens: four
+// runs of columns at a time then; many splits with few tokens: eight splits' loads at a time (38 splits of 64 tokens by
+// 1024, 10 MB: 56 us one split after another, 9 so).
+template <bool F32, bool MANY>
+__global__ void __launch_bounds__(kThreads) k_join(const __grid_constant__ LossGroup g, const __grid_constant__ LossCall c, int splits,
+                                                   int parts) {
+    constexpr int kSteps = MANY ? 1 : 4, kSplits = MANY ? 8 : 1;
     pdl_release();
     pdl_acquire();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int first = g.row0[0], last = g.row0[g.n];
-    for (int at = first + blockIdx.x * kWarps + warp; at < last; at += gridDim.x * kWarps) {
-        const int i = rank_of(g, at), t = at - g.row0[i];
+    const int first = g.row0[0];
+    const int64_t items = (int64_t)(g.row0[g.n] - first) * parts;
+    for (int64_t item = (int64_t)blockIdx.x * kWarps + warp; item < items; item += (int64_t)gridDim.x * kWarps) {
+        const int at = first + (int)(item / parts), i = rank_of(g, at), t = at - g.row0[i];
         if (t >= g.tokens[i]) continue;
-        const int r = c.token_row[at];
+        const int r = c.token_row[at], x0 = (int)(item % parts) * 128 * kSteps + lane * 4;
         char* out = static_cast<char*>(g.grad_hidden[i]) + (int64_t)t * c.dim * (F32 ? 4 : 2);
         const bool vec = ((uintptr_t)g.grad_hidden[i] | (uintptr_t)(c.dim * (F32 ? 4 : 2))) % (F32 ? 16 : 8) == 0;
-        constexpr int kSteps = 4;                      // columns' loads at a time
-        for (int x0 = lane * 4; x0 < c.dim; x0 += 128 * kSteps) {
-            float4 v[kSteps] = {};
-            if (r >= 0) {
-                const float* p = c.acc + ((int64_t)g.row0[i] + r) * c.dimp + x0;
-                for (int s = 0; s < splits; ++s, p += c.rows * c.dimp)
+        float4 v[kSteps] = {};
+        if (r >= 0 && x0 < c.dim) {
+            const float* p = c.acc + ((int64_t)g.row0[i] + r) * c.dimp + x0;
+            const int64_t step = c.rows * c.dimp;
+            for (int s0 = 0; s0 < splits; s0 += kSplits) {
+                float4 q[kSplits][kSteps];
+#pragma unroll
+                for (int s = 0; s < kSplits; ++s)
 #pragma unroll
                     for (int j = 0; j < kSteps; ++j)
-                        if (x0 + j * 128 < c.dim) {
-                            const float4 q = *reinterpret_cast<const float4*>(p + j * 128);
-                            v[j] = make_float4(v[j].x + q.x, v[j].y + q.y, v[j].z + q.z, v[j].w + q.w);
-                        }
+                        if (x0 + j * 128 < c.dim) q[s][j] = *reinterpret_cast<const float4*>(p + min(s0 + s, splits - 1) * step + j * 128);
+#pragma unroll
+                for (int s = 0; s < kSplits; ++s)
+#pragma unroll
+                    for (int j = 0; j < kSteps; ++j)
+                        if (s0 + s < splits && x0 + j * 128 < c.dim)
+                            v[j] = make_float4(v[j].x + q[s][j].x, v[j].y + q[s][j].y, v[j].z + q[s][j].z, v[j].w + q[s][j].w);
             }
+        }
 #pragma unroll
-            for (int j = 0; j < kSteps; ++j) {
-                const int x = x0 + j * 128;
-                if (x >= c.dim) break;
-                const float e[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
-                if (F32) {
-                    float* o = reinterpret_cast<float*>(out) + x;
-                    if (vec) *reinterpret_cast<float4*>(o) = v[j];
-                    else
+        for (int j = 0; j < kSteps; ++j) {
+            const int x = x0 + j * 128;
+            if (x >= c.dim) break;
+            const float e[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+            if (F32) {
+                float* o = reinterpret_cast<float*>(out) + x;
+                if (vec) *reinterpret_cast<float4*>(o) = v[j];
+                else
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            if (x + k < c.dim) o[k] = e[k];
-                } else {
-                    uint16_t* o = reinterpret_cast<uint16_t*>(out) + x;
-                    if (vec) *reinterpret_cast<uint2*>(o) = make_uint2(bf16x2_rn(e[0], e[1]), bf16x2_rn(e[2], e[3]));
-                    else
+                    for (int k = 0; k < 4; ++k)
+                        if (x + k < c.dim) o[k] = e[k];
+            } else {
+                uint16_t* o = reinterpret_cast<uint16_t*>(out) + x;
+                if (vec) *reinterpret_cast<uint2*>(o) = make_uint2(bf16x2_rn(e[0], e[1]), bf16x2_rn(e[2], e[3]));
+                else
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            if (x + k < c.dim) o[k] = f32_to_bf16_rn(e[k]);
-                }
+                    for (int k = 0; k < 4; ++k)
+                        if (x + k < c.dim) o[k] = f32_to_bf16_rn(e[k]);
             }
         }
     }
@@ -634,8 +645,12 @@ cudaError_t launch_loss_convert(const LossGroup& g, const LossCall& c, const voi
 }
 
 cudaError_t launch_loss_join(const LossGroup& g, const LossCall& c, int splits, cudaStream_t stream) {
-    return launch_dependent(c.dtype == DDP_F32 ? k_join<true> : k_join<false>, dim3(warp_grid(g.row0[g.n] - g.row0[0])),
-                            dim3(kThreads), 0, stream, g, c, splits);
+    const bool many = splits > 4;
+    const int parts = (c.dim + (many ? 127 : 511)) / (many ? 128 : 512);
+    const auto kernel = c.dtype == DDP_F32 ? (many ? k_join<true, true> : k_join<true, false>)
+                                           : (many ? k_join<false, true> : k_join<false, false>);
+    return launch_dependent(kernel, dim3(warp_grid((int64_t)(g.row0[g.n] - g.row0[0]) * parts)), dim3(kThreads), 0, stream, g, c,
+                            splits, parts);
 }
 
 }  // namespace ddpk

@@ -87,7 +87,7 @@ def test_cross_entropy_gradients(tokens, vocab, dim, dtype):
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("temperature,alpha,targets", [(1.0, 1.0, False), (2.0, 1.0, False), (1.0, 0.3, True), (2.5, 0.7, True),
                                                        (0.5, 1.0, True), (0.4, 0.5, True), (9.0, 0.5, True)])
-@pytest.mark.parametrize("tokens,vocab,dim,k", [([5], 40, 32, 1), ([16, 7], 100, 32, 8), ([130, 200], 777, 128, 64), ([500, 256], 515, 72, 20),
+@pytest.mark.parametrize("tokens,vocab,dim,k", [([5], 40, 32, 1), ([16, 7], 100, 32, 8), ([130, 200], 777, 128, 64), ([500, 512], 515, 72, 20),
                                                 ([64], 300, 66, 256), ([3, 1], 1100, 64, 5)])
 def test_distillation(tokens, vocab, dim, k, temperature, alpha, targets, dtype):
     x = _inputs(tokens, vocab, dim, dtype, ignored=0.2 if targets else 0.0, seed=k + dim, teacher=k)
@@ -99,7 +99,7 @@ def test_distillation(tokens, vocab, dim, k, temperature, alpha, targets, dtype)
 
 
 SMALL, TILES = ([16, 7], 100, 32), ([130, 40], 777, 128)      # one launch; the tensor cores' kernels
-PAIRS = ([256, 500], 777, 200)                                # whose blocks work in pairs
+PAIRS = ([512, 500], 777, 200)                                # whose blocks work in pairs
 BOTH = pytest.mark.parametrize("tokens,vocab,dim", [SMALL, TILES, PAIRS])
 TYPES = pytest.mark.parametrize("dtype", [BF16, F32])
 
