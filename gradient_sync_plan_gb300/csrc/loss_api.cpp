@@ -58,7 +58,7 @@ int64_t piece_width(int64_t bytes, int64_t rows, int64_t vocab, int64_t planes) 
 }
 
 struct Sizes {
-    int64_t counts, done, row_token, token_row, row_column, valid, columns, starts, share, entropy, z, value, partial, coef,
+    int64_t counts, factor, done, row_token, token_row, row_column, valid, columns, starts, share, entropy, z, value, partial, coef,
         block_loss, gathered, acc, kept, piece, weights;    // offsets
     int64_t keep_rows;                            // rows of a group whose exponentials are kept
     int64_t acc_bytes, piece_bytes, weights_bytes, total;
@@ -102,6 +102,7 @@ Sizes layout(int64_t world, int64_t vocab, int64_t dim, int32_t dtype, int64_t m
         at += round_up(bytes, 256);
     };
     put(&s.counts, 4 * world);
+    put(&s.factor, 4 * world);
     put(&s.done, 12);
     put(&s.row_token, 4 * rows);
     put(&s.token_row, 4 * rows);
@@ -324,6 +325,7 @@ int32_t run(ddp_loss_head* h, const Args& a, cudaStream_t stream) {
     char* w = h->workspace;
     const Sizes& at = h->at;
     c.counts = reinterpret_cast<int32_t*>(w + at.counts);
+    c.factor = reinterpret_cast<float*>(w + at.factor);
     c.done = reinterpret_cast<int32_t*>(w + at.done);
     c.next = c.done + 1;
     c.row_token = reinterpret_cast<int32_t*>(w + at.row_token);
@@ -401,13 +403,14 @@ int32_t run(ddp_loss_head* h, const Args& a, cudaStream_t stream) {
     // A pair's tiles are 256 rows, 3/4 of which at least should hold tokens; below some rows its fewer, larger tiles fill
     // the SMs worse.  Single blocks and pairs, in us, decoder's head (50257 x 1024, bf16): with gradients 256 tokens 172
     // and 209, 600 213 and 220, 1000 290 and 271, 2048 499 and 449; losses alone 256 43 and 37, 300 49 and 51, 600 61 and
-    // 63, 1000 81 and 76.
+    // 63, 1000 81 and 76.  bf16 only: pairs with float32's parts of the depth did not always finish.
     int64_t tokens = 0, pair_rows = 0;
     for (int32_t r = 0; r < h->world; ++r) {
         tokens += a.tokens[r];
         pair_rows += round_up(a.tokens[r], 2 * kTileM);
     }
-    m.pairs = 4 * tokens >= 3 * pair_rows && (tokens >= 768 || (!a.grad && pair_rows == 2 * kTileM)) && cap_ctas(2) == 2;
+    m.pairs = 4 * tokens >= 3 * pair_rows && (tokens >= 768 || (!a.grad && pair_rows == 2 * kTileM)) &&
+              h->dtype == DDP_BF16 && cap_ctas(2) == 2;
     const int cg = m.pairs ? 2 : 1;
     CUtensorMap hidden[2];                 // along, across
     if ((st = map_along(&hidden[0], c.gathered, c.dimp, c.rows, c.planes, kTileM)) ||

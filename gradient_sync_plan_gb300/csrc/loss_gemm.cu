@@ -9,8 +9,10 @@
 //   kKeep      the same, and the exponentials themselves in 16 bits, where those of
 //              all columns have room; a pass of its own makes dz of them;
 //   kGrad      where they have not: z again, piece by piece, and
-//              dz = f (softmax(z) - target), bf16;
-//   kProducts  dh += dz w (over the piece's columns) and dw = dz^T h (over T).
+//              dz = softmax(z) - target, bf16;
+//   kProducts  dh += dz w (over the piece's columns) and dw = f dz^T h (over T).
+// The factor f (scale and reduction) stays out of dz: a target's dz lies just above -1, where bf16 is off by 2^-9 of it at
+// most; times an arbitrary f it could be off by twice that, and by the same in every row.
 // Both operands of kProducts are read as they lie in memory: the tensor cores
 // take matrices whose rows run along the depth or across it.
 //
@@ -76,6 +78,7 @@ struct Control {
     int32_t stop;
     int32_t go[2][2];                                  // by group and accumulators: the tile is there
     int32_t counts[kLossRanks];
+    float factors[kLossRanks];
 };
 constexpr int kStageBytes = 192 * 1024;
 static_assert(Shape<1>::kStages * Shape<1>::kBytesStage == kStageBytes && Shape<2>::kStages * Shape<2>::kBytesStage == kStageBytes,
@@ -807,15 +810,12 @@ __device__ __forceinline__ void grad_tile(const LossGemm& g, const Tile& w, cons
     }
 }
 
-// What a sum lost where the tensor cores cut it (kCutPerStep), for results in float32; of the six passes the last
-// adds what counts.
-template <bool F32, int N>
-__device__ __forceinline__ void uncut(float (&v)[N], const Tile& w) {
-    if constexpr (F32) {
-        const float f = 1.f + kCutPerStep * (float)((w.k1 - w.k0) * (kTileK / 16));
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] *= f;
-    }
+// A gradient's factor, and what its sum lost where the tensor cores cut it (kCutPerStep) if the result is float32; of
+// the six passes the last adds what counts.
+template <bool F32>
+__device__ __forceinline__ float factor_of(const Tile& w, const Control* s) {
+    const float f = s->factors[w.rank];
+    return F32 ? f + f * (kCutPerStep * (float)((w.k1 - w.k0) * (kTileK / 16))) : f;
 }
 
 // dh: the tile goes to its split's part of acc, added there by the copy engine from the second piece on (one
@@ -853,8 +853,9 @@ __device__ __forceinline__ void hidden_tile(const LossGemm& g, const Tile& w, co
 // dw: rows of the weights' gradients, rounded once.  Where rows start on 16-byte boundaries the copy engine writes
 // them; else, and to add to what is there, a warp goes row by row, a lane a column.
 template <bool F32, int CG>
-__device__ __forceinline__ void weights_tile(const LossGemm& g, const Tile& w, const Lane& l, uint64_t* taken) {
+__device__ __forceinline__ void weights_tile(const LossGemm& g, const Tile& w, const Lane& l, const Control* s, uint64_t* taken) {
     const LossCall& c = g.c;
+    const float f = factor_of<F32>(w, s);
     const bool none = w.k1 <= w.k0;                    // a rank without learned tokens
     constexpr int kColumns = F32 ? 32 : 64;            // of 128 bytes
     if (g.store) {
@@ -870,11 +871,8 @@ __device__ __forceinline__ void weights_tile(const LossGemm& g, const Tile& w, c
             }
             const int col = w.n + l.group * (kTileN / 2) + j * kColumns;
             if (col >= c.dim) continue;                // the same for the whole group
-            if (none) {
 #pragma unroll
-                for (int i = 0; i < kColumns; ++i) v[i] = 0.f;
-            }
-            uncut<F32>(v, w);
+            for (int i = 0; i < kColumns; ++i) v[i] = none ? 0.f : f * v[i];
             if (l.leader) {
                 if (F32 && w.more()) tma_all_done();
                 else tma_read_done();
@@ -914,11 +912,8 @@ __device__ __forceinline__ void weights_tile(const LossGemm& g, const Tile& w, c
         }
         const int col = w.n + l.group * (kTileN / 2) + j * 32;
         if (col >= c.dim) continue;
-        if (none) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 0.f;
-        }
-        uncut<F32>(v, w);
+        for (int i = 0; i < 32; ++i) v[i] = none ? 0.f : f * v[i];
         __syncwarp();
         stage_floats(l, v);
         __syncwarp();
@@ -926,24 +921,24 @@ __device__ __forceinline__ void weights_tile(const LossGemm& g, const Tile& w, c
         if (x >= c.dim) continue;
         constexpr int kRows = 8;                       // rows' loads at a time
         for (int i0 = 0; i0 < rows; i0 += kRows) {
-            float f[kRows];
+            float x32[kRows];
             const int64_t at = (int64_t)(v0 + i0) * c.dim + x;
             float* out32 = static_cast<float*>(g.grads[w.rank]) + at;
             uint16_t* out16 = static_cast<uint16_t*>(g.grads[w.rank]) + at;
 #pragma unroll
             for (int i = 0; i < kRows; ++i)
-                f[i] = *reinterpret_cast<const float*>(l.staging + (l.quarter * 32 + i0 + i) * 128 +
+                x32[i] = *reinterpret_cast<const float*>(l.staging + (l.quarter * 32 + i0 + i) * 128 +
                                                        (((l.lane >> 2) ^ ((i0 + i) & 7)) << 4) + (l.lane & 3) * 4);
             if (g.accumulate || (F32 && w.more())) {
 #pragma unroll
                 for (int i = 0; i < kRows; ++i)
-                    if (i0 + i < rows) f[i] += F32 ? out32[(int64_t)i * c.dim] : bf16_to_f32(out16[(int64_t)i * c.dim]);
+                    if (i0 + i < rows) x32[i] += F32 ? out32[(int64_t)i * c.dim] : bf16_to_f32(out16[(int64_t)i * c.dim]);
             }
 #pragma unroll
             for (int i = 0; i < kRows; ++i)
                 if (i0 + i < rows) {
-                    if (F32) out32[(int64_t)i * c.dim] = f[i];
-                    else out16[(int64_t)i * c.dim] = f32_to_bf16_rn(f[i]);
+                    if (F32) out32[(int64_t)i * c.dim] = x32[i];
+                    else out16[(int64_t)i * c.dim] = f32_to_bf16_rn(x32[i]);
                 }
         }
     }
@@ -988,7 +983,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_loss_gemm(const __grid_cons
         }
     }
     pdl_acquire();
-    if (threadIdx.x < g.n) s->counts[threadIdx.x] = g.c.counts[g.first + threadIdx.x];
+    if (threadIdx.x < g.n) {
+        s->counts[threadIdx.x] = g.c.counts[g.first + threadIdx.x];
+        if (PHASE == LossPhase::kProducts) s->factors[threadIdx.x] = g.c.factor[g.first + threadIdx.x];
+    }
     fence_before();
     __syncthreads();
     if constexpr (CG == 2) cluster_sync();             // the other block's barriers are there
@@ -1040,7 +1038,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_loss_gemm(const __grid_cons
                 stats_tile<F32, TWO, LIST, PHASE == LossPhase::kKeep, CG>(g, w, l, s, taken);
             else if (PHASE == LossPhase::kGrad) grad_tile<F32, TWO, LIST, CG>(g, w, l, s, taken);
             else if (!w.weights()) hidden_tile(g, w, l, taken);
-            else weights_tile<F32, CG>(g, w, l, taken);
+            else weights_tile<F32, CG>(g, w, l, s, taken);
             if (buf == 1) phase ^= 1;
             buf ^= 1;
         }
@@ -1095,7 +1093,9 @@ int64_t tile_count(LossPhase phase, const LossGemm& g, int cg) {
 
 template <LossPhase PHASE, bool F32, bool TWO, bool LIST>
 cudaError_t launch_shape(const LossGemm& g, cudaStream_t stream) {
-    if (g.pairs) return launch<PHASE, F32, TWO, LIST, 2>(g, tile_count(PHASE, g, 2), stream);
+    if constexpr (!F32) {                  // float32's parts of the depth stay on single blocks (the call chooses so)
+        if (g.pairs) return launch<PHASE, F32, TWO, LIST, 2>(g, tile_count(PHASE, g, 2), stream);
+    }
     return launch<PHASE, F32, TWO, LIST, 1>(g, tile_count(PHASE, g, 1), stream);
 }
 

@@ -67,9 +67,10 @@ struct LossCall {
     float* share;                         // [rows][list] by token: teacher's probability of the entry
     float* entropy;                       // [rows] by token: sum of q log q
     float* z;                             // [rows][list] logits at the listed columns
-    float* value;                         // [rows][list] gradients there
+    float* value;                         // [rows][list] gradients there, without the factor
     float* partial;                       // [units][rows] float2, or float4 for two temperatures
-    float4* coef;                         // [rows] {lse, factor, lse at the temperature, its factor}, lse in bits (log2)
+    float* factor;                        // [world] of the gradients: scale and reduction
+    float4* coef;                         // [rows] {lse, share, lse at the temperature, its share}, lse in bits (log2)
     double* block_loss;                   // [rows / kLossBlockRows]
     void* gathered;                       // [planes][rows][dimp] bf16
     float* acc;                           // [splits][rows][dimp]

@@ -334,8 +334,6 @@ __global__ void __launch_bounds__(32 * kCombineWarps) k_combine(const __grid_con
         sums[warp][lane] = s;
         sums2[warp][lane] = s2;
         __syncthreads();
-        const double f = c.reduction == DDP_LOSS_SUM ? 1.0 : c.reduction == DDP_LOSS_MEAN ? 1.0 / count : (double)g.world / total;
-        const float factor = (float)(f * c.scale);
         // a warp a row
         const int rr = block * kLossBlockRows + warp;
         if (rr - g.row0[i] < count) {
@@ -345,13 +343,13 @@ __global__ void __launch_bounds__(32 * kCombineWarps) k_combine(const __grid_con
             const float logit = c.unit * top;
             const float a = logit * (TWO ? 1.f : c.inv_temperature) + logf(sum), b = TWO ? logit * c.inv_temperature + logf(sum2) : a;
             if (c.value && lane == 0) {
-                float4 coef = make_float4(a * kLog2e, factor, 0.f, 0.f);
+                float4 coef = make_float4(a * kLog2e, 1.f, 0.f, 0.f);
                 if (TWO) {
-                    coef.y = (1.f - c.alpha) * factor;
+                    coef.y = 1.f - c.alpha;
                     coef.z = b * kLog2e;
-                    coef.w = c.alpha * c.temperature * factor;
+                    coef.w = c.alpha * c.temperature;
                 } else if (c.alpha != 0.f) {           // alpha 1, or temperature 1
-                    coef.y = (1.f - c.alpha + c.alpha * c.temperature) * factor;
+                    coef.y = 1.f - c.alpha + c.alpha * c.temperature;
                 }
                 c.coef[rr] = coef;
             }
@@ -359,7 +357,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) k_combine(const __grid_con
                 if (lane == 0) {
                     const float d = c.z[rr] - a;
                     losses[warp] = -d;
-                    if (c.value) c.value[rr] = factor * expm1f(d);
+                    if (c.value) c.value[rr] = expm1f(d);
                 }
             } else {
                 const int64_t token = g.row0[i] + c.row_token[rr], at = token * c.list;
@@ -382,7 +380,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) k_combine(const __grid_con
                     }
                     const float soft = c.alpha * c.temperature * (expf(z * c.inv_temperature - b) - shares);
                     const float label = c.alpha < 1.f ? (1.f - c.alpha) * (expf(z - a) - targets) : 0.f;
-                    c.value[at + e] = factor * (soft + label);
+                    c.value[at + e] = soft + label;
                 }
                 cross = warp_sum(cross);
                 hard = warp_sum(hard);
@@ -417,13 +415,14 @@ __global__ void __launch_bounds__(32 * kCombineWarps) k_combine(const __grid_con
         if (lane == 0) {
             const double f = c.reduction == DDP_LOSS_SUM ? 1.0 : c.reduction == DDP_LOSS_MEAN ? 1.0 / count : (double)g.world / total;
             loss[g.first + i] = count > 0 ? (float)(sum * f) : 0.f;
+            if (c.value) c.factor[g.first + i] = count > 0 ? (float)(f * c.scale) : 0.f;
         }
     }
     if (threadIdx.x == 0) *c.done = 0;     // for the next group's launch
 }
 
 // ---- kept exponentials to the logits' gradients ---------------------------------------
-// dz = f e 2^(reference - lse): what the products' own epilogue computes where exponentials are not kept, from 11 bits
+// dz / f = e 2^(reference - lse): what the products' own epilogue computes where exponentials are not kept, from 11 bits
 // of them for bf16 operands and all for float32.  Of two softmaxes the flatter one's exponentials x are kept; the other's
 // are x^r with r <= kKeepPower, which multiplies their rounding by r.  A warp takes kConvertColumns columns of a row.
 // Memory bound: 8 x 1024 x 50257 bf16, 1.65 GB read and written, in 0.24 ms.
@@ -563,6 +562,7 @@ __global__ void __launch_bounds__(kThreads) k_join(const __grid_constant__ LossG
         char* out = static_cast<char*>(g.grad_hidden[i]) + (int64_t)t * c.dim * (F32 ? 4 : 2);
         const bool vec = ((uintptr_t)g.grad_hidden[i] | (uintptr_t)(c.dim * (F32 ? 4 : 2))) % (F32 ? 16 : 8) == 0;
         float4 v[kSteps] = {};
+        const float f = c.factor[g.first + i];
         if (r >= 0 && x0 < c.dim) {
             const float* p = c.acc + ((int64_t)g.row0[i] + r) * c.dimp + x0;
             const int64_t step = c.rows * c.dimp;
@@ -585,10 +585,10 @@ __global__ void __launch_bounds__(kThreads) k_join(const __grid_constant__ LossG
         for (int j = 0; j < kSteps; ++j) {
             const int x = x0 + j * 128;
             if (x >= c.dim) break;
-            const float e[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+            const float e[4] = {f * v[j].x, f * v[j].y, f * v[j].z, f * v[j].w};
             if (F32) {
                 float* o = reinterpret_cast<float*>(out) + x;
-                if (vec) *reinterpret_cast<float4*>(o) = v[j];
+                if (vec) *reinterpret_cast<float4*>(o) = make_float4(e[0], e[1], e[2], e[3]);
                 else
 #pragma unroll
                     for (int k = 0; k < 4; ++k)

@@ -144,14 +144,21 @@ __global__ void __launch_bounds__(kSmallThreads) k_small(const __grid_constant__
             top = all_lanes_max(top);
             const float ref = top == -INFINITY ? 0.f : top;
             const bool hard = c.alpha < 1.f, soft = c.alpha != 0.f;
-            float s1 = 0.f, s2 = 0.f;
+            // the largest terms are ones, counted apart: a confident token's sum is 1 and little more
+            float s1 = 0.f, s2 = 0.f, ones = 0.f;
             for (int v = lane; v < c.vocab; v += 32) {
+                if (z[v] == ref) {
+                    ones += 1.f;
+                    continue;
+                }
                 if (hard) s1 += expf(z[v] - ref);
                 if (soft) s2 += expf((z[v] - ref) * c.inv_temperature);
             }
+            ones = all_lanes_sum(ones);
             s1 = all_lanes_sum(s1);
             s2 = all_lanes_sum(s2);
-            const float lse1 = ref + logf(s1), lse2 = ref * c.inv_temperature + logf(s2);
+            const auto log_of = [&](float rest) { return ones == 1.f ? log1pf(rest) : logf(ones + rest); };
+            const float lse1 = ref + log_of(s1), lse2 = ref * c.inv_temperature + log_of(s2);
             const int y = hard ? (int)g.targets[i][t] : 0;
             float result = hard ? (1.f - c.alpha) * (lse1 - z[y]) : 0.f;
             const float a = hard ? (1.f - c.alpha) : 0.f, b = c.alpha * c.temperature;

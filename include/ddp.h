@@ -764,10 +764,12 @@ int32_t ddp_adamw_destroy(ddp_adamw* adamw);
 /*
  * ddp_loss_head -- where a step's gradients begin: the loss of every rank's tokens
  * over a vocabulary, and its gradients, from the hidden states before the head
- * projection and the head's weights.  The logits are never kept: they are computed
- * in tiles on the tensor cores, and of a tile only its rows' softmax statistics
- * leave the SM; the gradients go through the vocabulary in pieces that fit the
- * workspace.
+ * projection and the head's weights.  Logits are not kept: they are computed in
+ * tiles on the tensor cores, and a tile leaves its rows' softmax statistics.  For
+ * gradients it also leaves its exponentials in the workspace, in 16 bits (32 for
+ * float32), while those of a rank's tokens by the vocabulary take no more than 2
+ * GiB; beyond that the gradients go through the vocabulary in pieces and compute
+ * the logits again.
  *
  * Rank r has tokens[r] tokens, h_t its hidden states and w_j its weights' rows:
  *     z_tj = h_t . w_j      p = softmax(z_t)      u = z_t / temperature
