@@ -25,6 +25,10 @@
 // significand each); of the nine products of planes the six larger are summed,
 // smallest first: what is left out is below 2^-24 of the terms.
 //
+// Bound by the tensor cores and, in long runs, by power: 8 x 1024 tokens by 50257 x 1024 take 0.50 ms for the logits and
+// 1.01 ms for the products (1.68 PFLOP/s both), 4096 by 131072 x 4096 2.49 and 5.11 ms (1.77 and 1.72).  Tiles are as large
+// as two of them fit tensor memory: 128 x 256 a block, or 256 x 256 a pair, whose blocks load half of B each.
+//
 // All waits are bounded: one that runs out sets DDP_ERR_TIMEOUT in the device
 // status word, the block's roles stop, loads in flight and products are waited
 // for, and tensor memory is freed.
