@@ -73,7 +73,7 @@ struct ddp_loss_head {
     char* workspace = nullptr;
     Sizes at{};
     std::vector<std::pair<uintptr_t, uintptr_t>> read, written;    // the weights; the workspace and the gradients
-    std::vector<CUtensorMap> maps;                                 // of a rank's weights or planes: along and across, for single blocks and pairs
+    std::vector<CUtensorMap> maps;                                 // of a rank's weights or planes: along and across
     std::vector<CUtensorMap> outs;                                 // of the gradients
     bool stores = false;                                           // whose rows all start on 16-byte boundaries
     int64_t copied = 0;                                            // bytes of a rank's planes in the workspace, 0: none
@@ -210,14 +210,13 @@ int32_t bind_device(ddp_loss_head* h) {
     if (h->device >= 0) return device == h->device ? DDP_OK : DDP_ERR_INVALID;
     if ((st = cuda_status(device_status_address(&h->status)))) return st;
     const int64_t dimp = round_up(h->dim, kTileK), planes = planes_of(h->dtype);
-    h->maps.resize(4 * h->world);
+    h->maps.resize(2 * h->world);
     h->outs.resize(h->stores ? h->world : 0);
     for (int32_t r = 0; r < h->world; ++r) {
         const void* base = h->copied ? h->workspace + h->at.weights + r * h->copied : static_cast<const void*>(h->weights[r]);
-        for (int cg = 1; cg <= 2; ++cg)
-            if ((st = map_along(&h->maps[4 * r + 2 * (cg - 1)], base, dimp, h->vocab, planes, kTileN / cg)) ||
-                (st = map_across(&h->maps[4 * r + 2 * (cg - 1) + 1], base, dimp, h->vocab, planes, kTileN / cg)))
-                return st;
+        if ((st = map_along(&h->maps[2 * r], base, dimp, h->vocab, planes, kTileN)) ||
+            (st = map_across(&h->maps[2 * r + 1], base, dimp, h->vocab, planes, kTileN)))
+            return st;
         if (h->stores && (st = map_out(&h->outs[r], h->grads[r], h->dtype, h->dim, h->vocab))) return st;
     }
     h->device = device;
@@ -400,21 +399,9 @@ int32_t run(ddp_loss_head* h, const Args& a, cudaStream_t stream) {
     m.c = c;
     m.limit_ns = std::max(wait_limit_ns(), 2000000000ull);
     m.accumulate = a.accumulate;
-    // A pair's tiles are 256 rows, 3/4 of which at least should hold tokens; below some rows its fewer, larger tiles fill
-    // the SMs worse.  Single blocks and pairs, in us, decoder's head (50257 x 1024, bf16): with gradients 256 tokens 172
-    // and 209, 600 213 and 220, 1000 290 and 271, 2048 499 and 449; losses alone 256 43 and 37, 300 49 and 51, 600 61 and
-    // 63, 1000 81 and 76.  bf16 only: pairs with float32's parts of the depth did not always finish.
-    int64_t tokens = 0, pair_rows = 0;
-    for (int32_t r = 0; r < h->world; ++r) {
-        tokens += a.tokens[r];
-        pair_rows += round_up(a.tokens[r], 2 * kTileM);
-    }
-    m.pairs = 4 * tokens >= 3 * pair_rows && (tokens >= 768 || (!a.grad && pair_rows == 2 * kTileM)) &&
-              h->dtype == DDP_BF16 && cap_ctas(2) == 2;
-    const int cg = m.pairs ? 2 : 1;
     CUtensorMap hidden[2];                 // along, across
     if ((st = map_along(&hidden[0], c.gathered, c.dimp, c.rows, c.planes, kTileM)) ||
-        (st = map_across(&hidden[1], c.gathered, c.dimp, c.rows, c.planes, kTileN / cg)))
+        (st = map_across(&hidden[1], c.gathered, c.dimp, c.rows, c.planes, kTileN)))
         return st;
     if (a.grad) m.store = h->stores && !a.accumulate;
     for (const LossGroup& g : groups) {
@@ -441,7 +428,7 @@ int32_t run(ddp_loss_head* h, const Args& a, cudaStream_t stream) {
         }
         const auto operands = [&](bool across) {
             m.hidden = hidden[across];
-            for (int i = 0; i < g.n; ++i) m.weights[i] = h->maps[4 * (g.first + i) + 2 * (cg - 1) + across];
+            for (int i = 0; i < g.n; ++i) m.weights[i] = h->maps[2 * (g.first + i) + across];
         };
         operands(false);
         if (span > 0) {

@@ -27,11 +27,18 @@
 //
 // Bound by the tensor cores and, in long runs, by power: 8 x 1024 tokens by 50257 x 1024 take 0.50 ms for the logits and
 // 1.01 ms for the products (1.68 PFLOP/s both), 4096 by 131072 x 4096 2.49 and 5.11 ms (1.77 and 1.72).  Tiles are as large
-// as two of them fit tensor memory: 128 x 256 a block, or 256 x 256 a pair, whose blocks load half of B each.
+// as two of them fit tensor memory: 128 x 256.
 //
-// All waits are bounded: one that runs out sets DDP_ERR_TIMEOUT in the device
-// status word, the block's roles stop, loads in flight and products are waited
-// for, and tensor memory is freed.
+// Waits for loads, products, tiles and accumulators are bounded: one that runs
+// out sets DDP_ERR_TIMEOUT in the device status word, the block's roles stop,
+// loads in flight and products are waited for, and tensor memory is freed.  What
+// waits without a limit waits for nothing that can fail to come: a barrier of the
+// block or of a group's four warps, which all of them reach whatever has run out;
+// the copy engine's own stores; and tensor memory at the start, which no other
+// block of this kernel holds, for its shared memory leaves room for one an SM.
+// No block waits for another one.  Pairs of SMs on one tile (cta_group::2) did,
+// and were up to a tenth faster on large batches, but a float32 call in pairs
+// once did not finish and no cause was found.
 #include <algorithm>
 #include <mutex>
 #include <set>
@@ -43,14 +50,8 @@
 namespace ddpk {
 namespace {
 
-// CG blocks of a cluster work on one tile of CG * 128 rows: each has its rows of A and 1 / CG of B's columns.
-template <int CG>
-struct Shape {
-    static constexpr int kStages = CG == 2 ? 6 : 4;
-    static constexpr int kBytesA = kTileM * kTileK * 2, kBytesB = kTileN / CG * kTileK * 2;
-    static constexpr int kBytesStage = kBytesA + kBytesB;
-};
-constexpr int kMostStages = 6;
+constexpr int kStages = 4;
+constexpr int kBytesA = kTileM * kTileK * 2, kBytesB = kTileN * kTileK * 2, kBytesStage = kBytesA + kBytesB;
 constexpr int kBytesBox = 64 * 64 * 2;
 constexpr int kBytesStaging = 128 * 128;               // 128 rows of 128 bytes
 constexpr int kFirstEpilogueWarp = 4, kEpilogueWarps = 8;
@@ -59,7 +60,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kKeepScale = (float)(1 << kKeepBits);
 
 // A tile: rank (-1: no more tiles), first row (of all ranks' rows; a column of the piece for dw), first column, columns (of
-// the products: a multiple of 64 for each block), k blocks.
+// the products: a multiple of 64), k blocks.
 struct alignas(16) Tile {
     int32_t rank, m, n, columns, k0, k1, split;
     int32_t flags;
@@ -69,14 +70,13 @@ struct alignas(16) Tile {
 // float32 sums are taken out of tensor memory and added up elsewhere every so many k blocks: the tensor cores cut what they
 // add to a long sum (kCutPerStep), by 2e-5 of the result over a depth of 50257.
 constexpr int kMostDepth = 16;
-constexpr int kTileWords = sizeof(Tile) / 4;
 constexpr int kQueue = 4;
 
 struct Control {
-    Tile queue[kQueue], mail[kQueue];
-    uint64_t full[kMostStages], empty[kMostStages];
+    Tile queue[kQueue];
+    uint64_t full[kStages], empty[kStages];
     uint64_t ready[2], taken[2];                       // accumulators
-    uint64_t tile_full[kQueue], tile_empty[kQueue], mail_full[kQueue];
+    uint64_t tile_full[kQueue], tile_empty[kQueue];
     uint64_t drain;
     uint32_t tmem;
     int32_t stop;
@@ -84,11 +84,9 @@ struct Control {
     int32_t counts[kLossRanks];
     float factors[kLossRanks];
 };
-constexpr int kStageBytes = 192 * 1024;
-static_assert(Shape<1>::kStages * Shape<1>::kBytesStage == kStageBytes && Shape<2>::kStages * Shape<2>::kBytesStage == kStageBytes,
-              "stages of either shape");
-constexpr int kSmem = 1024 + kStageBytes + 2 * kBytesStaging + (int)sizeof(Control);
+constexpr int kSmem = 1024 + kStages * kBytesStage + 2 * kBytesStaging + (int)sizeof(Control);
 static_assert(kSmem <= 227 * 1024, "shared memory of a block");
+static_assert(2 * kSmem > 228 * 1024, "one block an SM: each takes all tensor memory");
 
 __device__ __forceinline__ uint32_t smem_of(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
@@ -101,46 +99,15 @@ __device__ __forceinline__ void bar_expect(uint64_t* b, uint32_t bytes) {
 __device__ __forceinline__ void bar_arrive(uint64_t* b) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_of(b)) : "memory");
 }
-// The address, in the cluster, of this block's `p` in the cluster's block `to`.
-__device__ __forceinline__ uint32_t in_block(const void* p, int to) {
-    uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_of(p)), "r"(to));
-    return a;
-}
-// An arrival at another block's barrier.  Its release at cluster scope takes about a thousand cycles: only threads that
-// nothing waits for in the meantime come here.
-__device__ __forceinline__ void arrive_at(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
 __device__ __forceinline__ void warp_arrive(uint64_t* b, int lane) {
     __syncwarp();
     if (lane == 0) bar_arrive(b);
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ int cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return (int)r;
 }
 __device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_of(b)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-// For what another block of the cluster has written: about two thousand cycles.
-__device__ __forceinline__ bool bar_try_cluster(uint64_t* b, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
         : "r"(smem_of(b)), "r"(parity)
@@ -165,12 +132,10 @@ __device__ __forceinline__ unsigned long long now_ns() {
     return t;
 }
 // At most limit_ns, or until another role of the block has given up; false then.
-template <bool CLUSTER = false>
 __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, Control* s, const LossGemm& g) {
-    const auto complete = [&] { return CLUSTER ? bar_try_cluster(b, parity) : bar_try(b, parity); };
-    if (complete()) return true;
+    if (bar_try(b, parity)) return true;
     const unsigned long long t0 = now_ns();
-    while (!complete()) {
+    while (!bar_try(b, parity)) {
         if (*(volatile int32_t*)&s->stop) return false;
         if (now_ns() - t0 > g.limit_ns) {
             *(volatile int32_t*)&s->stop = 1;
@@ -188,19 +153,11 @@ __device__ __forceinline__ void bar_wait_rest(uint64_t* b, uint32_t parity, cons
 }
 
 // A box of a matrix seen as [planes][columns / 64][rows][64], from column x (a multiple of 64) and row y.
-// bar: an address in the cluster (this block's own or, of a pair, the first's).
-template <int CG>
-__device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int x, int y, int plane, uint32_t bar) {
-    if constexpr (CG == 1)
-        asm volatile(
-            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
-            ::"r"(smem_of(dst)), "l"(map), "r"(0), "r"(y), "r"(x / 64), "r"(plane), "r"(bar)
-            : "memory");
-    else
-        asm volatile(
-            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
-            "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_of(dst)), "l"(map), "r"(0), "r"(y), "r"(x / 64), "r"(plane), "r"(bar)
-            : "memory");
+__device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int x, int y, int plane, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+        ::"r"(smem_of(dst)), "l"(map), "r"(0), "r"(y), "r"(x / 64), "r"(plane), "r"(smem_of(bar))
+        : "memory");
 }
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int x, int y) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map),
@@ -217,7 +174,11 @@ __device__ __forceinline__ void tma_read_done() { asm volatile("cp.async.bulk.wa
 __device__ __forceinline__ void tma_all_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void to_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-__device__ __forceinline__ void group_sync(int group) { asm volatile("bar.sync %0, 128;" ::"r"(group + 1) : "memory"); }
+// A group's four warps meet, each of them whole: one lane may come from work of its own.
+__device__ __forceinline__ void group_sync(int group) {
+    __syncwarp();
+    asm volatile("bar.sync %0, 128;" ::"r"(group + 1) : "memory");
+}
 
 // Shared-memory matrix descriptor: 128-byte swizzle, groups of 8 rows of 128 bytes
 // 1024 bytes apart; lbo: bytes between runs of 64 elements across the depth.
@@ -230,37 +191,23 @@ __device__ __forceinline__ uint32_t product_desc(bool a_across, bool b_across, i
     return (1u << 4) | (1u << 7) | (1u << 10) | ((a_across ? 1u : 0u) << 15) | ((b_across ? 1u : 0u) << 16) |
            ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
-template <int CG>
 __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
-    if constexpr (CG == 1)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(desc), "r"((uint32_t)add)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(desc), "r"((uint32_t)add)
-            : "memory");
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(desc), "r"((uint32_t)add)
+        : "memory");
 }
-// The products issued so far arrive at the barrier, of a pair at both blocks'.
-template <int CG>
+// The products issued so far arrive at the barrier.
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
-    if constexpr (CG == 1)
-        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_of(bar)) : "memory");
-    else
-        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-                         smem_of(bar)),
-                     "h"((uint16_t)3)
-                     : "memory");
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_of(bar)) : "memory");
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
 __device__ __forceinline__ void tmem_load(float* v, uint32_t addr) {
     uint32_t* r = reinterpret_cast<uint32_t*>(v);
+    __syncwarp();                          // the load takes the whole warp
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -287,12 +234,11 @@ template <LossPhase PHASE>
 __device__ __forceinline__ int phase_columns(const LossGemm& g) {
     return PHASE == LossPhase::kProducts ? g.c.dim : PHASE == LossPhase::kGrad ? g.width : g.c.vocab;
 }
-template <LossPhase PHASE, int CG>
+template <LossPhase PHASE>
 __device__ __forceinline__ bool find_tile(const LossGemm& g, const int32_t* counts, int t, Tile* w) {
-    constexpr int M = CG * kTileM;
     const int all = phase_columns<PHASE>(g), nt = ceil_div(all, kTileN);
     for (int i = 0; i < g.n; ++i) {
-        const int m = ceil_div(counts[i], M), n = m * nt * (PHASE == LossPhase::kProducts ? g.splits : 1);
+        const int m = ceil_div(counts[i], kTileM), n = m * nt * (PHASE == LossPhase::kProducts ? g.splits : 1);
         if (t >= n) {
             t -= n;
             continue;
@@ -301,24 +247,24 @@ __device__ __forceinline__ bool find_tile(const LossGemm& g, const int32_t* coun
         w->flags = 0;
         w->split = 0;
         if (PHASE != LossPhase::kProducts) {           // rows' tiles of one column block together: they share the weights
-            w->m = g.row0[i] + t % m * M;
+            w->m = g.row0[i] + t % m * kTileM;
             w->n = t / m * kTileN;
             w->k0 = 0;
             w->k1 = g.c.dimp / kTileK;
         } else {
             w->n = t % nt * kTileN;
             t /= nt;
-            w->m = g.row0[i] + t % m * M;
+            w->m = g.row0[i] + t % m * kTileM;
             w->split = t / m;
             w->k0 = w->split * g.split_blocks;
             w->k1 = min(w->k0 + g.split_blocks, ceil_div(g.width, kTileK));
         }
-        w->columns = ceil_div(min(all - w->n, kTileN), 64 * CG) * 64 * CG;
+        w->columns = ceil_div(min(all - w->n, kTileN), 64) * 64;
         return true;
     }
     if constexpr (PHASE == LossPhase::kProducts) {
         for (int i = 0; i < g.n; ++i) {
-            const int n = counts[i] == 0 && g.accumulate ? 0 : ceil_div(g.width, M) * nt;
+            const int n = counts[i] == 0 && g.accumulate ? 0 : ceil_div(g.width, kTileM) * nt;
             if (t >= n) {
                 t -= n;
                 continue;
@@ -327,10 +273,10 @@ __device__ __forceinline__ bool find_tile(const LossGemm& g, const int32_t* coun
             w->flags = 1;
             w->split = 0;
             w->n = t % nt * kTileN;
-            w->m = t / nt * M;
+            w->m = t / nt * kTileM;
             w->k0 = 0;
             w->k1 = ceil_div(counts[i], kTileK);
-            w->columns = ceil_div(min(all - w->n, kTileN), 64 * CG) * 64 * CG;
+            w->columns = ceil_div(min(all - w->n, kTileN), 64) * 64;
             return true;
         }
     }
@@ -358,33 +304,17 @@ __device__ __forceinline__ void get_tile(Tile* w, const Tile* at) {
 
 // ---- the tiles' queue -----------------------------------------------------------
 // Tiles differ in depth, so blocks take them as they come: the first each by its number, the others from a counter in
-// device memory.  A thread of the cluster's first block decodes them ahead of the other roles and puts them into its
-// queue and the second block's mail, which a thread there copies to its own queue: waiting for another block's writes,
-// like reporting to one, takes some two thousand cycles, which no role that works on tiles should spend.  Who computes a
-// tile changes no value.  The last cluster to finish leaves the counters at zero.
-template <int CG>
-__device__ __forceinline__ void enqueue(Control* s, int slot, const Tile& w) {
-    put_tile(&s->queue[slot], w);
-    bar_arrive(&s->tile_full[slot]);
-    if constexpr (CG == 2) {
-        const int32_t* words = reinterpret_cast<const int32_t*>(&w);
-        const uint32_t at = in_block(&s->mail[slot], 1);
-#pragma unroll
-        for (int i = 0; i < kTileWords; ++i)
-            asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(at + 4 * i), "r"(words[i]) : "memory");
-        arrive_at(in_block(&s->mail_full[slot], 1));
-    }
-}
-template <LossPhase PHASE, bool F32, int CG>
+// device memory.  A thread decodes them ahead of the other roles.  Who computes a tile changes no value.  The last block
+// to finish leaves the counters at zero.
+template <LossPhase PHASE, bool F32>
 __device__ void schedule(const LossGemm& g, Control* s) {
-    const int clusters = gridDim.x / CG;
-    int slot = 0, t = blockIdx.x / CG;
+    int slot = 0, t = blockIdx.x;
     uint32_t phase = 1;
     bool more = true;
     while (more) {
         Tile w;
-        more = find_tile<PHASE, CG>(g, s->counts, t, &w);
-        if (more) t = clusters + atomicAdd(g.c.next, 1);
+        more = find_tile<PHASE>(g, s->counts, t, &w);
+        if (more) t = (int)gridDim.x + atomicAdd(g.c.next, 1);
         else w.rank = -1;
         const int end = w.k1;
         do {                               // a tile's depth, in parts that follow each other
@@ -393,7 +323,8 @@ __device__ void schedule(const LossGemm& g, Control* s) {
                 more = false;
                 break;
             }
-            enqueue<CG>(s, slot, w);
+            put_tile(&s->queue[slot], w);
+            bar_arrive(&s->tile_full[slot]);
             if (++slot == kQueue) {
                 slot = 0;
                 phase ^= 1;
@@ -403,7 +334,7 @@ __device__ void schedule(const LossGemm& g, Control* s) {
         } while (more && w.k1 < end);
     }
     __threadfence();
-    if (atomicAdd(g.c.next + 1, 1) == clusters - 1) {
+    if (atomicAdd(g.c.next + 1, 1) == (int)gridDim.x - 1) {
         g.c.next[0] = 0;
         g.c.next[1] = 0;
     }
@@ -439,47 +370,15 @@ struct Queue {
     }
 };
 
-// Who reads a block's queue: the loads and the epilogue's warps; in the first block also the products, and of a pair the
-// other block's word that all there have.
-__device__ constexpr int queue_readers(int cg, int block) { return 1 + kEpilogueWarps + (block == 0 ? cg : 0); }
-
-// The second block of a pair: a thread copies its mail to its queue (a place whose mail has come is free there: its readers'
-// arrivals were passed on before).
-__device__ void copy_mail(const LossGemm& g, Control* s) {
-    Queue queue;
-    Tile w;
-    do {
-        if (!bar_wait<true>(&s->mail_full[queue.slot], queue.phase, s, g)) return;
-        get_tile(&w, &s->mail[queue.slot]);
-        put_tile(&s->queue[queue.slot], w);
-        bar_arrive(&s->tile_full[queue.slot]);
-        queue.step();
-    } while (w.rank >= 0);
-}
-// Another passes on to the first block's queue and products what its warps are through with.
-__device__ void pass_on(const LossGemm& g, Control* s) {
-    Queue queue;
-    Tile w;
-    for (int n = 0;; ++n) {
-        if (!queue.wait(s, g)) return;
-        queue.read(s, &w);                 // not one of the readers: the place is free only after its own arrival there
-        if (!bar_wait(&s->tile_empty[queue.slot], queue.phase, s, g)) return;
-        arrive_at(in_block(&s->tile_empty[queue.slot], 0));
-        if (w.rank < 0) return;
-        queue.step();
-        if (!bar_wait(&s->taken[n & 1], (n >> 1) & 1, s, g)) return;
-        arrive_at(in_block(&s->taken[n & 1], 0));
-    }
-}
+// Who reads the queue: the loads, the products and the epilogue's warps.
+constexpr int kQueueReaders = 2 + kEpilogueWarps;
 
 __device__ constexpr int8_t kPlaneA[6] = {2, 1, 0, 1, 0, 0};
 __device__ constexpr int8_t kPlaneB[6] = {0, 1, 2, 0, 1, 0};
 
 // ---- producer -----------------------------------------------------------------
-// Of a pair, each block loads its own operands; all arrive at the first block's barrier.
-template <LossPhase PHASE, bool F32, int CG>
-__device__ void produce(const LossGemm& g, Control* s, char* stages, int block) {
-    using S = Shape<CG>;
+template <LossPhase PHASE, bool F32>
+__device__ void produce(const LossGemm& g, Control* s, char* stages) {
     int stage = 0, issued = 0;
     uint32_t phase = 0;
     bool ok = true;
@@ -487,7 +386,6 @@ __device__ void produce(const LossGemm& g, Control* s, char* stages, int block) 
     Tile w;
     while (ok && queue.next(s, g, &w)) {
         const CUtensorMap* wmap = &g.weights[w.rank];
-        const int bm = w.m + block * kTileM, bn = w.n + block * (w.columns / CG);
         for (int q = 0; ok && q < (F32 ? 6 : 1); ++q) {
             const int pa = F32 ? kPlaneA[q] : 0, pb = F32 ? kPlaneB[q] : 0;
             for (int kb = w.k0; kb < w.k1; ++kb) {
@@ -495,24 +393,24 @@ __device__ void produce(const LossGemm& g, Control* s, char* stages, int block) 
                     ok = false;
                     break;
                 }
-                char* a = stages + stage * S::kBytesStage;
-                char* b = a + S::kBytesA;
-                if (block == 0) bar_expect(&s->full[stage], CG * S::kBytesStage);
-                const uint32_t bar = CG == 1 ? smem_of(&s->full[stage]) : in_block(&s->full[stage], 0);
+                char* a = stages + stage * kBytesStage;
+                char* b = a + kBytesA;
+                uint64_t* const bar = &s->full[stage];
+                bar_expect(bar, kBytesStage);
                 const int k = kb * kTileK;
                 if (PHASE != LossPhase::kProducts) {
-                    tma_load<CG>(a, &g.hidden, k, bm, pa, bar);
-                    tma_load<CG>(b, wmap, k, g.piece0 + bn, pb, bar);
+                    tma_load(a, &g.hidden, k, w.m, pa, bar);
+                    tma_load(b, wmap, k, g.piece0 + w.n, pb, bar);
                 } else if (!w.weights()) {
-                    tma_load<CG>(a, &g.piece, k, bm - g.row0[0], pa, bar);
-                    tma_load<CG>(b, wmap, bn, g.piece0 + k, pb, bar);
+                    tma_load(a, &g.piece, k, w.m - g.row0[0], pa, bar);
+                    tma_load(b, wmap, w.n, g.piece0 + k, pb, bar);
                 } else {
                     const int row = g.row0[w.rank] + k;
-                    tma_load<CG>(a, &g.piece_across, bm, row - g.row0[0], pa, bar);
-                    tma_load<CG>(b, &g.hidden, bn, row, pb, bar);
+                    tma_load(a, &g.piece_across, w.m, row - g.row0[0], pa, bar);
+                    tma_load(b, &g.hidden, w.n, row, pb, bar);
                 }
                 ++issued;
-                if (++stage == S::kStages) {
+                if (++stage == kStages) {
                     stage = 0;
                     phase ^= 1;
                 }
@@ -521,30 +419,22 @@ __device__ void produce(const LossGemm& g, Control* s, char* stages, int block) 
     }
     ok = ok && w.rank == -1;
     // what the products still have to report arrives here before the block ends
-    for (int i = 0; ok && i < S::kStages; ++i) {
+    for (int i = 0; ok && i < kStages; ++i) {
         ok = bar_wait(&s->empty[stage], phase ^ 1, s, g);
-        if (++stage == S::kStages) {
+        if (++stage == kStages) {
             stage = 0;
             phase ^= 1;
         }
     }
-    if (!ok) {                             // loads in flight, before the block's shared memory goes
-        if (block == 0) {
-            for (int i = max(0, issued - S::kStages); i < issued; ++i)
-                bar_wait_rest(&s->full[i % S::kStages], (i / S::kStages) & 1, g);
-        } else {                           // they report to the other block: far longer than a load takes
-            const unsigned long long t1 = now_ns();
-            while (now_ns() - t1 < 10000000ull) {}
-        }
-    }
+    if (!ok)                               // loads in flight, before the block's shared memory goes
+        for (int i = max(0, issued - kStages); i < issued; ++i) bar_wait_rest(&s->full[i % kStages], (i / kStages) & 1, g);
 }
 
 // ---- products -----------------------------------------------------------------
 // The tensor cores' own queue is short: the next stage is looked up before a stage's last product is issued, and the next
 // tile while the present one's are.
-template <LossPhase PHASE, bool F32, int CG>
+template <LossPhase PHASE, bool F32>
 __device__ void multiply(const LossGemm& g, Control* s, char* stages, uint32_t tmem) {
-    using S = Shape<CG>;
     int stage = 0, buf = 0;
     uint32_t phase = 0, taken = 1;
     bool ok = true, there = false;
@@ -553,7 +443,7 @@ __device__ void multiply(const LossGemm& g, Control* s, char* stages, uint32_t t
     bool more = queue.next(s, g, &w);
     while (more) {
         const bool a_across = PHASE == LossPhase::kProducts && w.weights(), b_across = PHASE == LossPhase::kProducts;
-        const uint32_t desc = product_desc(a_across, b_across, CG * kTileM, w.columns);
+        const uint32_t desc = product_desc(a_across, b_across, kTileM, w.columns);
         // 16 elements of depth: 32 bytes along a row, or 16 rows of 128 bytes
         const uint32_t step_a = a_across ? 16 * 128 / 16 : 2, step_b = b_across ? 16 * 128 / 16 : 2;
         if (!(ok = bar_wait(&s->taken[buf], taken, s, g))) break;
@@ -562,30 +452,30 @@ __device__ void multiply(const LossGemm& g, Control* s, char* stages, uint32_t t
         for (int i = 0; i < blocks; ++i) {
             if (!there && !(ok = bar_wait(&s->full[stage], phase, s, g))) break;
             fence_after();
-            const uint32_t a = smem_of(stages + stage * S::kBytesStage);
-            const uint64_t da = matrix_desc(a, kBytesBox), db = matrix_desc(a + S::kBytesA, kBytesBox);
+            const uint32_t a = smem_of(stages + stage * kBytesStage);
+            const uint64_t da = matrix_desc(a, kBytesBox), db = matrix_desc(a + kBytesA, kBytesBox);
             uint64_t* const empty = &s->empty[stage];
-            if (++stage == S::kStages) {
+            if (++stage == kStages) {
                 stage = 0;
                 phase ^= 1;
             }
 #pragma unroll
             for (int k = 0; k < kTileK / 16; ++k) {
                 if (k == kTileK / 16 - 1) there = bar_test(&s->full[stage], phase);
-                mma<CG>(tmem + buf * kTileN, da + k * step_a, db + k * step_b, desc, i > 0 || k > 0);
+                mma(tmem + buf * kTileN, da + k * step_a, db + k * step_b, desc, i > 0 || k > 0);
             }
-            mma_commit<CG>(empty);
+            mma_commit(empty);
             if (i == 0) more = queue.next(s, g, &after);
         }
         if (!ok) break;
-        mma_commit<CG>(&s->ready[buf]);
+        mma_commit(&s->ready[buf]);
         if (blocks == 0) more = queue.next(s, g, &after);
         if (buf == 1) taken ^= 1;
         buf ^= 1;
         w = after;
     }
     if (!ok || w.rank == -2) {             // products in flight, before tensor memory goes
-        mma_commit<CG>(&s->drain);
+        mma_commit(&s->drain);
         bar_wait_rest(&s->drain, 0, g);
     }
 }
@@ -641,7 +531,7 @@ struct Listed {
 // Twice over the row's 128 logits: their maximum, and their exponentials relative to it.  KEEP: the exponentials are
 // stored, for bf16 operands as binary16, 2^kKeepBits for the row's largest, so that those down to 2^-29 of it keep 11
 // bits, for float32 as they are.
-template <bool F32, bool TWO, bool LIST, bool KEEP, int CG>
+template <bool F32, bool TWO, bool LIST, bool KEEP>
 __device__ __forceinline__ void stats_tile(const LossGemm& g, const Tile& w, const Lane& l, Control* s, uint64_t* taken) {
     const LossCall& c = g.c;
     const int row = w.m + l.row, first = w.n + l.group * kLossUnit;
@@ -749,7 +639,7 @@ __device__ __forceinline__ void stats_tile(const LossGemm& g, const Tile& w, con
     }
 }
 
-template <bool F32, bool TWO, bool LIST, int CG>
+template <bool F32, bool TWO, bool LIST>
 __device__ __forceinline__ void grad_tile(const LossGemm& g, const Tile& w, const Lane& l, Control* s, uint64_t* taken) {
     const LossCall& c = g.c;
     const int row = w.m + l.row, first = g.piece0 + w.n + l.group * kLossUnit;
@@ -856,7 +746,7 @@ __device__ __forceinline__ void hidden_tile(const LossGemm& g, const Tile& w, co
 
 // dw: rows of the weights' gradients, rounded once.  Where rows start on 16-byte boundaries the copy engine writes
 // them; else, and to add to what is there, a warp goes row by row, a lane a column.
-template <bool F32, int CG>
+template <bool F32>
 __device__ __forceinline__ void weights_tile(const LossGemm& g, const Tile& w, const Lane& l, const Control* s, uint64_t* taken) {
     const LossCall& c = g.c;
     const float f = factor_of<F32>(w, s);
@@ -893,7 +783,7 @@ __device__ __forceinline__ void weights_tile(const LossGemm& g, const Tile& w, c
             }
             to_async_proxy();
             group_sync(l.group);
-            if (l.leader && g.piece0 + w.m < c.vocab) {    // a pair's second block may be past the last row
+            if (l.leader) {
                 if (F32 && w.more()) tma_add_2d(&g.out[w.rank], l.staging, col, g.piece0 + w.m);
                 else tma_store_2d(&g.out[w.rank], l.staging, col, g.piece0 + w.m);
                 tma_commit();
@@ -948,29 +838,26 @@ __device__ __forceinline__ void weights_tile(const LossGemm& g, const Tile& w, c
     }
 }
 
-template <LossPhase PHASE, bool F32, bool TWO, bool LIST, int CG>
+template <LossPhase PHASE, bool F32, bool TWO, bool LIST>
 __global__ void __launch_bounds__(kGemmThreads, 1) k_loss_gemm(const __grid_constant__ LossGemm g) {
-    using S = Shape<CG>;
     extern __shared__ char raw[];
     char* smem = raw + (1024 - (smem_of(raw) & 1023)) % 1024;
-    char* staging = smem + kStageBytes;
+    char* staging = smem + kStages * kBytesStage;
     Control* s = reinterpret_cast<Control*>(staging + 2 * kBytesStaging);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int block = CG == 1 ? 0 : cluster_rank();
     pdl_release();
     if (threadIdx.x == 0) {
-        for (int i = 0; i < S::kStages; ++i) {
+        for (int i = 0; i < kStages; ++i) {
             bar_init(&s->full[i], 1);
             bar_init(&s->empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(&s->ready[i], 1);
-            bar_init(&s->taken[i], kEpilogueWarps + (CG == 2 && block == 0));
+            bar_init(&s->taken[i], kEpilogueWarps);
         }
         for (int i = 0; i < kQueue; ++i) {
             bar_init(&s->tile_full[i], 1);
-            bar_init(&s->mail_full[i], 1);
-            bar_init(&s->tile_empty[i], queue_readers(CG, block));
+            bar_init(&s->tile_empty[i], kQueueReaders);
         }
         bar_init(&s->drain, 1);
         s->stop = 0;
@@ -978,13 +865,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_loss_gemm(const __grid_cons
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     if (warp == 2) {
-        if constexpr (CG == 1) {
-            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_of(&s->tmem)) : "memory");
-            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-        } else {
-            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_of(&s->tmem)) : "memory");
-            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-        }
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_of(&s->tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     pdl_acquire();
     if (threadIdx.x < g.n) {
@@ -993,18 +875,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_loss_gemm(const __grid_cons
     }
     fence_before();
     __syncthreads();
-    if constexpr (CG == 2) cluster_sync();             // the other block's barriers are there
     fence_after();
     const uint32_t tmem = *(volatile uint32_t*)&s->tmem;
     if (warp == 0) {
-        if (lane == 0) produce<PHASE, F32, CG>(g, s, smem, block);
+        if (lane == 0) produce<PHASE, F32>(g, s, smem);
     } else if (warp == 1) {
-        if (lane == 0 && block == 0) multiply<PHASE, F32, CG>(g, s, smem, tmem);
+        if (lane == 0) multiply<PHASE, F32>(g, s, smem, tmem);
     } else if (warp == 3) {
-        if (lane == 0 && block == 0) schedule<PHASE, F32, CG>(g, s);
-        if (lane == 0 && block == 1) copy_mail(g, s);
-    } else if (warp == 2) {
-        if (lane == 0 && block == 1) pass_on(g, s);
+        if (lane == 0) schedule<PHASE, F32>(g, s);
     } else if (warp >= kFirstEpilogueWarp) {
         Lane l;
         l.group = (warp - kFirstEpilogueWarp) / 4;
@@ -1035,14 +913,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_loss_gemm(const __grid_cons
             queue.step();
             if (w.rank < 0) break;
             fence_after();
-            w.m += block * kTileM;
             l.tmem = tmem + ((uint32_t)(l.quarter * 32) << 16) + buf * kTileN + l.group * (kTileN / 2);
             uint64_t* taken = &s->taken[buf];
             if (PHASE == LossPhase::kStats || PHASE == LossPhase::kKeep)
-                stats_tile<F32, TWO, LIST, PHASE == LossPhase::kKeep, CG>(g, w, l, s, taken);
-            else if (PHASE == LossPhase::kGrad) grad_tile<F32, TWO, LIST, CG>(g, w, l, s, taken);
+                stats_tile<F32, TWO, LIST, PHASE == LossPhase::kKeep>(g, w, l, s, taken);
+            else if (PHASE == LossPhase::kGrad) grad_tile<F32, TWO, LIST>(g, w, l, s, taken);
             else if (!w.weights()) hidden_tile(g, w, l, taken);
-            else weights_tile<F32, CG>(g, w, l, s, taken);
+            else weights_tile<F32>(g, w, l, s, taken);
             if (buf == 1) phase ^= 1;
             buf ^= 1;
         }
@@ -1051,64 +928,39 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_loss_gemm(const __grid_cons
     __syncwarp();
     fence_before();
     __syncthreads();
-    if constexpr (CG == 2) cluster_sync();             // nothing of the other block's is under way to this one
     if (warp == 2) {
         fence_after();
-        if constexpr (CG == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
-        else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
 }
 
-template <LossPhase PHASE, bool F32, bool TWO, bool LIST, int CG>
-cudaError_t launch(const LossGemm& g, int64_t most_tiles, cudaStream_t stream) {
-    const auto kernel = k_loss_gemm<PHASE, F32, TWO, LIST, CG>;
-    cudaError_t e = allow_shared_memory((const void*)kernel, kSmem);
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(cap_ctas(std::min<int64_t>(most_tiles * CG, sm_count())) / CG * CG);
-    cfg.blockDim = dim3(kGemmThreads);
-    cfg.dynamicSmemBytes = kSmem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = CG;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = CG == 1 ? 1 : 2;
-    e = cudaLaunchKernelEx(&cfg, kernel, g);
-    const cudaError_t last = cudaGetLastError();
-    return e != cudaSuccess ? e : last;
-}
-
-// Tiles of `rows` rows and `columns` columns, both in tiles of the shape.
-int64_t tile_count(LossPhase phase, const LossGemm& g, int cg) {
+int64_t tile_count(LossPhase phase, const LossGemm& g) {
     int64_t rows = 0, weights = 0;
-    for (int i = 0; i < g.n; ++i) rows += (g.row0[i + 1] - g.row0[i] + cg * kTileM - 1) / (cg * kTileM);
+    for (int i = 0; i < g.n; ++i) rows += (g.row0[i + 1] - g.row0[i]) / kTileM;
     const int64_t columns = phase == LossPhase::kProducts ? g.c.dim : phase == LossPhase::kGrad ? g.width : g.c.vocab;
     const int64_t nt = (columns + kTileN - 1) / kTileN;
     if (phase == LossPhase::kProducts) {
         rows *= g.splits;
-        weights = (int64_t)g.n * ((g.width + cg * kTileM - 1) / (cg * kTileM));
+        weights = (int64_t)g.n * ((g.width + kTileM - 1) / kTileM);
     }
     return (rows + weights) * nt;
 }
 
 template <LossPhase PHASE, bool F32, bool TWO, bool LIST>
-cudaError_t launch_shape(const LossGemm& g, cudaStream_t stream) {
-    if constexpr (!F32) {                  // float32's parts of the depth stay on single blocks (the call chooses so)
-        if (g.pairs) return launch<PHASE, F32, TWO, LIST, 2>(g, tile_count(PHASE, g, 2), stream);
-    }
-    return launch<PHASE, F32, TWO, LIST, 1>(g, tile_count(PHASE, g, 1), stream);
+cudaError_t launch(const LossGemm& g, cudaStream_t stream) {
+    const auto kernel = k_loss_gemm<PHASE, F32, TWO, LIST>;
+    const cudaError_t e = allow_shared_memory((const void*)kernel, kSmem);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(kernel, dim3(cap_ctas(std::min<int64_t>(tile_count(PHASE, g), sm_count()))), dim3(kGemmThreads), kSmem,
+                            stream, g);
 }
 
 template <LossPhase PHASE, bool F32>
 cudaError_t launch_kind(const LossGemm& g, cudaStream_t stream) {
-    if (PHASE == LossPhase::kProducts) return launch_shape<PHASE, F32, false, false>(g, stream);
-    if (g.c.alpha == 0.f) return launch_shape<PHASE, F32, false, false>(g, stream);
-    if (g.c.two) return launch_shape<PHASE, F32, true, true>(g, stream);
-    return launch_shape<PHASE, F32, false, true>(g, stream);
+    if (PHASE == LossPhase::kProducts) return launch<PHASE, F32, false, false>(g, stream);
+    if (g.c.alpha == 0.f) return launch<PHASE, F32, false, false>(g, stream);
+    if (g.c.two) return launch<PHASE, F32, true, true>(g, stream);
+    return launch<PHASE, F32, false, true>(g, stream);
 }
 
 template <LossPhase PHASE>
@@ -1133,7 +985,7 @@ cudaError_t allow_shared_memory(const void* kernel, int bytes) {
 }
 
 cudaError_t launch_loss_gemm(LossPhase phase, const LossGemm& g, cudaStream_t stream) {
-    if (tile_count(phase, g, 1) == 0) return cudaSuccess;
+    if (tile_count(phase, g) == 0) return cudaSuccess;
     if (phase == LossPhase::kStats) return launch_type<LossPhase::kStats>(g, stream);
     if (phase == LossPhase::kKeep) return launch_type<LossPhase::kKeep>(g, stream);
     if (phase == LossPhase::kGrad) return launch_type<LossPhase::kGrad>(g, stream);

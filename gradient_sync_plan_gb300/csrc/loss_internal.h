@@ -57,7 +57,7 @@ struct LossCall {
 
     int32_t* counts;                      // [world]
     int32_t* done;                        // blocks of a combine launch that are through
-    int32_t* next;                        // [2] tiles taken of a products' launch, and clusters that are through
+    int32_t* next;                        // [2] tiles taken of a products' launch, and blocks that are through
     int32_t* row_token;                   // [rows] the token (of its rank) that a row holds
     int32_t* token_row;                   // [rows] the row (of its rank) of a token, -1: not learned
     int32_t* row_column;                  // [rows] target's column
@@ -102,7 +102,6 @@ struct LossGemm {
     int32_t add;                          // add to acc (else write)
     int32_t accumulate;                   // add to the weights' gradients
     int32_t store;                        // the copy engine writes them: 16-byte aligned rows, not accumulated
-    int32_t pairs;                        // blocks work in pairs
     unsigned long long limit_ns;
     LossCall c;
 };
