@@ -315,7 +315,11 @@ __global__ void __launch_bounds__(32 * kCombineWarps) k_combine(const __grid_con
             float top = m;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                if (u0 + e * kCombineWarps >= c.units) p[e].x = -INFINITY;
+                if (u0 + e * kCombineWarps >= c.units) {
+                    p[e].x = -INFINITY;
+                    p[e].y = 0.f;
+                    if constexpr (TWO) p[e].z = 0.f;
+                }
                 top = fmaxf(top, p[e].x);
             }
             const float ref = top == -INFINITY ? 0.f : top;
@@ -323,10 +327,10 @@ __global__ void __launch_bounds__(32 * kCombineWarps) k_combine(const __grid_con
             if constexpr (TWO) s2 *= exp2f((m - ref) * k2);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                // a unit of nothing but -infinity, or none: no terms
+                // a unit of nothing but -infinity, or none: 0; of those and NaN, which no maximum shows: NaN
                 const bool none = p[e].x == -INFINITY;
-                s += none ? 0.f : p[e].y * exp2f((p[e].x - ref) * k1);
-                if constexpr (TWO) s2 += none ? 0.f : p[e].z * exp2f((p[e].x - ref) * k2);
+                s += none ? p[e].y : p[e].y * exp2f((p[e].x - ref) * k1);
+                if constexpr (TWO) s2 += none ? p[e].z : p[e].z * exp2f((p[e].x - ref) * k2);
             }
             m = top;
         }
