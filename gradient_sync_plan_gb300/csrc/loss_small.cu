@@ -145,7 +145,8 @@ __global__ void __launch_bounds__(kSmallThreads) k_small(const __grid_constant__
             top = all_lanes_max(top);
             const float ref = top == -INFINITY ? 0.f : top;
             const bool hard = c.alpha < 1.f, soft = c.alpha != 0.f;
-            // the largest terms are ones, counted apart: a confident token's sum is 1 and little more
+            // the largest terms are ones, counted apart, and the reference stays apart from the sums' logarithms: of a
+            // confident token the sum is 1 and little more, and its loss far below a step of its logits
             float s1 = 0.f, s2 = 0.f, ones = 0.f;
             for (int v = lane; v < c.vocab; v += 32) {
                 if (z[v] == ref) {
@@ -159,9 +160,9 @@ __global__ void __launch_bounds__(kSmallThreads) k_small(const __grid_constant__
             s1 = all_lanes_sum(s1);
             s2 = all_lanes_sum(s2);
             const auto log_of = [&](float rest) { return ones == 1.f ? log1pf(rest) : logf(ones + rest); };
-            const float lse1 = ref + log_of(s1), lse2 = ref * c.inv_temperature + log_of(s2);
+            const float log1 = log_of(s1), log2 = log_of(s2);
             const int y = hard ? (int)g.targets[i][t] : 0;
-            float result = hard ? (1.f - c.alpha) * (lse1 - z[y]) : 0.f;
+            float result = hard ? (1.f - c.alpha) * ((ref - z[y]) + log1) : 0.f;
             const float a = hard ? (1.f - c.alpha) : 0.f, b = c.alpha * c.temperature;
             const int64_t base = (int64_t)t * c.n_teacher;
             float t_top = -INFINITY, t_sum = 0.f;
@@ -185,7 +186,7 @@ __global__ void __launch_bounds__(kSmallThreads) k_small(const __grid_constant__
                     const float x = c.teacher_dtype == DDP_F32 ? load<true>(g.teacher[i], base + k) : load<false>(g.teacher[i], base + k);
                     if (j < 0 || j >= c.vocab || x == -INFINITY) continue;
                     const float u = (x - t_top) * c.inv_temperature, q = expf(u) / t_sum;
-                    if (q != 0.f) kl += q * (u - logf(t_sum) + (lse2 - z[j] * c.inv_temperature));
+                    if (q != 0.f) kl += q * (u - logf(t_sum) + (log2 - (z[j] - ref) * c.inv_temperature));
                 }
                 result += b * c.temperature * all_lanes_sum(kl);
             }
@@ -196,10 +197,10 @@ __global__ void __launch_bounds__(kSmallThreads) k_small(const __grid_constant__
             if (!m.grad) continue;
             __syncwarp();
             for (int v = lane; v < c.vocab; v += 32) {
-                const float x = z[v];
+                const float x = z[v] - ref;
                 float d = 0.f;
-                if (hard) d = a * (v == y ? expm1f(x - lse1) : expf(x - lse1));
-                if (soft) d += b * expf(x * c.inv_temperature - lse2);
+                if (hard) d = a * (v == y ? expm1f(x - log1) : expf(x - log1));
+                if (soft) d += b * expf(x * c.inv_temperature - log2);
                 z[v] = d;
             }
             __syncwarp();

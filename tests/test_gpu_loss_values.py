@@ -99,3 +99,76 @@ def test_logits_of_minus_infinity_have_no_share(tokens, vocab, dim):
     size = float((x["hidden"][0].double().abs() @ x["weights"][0][keep].double().abs().t()).max())
     bound = 2 * size * (dim // 16 + 16) * 2.0 ** -23 + 40 * 2.0 ** -21
     assert float((out["token_losses"][0].double() - want).abs().max()) <= bound
+
+
+CONFIDENT = [(16, 100, 32)]
+
+
+def _confident(tokens, vocab, dim, dtype, top, seed):
+    """Logits that are what they are: token t's hidden state is the t-th unit vector, so column t of the weights holds its
+    logits, and column t of the weights' gradients its logits' gradients.  The target's is `top`, the others' 8 to 20 below;
+    all are bf16 values.  Returns the inputs and the logits."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    kw = dict(device="cuda", generator=gen)
+    y = torch.randint(0, vocab, (tokens,), **kw)
+    z = top - 8.0 - 4.0 * torch.randint(0, 3, (tokens, 1), **kw) - 4.0 * torch.randint(0, 2, (tokens, vocab), **kw)
+    z.scatter_(1, y.unsqueeze(1), torch.full((tokens, 1), float(top), device="cuda"))
+    weights = torch.zeros(vocab, dim, device="cuda")
+    weights[:, :tokens] = z.t()
+    x = dict(weights=[weights.to(dtype)], hidden=[torch.eye(tokens, dim, device="cuda").to(dtype)], targets=[y],
+             indices=[y.unsqueeze(1).contiguous()], teacher=[torch.randn(tokens, 1, **kw)])
+    return x, z.double()
+
+
+@pytest.mark.parametrize("tokens,vocab,dim", CONFIDENT)
+@TYPES
+@pytest.mark.parametrize("top", [28, 100, 1000, -100])
+@pytest.mark.parametrize("op", ["ce", "distill"])
+def test_losses_of_confident_tokens_keep_their_digits(tokens, vocab, dim, dtype, top, op):
+    """A target that leads by 8 to 20 has a loss of log(1 + rest), 1e-9 to 0.3, whatever its logit; the teacher's one entry is
+    the target, so the distillation's part is the same at its temperature.
+
+    Relative error of the rest: an exponent of up to 20 from three roundings (2^-24 each) and the logits' own scale for the
+    tensor cores (1.6e-8 a 16 of the depth, itself rounded by 2^-24), an exponential's 2^-22, a sum's 2^-24 times its 64
+    additions in a row at most; a logarithm adds 2^-22.  Gradients are 1 / (1 + rest) times that with one more exponential
+    and, of bf16, two roundings: kept exponentials' 2^-12, times 2 for the steeper softmax's, and bf16's 2^-8."""
+    x, z = _confident(tokens, vocab, dim, dtype, top, seed=4)
+    out = _run(x, op, reduction=ddp.DDP_LOSS_SUM)
+    y = x["targets"][0].unsqueeze(1)
+    gap = z - z.gather(1, y)
+    # the target's own term stays out of the sums, so that nothing cancels
+    others = torch.ones_like(z).scatter(1, y, 0.0)
+    rest1, rest2 = (((gap / tau).exp() * others).sum(1) for tau in (1.0, 2.0))
+    loss1, loss2 = rest1.log1p(), rest2.log1p()
+    want = loss1 if op == "ce" else 0.5 * loss1 + 0.5 * 4.0 * loss2
+    rel = 20 * (3 * 2.0 ** -24 + 1.6e-8 * dim / 16 + 2.0 ** -24) + 2.0 ** -22 + 64 * 2.0 ** -24 + 2.0 ** -22
+    got = out["token_losses"][0].double()
+    assert bool((got > 0).all())
+    assert float((got / want - 1).abs().max()) <= rel
+    assert abs(float(out["loss"][0]) / float(want.sum()) - 1) <= rel + 2.0 ** -23
+    p1, p2 = gap.exp() * others / (1 + rest1).unsqueeze(1), (gap / 2).exp() * others / (1 + rest2).unsqueeze(1)
+    p1 -= torch.zeros_like(p1).scatter(1, y, (rest1 / (1 + rest1)).unsqueeze(1))
+    p2 -= torch.zeros_like(p2).scatter(1, y, (rest2 / (1 + rest2)).unsqueeze(1))
+    dz = p1 if op == "ce" else 0.5 * p1 + 0.5 * 2.0 * p2
+    got = out["gw"][0].double().t()[:tokens]
+    # float32 products: three parts of a gradient, their sum scaled for one step of depth's cut at each k block
+    rel += 2.0 ** -22 + (2 * 2.0 ** -12 + 2.0 ** -8 if dtype == BF16 else 2.0 ** -22 + 2.0 ** -18)
+    assert float((got / dz - 1).abs().max()) <= rel
+
+
+@pytest.mark.parametrize("tokens,vocab,dim", [(16, 100, 32)])
+@TYPES
+@pytest.mark.parametrize("top", [15.0, 90.0, 1000.0])
+def test_no_loss_is_below_zero(tokens, vocab, dim, dtype, top):
+    # targets that lead by so much that nothing else counts; logits of no particular value
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    kw = dict(device="cuda", generator=gen)
+    x = _inputs([tokens], vocab, dim, dtype, seed=6)
+    w = x["weights"][0].float()
+    lean = top * (1.0 + torch.rand(tokens, 1, **kw)) / (w[x["targets"][0]] ** 2).sum(1, keepdim=True)
+    x["hidden"][0] = (lean * w[x["targets"][0]]).to(dtype)
+    for op in ("ce", "distill"):
+        if op == "distill":
+            x["indices"], x["teacher"] = [x["targets"][0].unsqueeze(1).contiguous()], [torch.zeros(tokens, 1, device="cuda")]
+        out = _run(x, op)
+        assert bool((out["token_losses"][0] >= 0).all()) and float(out["loss"][0]) >= 0
