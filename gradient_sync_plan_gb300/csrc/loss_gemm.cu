@@ -227,6 +227,32 @@ __device__ __forceinline__ float exp2_of(float x) {
     return y;
 }
 
+// Two floats at a time.
+struct Pair {
+    uint64_t bits;
+    __device__ __forceinline__ Pair(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(bits) : "f"(a), "f"(b)); }
+    __device__ __forceinline__ explicit Pair(uint64_t x) : bits(x) {}
+    __device__ __forceinline__ float2 get() const {
+        float2 v;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(bits));
+        return v;
+    }
+};
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a.bits), "l"(b.bits));
+    return Pair(r);
+}
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a.bits), "l"(b.bits));
+    return Pair(r);
+}
+__device__ __forceinline__ Pair exp2_of(Pair x) {
+    const float2 v = x.get();
+    return Pair(exp2_of(v.x), exp2_of(v.y));
+}
+
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 // Tiles of rank i in the phase: of its rows first, of its weights' gradients behind those of all ranks.
@@ -528,9 +554,30 @@ struct Listed {
     }
 };
 
-// Twice over the row's 128 logits: their maximum, and their exponentials relative to it.  KEEP: the exponentials are
-// stored, for bf16 operands as binary16, 2^kKeepBits for the row's largest, so that those down to 2^-29 of it keep 11
-// bits, for float32 as they are.
+// Twice over the row's 128 logits: their maximum, and their exponentials relative to it, whose arguments are taken after
+// the subtraction: the largest is 1 whatever the logits' size.  One of the ones stays out of the sum (LossCall::partial): it
+// is taken off, or, of a sum below kConfident, whose rest would lack digits, left out in going over the logits again.
+// KEEP: the exponentials are stored, for bf16 operands as binary16, 2^kKeepBits for the row's largest, so that those down
+// to 2^-29 of it keep 11 bits, for float32 as they are.
+constexpr float kConfident = 1.125f;                   // the rest is off by 9 steps of a sum at most
+
+// The sum of the unit's exponentials but for the largest, which is there once.
+__device__ __forceinline__ float rest_of(const Lane& l, float ref, float k, int columns) {
+    float rest = 0.f;
+#pragma unroll 1
+    for (int j = 0; j < kLossUnit / 32; ++j) {
+        float v[32];
+        tmem_load(v, l.tmem + j * 32);
+        tmem_wait();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const float d = v[i] - ref;
+            if (j * 32 + i < columns && d != 0.f) rest += exp2_of(d * k);
+        }
+    }
+    return rest;
+}
+
 template <bool F32, bool TWO, bool LIST, bool KEEP>
 __device__ __forceinline__ void stats_tile(const LossGemm& g, const Tile& w, const Lane& l, Control* s, uint64_t* taken) {
     const LossCall& c = g.c;
@@ -553,7 +600,7 @@ __device__ __forceinline__ void stats_tile(const LossGemm& g, const Tile& w, con
         if (__any_sync(0xffffffffu, hit.column < col + 32)) {
             stage_floats(l, v);
             while (hit.column < col + 32) {
-                c.z[hit.at] = c.unit * staged_float(l, hit.column - col);
+                c.z[hit.at] = staged_float(l, hit.column - col);
                 hit.next();
             }
         }
@@ -569,9 +616,10 @@ __device__ __forceinline__ void stats_tile(const LossGemm& g, const Tile& w, con
         top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
     }
     const float ref = top == -INFINITY ? 0.f : top;    // nothing but -infinity: no terms
-    const float a1 = -ref * k1, a2 = -ref * k2;
     const bool flat = TWO && k2 < k1;                  // the flatter softmax's exponentials are kept
-    float sum[4] = {0.f, 0.f, 0.f, 0.f}, sum2[4] = {0.f, 0.f, 0.f, 0.f};
+    const Pair from(-ref, -ref), k1s(k1, k1), k2s(k2, k2);
+    Pair sum[2] = {Pair(0.f, 0.f), Pair(0.f, 0.f)}, sum2[2] = {Pair(0.f, 0.f), Pair(0.f, 0.f)};
+    float rest = 0.f, rest2 = 0.f;
     constexpr int kColumns = KEEP && !F32 ? 64 : 32;   // kept in 128 bytes
 #pragma unroll 1
     for (int j = 0; j < kLossUnit / kColumns; ++j) {
@@ -582,10 +630,6 @@ __device__ __forceinline__ void stats_tile(const LossGemm& g, const Tile& w, con
             float v[32];
             tmem_load(v, l.tmem + j * kColumns + h * 32);
             tmem_wait();
-            if (h == kColumns / 32 - 1 && j == kLossUnit / kColumns - 1) {
-                fence_before();
-                warp_arrive(taken, l.lane);
-            }
             if (col + h * 32 + 32 > c.vocab) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
@@ -593,26 +637,40 @@ __device__ __forceinline__ void stats_tile(const LossGemm& g, const Tile& w, con
             }
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
-                float e[2];
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const float x = exp2_of(fmaf(v[i + k], k1, a1));
-                    sum[(i + k) & 3] += x;
-                    e[k] = x;
-                    if (TWO) {
-                        const float y = exp2_of(fmaf(v[i + k], k2, a2));
-                        sum2[(i + k) & 3] += y;
-                        e[k] = flat ? y : x;
-                    }
+                const Pair d = Pair(v[i], v[i + 1]) + from, x = exp2_of(d * k1s);
+                sum[i / 2 & 1] = sum[i / 2 & 1] + x;
+                float2 e = x.get();
+                if (TWO) {
+                    const Pair y = exp2_of(d * k2s);
+                    sum2[i / 2 & 1] = sum2[i / 2 & 1] + y;
+                    if (flat) e = y.get();
                 }
                 if (KEEP && F32) {
-                    kept[i] = __float_as_uint(e[0]);
-                    kept[i + 1] = __float_as_uint(e[1]);
+                    kept[i] = __float_as_uint(e.x);
+                    kept[i + 1] = __float_as_uint(e.y);
                 } else if (KEEP) {
-                    const __half2 p = __floats2half2_rn(e[0] * kKeepScale, e[1] * kKeepScale);
+                    const __half2 p = __floats2half2_rn(e.x * kKeepScale, e.y * kKeepScale);
                     kept[h * 16 + i / 2] = *reinterpret_cast<const uint32_t*>(&p);
                 }
             }
+        }
+        if (j == kLossUnit / kColumns - 1) {
+            const float2 a = (sum[0] + sum[1]).get(), b = (sum2[0] + sum2[1]).get();
+            const float total = a.x + a.y, total2 = b.x + b.y;
+            const bool some = top != -INFINITY;        // else no 1: 0, or NaN
+            rest = some ? total - 1.f : total;
+            rest2 = some ? total2 - 1.f : total2;
+            const bool confident = valid && some && total < kConfident, confident2 = TWO && valid && some && total2 < kConfident;
+            if (__any_sync(0xffffffffu, confident)) {
+                const float r = rest_of(l, ref, k1, c.vocab - first);
+                if (confident) rest = r;
+            }
+            if (TWO && __any_sync(0xffffffffu, confident2)) {
+                const float r = rest_of(l, ref, k2, c.vocab - first);
+                if (confident2) rest2 = r;
+            }
+            fence_before();
+            warp_arrive(taken, l.lane);
         }
         if (KEEP) {
             if (j > 0) {
@@ -633,9 +691,8 @@ __device__ __forceinline__ void stats_tile(const LossGemm& g, const Tile& w, con
     }
     if (valid && first < c.vocab) {
         const int64_t at = (int64_t)(first / kLossUnit) * c.rows + row;
-        const float t = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        if (TWO) reinterpret_cast<float4*>(c.partial)[at] = make_float4(top, t, (sum2[0] + sum2[1]) + (sum2[2] + sum2[3]), 0.f);
-        else reinterpret_cast<float2*>(c.partial)[at] = make_float2(top, t);
+        if (TWO) reinterpret_cast<float4*>(c.partial)[at] = make_float4(top, rest, rest2, 0.f);
+        else reinterpret_cast<float2*>(c.partial)[at] = make_float2(top, rest);
     }
 }
 
@@ -660,10 +717,12 @@ __device__ __forceinline__ void grad_tile(const LossGemm& g, const Tile& w, cons
         }
         const int col = first + j * 64;
 #pragma unroll
-        for (int i = 0; i < 64; ++i) {
-            float p = coef.y * exp2_of(fmaf(v[i], k1, -coef.x));
-            if (TWO) p = fmaf(coef.w, exp2_of(fmaf(v[i], k2, -coef.z)), p);
-            v[i] = valid && col + i < c.vocab ? p : 0.f;
+        for (int i = 0; i < 64; i += 2) {
+            const Pair d = Pair(v[i], v[i + 1]) + Pair(-coef.x, -coef.x);
+            Pair p = Pair(coef.y, coef.y) * exp2_of(d * Pair(k1, k1));
+            if (TWO) p = p + Pair(coef.w, coef.w) * exp2_of(d * Pair(k2, k2));
+            v[i] = valid && col + i < c.vocab ? p.get().x : 0.f;
+            v[i + 1] = valid && col + i + 1 < c.vocab ? p.get().y : 0.f;
         }
         const Listed<LIST> before = hit;
 #pragma unroll

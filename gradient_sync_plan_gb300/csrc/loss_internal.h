@@ -66,11 +66,13 @@ struct LossCall {
     uint16_t* starts;                     // [rows][units + 1] by token: entries before a unit
     float* share;                         // [rows][list] by token: teacher's probability of the entry
     float* entropy;                       // [rows] by token: sum of q log q
-    float* z;                             // [rows][list] logits at the listed columns
+    float* z;                             // [rows][list] logits at the listed columns, without `unit`
     float* value;                         // [rows][list] gradients there, without the factor
-    float* partial;                       // [units][rows] float2, or float4 for two temperatures
+    float* partial;                       // [units][rows] float2, or float4 for two temperatures: the largest logit (without
+                                          // `unit`), and the sum of exponentials relative to it but for one of the largest
     float* factor;                        // [world] of the gradients: scale and reduction
-    float4* coef;                         // [rows] {lse, share, lse at the temperature, its share}, lse in bits (log2)
+    float4* coef;                         // [rows] {largest logit, share over the sum of exponentials relative to it, -, the
+                                          // same at the temperature}
     double* block_loss;                   // [rows / kLossBlockRows]
     void* gathered;                       // [planes][rows][dimp] bf16
     float* acc;                           // [splits][rows][dimp]

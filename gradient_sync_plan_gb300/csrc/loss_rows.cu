@@ -273,12 +273,16 @@ __global__ void __launch_bounds__(kThreads) k_planes(const __grid_constant__ Los
 // ---- losses and coefficients -------------------------------------------------------
 // A block takes 32 rows of a rank, a row a lane: each warp joins every 32nd unit's statistics; then a warp a
 // row joins the warps' and takes the row's target or list.  The last block adds the blocks' losses.
+//
+// A sum of exponentials is 1 and the rest, and they stay apart to the end (LossCall::partial): log(1 + rest) of a confident
+// row has the rest's digits.  The largest logit stays apart from that logarithm too: a loss is the target's distance from the
+// largest logit, 0 where it is that, plus the logarithm.
 constexpr int kCombineWarps = 32;
 static_assert(kCombineWarps == kLossBlockRows, "a warp a row joins the warps' parts");
 
 template <bool TWO>
-__global__ void __launch_bounds__(32 * kCombineWarps) k_combine(const __grid_constant__ LossGroup g, const __grid_constant__ LossCall c,
-                                                      float* loss) {
+__global__ void __launch_bounds__(32 * kCombineWarps, 1) k_combine(const __grid_constant__ LossGroup g,
+                                                                   const __grid_constant__ LossCall c, float* loss) {
     using Part = std::conditional_t<TWO, float4, float2>;
     __shared__ float tops[kCombineWarps][33], sums[kCombineWarps][33], sums2[kCombineWarps][33];
     __shared__ float losses[32];
@@ -323,15 +327,24 @@ __global__ void __launch_bounds__(32 * kCombineWarps) k_combine(const __grid_con
                 top = fmaxf(top, p[e].x);
             }
             const float ref = top == -INFINITY ? 0.f : top;
-            s *= exp2f((m - ref) * k1);
-            if constexpr (TWO) s2 *= exp2f((m - ref) * k2);
+            int ones = 0;
+            // a sum's rest and its 1 relative to the new reference.  A unit of nothing but -infinity, or none: 0; of those
+            // and NaN, which no maximum shows, NaN
+            const auto term = [&](float x, float rest, float k) {
+                const float scale = exp2f((x - ref) * k);
+                return fmaf(rest, scale, x == ref ? 0.f : scale);
+            };
+            s = term(m, s, k1);
+            if constexpr (TWO) s2 = term(m, s2, k2);
+            ones += m == ref;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                // a unit of nothing but -infinity, or none: 0; of those and NaN, which no maximum shows: NaN
-                const bool none = p[e].x == -INFINITY;
-                s += none ? p[e].y : p[e].y * exp2f((p[e].x - ref) * k1);
-                if constexpr (TWO) s2 += none ? p[e].z : p[e].z * exp2f((p[e].x - ref) * k2);
+                s += term(p[e].x, p[e].y, k1);
+                if constexpr (TWO) s2 += term(p[e].x, p[e].z, k2);
+                ones += p[e].x == ref;
             }
+            s += (float)max(ones - 1, 0);
+            if constexpr (TWO) s2 += (float)max(ones - 1, 0);
             m = top;
         }
         tops[warp][lane] = m;
@@ -342,24 +355,28 @@ __global__ void __launch_bounds__(32 * kCombineWarps) k_combine(const __grid_con
         const int rr = block * kLossBlockRows + warp;
         if (rr - g.row0[i] < count) {
             const float part = tops[lane][warp], top = warp_max(part), ref = top == -INFINITY ? 0.f : top;
-            const float sum = warp_sum(sums[lane][warp] * exp2f((part - ref) * k1));
-            const float sum2 = TWO ? warp_sum(sums2[lane][warp] * exp2f((part - ref) * k2)) : 0.f;
-            const float logit = c.unit * top;
-            const float a = logit * (TWO ? 1.f : c.inv_temperature) + logf(sum), b = TWO ? logit * c.inv_temperature + logf(sum2) : a;
+            const int more = max(__popc(__ballot_sync(0xffffffffu, part == ref)) - 1, 0);
+            const auto join = [&](float rest, float k) {
+                const float scale = exp2f((part - ref) * k);
+                return warp_sum(fmaf(rest, scale, part == ref ? 0.f : scale)) + (float)more;
+            };
+            const float rest = join(sums[lane][warp], k1), rest2 = TWO ? join(sums2[lane][warp], k2) : rest;
+            const bool none = top == -INFINITY;        // no terms at all: no 1 either
+            const float log1 = none ? logf(rest) : log1pf(rest), log2 = TWO ? (none ? logf(rest2) : log1pf(rest2)) : log1;
             if (c.value && lane == 0) {
-                float4 coef = make_float4(a * kLog2e, 1.f, 0.f, 0.f);
+                const float sum = none ? rest : 1.f + rest, sum2 = none ? rest2 : 1.f + rest2;
+                float4 coef = make_float4(ref, 1.f / sum, 0.f, 0.f);
                 if (TWO) {
-                    coef.y = 1.f - c.alpha;
-                    coef.z = b * kLog2e;
-                    coef.w = c.alpha * c.temperature;
+                    coef.y = (1.f - c.alpha) / sum;
+                    coef.w = c.alpha * c.temperature / sum2;
                 } else if (c.alpha != 0.f) {           // alpha 1, or temperature 1
-                    coef.y = 1.f - c.alpha + c.alpha * c.temperature;
+                    coef.y = (1.f - c.alpha + c.alpha * c.temperature) / sum;
                 }
                 c.coef[rr] = coef;
             }
             if (c.alpha == 0.f) {
                 if (lane == 0) {
-                    const float d = c.z[rr] - a;
+                    const float d = c.unit * (c.z[rr] - ref) - log1;
                     losses[warp] = -d;
                     if (c.value) c.value[rr] = expm1f(d);
                 }
@@ -368,9 +385,9 @@ __global__ void __launch_bounds__(32 * kCombineWarps) k_combine(const __grid_con
                 const int n = c.starts[token * (c.units + 1) + c.units];
                 float cross = 0.f, hard = 0.f;
                 for (int e = lane; e < n; e += 32) {
-                    const float q = c.share[at + e], z = c.z[at + e];
-                    if (q < 0.f) hard += a - z;        // the target's entry (its lse is the first: alpha < 1)
-                    else if (q != 0.f) cross += q * (b - z * c.inv_temperature);
+                    const float q = c.share[at + e], z = c.unit * (c.z[at + e] - ref);
+                    if (q < 0.f) hard += log1 - z;     // the target's entry (its sum is the first: alpha < 1)
+                    else if (q != 0.f) cross += q * (log2 - z * c.inv_temperature);
                     if (!c.value) continue;
                     // entries of one column follow each other, and hold one gradient
                     const int32_t column = c.columns[at + e];
@@ -382,8 +399,10 @@ __global__ void __launch_bounds__(32 * kCombineWarps) k_combine(const __grid_con
                         if (o < 0.f) targets += 1.f;
                         else shares += o;
                     }
-                    const float soft = c.alpha * c.temperature * (expf(z * c.inv_temperature - b) - shares);
-                    const float label = c.alpha < 1.f ? (1.f - c.alpha) * (expf(z - a) - targets) : 0.f;
+                    // e^x - q; where both may be near 1, from e^x - 1
+                    const auto less = [](float x, float q) { return x > -0.7f ? expm1f(x) + (1.f - q) : expf(x) - q; };
+                    const float soft = c.alpha * c.temperature * less(z * c.inv_temperature - log2, shares);
+                    const float label = c.alpha < 1.f ? (1.f - c.alpha) * less(z - log1, targets) : 0.f;
                     c.value[at + e] = soft + label;
                 }
                 cross = warp_sum(cross);
@@ -426,7 +445,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) k_combine(const __grid_con
 }
 
 // ---- kept exponentials to the logits' gradients ---------------------------------------
-// dz / f = e 2^(reference - lse): what the products' own epilogue computes where exponentials are not kept, from 11 bits
+// dz / f = e 2^(reference - largest) / sum: what the products' own epilogue computes where exponentials are not kept, from 11 bits
 // of them for bf16 operands and all for float32.  Of two softmaxes the flatter one's exponentials x are kept; the other's
 // are x^r with r <= kKeepPower, which multiplies their rounding by r.  A warp takes kConvertColumns columns of a row.
 // Memory bound: 8 x 1024 x 50257 bf16, 1.65 GB read and written, in 0.24 ms.
@@ -500,7 +519,7 @@ __global__ void __launch_bounds__(kThreads) k_convert(const __grid_constant__ Lo
                     v[2 * e + 1] = f.y;
                 }
             }
-            const float b1 = fmaf(ref, k1, -coef.x), b2 = fmaf(ref, k2, -coef.z);
+            const float b1 = (ref - coef.x) * k1, b2 = (ref - coef.x) * k2;
             if (TWO) {
                 const float own = flat ? exp2f(b2 - kBits) * coef.w : exp2f(b1 - kBits) * coef.y;
                 const float other = (flat ? b1 : b2) - kBits * r, factor = flat ? coef.y : coef.w;

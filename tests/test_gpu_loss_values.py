@@ -101,7 +101,7 @@ def test_logits_of_minus_infinity_have_no_share(tokens, vocab, dim):
     assert float((out["token_losses"][0].double() - want).abs().max()) <= bound
 
 
-CONFIDENT = [(16, 100, 32)]
+CONFIDENT = [(16, 100, 32), (100, 769, 128), (60, 5000, 64)]
 
 
 def _confident(tokens, vocab, dim, dtype, top, seed):
@@ -156,7 +156,29 @@ def test_losses_of_confident_tokens_keep_their_digits(tokens, vocab, dim, dtype,
     assert float((got / dz - 1).abs().max()) <= rel
 
 
-@pytest.mark.parametrize("tokens,vocab,dim", [(16, 100, 32)])
+@pytest.mark.parametrize("tokens,vocab,dim", CONFIDENT)
+@TYPES
+@pytest.mark.parametrize("op", ["ce", "distill"])
+@pytest.mark.parametrize("places", [[0, 1], [3, -1], [0, 50, 99], list(range(100))])
+def test_equal_largest_logits_count_each(tokens, vocab, dim, dtype, op, places):
+    # several columns hold the largest logit, in one unit of 128 and in many; the others lie 8 to 20 below
+    x, z = _confident(tokens, vocab, dim, dtype, 64, seed=7)
+    places = sorted({(p if p < 0 else p * vocab // 100) % vocab for p in places})
+    w = x["weights"][0]
+    w[:, :tokens] = torch.where(w[:, :tokens] == 64, torch.full_like(w[:, :tokens], 56), w[:, :tokens])
+    w[places, :tokens] = 64
+    x["targets"][0][:] = places[-1]
+    x["indices"][0][:] = places[-1]
+    z = w[:, :tokens].double().t()
+    out = _run(x, op, grads=False, reduction=ddp.DDP_LOSS_SUM)
+    loss1, loss2 = (-torch.log_softmax(z / tau, 1)[:, places[-1]] for tau in (1.0, 2.0))
+    want = loss1 if op == "ce" else 0.5 * loss1 + 0.5 * 4.0 * loss2
+    # as above, of losses from log 2 on; the sums' steps are relative to them, log 2 is 0.69
+    rel = (20 * (4 * 2.0 ** -24 + 1.6e-8 * dim / 16) + 2 * 2.0 ** -22 + 64 * 2.0 ** -24) / 0.69
+    assert float((out["token_losses"][0].double() / want - 1).abs().max()) <= rel
+
+
+@pytest.mark.parametrize("tokens,vocab,dim", [(16, 100, 32), (300, 769, 128)])
 @TYPES
 @pytest.mark.parametrize("top", [15.0, 90.0, 1000.0])
 def test_no_loss_is_below_zero(tokens, vocab, dim, dtype, top):
