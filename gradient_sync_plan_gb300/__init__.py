@@ -270,7 +270,8 @@ def ddp_abi_version() -> int:
 
 
 def ddp_device_status(clear: bool = True) -> int:
-    """The sticky device status word (0, or DDP_ERR_TIMEOUT); synchronise first."""
+    """The sticky device status word (0, DDP_ERR_TIMEOUT, or DDP_ERR_INVALID for a loss's
+    column outside the vocabulary); synchronise first."""
     v = ctypes.c_int32(0)
     _check("ddp_device_status", lib().ddp_device_status(ctypes.byref(v), 1 if clear else 0))
     return int(v.value)

@@ -148,6 +148,11 @@ cudaError_t launch_loss_small(const LossGroup& g, const LossCall& c, LossSmall m
 // Lets a kernel take this much dynamic shared memory, once a process and device.
 cudaError_t allow_shared_memory(const void* kernel, int bytes);
 
+#ifdef __CUDACC__
+// The device status word: DDP_ERR_INVALID leaves a DDP_ERR_TIMEOUT as it is, whose buffers hold partial results.
+__device__ __forceinline__ void report_invalid(int32_t* status) { atomicCAS(status, (int32_t)DDP_OK, (int32_t)DDP_ERR_INVALID); }
+#endif
+
 // The address of the device status word, and the TMA kernels' wait limit (ring_tma.cu).
 cudaError_t device_status_address(int32_t** word);
 unsigned long long wait_limit_ns();

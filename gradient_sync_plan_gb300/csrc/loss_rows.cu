@@ -45,7 +45,7 @@ __device__ __forceinline__ int padded(int count) { return (count + kTileK - 1) /
 __device__ __forceinline__ bool learned(int64_t y, const LossCall& c) {
     if (y == c.ignore_index) return false;
     if (y >= 0 && y < c.vocab) return true;
-    atomicExch(c.status, DDP_ERR_INVALID);
+    report_invalid(c.status);
     return false;
 }
 
@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kThreads) k_teacher(const __grid_constant__ Lo
                 const int64_t j = g.indices[i][base + k];
                 const float x = c.teacher_dtype == DDP_F32 ? static_cast<const float*>(g.teacher[i])[base + k]
                                                            : bf16_to_f32(static_cast<const uint16_t*>(g.teacher[i])[base + k]);
-                if (j >= c.vocab) atomicExch(c.status, DDP_ERR_INVALID);
+                if (j >= c.vocab) report_invalid(c.status);
                 const bool there = j >= 0 && j < c.vocab && x != -INFINITY;
                 column[warp][k] = there ? (int32_t)j : INT32_MAX;
                 share[warp][k] = x;

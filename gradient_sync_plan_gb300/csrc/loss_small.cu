@@ -46,7 +46,7 @@ __device__ __forceinline__ bool is_learned(const LossGroup& g, const LossCall& c
         const int64_t y = g.targets[i][t];
         if (y == c.ignore_index) return false;
         if (y < 0 || y >= c.vocab) {
-            if (report) atomicExch(c.status, DDP_ERR_INVALID);
+            if (report) report_invalid(c.status);
             return false;
         }
     }
@@ -54,7 +54,7 @@ __device__ __forceinline__ bool is_learned(const LossGroup& g, const LossCall& c
     bool any = false;
     for (int k = lane; k < c.n_teacher; k += 32) {
         const int64_t at = (int64_t)t * c.n_teacher + k, j = g.indices[i][at];
-        if (report && j >= c.vocab) atomicExch(c.status, DDP_ERR_INVALID);
+        if (report && j >= c.vocab) report_invalid(c.status);
         const float x = c.teacher_dtype == DDP_F32 ? load<true>(g.teacher[i], at) : load<false>(g.teacher[i], at);
         any |= j >= 0 && j < c.vocab && x != -INFINITY;
     }

@@ -42,7 +42,7 @@
 
 namespace ddpk {
 
-__device__ int32_t g_device_status = 0;     // sticky DDP_ERR_TIMEOUT flag, read by ddp_device_status()
+__device__ int32_t g_device_status = 0;     // sticky, read by ddp_device_status(): DDP_ERR_TIMEOUT, or report_invalid's
 
 constexpr int kTmaStages = 2;
 constexpr int kTmaConsumerWarps = 8;

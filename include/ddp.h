@@ -154,8 +154,10 @@ int32_t ddp_set_fused_kernel(int32_t kind, int32_t* previous);
  * current device: DDP_OK, or DDP_ERR_TIMEOUT if a kernel's bounded wait on an
  * asynchronous copy gave up (the kernel then stopped early, so the buffers
  * of that call hold partial results), or DDP_ERR_INVALID if a loss met a target
- * or a teacher's index that is no column of the vocabulary.  Synchronous: call it after the
- * stream of interest has been synchronised.  clear != 0 resets the word.
+ * or a teacher's index that is no column of the vocabulary (which was left out;
+ * everything else of that call is there).  Of both, in either order, the word
+ * holds DDP_ERR_TIMEOUT.  Synchronous: call it after the stream of interest has
+ * been synchronised.  clear != 0 resets the word.
  * Returns DDP_OK, DDP_ERR_INVALID (status NULL) or DDP_ERR_CUDA.
  */
 int32_t ddp_device_status(int32_t* status, int32_t clear);
