@@ -763,16 +763,19 @@ __device__ __forceinline__ void grad_tile(const LossGemm& g, const Tile& w, cons
     }
 }
 
+// What the sum over a tile's depth lost, relative to it.
+__device__ __forceinline__ float cut_of(const Tile& w) { return kCutPerStep * (float)((w.k1 - w.k0) * (kTileK / 16)); }
 // A gradient's factor, and what its sum lost where the tensor cores cut it (kCutPerStep) if the result is float32; of
 // the six passes the last adds what counts.
 template <bool F32>
 __device__ __forceinline__ float factor_of(const Tile& w, const Control* s) {
     const float f = s->factors[w.rank];
-    return F32 ? f + f * (kCutPerStep * (float)((w.k1 - w.k0) * (kTileK / 16))) : f;
+    return F32 ? fmaf(f, cut_of(w), f) : f;
 }
 
 // dh: the tile goes to its split's part of acc, added there by the copy engine from the second piece on (one
 // writer an element and launch, so the order is fixed).
+template <bool F32>
 __device__ __forceinline__ void hidden_tile(const LossGemm& g, const Tile& w, const Lane& l, uint64_t* taken) {
 #pragma unroll 1
     for (int j = 0; j < kTileN / 2 / 32; ++j) {
@@ -791,6 +794,10 @@ __device__ __forceinline__ void hidden_tile(const LossGemm& g, const Tile& w, co
             else tma_read_done();
         }
         group_sync(l.group);
+        if constexpr (F32) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = fmaf(v[i], cut_of(w), v[i]);
+        }
         stage_floats(l, v);
         to_async_proxy();
         group_sync(l.group);
@@ -977,7 +984,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_loss_gemm(const __grid_cons
             if (PHASE == LossPhase::kStats || PHASE == LossPhase::kKeep)
                 stats_tile<F32, TWO, LIST, PHASE == LossPhase::kKeep>(g, w, l, s, taken);
             else if (PHASE == LossPhase::kGrad) grad_tile<F32, TWO, LIST>(g, w, l, s, taken);
-            else if (!w.weights()) hidden_tile(g, w, l, taken);
+            else if (!w.weights()) hidden_tile<F32>(g, w, l, taken);
             else weights_tile<F32>(g, w, l, s, taken);
             if (buf == 1) phase ^= 1;
             buf ^= 1;

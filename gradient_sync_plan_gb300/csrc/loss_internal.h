@@ -21,8 +21,9 @@ constexpr int kTileM = 128, kTileN = 256, kTileK = 64;
 
 // The tensor cores cut a sum's low bits where they add 16 products to it, so sums come out a little small: by 1.6e-8 of
 // the result a step of 16 where the sum grows evenly or wanders (measured on sums of 256 to 16384 products of either
-// sign, 1.4e-8 to 1.6e-8; of one sign 2.5e-8 and more).  Sums whose float32 is the result, and logits, are scaled back
-// by that: 4096 products' mean error of 4.0e-6 becomes 0.1e-6, of products of one sign 1.4e-5 becomes 1.0e-5.
+// sign, 1.4e-8 to 1.6e-8; of one sign 2.5e-8 and more).  Logits and float32 gradients, each part of a depth taken out of
+// tensor memory by itself, are scaled back by that: 4096 products' mean error of 4.0e-6 becomes 0.1e-6, of products of one
+// sign 1.4e-5 becomes 1.0e-5.
 constexpr float kCutPerStep = 1.6e-8f;
 
 // One group of ranks as the row kernels see it.  Rows are numbered through all
