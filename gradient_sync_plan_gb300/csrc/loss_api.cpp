@@ -317,7 +317,11 @@ int32_t run(ddp_loss_head* h, const Args& a, cudaStream_t stream) {
     c.temperature = (float)a.temperature;
     c.inv_temperature = (float)(1.0 / a.temperature);
     c.two = distill && c.alpha < 1.f && c.temperature != 1.f;
-    c.unit = 1.f + kCutPerStep * (float)(c.dimp / 16);
+    // 1 + cut itself may lie between two floats: it multiplies in double here, and by fmaf in the kernels
+    const double cut = (double)kCutPerStep * (c.dimp / 16), bits = 1.4426950408889634 * (1.0 + cut);
+    c.cut = (float)cut;
+    c.k2 = (float)(bits / a.temperature);
+    c.k1 = c.two ? (float)bits : c.k2;
     c.hidden_stride = a.hidden_stride;
     c.ignore_index = a.ignore_index;
     c.scale = (float)a.scale;

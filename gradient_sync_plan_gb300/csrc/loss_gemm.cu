@@ -56,7 +56,6 @@ constexpr int kBytesBox = 64 * 64 * 2;
 constexpr int kBytesStaging = 128 * 128;               // 128 rows of 128 bytes
 constexpr int kFirstEpilogueWarp = 4, kEpilogueWarps = 8;
 constexpr int kGemmThreads = 32 * (kFirstEpilogueWarp + kEpilogueWarps);
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kKeepScale = (float)(1 << kKeepBits);
 
 // A tile: rank (-1: no more tiles), first row (of all ranks' rows; a column of the piece for dw), first column, columns (of
@@ -585,7 +584,7 @@ __device__ __forceinline__ void stats_tile(const LossGemm& g, const Tile& w, con
     const bool valid = row - g.row0[w.rank] < s->counts[w.rank];
     Listed<LIST> hit;
     hit.start(c, row, LIST && valid ? g.row0[w.rank] + c.row_token[row] : 0, first, valid && first < c.vocab);
-    const float k1 = c.unit * (TWO ? kLog2e : c.inv_temperature * kLog2e), k2 = c.unit * (c.inv_temperature * kLog2e);
+    const float k1 = c.k1, k2 = c.k2;
     if (KEEP) {
         if (l.leader) tma_read_done();
         group_sync(l.group);               // the staging buffer is free
@@ -704,7 +703,7 @@ __device__ __forceinline__ void grad_tile(const LossGemm& g, const Tile& w, cons
     Listed<LIST> hit;
     hit.start(c, row, LIST && valid ? g.row0[w.rank] + c.row_token[row] : 0, first, valid && first < c.vocab);
     const float4 coef = valid ? c.coef[row] : make_float4(0.f, 0.f, 0.f, 0.f);
-    const float k1 = c.unit * (TWO ? kLog2e : c.inv_temperature * kLog2e), k2 = c.unit * (c.inv_temperature * kLog2e);
+    const float k1 = c.k1, k2 = c.k2;
 #pragma unroll 1
     for (int j = 0; j < kLossUnit / 64; ++j) {
         float v[64];

@@ -52,7 +52,9 @@ struct LossCall {
     int64_t hidden_stride, ignore_index;
     float inv_temperature, temperature;   // of the distillation
     float alpha;                          // its share; 0: cross entropy alone
-    float unit;                           // what the tensor cores' logits are multiplied by (kCutPerStep)
+    float cut;                            // of the tensor cores' logits' sums (kCutPerStep)
+    float k1, k2;                         // from a difference of them to bits: log2 e (1 + cut), of the softmax or the first
+                                          // of two, and at the temperature
     float scale;                          // of the gradients
     int64_t rows;                         // rows of all ranks
 
@@ -67,10 +69,10 @@ struct LossCall {
     uint16_t* starts;                     // [rows][units + 1] by token: entries before a unit
     float* share;                         // [rows][list] by token: teacher's probability of the entry
     float* entropy;                       // [rows] by token: sum of q log q
-    float* z;                             // [rows][list] logits at the listed columns, without `unit`
+    float* z;                             // [rows][list] the tensor cores' logits at the listed columns
     float* value;                         // [rows][list] gradients there, without the factor
-    float* partial;                       // [units][rows] float2, or float4 for two temperatures: the largest logit (without
-                                          // `unit`), and the sum of exponentials relative to it but for one of the largest
+    float* partial;                       // [units][rows] float2, or float4 for two temperatures: the tensor cores' largest
+                                          // logit, and the sum of exponentials relative to it but for one of the largest
     float* factor;                        // [world] of the gradients: scale and reduction
     float4* coef;                         // [rows] {largest logit, share over the sum of exponentials relative to it, -, the
                                           // same at the temperature}

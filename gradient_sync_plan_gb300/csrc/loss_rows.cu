@@ -16,7 +16,6 @@
 namespace ddpk {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMostList = DDP_MAX_TEACHER + 1;
 
@@ -299,7 +298,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps, 1) k_combine(const __grid_
         if (lane == 0) total = n;
     }
     __syncthreads();
-    const float k1 = c.unit * (TWO ? kLog2e : c.inv_temperature * kLog2e), k2 = c.unit * (c.inv_temperature * kLog2e);
+    const float k1 = c.k1, k2 = c.k2;
     const int first = g.row0[0] / kLossBlockRows, last = g.row0[g.n] / kLossBlockRows;
     for (int block = first + blockIdx.x; block < last; block += gridDim.x) {
         const int row = block * kLossBlockRows + lane, i = rank_of(g, block * kLossBlockRows);
@@ -362,6 +361,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps, 1) k_combine(const __grid_
             };
             const float rest = join(sums[lane][warp], k1), rest2 = TWO ? join(sums2[lane][warp], k2) : rest;
             const bool none = top == -INFINITY;        // no terms at all: no 1 either
+            const auto logit = [&](float z) { return fmaf(z - ref, c.cut, z - ref); };     // relative to the largest
             const float log1 = none ? logf(rest) : log1pf(rest), log2 = TWO ? (none ? logf(rest2) : log1pf(rest2)) : log1;
             if (c.value && lane == 0) {
                 const float sum = none ? rest : 1.f + rest, sum2 = none ? rest2 : 1.f + rest2;
@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps, 1) k_combine(const __grid_
             }
             if (c.alpha == 0.f) {
                 if (lane == 0) {
-                    const float d = c.unit * (c.z[rr] - ref) - log1;
+                    const float d = logit(c.z[rr]) - log1;
                     losses[warp] = -d;
                     if (c.value) c.value[rr] = expm1f(d);
                 }
@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps, 1) k_combine(const __grid_
                 const int n = c.starts[token * (c.units + 1) + c.units];
                 float cross = 0.f, hard = 0.f;
                 for (int e = lane; e < n; e += 32) {
-                    const float q = c.share[at + e], z = c.unit * (c.z[at + e] - ref);
+                    const float q = c.share[at + e], z = logit(c.z[at + e]);
                     if (q < 0.f) hard += log1 - z;     // the target's entry (its sum is the first: alpha < 1)
                     else if (q != 0.f) cross += q * (log2 - z * c.inv_temperature);
                     if (!c.value) continue;
@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(kThreads) k_convert(const __grid_constant__ Lo
     pdl_release();
     pdl_acquire();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const float k1 = c.unit * (TWO ? kLog2e : c.inv_temperature * kLog2e), k2 = c.unit * (c.inv_temperature * kLog2e);
+    const float k1 = c.k1, k2 = c.k2;
     const bool flat = TWO && k2 < k1;                  // the second softmax's were kept
     const float r = TWO ? (flat ? k1 / k2 : k2 / k1) : 1.f;
     const int64_t parts = (width + kConvertColumns - 1) / kConvertColumns;

@@ -39,6 +39,22 @@ def test_logits_are_not_small_on_average(dim, tokens, dtype):
     assert abs(_bias(losses, z + torch.log1p(torch.exp(-z)))) < 0.5 * CUT * dim / 16
 
 
+@TYPES
+def test_a_small_correction_is_no_larger_than_it_is(dtype):
+    # logits that are exact, over a depth whose correction, 6.4e-8, is no multiple of a float's step from 1: they may come
+    # out larger by it and half of it, not by 1.2e-7
+    tokens, dim = 2000, 64
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    w = torch.zeros(2, dim, device="cuda")
+    w[1] = (32.0 + 31.0 * torch.rand(dim, device="cuda", generator=gen)).bfloat16().float()
+    h = torch.eye(dim, device="cuda").repeat(tokens // dim + 1, 1)[:tokens]
+    losses = torch.empty(tokens, device="cuda")
+    ddp.LossHead([w.to(dtype)], max_tokens=tokens).cross_entropy([h.to(dtype)], [torch.zeros(tokens, dtype=torch.int64, device="cuda")],
+                                                                 token_losses=[losses])
+    torch.cuda.synchronize()
+    assert abs(_bias(losses, h.double() @ w[1].double())) < 1.5 * CUT * dim / 16
+
+
 @pytest.mark.parametrize("tokens,vocab,dim", [(1024, 50257, 512), (2000, 20000, 1024), (1500, 2048, 256)])
 def test_float32_gradients_are_not_small_on_average(tokens, vocab, dim):
     # of 1024 of the depth (or all of it) a part: 1e-6; an element's own error, some 1e-6 of the mean, over 1e5 elements
