@@ -31,7 +31,7 @@ def hidden_states(weights, tokens):
 
 
 def train(ranks: int = 4, steps: int = 50, distill: bool = False, max_norm: float = 1.0, seed: int = 0):
-    """Returns every step's mean loss over all tokens, and the last step's inputs and gradients of every rank."""
+    """Returns every step's mean loss over all tokens, and the last step's inputs, losses and gradients of every rank."""
     gen = torch.Generator(device="cuda").manual_seed(seed)
     rand = lambda *shape: torch.randn(*shape, device="cuda", generator=gen)
     follows = torch.randperm(VOCAB, device="cuda", generator=gen)         # the language: each token has a successor
@@ -68,7 +68,7 @@ def train(ranks: int = 4, steps: int = 50, distill: bool = False, max_norm: floa
             loss = head.cross_entropy_grad(states, grad_hidden=grad_hidden, **how)
         if last is None or len(losses) == steps - 1:
             last = dict(states=states, targets=targets, teacher=teacher, weights=[row[0].detach().clone() for row in copies],
-                        head=[row[0].clone() for row in grads], grad_hidden=grad_hidden)
+                        head=[row[0].clone() for row in grads], grad_hidden=grad_hidden, loss=loss.clone())
         for r in range(ranks):
             fresh = torch.autograd.grad(hidden[r], copies[r], grad_hidden[r])
             grads[r][0] += fresh[0]                                       # the embedding's rows, beside the head's
