@@ -131,7 +131,7 @@ def test_losses_of_confident_tokens_keep_their_digits(tokens, vocab, dim, dtype,
     Relative error of the rest: an exponent of up to 20 from three roundings (2^-24 each) and the logits' own scale for the
     tensor cores (1.6e-8 a 16 of the depth, itself rounded by 2^-24), an exponential's 2^-22, a sum's 2^-24 times its 64
     additions in a row at most; a logarithm adds 2^-22.  Gradients are 1 / (1 + rest) times that with one more exponential
-    and, of bf16, two roundings: kept exponentials' 2^-12, times 2 for the steeper softmax's, and bf16's 2^-8."""
+    and, of bf16, two roundings: kept exponentials' 2^-11 (11 bits), times 2 for the steeper softmax's, and bf16's 2^-8."""
     x, z = _confident(tokens, vocab, dim, dtype, top, seed=4)
     out = _run(x, op, reduction=ddp.DDP_LOSS_SUM)
     y = x["targets"][0].unsqueeze(1)
@@ -152,7 +152,7 @@ def test_losses_of_confident_tokens_keep_their_digits(tokens, vocab, dim, dtype,
     dz = p1 if op == "ce" else 0.5 * p1 + 0.5 * 2.0 * p2
     got = out["gw"][0].double().t()[:tokens]
     # float32 products: three parts of a gradient, their sum scaled for one step of depth's cut at each k block
-    rel += 2.0 ** -22 + (2 * 2.0 ** -12 + 2.0 ** -8 if dtype == BF16 else 2.0 ** -22 + 2.0 ** -18)
+    rel += 2.0 ** -22 + (2 * 2.0 ** -11 + 2.0 ** -8 if dtype == BF16 else 2.0 ** -22 + 2.0 ** -18)
     assert float((got / dz - 1).abs().max()) <= rel
 
 
