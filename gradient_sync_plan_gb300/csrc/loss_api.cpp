@@ -434,11 +434,15 @@ int32_t run(ddp_loss_head* h, const Args& a, cudaStream_t stream) {
             m.hidden = hidden[across];
             for (int i = 0; i < g.n; ++i) m.weights[i] = h->maps[2 * (g.first + i) + across];
         };
+        const auto products = [&](LossPhase phase) {
+            m.stall = take_planted_stall();
+            return cuda_status(launch_loss_gemm(phase, m, stream));
+        };
         operands(false);
         if (span > 0) {
             m.piece0 = 0;
             m.width = h->vocab;
-            if ((st = cuda_status(launch_loss_gemm(keep ? LossPhase::kKeep : LossPhase::kStats, m, stream)))) return st;
+            if ((st = products(keep ? LossPhase::kKeep : LossPhase::kStats))) return st;
         }
         if ((st = cuda_status(launch_loss_combine(g, c, a.loss, stream)))) return st;
         if (!a.grad) continue;
@@ -448,9 +452,9 @@ int32_t run(ddp_loss_head* h, const Args& a, cudaStream_t stream) {
             m.add = v > 0;
             operands(false);
             if (keep) st = cuda_status(launch_loss_convert(g, c, h->dtype == DDP_F32 ? w + at.kept : w + at.piece, w + at.piece, width, stream));
-            else st = cuda_status(launch_loss_gemm(LossPhase::kGrad, m, stream));
+            else st = products(LossPhase::kGrad);
             operands(true);
-            if (st || (st = cuda_status(launch_loss_gemm(LossPhase::kProducts, m, stream)))) return st;
+            if (st || (st = products(LossPhase::kProducts))) return st;
         }
         if (span > 0 && (st = cuda_status(launch_loss_join(g, c, m.splits, stream)))) return st;
     }

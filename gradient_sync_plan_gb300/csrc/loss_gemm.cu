@@ -65,6 +65,7 @@ struct alignas(16) Tile {
     int32_t flags;
     __device__ __forceinline__ bool weights() const { return flags & 1; }      // of dw
     __device__ __forceinline__ bool more() const { return flags & 2; }         // added to the depth before
+    __device__ __forceinline__ bool stalls() const { return flags & 4; }       // where a planted stall begins
 };
 // float32 sums are taken out of tensor memory and added up elsewhere every so many k blocks: the tensor cores cut what they
 // add to a long sum (kCutPerStep), by 2e-5 of the result over a depth of 50257.
@@ -339,6 +340,7 @@ __device__ void schedule(const LossGemm& g, Control* s) {
     while (more) {
         Tile w;
         more = find_tile<PHASE>(g, s->counts, t, &w);
+        if (more && t == g.stall) w.flags |= 4;
         if (more) t = (int)gridDim.x + atomicAdd(g.c.next, 1);
         else w.rank = -1;
         const int end = w.k1;
@@ -409,7 +411,7 @@ __device__ void produce(const LossGemm& g, Control* s, char* stages) {
     bool ok = true;
     Queue queue;
     Tile w;
-    while (ok && queue.next(s, g, &w)) {
+    while (ok && queue.next(s, g, &w) && !w.stalls()) {
         const CUtensorMap* wmap = &g.weights[w.rank];
         for (int q = 0; ok && q < (F32 ? 6 : 1); ++q) {
             const int pa = F32 ? kPlaneA[q] : 0, pb = F32 ? kPlaneB[q] : 0;

@@ -108,6 +108,7 @@ struct LossGemm {
     int32_t accumulate;                   // add to the weights' gradients
     int32_t store;                        // the copy engine writes them: 16-byte aligned rows, not accumulated
     unsigned long long limit_ns;
+    int64_t stall;                        // the tile from which on its block loads nothing (ddp_plant_stall), -1: none
     LossCall c;
 };
 static_assert(sizeof(LossGemm) < 8192, "travels in the kernel's parameters");
@@ -156,8 +157,10 @@ cudaError_t allow_shared_memory(const void* kernel, int bytes);
 __device__ __forceinline__ void report_invalid(int32_t* status) { atomicCAS(status, (int32_t)DDP_OK, (int32_t)DDP_ERR_INVALID); }
 #endif
 
-// The address of the device status word, and the TMA kernels' wait limit (ring_tma.cu).
+// The address of the device status word, the TMA kernels' wait limit, and a tile that a test has planted for the next
+// launch's loads to stop at, or -1 (ring_tma.cu).
 cudaError_t device_status_address(int32_t** word);
 unsigned long long wait_limit_ns();
+long long take_planted_stall();
 
 }  // namespace ddpk

@@ -447,12 +447,14 @@ namespace {
 std::atomic<unsigned long long> g_wait_limit_ns{2000000000ull};   // ddp_set_wait_limit_ms
 std::atomic<long long> g_stall_tile{-1};                          // ddp_plant_stall (one launch)
 
+long long take_stall() { return g_stall_tile.load(std::memory_order_relaxed) < 0 ? -1 : g_stall_tile.exchange(-1); }
+
 // Control of one launch: the current limit, and a planted stall, which only
 // this launch takes.
 TmaCtl take_ctl() {
     TmaCtl c;
     c.limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
-    c.stall_tile = g_stall_tile.load(std::memory_order_relaxed) < 0 ? -1 : g_stall_tile.exchange(-1);
+    c.stall_tile = take_stall();
     return c;
 }
 
@@ -669,6 +671,8 @@ void set_wait_limit_ns(unsigned long long ns, unsigned long long* previous) {
 void plant_stall(long long tile) { g_stall_tile.store(tile < 0 ? -1 : tile); }
 
 unsigned long long wait_limit_ns() { return g_wait_limit_ns.load(); }
+
+long long take_planted_stall() { return take_stall(); }
 
 cudaError_t device_status_address(int32_t** word) {
     void* p = nullptr;

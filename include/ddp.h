@@ -180,10 +180,10 @@ int32_t ddp_set_wait_limit_ms(int32_t limit_ms, int32_t* previous_ms);
 /*
  * ddp_plant_stall -- a test hook that plants the hang of [P2] "常见疑问" Q2 on
  * the GPU.  The next launch of a TMA-staged kernel (see
- * ddp_set_wait_limit_ms) takes the plant: the producer warp of the CTA that
- * owns tile `tile` of that launch issues no bulk copy for that tile or any
- * later one, and waits for the copies it did issue to be consumed; the CTA's
- * consumers wait for the missing tile until the wait limit runs out, set
+ * ddp_set_wait_limit_ms; of a loss's kernels the products) takes the plant: the
+ * producer warp of the CTA that owns tile `tile` of that launch issues no bulk
+ * copy for that tile or any later one, and waits for the copies it did issue;
+ * the CTA's consumers wait for the missing tile until the wait limit runs out, set
  * DDP_ERR_TIMEOUT and stop.  No copy is left in flight and no memory is
  * touched out of bounds; the call's buffers hold partial results.  A tile
  * number beyond the launch's tiles plants nothing (the launch still takes

@@ -1,4 +1,6 @@
 """Calls of the loss head that follow each other closely: every one ends, and repeats its bits."""
+import time
+
 import pytest
 import torch
 
@@ -64,3 +66,51 @@ def test_one_call_after_another(dtype):
     torch.cuda.synchronize()
     assert _same(rank.results(), want)
     assert ddp.ddp_device_status() == 0
+
+
+TIMEOUT = -4
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("grads,tile", [(False, 0), (False, 11), (True, 5)])
+def test_a_products_wait_that_runs_out_ends_the_call(dtype, grads, tile):
+    """A planted stall: the loads of one block stop before a tile, as if it never came.  Nothing is in flight then and every
+    wait has its limit, 2 s for these kernels, so the call ends, says so, and the next one gives its bits again."""
+    rank = Rank([300, 200], 3000, 192, dtype, 9)          # 2 to 3 tiles of rows by 12 of columns
+
+    def call():
+        if grads:
+            rank.call()
+            return rank.results()
+        return [rank.head.cross_entropy(rank.hidden, rank.targets).clone()]
+
+    ddp.ddp_device_status(clear=True)
+    want = call()
+    torch.cuda.synchronize()
+    limit = ddp.ddp_set_wait_limit_ms(100)
+    try:
+        ddp.ddp_plant_stall(tile)
+        t0 = time.perf_counter()
+        call()
+        torch.cuda.synchronize()
+        dt = time.perf_counter() - t0
+    finally:
+        ddp.ddp_plant_stall(-1)
+        ddp.ddp_set_wait_limit_ms(limit)
+    assert ddp.ddp_device_status(clear=True) == TIMEOUT
+    assert 1.9 <= dt < 8.0, dt
+    for _ in range(2):
+        assert _same(call(), want)
+    torch.cuda.synchronize()
+    assert ddp.ddp_device_status() == 0
+
+
+def test_a_plant_beyond_the_products_tiles_stalls_nothing():
+    rank = Rank([300, 200], 3000, 192, torch.bfloat16, 9)
+    want = rank.head.cross_entropy(rank.hidden, rank.targets).clone()
+    for _ in range(2):
+        ddp.ddp_plant_stall(1 << 40)
+        got = rank.head.cross_entropy(rank.hidden, rank.targets)
+        torch.cuda.synchronize()
+        assert ddp.ddp_device_status() == 0 and torch.equal(got, want)
+    ddp.ddp_plant_stall(-1)
