@@ -31,7 +31,8 @@ namespace {
 // of ranks by group of ranks; else the vocabulary goes in pieces of kPieceBytes.  A piece is written once and read a few
 // times, so that it need not fit the L2.
 constexpr int64_t kKeepBytes = (int64_t)2 << 30, kPieceBytes = (int64_t)512 << 20;
-// Temperatures whose two softmaxes' exponentials come from one another by a power up to this.
+// Temperatures whose two softmaxes' exponentials come from one another by a power up to this: kept ones' rounding (2^-11) is
+// multiplied by it, and 4 leaves it at half of what bf16 rounds off the result (2^-8).
 constexpr float kKeepPower = 4.f;
 constexpr int64_t kSms = 152;
 constexpr int64_t kPieceAlign = 256;              // columns of a piece: a multiple of the tiles'

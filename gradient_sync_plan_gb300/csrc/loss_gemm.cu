@@ -25,9 +25,9 @@
 // significand each); of the nine products of planes the six larger are summed,
 // smallest first: what is left out is below 2^-24 of the terms.
 //
-// Bound by the tensor cores and, in long runs, by power: 8 x 1024 tokens by 50257 x 1024 take 0.50 ms for the logits and
-// 1.01 ms for the products (1.68 PFLOP/s both), 4096 by 131072 x 4096 2.49 and 5.11 ms (1.77 and 1.72).  Tiles are as large
-// as two of them fit tensor memory: 128 x 256.
+// Bound by the tensor cores and, in calls after one another, by power: 8 x 1024 tokens by 50257 x 1024 take 0.55 ms for the
+// logits and 1.03 ms for the products by themselves (1.52 and 1.64 PFLOP/s), 4096 by 131072 x 4096 2.37 and 4.78 ms (1.85
+// and 1.84), in a row 2.61 and 5.48 (1.69 and 1.60).  Tiles are as large as two of them fit tensor memory: 128 x 256.
 //
 // Waits for loads, products, tiles and accumulators are bounded: one that runs
 // out sets DDP_ERR_TIMEOUT in the device status word, the block's roles stop,

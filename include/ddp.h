@@ -801,12 +801,17 @@ int32_t ddp_adamw_destroy(ddp_adamw* adamw);
  * that is >= vocab (a target also < 0 and not ignore_index) makes the device status
  * DDP_ERR_INVALID; such a token, or entry, is left out.
  *
- * Types.  DDP_BF16: products of bf16 values, summed in binary32; the logits'
- * gradients are rounded to bf16 for the two products with them, everything else is
- * binary32 and rounded once at the end.  DDP_F32: operands are split into three bf16
- * parts and the six larger products of parts summed, which loses less than
- * binary32's own rounding.  Sums have a fixed order: the same call gives the same
- * bits, under any ddp_set_max_ctas.
+ * Types.  DDP_BF16: products of bf16 values, summed in binary32.  For the two
+ * products of the gradients each logit's gradient (without scale and reduction) is
+ * rounded to bf16, by 2^-8 of it at most; but for targets and teachers' entries it
+ * comes from an exponential that was kept in 11 bits, which adds 2^-11, with two
+ * softmaxes of temperatures between 1/4 and 4 up to 2^-9.  Statistics, losses and
+ * sums are binary32, results are rounded once at the end.  DDP_F32: operands are
+ * split into three bf16 parts and the six larger products of parts summed, which
+ * loses less than binary32's own rounding; values beyond bf16's largest (3.39e38)
+ * and infinities give NaN.  NaN among a rank's weights, or in a learned token's
+ * hidden states, makes the losses and gradients that it enters NaN.  Sums have a
+ * fixed order: the same call gives the same bits, under any ddp_set_max_ctas.
  *
  *   weights[world]       host table of device pointers, [vocab][dim] of dtype; bf16
  *                        weights with dim a multiple of 64 start on 16-byte boundaries
