@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(kThreads) k_convert(const __grid_constant__ Lo
         for (int j = 0; j < kSteps; ++j) {
             if (first + j * 256 >= width) break;
             const int col = (int)first + j * 256 + lane * 8;
-            const float ref = top[j] == -INFINITY ? 0.f : top[j];
+            const float ref = top[j] == -INFINITY ? coef.x : top[j];       // of nothing but zeros: any that leaves them so
             float v[8];
             if constexpr (F32) {
                 const uint32_t w[8] = {x[j][0].x, x[j][0].y, x[j][0].z, x[j][0].w, x[j][1].x, x[j][1].y, x[j][1].z, x[j][1].w};

@@ -101,6 +101,35 @@ def test_logits_of_minus_infinity_have_no_share(tokens, vocab, dim):
     assert float((out["token_losses"][0].double() - want).abs().max()) <= bound
 
 
+@pytest.mark.parametrize("tokens,vocab,dim", [([16], 100, 32), ([130], 769, 128)])
+@pytest.mark.parametrize("op", ["ce", "distill"])
+@pytest.mark.parametrize("level", [0.0, -200.0, 200.0])
+def test_columns_of_minus_infinity_have_no_gradient(tokens, vocab, dim, op, level):
+    # whole units of 128 columns among them, beside logits around `level`; every other column's gradient is as without them
+    x = _inputs(tokens, vocab, dim, BF16, seed=3)
+    x["hidden"][0][:, :2] = 1.0
+    x["weights"][0][:, 1] = level
+    masked = torch.zeros(vocab, dtype=torch.bool, device="cuda")
+    masked[:64] = True
+    masked[128:384] = True
+    masked[vocab - 1] = True
+    kept = (~masked).nonzero()[:, 0]
+    x["targets"][0] = kept[x["targets"][0] % len(kept)]
+    x["indices"][0] = kept[(torch.arange(6, device="cuda") * 5 + x["targets"][0].unsqueeze(1)) % len(kept)].contiguous()
+    column = torch.full((vocab,), -1, dtype=torch.int64, device="cuda")
+    column[kept] = torch.arange(len(kept), device="cuda")
+    small = dict(x, weights=[x["weights"][0][kept].contiguous()], targets=[column[x["targets"][0]]], indices=[column[x["indices"][0]]])
+    x["weights"][0][masked, 0] = -float("inf")
+    out, want = _run(x, op), _run(small, op)
+    assert bool((out["gw"][0][masked] == 0).all())
+    # the same sums in other units of 128: a binary32 step or few of the loss, and of a logit's gradient what bf16 rounds twice
+    assert float((out["token_losses"][0] - want["token_losses"][0]).abs().max()) <= 2.0 ** -16
+    a, b = out["gw"][0][kept].double(), want["gw"][0].double()
+    h = x["hidden"][0].double().abs()
+    bound = 2 * (2.0 ** -8 + 2.0 ** -10) * (h.sum(0) / tokens[0]) + 2 * 2.0 ** -8 * b.abs()
+    assert bool(((a - b).abs() <= bound).all())
+
+
 CONFIDENT = [(16, 100, 32), (100, 769, 128), (60, 5000, 64)]
 
 
