@@ -256,8 +256,9 @@ int32_t check_args(const ddp_loss_head& h, const Args& a) {
         if (!a.teacher || !a.indices || a.n_teacher < 1) return DDP_ERR_INVALID;
         if (a.n_teacher > h.max_teacher) return DDP_ERR_CAPACITY;
         if (a.teacher_dtype != DDP_F32 && a.teacher_dtype != DDP_BF16) return DDP_ERR_INVALID;
-        if (!((float)a.temperature > 0.f) || !std::isfinite((float)a.temperature) ||
-            !std::isfinite((float)(1.0 / a.temperature)) || !(a.alpha > 0.0 && a.alpha <= 1.0) || !((float)a.alpha > 0.f))
+        // its square is a factor of the loss, log2 e over it (and a little) of logits
+        if (!((float)a.temperature > 0.f) || !std::isfinite((float)(a.temperature * a.temperature)) ||
+            !std::isfinite((float)(1.5 / a.temperature)) || !(a.alpha > 0.0 && a.alpha <= 1.0) || !((float)a.alpha > 0.f))
             return DDP_ERR_INVALID;
         if (!a.targets && a.alpha != 1.0) return DDP_ERR_INVALID;
     }

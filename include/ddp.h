@@ -834,7 +834,8 @@ int32_t ddp_adamw_destroy(ddp_adamw* adamw);
  *   targets[world]       device int64; for ddp_distill NULL: none (alpha is 1 then)
  *   teacher[world]       device [tokens][n_teacher] logits of teacher_dtype
  *   indices[world]       device int64 [tokens][n_teacher]
- *   temperature > 0, 0 < alpha <= 1, 1 <= n_teacher <= max_teacher
+ *   temperature > 0 (its square and 1.5 / temperature within binary32), 0 < alpha <= 1,
+ *   1 <= n_teacher <= max_teacher
  *   token_losses[world]  device float32 L_t (0: not learned); NULL, or NULL entries:
  *                        not wanted
  *   loss[world]          device float32
